@@ -65,15 +65,19 @@ typedef enum {
   MOE_ERR_BAD_ROUTING = 4, /* from moe_check_status: an expert id was out of range */
   MOE_ERR_CUDA = 5,
   MOE_ERR_TIMEOUT = 6,     /* from moe_check_status: a device pipeline wait gave up */
-  MOE_ERR_BAD_LAYOUT = 7   /* from moe_check_status: offsets/perm inconsistent */
+  MOE_ERR_BAD_LAYOUT = 7,  /* from moe_check_status: offsets/perm inconsistent */
+  MOE_ERR_BAD_CACHE = 8    /* from moe_check_status: a sequence, position or page out of range */
 } moe_status_t;
 
 /* Bits of the device status word. */
 #define MOE_DEV_BAD_ROUTING 0x1
 #define MOE_DEV_BAD_LAYOUT 0x2
 #define MOE_DEV_TIMEOUT 0x4
+#define MOE_DEV_BAD_CACHE 0x8
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype_t;
+/* MOE_E4M3 (8-bit float, 4 exponent bits, largest value 448) is a type of
+ * key-value caches only. */
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_E4M3 = 2 } moe_dtype_t;
 
 /*
  * Layout of the expert weights w13 (E,H,2I) and w2 (E,I,H) that the expert
@@ -433,6 +437,159 @@ moe_status_t moe_prepare_router(const moe_layer_desc_t *desc, const void *w_gate
                                 void *w_gate_t, moe_stream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Serving: one new token per sequence through a decoder layer.
+ *
+ * The layer of the pages is one part of a decoder's step; these calls are the
+ * parts around it for a step that adds a token to each of a few sequences:
+ * the keys and values of the new tokens enter a paged cache, each new token
+ * attends to its sequence's cache, and the routed experts run on the few
+ * tokens with 4-bit weights.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * A paged key-value cache of one layer (sizes and the caller's device memory).
+ *   k_cache, v_cache: num_pages pages of (kv_heads, page_size, head_dim)
+ *     values, a page every page_stride elements; type cache_dtype.  Inside a
+ *     page each head's tokens are one contiguous run.
+ *   page_table (num_seqs, max_pages) int32: sequence s holds its token p at
+ *     slot p % page_size of page page_table[s][p / page_size].  Entries past
+ *     a sequence's end are not read.
+ *   dtype: type of q, k, v and of the results (MOE_F32 or MOE_BF16).
+ *   cache_dtype: dtype, or MOE_E4M3 with dtype MOE_BF16.
+ *   k_scale, v_scale (kv_heads) float32, MOE_E4M3 caches only: a cached value
+ *     c of head h stands for c * scale[h].  NULL: 1.
+ *   rope (rope_rows, rope_dim) float32: row p holds the cosines and then the
+ *     sines of position p's rope_dim / 2 angles; NULL (and rope_dim 0): no
+ *     rotation.  rope_interleaved 0 pairs dimension i with i + rope_dim / 2,
+ *     1 pairs 2i with 2i + 1; dimensions from rope_dim on are not rotated.
+ * Rules: q_heads a multiple of kv_heads; head_dim 64, 128 or 256; page_size a
+ * multiple of 16; rope_dim a multiple of 16, at most head_dim; page_stride a
+ * multiple of 16 and at least kv_heads * page_size * head_dim; num_seqs at
+ * most 65536 (else MOE_ERR_UNSUPPORTED, a nonsensical value
+ * MOE_ERR_INVALID_ARG).  Pointers 16-byte aligned.
+ * Found on the device: a sequence, position or page out of range sets
+ * MOE_DEV_BAD_CACHE in the status word; such an access is skipped.
+ */
+typedef struct {
+  int32_t num_seqs;         /* rows of page_table (may be 0) */
+  int32_t q_heads;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t page_size;        /* tokens per page */
+  int32_t num_pages;
+  int32_t max_pages;        /* columns of page_table */
+  int32_t dtype;            /* moe_dtype_t */
+  int32_t cache_dtype;      /* moe_dtype_t */
+  int32_t rope_rows;
+  int32_t rope_dim;
+  int32_t rope_interleaved;
+  int64_t page_stride;      /* elements from one page to the next */
+  void *k_cache;
+  void *v_cache;
+  const int32_t *page_table;
+  const float *k_scale;
+  const float *v_scale;
+  const float *rope;
+} moe_kv_cache_t;
+
+/*
+ * Append n tokens to the cache.  Token t belongs to sequence seq_ids[t] and
+ * has position p = positions[t]:
+ *   q_out[t] = rot_p(q[t]);  K[p] = rot_p(k[t]);  V[p] = v[t]
+ * with rot_p(x)[i] = x[i] cos - x[j] sin, rot_p(x)[j] = x[j] cos + x[i] sin
+ * for every rotated pair (i, j), in float32 with each product and sum rounded
+ * (no contraction), rounded once to the stored type; a MOE_E4M3 cache stores
+ * x / scale[h] rounded to nearest even and limited to +-448 (NaN stays NaN).
+ *   q (n, q_heads, head_dim), k and v (n, kv_heads, head_dim), dtype: heads
+ *   of a token contiguous, tokens q_stride, k_stride, v_stride elements apart
+ *   (multiples of 8; views of one fused projection buffer will do).
+ *   q_out (n, q_heads, head_dim) contiguous; may be q itself when q is
+ *   contiguous.  q and q_out may both be NULL (keys and values only).
+ *   seq_ids (n), positions (n) int32.  A negative seq_ids[t] marks a padding
+ *   token: nothing of it is read or written.
+ * Two tokens of one call must not share a sequence and position.  A token
+ * whose sequence, position (also against rope_rows) or page is out of range
+ * is skipped and sets MOE_DEV_BAD_CACHE.  status_word may be NULL.
+ */
+moe_status_t moe_kv_append(const moe_kv_cache_t *cache, int32_t n, const void *q,
+                           int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                           int64_t v_stride, const int32_t *seq_ids, const int32_t *positions,
+                           void *q_out, int32_t *status_word, moe_stream_t stream);
+
+/*
+ * Attention of one new token per sequence over the cache:
+ *   out[s][h] = sum_j softmax_j(scale q[s][h] . K[j]) V[j],
+ *   j in [max(0, len - window), len), len = seq_lens[s]  (window 0: all),
+ * K and V of kv head h / (q_heads / kv_heads), read through page_table.
+ *   q (num_seqs, q_heads, head_dim) dtype, sequences q_stride elements apart
+ *   (a multiple of 8); seq_lens (num_seqs) int32, the new token included;
+ *   out (num_seqs, q_heads, head_dim) dtype, contiguous; lse (num_seqs,
+ *   q_heads) float32 or NULL: the natural logarithm of the softmax's
+ *   denominator.  A sequence of length 0 gives a zero row and lse -inf.
+ *   Cached values outside the range of j never reach the result, whatever
+ *   they hold (infinities and NaN included).
+ *   ws: moe_paged_attention_workspace_size(cache) bytes, 256-byte aligned.
+ *   It has to be zero-filled once before its first use; every call leaves the
+ *   part that it needs zeroed that way.  Calls that may run at the same time
+ *   need a workspace each.
+ * Scores, the softmax's statistics and the sums are float32.  The work is
+ * split over the tokens of long sequences and joined in a fixed order: results
+ * are bitwise reproducible on one GPU.  A length outside
+ * [0, max_pages * page_size] or a page outside [0, num_pages) sets
+ * MOE_DEV_BAD_CACHE and leaves that sequence's row unspecified (status_word
+ * may be NULL).
+ */
+size_t moe_paged_attention_workspace_size(const moe_kv_cache_t *cache);
+moe_status_t moe_paged_attention(const moe_kv_cache_t *cache, const void *q, int64_t q_stride,
+                                 const int32_t *seq_lens, int32_t window, float scale, void *out,
+                                 float *lse, void *ws, size_t ws_bytes, int32_t *status_word,
+                                 moe_stream_t stream);
+
+/*
+ * 4-bit expert weights.  A weight matrix is held by output column: row c of
+ * w13_q[e] (2I rows; [0, I) gate, [I, 2I) up) and of w2_q[e] (H rows) holds
+ * column c's codes along the reduction, eight to a 32-bit word; the code of
+ * reduction index 8w + j lies at bits 4 (j / 2) + 16 (j % 2) of word w, and
+ * `group` consecutive indices share a bf16 scale:
+ *   W[r][c] = (code - 8) * scale[c][r / group],  code in 0..15.
+ *   w13_q (E, 2I, H/8) int32, w13_s (E, 2I, H/group) bf16,
+ *   w2_q (E, H, I/8) int32,   w2_s (E, H, I/group) bf16.
+ * group 32, 64 or 128; H % 128 == 0 and I % 128 == 0 (else
+ * MOE_ERR_UNSUPPORTED).
+ *
+ * moe_quantize_weights_w4 makes them from row-major bf16 w13 (E,H,2I) and w2
+ * (E,I,H): scale = bf16(max |w| of the group / 7), code = 8 + w / scale
+ * rounded to nearest even and limited to 0..15 (a group of zeros: scale 0, codes 8).
+ * The descriptor's n, K and weight_layout are not used.
+ */
+moe_status_t moe_quantize_weights_w4(const moe_layer_desc_t *desc, int group, const void *w13,
+                                     const void *w2, int32_t *w13_q, void *w13_s, int32_t *w2_q,
+                                     void *w2_s, moe_stream_t stream);
+
+/*
+ * The routed experts of a few tokens on 4-bit weights (bf16 layers):
+ *   y[t] = sum_k topk_w[t,k] W2[e]^T h,  h = SiLU(W13[e]^T x[t], gate) * up,
+ *   e = topk_idx[t,k]
+ * (Algorithm 2 steps 4-11 with the weights above).  Each hit expert's weights
+ * are read once for every 32 of its tokens; sums are float32, h is carried in
+ * two bf16 parts (about 16 significant bits), y is rounded once.  Results are
+ * bitwise reproducible.
+ *   x (n,H) bf16, topk_idx (n,K) int32, topk_w (n,K) float32, y (n,H) bf16;
+ *   n * K <= 4096 (else MOE_ERR_UNSUPPORTED): above that the bf16 grouped
+ *   GEMMs are the better path.  An expert id outside [0, E) contributes
+ *   nothing and sets MOE_DEV_BAD_ROUTING (status_word may be NULL).
+ *   ws: moe_experts_w4_workspace_size(desc) bytes, 256-byte aligned, contents
+ *   need no initialisation.
+ */
+size_t moe_experts_w4_workspace_size(const moe_layer_desc_t *desc);
+moe_status_t moe_experts_w4(const moe_layer_desc_t *desc, int group, const void *x,
+                            const int32_t *topk_idx, const float *topk_w, const int32_t *w13_q,
+                            const void *w13_s, const int32_t *w2_q, const void *w2_s, void *y,
+                            void *ws, size_t ws_bytes, int32_t *status_word, moe_stream_t stream);
+
+/*
  * Test control for the device timeout path (failure detection without a
  * fault): the number of SM clock cycles a pipeline wait of the tensor-core
  * grouped GEMMs (moe_expert_gemm1_swiglu, moe_expert_gemm2,
@@ -481,8 +638,8 @@ moe_status_t moe_set_gemm_tails(int mode);
 
 /*
  * Blocks until `stream` is idle, then reads *status_word and maps it to
- * MOE_OK, MOE_ERR_BAD_ROUTING, MOE_ERR_BAD_LAYOUT or MOE_ERR_TIMEOUT (first
- * match in that order).  Intended for tests and debugging.
+ * MOE_OK, MOE_ERR_BAD_ROUTING, MOE_ERR_BAD_LAYOUT, MOE_ERR_TIMEOUT or
+ * MOE_ERR_BAD_CACHE (first match in that order).  Intended for tests and debugging.
  */
 moe_status_t moe_check_status(const int32_t *status_word, moe_stream_t stream);
 

@@ -16,3 +16,4 @@ from .api import (  # noqa: E402,F401
     moe_prepare_weights, moe_set_pipeline_wait_limit, moe_set_gemm_pairs, moe_prepare_router,
     moe_set_gemm_tails,
 )
+from .decode import PagedKVCache, W4Experts, quantize_weights_w4, rope_table  # noqa: E402,F401

@@ -21,14 +21,17 @@ SYMBOLS = (
     "moe_combine_slots", "moe_backward_workspace_size", "moe_backward",
     "moe_set_pipeline_wait_limit", "moe_prepare_weights", "moe_set_gemm_pairs",
     "moe_prepare_router", "moe_set_gemm_tails",
+    "moe_kv_append", "moe_paged_attention_workspace_size", "moe_paged_attention",
+    "moe_quantize_weights_w4", "moe_experts_w4_workspace_size", "moe_experts_w4",
 )
 
-MOE_F32, MOE_BF16 = 0, 1
+MOE_F32, MOE_BF16, MOE_E4M3 = 0, 1, 2
 MOE_WEIGHTS_ROW_MAJOR, MOE_WEIGHTS_TILED = 0, 1
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_WORKSPACE",
           4: "MOE_ERR_BAD_ROUTING", 5: "MOE_ERR_CUDA", 6: "MOE_ERR_TIMEOUT",
-          7: "MOE_ERR_BAD_LAYOUT"}
-DEV_BAD_ROUTING, DEV_BAD_LAYOUT, DEV_TIMEOUT = 0x1, 0x2, 0x4
+          7: "MOE_ERR_BAD_LAYOUT", 8: "MOE_ERR_BAD_CACHE"}
+DEV_BAD_ROUTING, DEV_BAD_LAYOUT, DEV_TIMEOUT, DEV_BAD_CACHE = 0x1, 0x2, 0x4, 0x8
+W4_MAX_PAIRS = 4096  # largest n * K of moe_experts_w4
 NOALLOC_MAX_PAIRS = 524288  # MOE_NOALLOC_MAX_PAIRS
 
 # workspace slots of moe_workspace_slot
@@ -43,9 +46,20 @@ class LayerDesc(ctypes.Structure):
                 ("w_gate_t", ctypes.c_void_p)]
 
 
+class KVCacheDesc(ctypes.Structure):
+    """moe_kv_cache_t"""
+    _fields_ = [(name, ctypes.c_int32) for name in (
+        "num_seqs", "q_heads", "kv_heads", "head_dim", "page_size", "num_pages", "max_pages",
+        "dtype", "cache_dtype", "rope_rows", "rope_dim", "rope_interleaved")] + [
+        ("page_stride", ctypes.c_int64)] + [(name, ctypes.c_void_p) for name in (
+            "k_cache", "v_cache", "page_table", "k_scale", "v_scale", "rope")]
+
+
 _vp = ctypes.c_void_p
 _desc_p = ctypes.POINTER(LayerDesc)
+_cache_p = ctypes.POINTER(KVCacheDesc)
 _st = ctypes.c_int
+_i32, _i64, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 
 
 def _declare(lib):
@@ -86,6 +100,14 @@ def _declare(lib):
         "moe_backward": (_st, [_desc_p] + [_vp] * 19 + [ctypes.c_size_t, _vp, _vp]),
         "moe_forward_host": (_st, [_desc_p, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t,
                                    ctypes.c_longlong, _vp, _vp, _vp, _vp]),
+        "moe_kv_append": (_st, [_cache_p, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                                _vp, _vp]),
+        "moe_paged_attention_workspace_size": (_sz, [_cache_p]),
+        "moe_paged_attention": (_st, [_cache_p, _vp, _i64, _vp, _i32, ctypes.c_float, _vp, _vp,
+                                      _vp, _sz, _vp, _vp]),
+        "moe_quantize_weights_w4": (_st, [_desc_p, ctypes.c_int] + [_vp] * 7),
+        "moe_experts_w4_workspace_size": (_sz, [_desc_p]),
+        "moe_experts_w4": (_st, [_desc_p, ctypes.c_int] + [_vp] * 9 + [_sz, _vp, _vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)

@@ -37,6 +37,9 @@ struct Desc {
   long long nK() const { return (long long)n * K; }
 };
 
+// Shared checks of the layer description (moe_api.cu).
+moe_status_t check_desc(const moe_layer_desc_t *d, Desc *out);
+
 inline size_t elem_bytes(const Desc &d) { return d.bf16 ? 2 : 4; }
 
 // ---- router.cu (dispatches to router_mma.cu or router_tc.cu for bf16 layers)

@@ -1,0 +1,221 @@
+// Appending keys and values to a paged cache, with the position rotation of
+// queries and keys on the way:
+//   q_out[t] = rot(q[t]), K[page][h][slot] = rot(k[t]), V[page][h][slot] = v[t]
+// with rot(x)_i = x_i cos - x_j sin, rot(x)_j = x_j cos + x_i sin over the
+// rotated pairs (i, j), page and slot from the token's sequence and position.
+//
+// Bound: HBM for a prefill chunk (every value is read once and written once),
+// latency for a decode batch (ids -> page -> store is a chain of dependent
+// loads).  A CTA owns one token, so the chain is walked once per CTA and the
+// token's cosines and sines are read once per thread and used for every head:
+// thread (row lane, j) moves the j-th 16 values of the head rows row lane,
+// row lane + lanes, ...  16 values are two vectors of 8 that rotate with each
+// other (i and i + rope_dim/2, or 16 neighbours when pairs are interleaved),
+// so no value is loaded twice and q may be rotated in place.
+#include <cuda_fp8.h>
+
+#include "kv_cache.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int AT = 128;  // threads per CTA
+constexpr int AU = 4;    // head rows in flight per thread
+
+struct AppendArgs {
+  const void *q, *k, *v;
+  long long qs, ks, vs;  // elements between tokens
+  const int32_t *seq_ids, *positions, *table;
+  const float *rope, *kscale, *vscale;
+  void *qout, *kc, *vc;
+  long long page_stride;
+  int num_seqs, Hq, Hkv, P, num_pages, max_pages, rope_rows, R, interleaved;
+  int rows_per_cta;  // head rows (q, k and v) of one CTA
+  int32_t *status;
+};
+
+struct Vec8 {
+  float f[8];
+};
+
+__device__ __forceinline__ Vec8 load8(const __nv_bfloat16 *p) {
+  const uint4 u = *reinterpret_cast<const uint4 *>(p);
+  const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
+  Vec8 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = __bfloat1622float2(h[i]);
+    v.f[2 * i] = x.x;
+    v.f[2 * i + 1] = x.y;
+  }
+  return v;
+}
+
+__device__ __forceinline__ Vec8 load8(const float *p) {
+  Vec8 v;
+  *reinterpret_cast<float4 *>(v.f) = *reinterpret_cast<const float4 *>(p);
+  *reinterpret_cast<float4 *>(v.f + 4) = *reinterpret_cast<const float4 *>(p + 4);
+  return v;
+}
+
+// Stored values are rounded once from float32; scale is used by e4m3 only.
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const Vec8 &v, float) {
+  uint4 u;
+  __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v.f[2 * i], v.f[2 * i + 1]);
+  *reinterpret_cast<uint4 *>(p) = u;
+}
+
+__device__ __forceinline__ void store8(float *p, const Vec8 &v, float) {
+  *reinterpret_cast<float4 *>(p) = *reinterpret_cast<const float4 *>(v.f);
+  *reinterpret_cast<float4 *>(p + 4) = *reinterpret_cast<const float4 *>(v.f + 4);
+}
+
+__device__ __forceinline__ void store8(__nv_fp8_e4m3 *p, const Vec8 &v, float scale) {
+  uint2 u;
+  __nv_fp8x2_storage_t *h = reinterpret_cast<__nv_fp8x2_storage_t *>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    h[i] = __nv_cvt_float2_to_fp8x2(
+        make_float2(__fdiv_rn(v.f[2 * i], scale), __fdiv_rn(v.f[2 * i + 1], scale)),
+        __NV_SATFINITE, __NV_E4M3);
+  *reinterpret_cast<uint2 *>(p) = u;
+}
+
+// One pair: products and sums are rounded one by one, so a value does not
+// depend on how the compiler contracts them.
+__device__ __forceinline__ void rotate(float &a, float &b, float c, float s) {
+  const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+  a = x;
+}
+
+template <int D, typename T, typename C>
+__global__ void __launch_bounds__(AT) kv_append_kernel(const AppendArgs a) {
+  pdl_enter();
+  constexpr int JT = D / 16, RL = AT / JT;
+  const int t = blockIdx.x;
+  const int j = threadIdx.x % JT, rl = threadIdx.x / JT;
+  const int seq = __ldg(a.seq_ids + t), pos = __ldg(a.positions + t);
+  if (seq < 0) return;  // padding
+  bool ok = seq < a.num_seqs && pos >= 0 && pos / a.P < a.max_pages &&
+            (a.R == 0 || pos < a.rope_rows);
+  int page = -1;
+  if (ok) page = __ldg(a.table + (size_t)seq * a.max_pages + pos / a.P);
+  ok = ok && page >= 0 && page < a.num_pages;
+  if (!ok) {
+    if (threadIdx.x == 0) flag_status(a.status, MOE_DEV_BAD_CACHE);
+    return;
+  }
+  const size_t slot = (size_t)page * a.page_stride + (size_t)(pos % a.P) * D;
+  const size_t head_step = (size_t)a.P * D;
+  // this thread's 16 dimensions of every head row, as two vectors of 8
+  const int half = a.R >> 1;
+  const bool rot = 16 * j < a.R;
+  const bool split = rot && !a.interleaved;
+  const int d0 = split ? 8 * j : 16 * j;
+  const int d1 = split ? half + 8 * j : d0 + 8;
+  Vec8 cs, sn;
+  if (rot) {
+    const float *row = a.rope + (size_t)pos * a.R + 8 * j;
+    cs = load8(row);
+    sn = load8(row + half);
+  }
+  const int r0 = blockIdx.y * a.rows_per_cta;
+  const int r1 = min(r0 + a.rows_per_cta, a.Hq + 2 * a.Hkv);
+  for (int rb = r0 + rl; rb < r1; rb += AU * RL) {
+    Vec8 lo[AU], hi[AU];
+#pragma unroll
+    for (int u = 0; u < AU; ++u) {
+      const int r = rb + u * RL;
+      if (r >= r1 || (r < a.Hq && !a.q)) continue;
+      const T *src = r < a.Hq ? (const T *)a.q + t * a.qs + (size_t)r * D
+                     : r < a.Hq + a.Hkv
+                         ? (const T *)a.k + t * a.ks + (size_t)(r - a.Hq) * D
+                         : (const T *)a.v + t * a.vs + (size_t)(r - a.Hq - a.Hkv) * D;
+      const bool v = r >= a.Hq + a.Hkv;  // values are not rotated: neighbours
+      lo[u] = load8(src + (v ? 16 * j : d0));
+      hi[u] = load8(src + (v ? 16 * j + 8 : d1));
+    }
+#pragma unroll
+    for (int u = 0; u < AU; ++u) {
+      const int r = rb + u * RL;
+      if (r >= r1 || (r < a.Hq && !a.q)) continue;
+      if (r >= a.Hq + a.Hkv) {
+        const int h = r - a.Hq - a.Hkv;
+        const float sc = a.vscale ? __ldg(a.vscale + h) : 1.f;
+        C *dst = (C *)a.vc + slot + h * head_step + 16 * j;
+        store8(dst, lo[u], sc);
+        store8(dst + 8, hi[u], sc);
+        continue;
+      }
+      if (split) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) rotate(lo[u].f[i], hi[u].f[i], cs.f[i], sn.f[i]);
+      } else if (rot) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          rotate(lo[u].f[2 * i], lo[u].f[2 * i + 1], cs.f[i], sn.f[i]);
+          rotate(hi[u].f[2 * i], hi[u].f[2 * i + 1], cs.f[4 + i], sn.f[4 + i]);
+        }
+      }
+      if (r < a.Hq) {
+        T *dst = (T *)a.qout + ((size_t)t * a.Hq + r) * D;
+        store8(dst + d0, lo[u], 1.f);
+        store8(dst + d1, hi[u], 1.f);
+      } else {
+        const int h = r - a.Hq;
+        const float sc = a.kscale ? __ldg(a.kscale + h) : 1.f;
+        C *dst = (C *)a.kc + slot + h * head_step;
+        store8(dst + d0, lo[u], sc);
+        store8(dst + d1, hi[u], sc);
+      }
+    }
+  }
+}
+
+template <int D, typename T, typename C>
+cudaError_t append_d(AppendArgs &a, int n, cudaStream_t s) {
+  constexpr int RL = AT / (D / 16);
+  const int rows = a.Hq + 2 * a.Hkv;
+  // few tokens: their head rows are spread over CTAs, one row per thread;
+  // many: one CTA per token
+  const int parts = (rows + RL - 1) / RL;
+  const bool spread = (long long)n * parts <= 8ll * device_sm_count();
+  a.rows_per_cta = spread ? RL : rows;
+  return launch_pdl(kv_append_kernel<D, T, C>, dim3(n, spread ? parts : 1), dim3(AT), 0, s, a);
+}
+
+template <typename T, typename C>
+cudaError_t append_t(AppendArgs &a, int D, int n, cudaStream_t s) {
+  if (D == 64) return append_d<64, T, C>(a, n, s);
+  if (D == 128) return append_d<128, T, C>(a, n, s);
+  return append_d<256, T, C>(a, n, s);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const KVCache &c, int n, const void *q, long long q_stride,
+                             const void *k, long long k_stride, const void *v, long long v_stride,
+                             const int32_t *seq_ids, const int32_t *positions, void *q_out,
+                             int32_t *status, cudaStream_t s) {
+  if (n == 0) return cudaSuccess;
+  AppendArgs a = {};
+  a.q = q, a.k = k, a.v = v;
+  a.qs = q_stride, a.ks = k_stride, a.vs = v_stride;
+  a.seq_ids = seq_ids, a.positions = positions, a.table = c.page_table;
+  a.rope = c.rope, a.kscale = c.k_scale, a.vscale = c.v_scale;
+  a.qout = q_out, a.kc = c.k_cache, a.vc = c.v_cache;
+  a.page_stride = c.page_stride;
+  a.num_seqs = c.num_seqs, a.Hq = c.q_heads, a.Hkv = c.kv_heads, a.P = c.page_size;
+  a.num_pages = c.num_pages, a.max_pages = c.max_pages;
+  a.rope_rows = c.rope_rows, a.R = c.rope ? c.rope_dim : 0, a.interleaved = c.rope_interleaved;
+  a.status = status;
+  if (c.dtype == MOE_F32) return append_t<float, float>(a, c.head_dim, n, s);
+  if (c.cache_dtype == MOE_E4M3)
+    return append_t<__nv_bfloat16, __nv_fp8_e4m3>(a, c.head_dim, n, s);
+  return append_t<__nv_bfloat16, __nv_bfloat16>(a, c.head_dim, n, s);
+}
+
+}  // namespace moe

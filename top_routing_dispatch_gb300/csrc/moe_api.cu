@@ -35,7 +35,8 @@ namespace {
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Shared checks of the layer description.
+}  // namespace
+
 moe_status_t check_desc(const moe_layer_desc_t *d, Desc *out) {
   if (!d) return MOE_ERR_INVALID_ARG;
   if (d->n < 0 || d->H < 1 || d->I < 1 || d->E < 1 || d->K < 1) return MOE_ERR_INVALID_ARG;
@@ -61,6 +62,8 @@ moe_status_t check_desc(const moe_layer_desc_t *d, Desc *out) {
   out->w_gate_t = bf16 ? d->w_gate_t : nullptr;
   return MOE_OK;
 }
+
+namespace {
 
 moe_status_t check_gemm_shape(const Desc &d) {
   if (d.bf16) {
@@ -178,6 +181,7 @@ const char *moe_status_string(moe_status_t s) {
     case MOE_ERR_CUDA: return "CUDA error";
     case MOE_ERR_TIMEOUT: return "device pipeline wait timed out";
     case MOE_ERR_BAD_LAYOUT: return "inconsistent dispatch layout";
+    case MOE_ERR_BAD_CACHE: return "sequence, position or page of the key-value cache out of range";
   }
   return "unknown status";
 }
@@ -752,6 +756,7 @@ moe_status_t moe_check_status(const int32_t *status_word, moe_stream_t stream) {
   if (v & MOE_DEV_BAD_ROUTING) return MOE_ERR_BAD_ROUTING;
   if (v & MOE_DEV_BAD_LAYOUT) return MOE_ERR_BAD_LAYOUT;
   if (v & MOE_DEV_TIMEOUT) return MOE_ERR_TIMEOUT;
+  if (v & MOE_DEV_BAD_CACHE) return MOE_ERR_BAD_CACHE;
   return MOE_OK;
 }
 
