@@ -38,25 +38,38 @@ struct Vec8 {
   float f[8];
 };
 
-__device__ __forceinline__ Vec8 load8(const __nv_bfloat16 *p) {
-  const uint4 u = *reinterpret_cast<const uint4 *>(p);
-  const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
-  Vec8 v;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 x = __bfloat1622float2(h[i]);
-    v.f[2 * i] = x.x;
-    v.f[2 * i + 1] = x.y;
+// 8 values as they lie in memory; widened when they are used
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+    u = __ldcs(reinterpret_cast<const uint4 *>(p));
   }
-  return v;
-}
-
-__device__ __forceinline__ Vec8 load8(const float *p) {
-  Vec8 v;
-  *reinterpret_cast<float4 *>(v.f) = *reinterpret_cast<const float4 *>(p);
-  *reinterpret_cast<float4 *>(v.f + 4) = *reinterpret_cast<const float4 *>(p + 4);
-  return v;
-}
+  __device__ __forceinline__ Vec8 widen() const {
+    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
+    Vec8 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = __bfloat1622float2(h[i]);
+      v.f[2 * i] = x.x;
+      v.f[2 * i + 1] = x.y;
+    }
+    return v;
+  }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float *p) {
+    a = __ldcs(reinterpret_cast<const float4 *>(p));
+    b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+  }
+  __device__ __forceinline__ Vec8 widen() const {
+    return Vec8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+  }
+};
 
 // Stored values are rounded once from float32; scale is used by e4m3 only.
 __device__ __forceinline__ void store8(__nv_bfloat16 *p, const Vec8 &v, float) {
@@ -98,80 +111,91 @@ __global__ void __launch_bounds__(AT) kv_append_kernel(const AppendArgs a) {
   const int t = blockIdx.x;
   const int j = threadIdx.x % JT, rl = threadIdx.x / JT;
   const int seq = __ldg(a.seq_ids + t), pos = __ldg(a.positions + t);
-  if (seq < 0) return;  // padding
-  bool ok = seq < a.num_seqs && pos >= 0 && pos / a.P < a.max_pages &&
-            (a.R == 0 || pos < a.rope_rows);
-  int page = -1;
-  if (ok) page = __ldg(a.table + (size_t)seq * a.max_pages + pos / a.P);
-  ok = ok && page >= 0 && page < a.num_pages;
-  if (!ok) {
-    if (threadIdx.x == 0) flag_status(a.status, MOE_DEV_BAD_CACHE);
-    return;
-  }
-  const size_t slot = (size_t)page * a.page_stride + (size_t)(pos % a.P) * D;
-  const size_t head_step = (size_t)a.P * D;
   // this thread's 16 dimensions of every head row, as two vectors of 8
   const int half = a.R >> 1;
   const bool rot = 16 * j < a.R;
   const bool split = rot && !a.interleaved;
   const int d0 = split ? 8 * j : 16 * j;
   const int d1 = split ? half + 8 * j : d0 + 8;
-  Vec8 cs, sn;
-  if (rot) {
-    const float *row = a.rope + (size_t)pos * a.R + 8 * j;
-    cs = load8(row);
-    sn = load8(row + half);
-  }
   const int r0 = blockIdx.y * a.rows_per_cta;
   const int r1 = min(r0 + a.rows_per_cta, a.Hq + 2 * a.Hkv);
-  for (int rb = r0 + rl; rb < r1; rb += AU * RL) {
-    Vec8 lo[AU], hi[AU];
+  const int rk = a.Hq, rv = a.Hq + a.Hkv;  // first key row, first value row
+  Raw8<T> lo[AU], hi[AU];
+  auto fetch = [&](int rb) {
 #pragma unroll
     for (int u = 0; u < AU; ++u) {
       const int r = rb + u * RL;
-      if (r >= r1 || (r < a.Hq && !a.q)) continue;
-      const T *src = r < a.Hq ? (const T *)a.q + t * a.qs + (size_t)r * D
-                     : r < a.Hq + a.Hkv
-                         ? (const T *)a.k + t * a.ks + (size_t)(r - a.Hq) * D
-                         : (const T *)a.v + t * a.vs + (size_t)(r - a.Hq - a.Hkv) * D;
-      const bool v = r >= a.Hq + a.Hkv;  // values are not rotated: neighbours
-      lo[u] = load8(src + (v ? 16 * j : d0));
-      hi[u] = load8(src + (v ? 16 * j + 8 : d1));
+      if (r >= r1 || (r < rk && !a.q)) continue;
+      const T *src = r < rk   ? (const T *)a.q + t * a.qs + r * D
+                     : r < rv ? (const T *)a.k + t * a.ks + (r - rk) * D
+                              : (const T *)a.v + t * a.vs + (r - rv) * D;
+      lo[u].load(src + (r >= rv ? 16 * j : d0));  // values are not rotated: neighbours
+      hi[u].load(src + (r >= rv ? 16 * j + 8 : d1));
     }
+  };
+  // the rows do not depend on where the token goes: they are on their way
+  // while its page is looked up
+  if (seq >= 0) fetch(r0 + rl);
+  if (seq < 0) return;  // padding
+  const int col = pos / a.P;
+  bool ok = seq < a.num_seqs && pos >= 0 && col < a.max_pages && (a.R == 0 || pos < a.rope_rows);
+  int page = -1;
+  Vec8 cs = {}, sn = {};
+  if (ok) {
+    page = __ldg(a.table + (size_t)seq * a.max_pages + col);
+    if (rot) {
+      const float4 *row = reinterpret_cast<const float4 *>(a.rope + (size_t)pos * a.R + 8 * j);
+      *reinterpret_cast<float4 *>(cs.f) = __ldg(row);
+      *reinterpret_cast<float4 *>(cs.f + 4) = __ldg(row + 1);
+      *reinterpret_cast<float4 *>(sn.f) = __ldg(row + half / 4);
+      *reinterpret_cast<float4 *>(sn.f + 4) = __ldg(row + half / 4 + 1);
+    }
+  }
+  ok = ok && page >= 0 && page < a.num_pages;
+  if (!ok) {
+    if (threadIdx.x == 0 && blockIdx.y == 0) flag_status(a.status, MOE_DEV_BAD_CACHE);
+    return;
+  }
+  const size_t slot = (size_t)page * a.page_stride + (size_t)(pos - col * a.P) * D;
+  const int head_step = a.P * D;
+  for (int rb = r0 + rl; rb < r1;) {
 #pragma unroll
     for (int u = 0; u < AU; ++u) {
       const int r = rb + u * RL;
-      if (r >= r1 || (r < a.Hq && !a.q)) continue;
-      if (r >= a.Hq + a.Hkv) {
-        const int h = r - a.Hq - a.Hkv;
+      if (r >= r1 || (r < rk && !a.q)) continue;
+      Vec8 x = lo[u].widen(), y = hi[u].widen();
+      if (r >= rv) {
+        const int h = r - rv;
         const float sc = a.vscale ? __ldg(a.vscale + h) : 1.f;
-        C *dst = (C *)a.vc + slot + h * head_step + 16 * j;
-        store8(dst, lo[u], sc);
-        store8(dst + 8, hi[u], sc);
+        C *dst = (C *)a.vc + slot + (size_t)h * head_step + 16 * j;
+        store8(dst, x, sc);
+        store8(dst + 8, y, sc);
         continue;
       }
       if (split) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) rotate(lo[u].f[i], hi[u].f[i], cs.f[i], sn.f[i]);
+        for (int i = 0; i < 8; ++i) rotate(x.f[i], y.f[i], cs.f[i], sn.f[i]);
       } else if (rot) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          rotate(lo[u].f[2 * i], lo[u].f[2 * i + 1], cs.f[i], sn.f[i]);
-          rotate(hi[u].f[2 * i], hi[u].f[2 * i + 1], cs.f[4 + i], sn.f[4 + i]);
+          rotate(x.f[2 * i], x.f[2 * i + 1], cs.f[i], sn.f[i]);
+          rotate(y.f[2 * i], y.f[2 * i + 1], cs.f[4 + i], sn.f[4 + i]);
         }
       }
-      if (r < a.Hq) {
+      if (r < rk) {
         T *dst = (T *)a.qout + ((size_t)t * a.Hq + r) * D;
-        store8(dst + d0, lo[u], 1.f);
-        store8(dst + d1, hi[u], 1.f);
+        store8(dst + d0, x, 1.f);
+        store8(dst + d1, y, 1.f);
       } else {
-        const int h = r - a.Hq;
+        const int h = r - rk;
         const float sc = a.kscale ? __ldg(a.kscale + h) : 1.f;
-        C *dst = (C *)a.kc + slot + h * head_step;
-        store8(dst + d0, lo[u], sc);
-        store8(dst + d1, hi[u], sc);
+        C *dst = (C *)a.kc + slot + (size_t)h * head_step;
+        store8(dst + d0, x, sc);
+        store8(dst + d1, y, sc);
       }
     }
+    rb += AU * RL;
+    if (rb < r1) fetch(rb);
   }
 }
 

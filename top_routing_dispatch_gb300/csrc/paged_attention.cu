@@ -33,7 +33,6 @@
 // float32 caches take the same road with multiply-adds on the FMA units in
 // place of the matrix instructions, which have no float32 operands.
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
 #include "kv_cache.cuh"
 #include "ptx.cuh"
@@ -45,7 +44,8 @@ constexpr int kMaxWorkers = 512;  // CTAs that may hold parts
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 8.f;
-constexpr int kMinUnits = 2;  // fewer units are not worth a part of their own
+constexpr int kItemCost = 2;  // a new item's overhead, in units
+constexpr int kSnap = 4;      // a range's end this near an item's edge moves to it (> kItemCost)
 
 struct AttnArgs {
   const void *q;
@@ -73,6 +73,24 @@ __device__ __forceinline__ void cp_async8_zfill(uint32_t dst, const void *src, b
   const int n = ok ? 8 : 0;
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n)
                : "memory");
+}
+// A piece of `bytes`; EDGE steps zero-fill what is not ok.
+template <int BYTES, bool EDGE>
+__device__ __forceinline__ void copy_piece(uint32_t dst, const uint8_t *src, bool ok) {
+  if constexpr (EDGE && BYTES == 16)
+    cp_async16_zfill(dst, src, ok);
+  else if constexpr (EDGE)
+    cp_async8_zfill(dst, src, ok);
+  else if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+// 2^x by the hardware's approximation (relative error 2^-22, tiny results 0)
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
@@ -103,16 +121,24 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// two e4m3 bytes (low half of x) as two halves
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
-  const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)x, __NV_E4M3);
-  return (uint32_t)r.x | ((uint32_t)r.y << 16);
+// four e4m3 bytes as two pairs of halves
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t &lo, uint32_t &hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
 }
 __device__ __forceinline__ uint32_t word(const uint4 &v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 __device__ __forceinline__ void store_out(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void store_out(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store_out2(__nv_bfloat16 *p, float x, float y) {
+  *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x, y);
+}
+__device__ __forceinline__ void store_out2(float *p, float x, float y) {
+  *reinterpret_cast<float2 *>(p) = make_float2(x, y);
+}
 
 // One lane's piece of a raise of the running maxima: the reduction over the
 // eight lanes that hold the same heads.
@@ -128,7 +154,7 @@ __device__ __forceinline__ float sum_over_g(float v) {
 }
 // exp2(a - b) of running maxima, 0 where the part is empty
 __device__ __forceinline__ float rescale(float a, float b) {
-  return a == -INFINITY ? 0.f : exp2f(a - b);
+  return a == -INFINITY ? 0.f : ex2(a - b);
 }
 
 // ---------------------------------------------------------------------------
@@ -148,68 +174,80 @@ struct MmaPath {
   static constexpr int NCH = MI;
   static constexpr int Q_SMEM = 0;
 
+  static constexpr int QP = E4M3 ? 2 : 1;  // 16-byte pieces of q to a piece of K
+  uint4 qr[NT][KJ][QP];  // the next item's queries, on their way
   uint32_t qf[NT][KJ][E4M3 ? 8 : 4];
   float o[MI][MJ][NT][4];
   float m[NT][2], l[NT][2], mult[NT][2];
 
-  __device__ __forceinline__ static void issue(uint32_t slot, const uint8_t *k, const uint8_t *v,
+  // a lane's first piece of K and of V within a step's rows
+  __device__ __forceinline__ static int k_lane(int lane) {
+    return (lane >> 2) * (D * EB) + (lane & 3) * 16;
+  }
+  __device__ __forceinline__ static int v_lane(int lane) {
+    return 2 * (lane & 3) * (D * EB) + (lane >> 2) * (VE * EB);
+  }
+  // k, v: this lane's first pieces; EDGE: only rows in [lo, hi), zeros elsewhere
+  template <bool EDGE>
+  __device__ __forceinline__ static void issue(uint32_t dst, const uint8_t *k, const uint8_t *v,
                                                int lo, int hi, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    uint32_t dst = slot + lane * 16;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int row = g + 8 * r;
-      const bool ok = row >= lo && row < hi;
-      const uint8_t *src = k + (size_t)row * (D * EB) + t * 16;
+      const bool ok = g + 8 * r >= lo && g + 8 * r < hi;
 #pragma unroll
-      for (int j = 0; j < KJ; ++j, dst += 512) cp_async16_zfill(dst, src + j * 64, ok);
+      for (int j = 0; j < KJ; ++j)
+        copy_piece<16, EDGE>(dst + (r * KJ + j) * 512, k + 8 * r * (D * EB) + j * 64, ok);
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int row = 2 * t + (r & 1) + 8 * (r >> 1);
-      const bool ok = row >= lo && row < hi;
-      const uint8_t *src = v + (size_t)row * (D * EB) + g * (VE * EB);
+      const int row = (r & 1) + 8 * (r >> 1);
+      const bool ok = 2 * t + row >= lo && 2 * t + row < hi;
 #pragma unroll
-      for (int i = 0; i < MI; ++i, dst += 512) {
-        if constexpr (VE * EB == 16)
-          cp_async16_zfill(dst, src + i * 128, ok);
-        else
-          cp_async8_zfill(dst, src + i * 64, ok);
-      }
+      for (int i = 0; i < MI; ++i)
+        copy_piece<VE * EB, EDGE>(dst + (2 * KJ + r * MI + i) * 512,
+                                  v + row * (D * EB) + i * (8 * VE * EB), ok);
     }
   }
 
-  // nh query heads from q (head rows contiguous); sc: scale (and k scale)
-  __device__ __forceinline__ void begin(const Out *q, int nh, float sc, int lane, float *) {
+  // asks for nh query heads (head rows contiguous)
+  __device__ __forceinline__ void fetch(const Out *q, int nh, int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const bool ok = 8 * n + g < nh;
       const uint4 *row = reinterpret_cast<const uint4 *>(q + (size_t)(ok ? 8 * n + g : 0) * D);
+#pragma unroll
+      for (int j = 0; j < KJ; ++j)
+#pragma unroll
+        for (int i = 0; i < QP; ++i)
+          qr[n][j][i] = ok ? __ldg(row + QP * (t + 4 * j) + i) : make_uint4(0, 0, 0, 0);
+    }
+  }
+
+  // starts an item on the queries fetched; sc: scale (and k scale)
+  __device__ __forceinline__ void begin(const Out *, int, float sc, int lane, float *) {
+    const int t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
       if constexpr (!E4M3) {
 #pragma unroll
-        for (int j = 0; j < KJ; ++j) {
-          const uint4 x = ok ? __ldg(row + t + 4 * j) : make_uint4(0, 0, 0, 0);
-          qf[n][j][0] = x.x, qf[n][j][1] = x.y, qf[n][j][2] = x.z, qf[n][j][3] = x.w;
-        }
+        for (int j = 0; j < KJ; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) qf[n][j][e] = word(qr[n][j][0], e);
         mult[n][0] = mult[n][1] = sc;
       } else {
         // e4m3 values are halves exactly; q as halves too, each head scaled by
         // a power of two so that its largest value is in [1, 2): bf16's 8
         // significant bits fit, and what falls under 2^-24 of the largest goes
-        float f[KJ][16], top = 0.f;
+        float top = 0.f;
 #pragma unroll
         for (int j = 0; j < KJ; ++j)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint4 x = ok ? __ldg(row + 2 * (t + 4 * j) + i) : make_uint4(0, 0, 0, 0);
-            const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&x);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 y = __bfloat1622float2(h[e]);
-              f[j][8 * i + 2 * e] = y.x, f[j][8 * i + 2 * e + 1] = y.y;
-              top = fmaxf(top, fmaxf(fabsf(y.x), fabsf(y.y)));
-            }
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t x = word(qr[n][j][e >> 2], e & 3);
+            const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&x));
+            top = fmaxf(top, fmaxf(fabsf(y.x), fabsf(y.y)));
           }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -221,7 +259,9 @@ struct MmaPath {
         for (int j = 0; j < KJ; ++j)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const __half2 h = __floats2half2_rn(f[j][2 * e] * down, f[j][2 * e + 1] * down);
+            const uint32_t x = word(qr[n][j][e >> 2], e & 3);
+            const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&x));
+            const __half2 h = __floats2half2_rn(y.x * down, y.y * down);
             qf[n][j][e] = *reinterpret_cast<const uint32_t *>(&h);
           }
         mult[n][0] = __shfl_sync(0xffffffffu, up, 8 * t);
@@ -238,14 +278,16 @@ struct MmaPath {
     }
   }
 
-  // keys [lo, hi) of the 16 in the slot
-  __device__ __forceinline__ void step(uint32_t slot, int lo, int hi, int nh, int lane,
+  // the 16 keys of a slot (src: this lane's pieces); EDGE: only [lo, hi) count
+  template <bool EDGE>
+  __device__ __forceinline__ void step(uint32_t src, int lo, int hi, int nh, int lane,
                                        const float *) {
     const int g = lane >> 2;
-    uint32_t src = slot + lane * 16;
-    float s[NT][4];
+    float s[NT][4], s2[NT][4];  // two chains of sums
 #pragma unroll
-    for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
 #pragma unroll
     for (int j = 0; j < KJ; ++j) {
       const uint4 a = lds128(src + j * 512), b = lds128(src + (KJ + j) * 512);
@@ -253,30 +295,31 @@ struct MmaPath {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           mma16816<false>(s[n], a.x, b.x, a.y, b.y, qf[n][j][0], qf[n][j][1]);
-          mma16816<false>(s[n], a.z, b.z, a.w, b.w, qf[n][j][2], qf[n][j][3]);
+          mma16816<false>(s2[n], a.z, b.z, a.w, b.w, qf[n][j][2], qf[n][j][3]);
         }
       } else {
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const uint32_t x = word(a, w), y = word(b, w);
-          const uint32_t a0 = e4m3x2_to_f16x2(x & 0xffffu), a2 = e4m3x2_to_f16x2(x >> 16);
-          const uint32_t a1 = e4m3x2_to_f16x2(y & 0xffffu), a3 = e4m3x2_to_f16x2(y >> 16);
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_f16(word(a, w), a0, a2);
+          e4m3x4_to_f16(word(b, w), a1, a3);
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            mma16816<true>(s[n], a0, a1, a2, a3, qf[n][j][2 * w], qf[n][j][2 * w + 1]);
+            mma16816<true>(w & 1 ? s2[n] : s[n], a0, a1, a2, a3, qf[n][j][2 * w],
+                           qf[n][j][2 * w + 1]);
         }
       }
     }
     src += 2 * KJ * 512;
     // scores in base 2; masked keys are -inf
-    const bool in0 = g >= lo && g < hi, in1 = g + 8 >= lo && g + 8 < hi;
+    const bool in0 = !EDGE || (g >= lo && g < hi), in1 = !EDGE || (g + 8 >= lo && g + 8 < hi);
     bool high = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        s[n][e] = in0 ? s[n][e] * mult[n][e] : -INFINITY;
-        s[n][2 + e] = in1 ? s[n][2 + e] * mult[n][e] : -INFINITY;
+        s[n][e] = in0 ? (s[n][e] + s2[n][e]) * mult[n][e] : -INFINITY;
+        s[n][2 + e] = in1 ? (s[n][2 + e] + s2[n][2 + e]) * mult[n][e] : -INFINITY;
         high |= fmaxf(s[n][e], s[n][2 + e]) > m[n][e] + kRaise;
       }
     }
@@ -305,7 +348,7 @@ struct MmaPath {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float mm = m[n][e & 1] == -INFINITY ? 0.f : m[n][e & 1];
-        p[e] = exp2f(s[n][e] - mm);
+        p[e] = ex2(s[n][e] - mm);
       }
       l[n][0] += p[0] + p[2];
       l[n][1] += p[1] + p[3];
@@ -342,16 +385,15 @@ struct MmaPath {
         } else {
           const int w = j >> 1;
           const uint32_t sel = j & 1 ? 0x7362 : 0x5140;
-          const uint32_t x = __byte_perm(word(v[0], w), word(v[1], w), sel);
-          const uint32_t y = __byte_perm(word(v[2], w), word(v[3], w), sel);
-          a0 = e4m3x2_to_f16x2(x & 0xffffu), a1 = e4m3x2_to_f16x2(x >> 16);
-          a2 = e4m3x2_to_f16x2(y & 0xffffu), a3 = e4m3x2_to_f16x2(y >> 16);
+          e4m3x4_to_f16(__byte_perm(word(v[0], w), word(v[1], w), sel), a0, a1);
+          e4m3x4_to_f16(__byte_perm(word(v[2], w), word(v[3], w), sel), a2, a3);
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          mma16816<E4M3>(o[i][j][n], a0, a1, a2, a3, ph[n][0], ph[n][1]);
-          if constexpr (!E4M3) mma16816<false>(o[i][j][n], a0, a1, a2, a3, pl[n][0], pl[n][1]);
-        }
+        for (int n = 0; n < NT; ++n) mma16816<E4M3>(o[i][j][n], a0, a1, a2, a3, ph[n][0], ph[n][1]);
+        if constexpr (!E4M3)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            mma16816<false>(o[i][j][n], a0, a1, a2, a3, pl[n][0], pl[n][1]);
       }
     }
   }
@@ -367,22 +409,23 @@ struct MmaPath {
       }
   }
 
-  // output chunk i times f[head] into buf (NH, CH)
-  __device__ __forceinline__ void chunk(int i, const float *f, float *buf, int lane) {
+  // output chunks [i0, i0 + R) of heads < nh into buf (NH, R CH)
+  template <int R>
+  __device__ __forceinline__ void chunks(int i0, int nh, float *buf, int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int ii = 0; ii < MI; ++ii) {
-      if (ii != i) continue;
+    for (int i = 0; i < MI; ++i) {
+      if (i < i0 || i >= i0 + R) continue;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int head = 8 * n + 2 * t + e;
-          const float ff = f[head];
+          if (head >= nh) continue;
+          float *to = buf + head * (R * CH) + (i - i0) * CH + VE * g;
 #pragma unroll
           for (int j = 0; j < MJ; ++j)
-            *reinterpret_cast<float2 *>(buf + head * CH + VE * g + 2 * j) =
-                make_float2(o[ii][j][n][e] * ff, o[ii][j][n][2 + e] * ff);
+            *reinterpret_cast<float2 *>(to + 2 * j) = make_float2(o[i][j][n][e], o[i][j][n][2 + e]);
         }
     }
   }
@@ -409,27 +452,33 @@ struct FmaPath {
   float m[NH], l[NH];
   float mult;
 
-  __device__ __forceinline__ static void issue(uint32_t slot, const uint8_t *k, const uint8_t *v,
+  __device__ __forceinline__ static int k_lane(int lane) {
+    return (lane >> 2) * (D * EB) + (lane & 3) * 16;
+  }
+  __device__ __forceinline__ static int v_lane(int lane) {
+    return VR == 2 ? (lane >> 4) * (D * EB) + (lane & 15) * 16 : lane * 16;
+  }
+  template <bool EDGE>
+  __device__ __forceinline__ static void issue(uint32_t dst, const uint8_t *k, const uint8_t *v,
                                                int lo, int hi, int lane) {
-    const int g = lane >> 2, t = lane & 3;
-    uint32_t dst = slot + lane * 16;
-    const bool okk = g >= lo && g < hi;
-    const uint8_t *ks = k + (size_t)g * (D * EB) + t * 16;
+    const bool okk = (lane >> 2) >= lo && (lane >> 2) < hi;
 #pragma unroll
-    for (int j = 0; j < KJ; ++j, dst += 512) cp_async16_zfill(dst, ks + j * 64, okk);
-    const int sub = VR == 2 ? lane >> 4 : 0, piece = VR == 2 ? lane & 15 : lane;
+    for (int j = 0; j < KJ; ++j) copy_piece<16, EDGE>(dst + j * 512, k + j * 64, okk);
+    const int sub = VR == 2 ? lane >> 4 : 0;
 #pragma unroll
     for (int r = 0; r < KEYS / VR; ++r) {
-      const int row = r * VR + sub;
-      const bool ok = row >= lo && row < hi;
-      const uint8_t *src = v + (size_t)row * (D * EB) + piece * 16;
+      const bool ok = r * VR + sub >= lo && r * VR + sub < hi;
 #pragma unroll
-      for (int j = 0; j < VJ; ++j, dst += 512) cp_async16_zfill(dst, src + j * 512, ok);
+      for (int j = 0; j < VJ; ++j)
+        copy_piece<16, EDGE>(dst + (KJ + r * VJ + j) * 512, v + r * VR * (D * EB) + j * 512, ok);
     }
   }
 
+  __device__ __forceinline__ void fetch(const Out *, int, int) {}
+
   __device__ __forceinline__ void begin(const Out *q, int nh, float sc, int, float *qs) {
     mult = sc;
+    __syncthreads();  // qs is free
     for (int e = threadIdx.x; e < nh * D; e += blockDim.x) qs[e] = __ldg(q + e);
     __syncthreads();
 #pragma unroll
@@ -442,10 +491,10 @@ struct FmaPath {
     }
   }
 
-  __device__ __forceinline__ void step(uint32_t slot, int lo, int hi, int nh, int lane,
+  template <bool EDGE>
+  __device__ __forceinline__ void step(uint32_t src, int lo, int hi, int nh, int lane,
                                        const float *qs) {
     const int g = lane >> 2, t = lane & 3;
-    const uint32_t src = slot + lane * 16;
     float4 k[KJ];
 #pragma unroll
     for (int j = 0; j < KJ; ++j) {
@@ -453,7 +502,7 @@ struct FmaPath {
       k[j] = make_float4(__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z),
                          __uint_as_float(x.w));
     }
-    const bool in = g >= lo && g < hi;
+    const bool in = !EDGE || (g >= lo && g < hi);
     float p[NH];
     bool high = false;
 #pragma unroll
@@ -490,7 +539,7 @@ struct FmaPath {
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
       if (h >= nh) break;
-      p[h] = exp2f(p[h] - (m[h] == -INFINITY ? 0.f : m[h]));
+      p[h] = ex2(p[h] - (m[h] == -INFINITY ? 0.f : m[h]));
       l[h] += p[h];  // the key's four lanes hold the same sum
     }
     const int sub = VR == 2 ? lane >> 4 : 0;
@@ -524,22 +573,23 @@ struct FmaPath {
     }
   }
 
-  __device__ __forceinline__ void chunk(int i, const float *f, float *buf, int lane) {
+  template <int R>
+  __device__ __forceinline__ void chunks(int i0, int nh, float *buf, int lane) {
 #pragma unroll
     for (int j = 0; j < VJ; ++j) {
-      if (j != i) continue;
+      if (j < i0 || j >= i0 + R) continue;
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
+        if (h >= nh) break;
         float x[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           x[e] = o[h][j][e];
           if (VR == 2) x[e] += __shfl_xor_sync(0xffffffffu, x[e], 16);
         }
-        const float ff = f[h];
         if (VR == 1 || lane < 16)
-          *reinterpret_cast<float4 *>(buf + h * CH + 4 * lane) =
-              make_float4(x[0] * ff, x[1] * ff, x[2] * ff, x[3] * ff);
+          *reinterpret_cast<float4 *>(buf + h * (R * CH) + (j - i0) * CH + 4 * lane) =
+              make_float4(x[0], x[1], x[2], x[3]);
       }
     }
   }
@@ -564,34 +614,28 @@ __device__ __forceinline__ Seq seq_info(const AttnArgs &a, int b) {
   return s;
 }
 
-// A place in the row of units: unit c of (sequence b, head group h).
+// Output chunks that the warps exchange at a time, and the queue's depth: what
+// two CTAs of an SM (one of eight warps) can hold.
 template <class P, int NW>
-struct Cursor {
-  int b, h, c;
-  Seq s;
-  __device__ __forceinline__ void next(const AttnArgs &a) {
-    if (++c < s.units) return;
-    c = 0;
-    if (++h < a.Hkv * a.VG) return;
-    h = 0;
-    do {
-      if (++b >= a.B) return;
-      s = seq_info<P, NW>(a, b);
-    } while (s.units == 0);
-  }
-  __device__ __forceinline__ int key(int warp) const { return s.base + (c * NW + warp) * P::KEYS; }
-};
-
+constexpr int round_chunks() {
+  constexpr int fit = (NW == 8 ? 32 : 16) * 1024 / (NW * P::NH * P::CH * 4);
+  return fit < 1 ? 1 : fit < P::NCH ? fit : P::NCH;
+}
+template <class P, int NW>
+constexpr size_t merge_bytes() {
+  return sizeof(float) *
+         (NW * P::NH * P::CH * round_chunks<P, NW>() + 3 * NW * P::NH + P::Q_SMEM);
+}
 template <class P, int NW>
 constexpr int stages() {
-  constexpr int want = (NW == 8 ? 24 : 26) * 1024 / P::STAGE_BYTES;
-  return want < 2 ? 2 : want > 8 ? 8 : want;
+  constexpr int fit = (int)(((NW == 8 ? 226 : 112) * 1024 - merge_bytes<P, NW>()) /
+                            (NW * P::STAGE_BYTES));
+  return fit < 2 ? 2 : fit > 8 ? 8 : fit;
 }
 
 template <class P, int NW>
 constexpr size_t smem_bytes() {
-  return (size_t)NW * stages<P, NW>() * P::STAGE_BYTES +
-         sizeof(float) * (NW * P::NH * P::CH + 3 * NW * P::NH + P::Q_SMEM);
+  return (size_t)NW * stages<P, NW>() * P::STAGE_BYTES + merge_bytes<P, NW>();
 }
 
 template <class P, int NW>
@@ -599,14 +643,14 @@ __global__ void __launch_bounds__(NW * 32, NW == 8 ? 1 : 2) paged_attention_kern
     const AttnArgs a) {
   pdl_enter();
   constexpr int NT = NW * 32, ST = stages<P, NW>();
-  constexpr int D = P::D, NH = P::NH, CH = P::CH;
+  constexpr int D = P::D, NH = P::NH, RC = round_chunks<P, NW>(), CH = P::CH * RC;
   using Out = typename P::Out;
   extern __shared__ __align__(128) uint8_t smem[];
   float *buf = reinterpret_cast<float *>(smem + (size_t)NW * ST * P::STAGE_BYTES);
   float *sm = buf + NW * NH * CH, *sl = sm + NW * NH, *sf = sl + NW * NH;
   float *qs = sf + NW * NH;
-  __shared__ long long sh_sum[NW], sh_u;
-  __shared__ int sh_b, sh_last;
+  __shared__ long long sh_sum[NW], sh_u[2], sh_S;
+  __shared__ int sh_b, sh_h, sh_c, sh_last;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int HV = a.Hkv * a.VG;
 
@@ -615,7 +659,8 @@ __global__ void __launch_bounds__(NW * 32, NW == 8 ? 1 : 2) paged_attention_kern
   const int b0 = tid * per, b1 = min(b0 + per, a.B);
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
-    mine += seq_info<P, NW>(a, b).units;
+    const int n = seq_info<P, NW>(a, b).units;
+    mine += n ? n + kItemCost : 0;
     const int len = __ldg(a.lens + b);
     if (blockIdx.x == 0 && (len < 0 || (long long)len > (long long)a.max_pages * a.P))
       flag_status(a.status, MOE_DEV_BAD_CACHE);
@@ -634,6 +679,8 @@ __global__ void __launch_bounds__(NW * 32, NW == 8 ? 1 : 2) paged_attention_kern
     if (i < w) before += sh_sum[i];
     total += sh_sum[i];
   }
+  // an item of n units stands for n + kItemCost in the row: what joining the
+  // warps and starting over costs
   const long long T = total * HV;
   // rows of empty sequences
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
@@ -643,58 +690,121 @@ __global__ void __launch_bounds__(NW * 32, NW == 8 ? 1 : 2) paged_attention_kern
     if (a.lse)
       for (int e = tid; e < a.Hq; e += NT) a.lse[(size_t)b * a.Hq + e] = -INFINITY;
   }
-  long long want = (T + kMinUnits - 1) / kMinUnits;
+  const long long want = (T + kSnap - 1) / kSnap;
   const long long W = want < (long long)gridDim.x ? want : (long long)gridDim.x;
   if ((long long)blockIdx.x >= W) return;
-  const long long u0 = blockIdx.x * T / W, u1 = (blockIdx.x + 1) * T / W;
-  if (u0 >= u1) return;
+  // this CTA's range, its ends moved to the edges of items that they nearly meet
   const long long excl = (before + inc - mine) * HV;
-  if (u0 >= excl && u0 < excl + mine * HV) {
+  if (tid == 0) sh_u[1] = T;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const long long x = ((long long)blockIdx.x + i) * T / W;
+    if (x < excl || x >= excl + mine * HV) continue;
     long long at = excl;
     for (int b = b0; b < b1; ++b) {
-      const long long n = (long long)seq_info<P, NW>(a, b).units * HV;
-      if (u0 < at + n) {
-        sh_b = b;
-        sh_u = u0 - at;
+      const int units = seq_info<P, NW>(a, b).units, n = units ? units + kItemCost : 0;
+      if (x < at + (long long)n * HV) {
+        int h = (int)((x - at) / n);
+        long long S = at + (long long)h * n;
+        long long to = x - S < kSnap ? S : S + n - x < kSnap ? S + n : x;
+        sh_u[i] = to;
+        if (i == 0) {
+          sh_b = b;
+          sh_h = to == S + n ? h + 1 : h;  // HV: the next sequence
+          sh_c = to == S || to == S + n ? 0 : (int)(to - S) - kItemCost;
+          sh_S = to == S + n ? to : S;
+        }
         break;
       }
-      at += n;
+      at += (long long)n * HV;
     }
   }
   __syncthreads();
+  const long long u1 = sh_u[1];
+  if (sh_u[0] >= u1) return;
+  int b_first = sh_b, h_first = sh_h;
+  const int c_first = sh_c;
+  Seq s_first = seq_info<P, NW>(a, b_first);
+  if (h_first == HV) {
+    h_first = 0;
+    do {
+      s_first = seq_info<P, NW>(a, ++b_first);
+    } while (s_first.units == 0);
+  }
+  long long S = sh_S;  // where the item begins in the row
+  const uint32_t ring = ptx::smem_u32(smem) + (uint32_t)w * (ST * P::STAGE_BYTES) + lane * 16;
+  constexpr int ROW = D * P::EB, STRIDE = NW * P::KEYS;
+  const size_t head_bytes = (size_t)a.P * ROW;
+  const int page_step = STRIDE / a.P, off_step = STRIDE - page_step * a.P;
 
-  Cursor<P, NW> in, cur;  // where copies are issued, where values are used
-  cur.b = sh_b;
-  cur.s = seq_info<P, NW>(a, cur.b);
-  cur.h = (int)(sh_u / cur.s.units);
-  cur.c = (int)(sh_u - (long long)cur.h * cur.s.units);
-  in = cur;
-  long long in_left = u1 - u0, left = u1 - u0, u = u0;
-  const uint32_t ring = ptx::smem_u32(smem) + (uint32_t)w * (ST * P::STAGE_BYTES);
-  const size_t head_bytes = (size_t)a.P * (D * P::EB);
-  int slot_in = 0, slot = 0;
-
-  // the page of the next copies is looked up one step ahead
-  auto lookup = [&]() -> int {
-    const int key = in.key(w);
-    return key < in.s.len ? __ldg(a.table + (size_t)in.b * a.max_pages + key / a.P) : 0;
+  // ---- the copying side: unit c of (sequence b, head group h), this warp's
+  // first token `key` of it, in place `off` of its page; the page's number is
+  // looked up one step ahead
+  struct {
+    int b, h, c, key, idx, off;
+    Seq s;
+  } in;
+  in.b = b_first;
+  in.s = s_first;
+  in.h = h_first;
+  in.c = c_first;
+  long long in_S = S;
+  // the units of the item that lie in the range
+  auto units_of = [&](long long at, int units) {
+    return (int)min((long long)units, u1 - at - kItemCost);
   };
-  int page = lookup();
+  int in_end = units_of(in_S, in.s.units);
+  bool more = true;
+  const uint8_t *k_lane = a.kc + P::k_lane(lane), *v_lane = a.vc + P::v_lane(lane);
+  int page = 0, slot_in = 0;
+  size_t head_off = 0;
+  auto lookup = [&]() {
+    if (in.key < in.s.len) page = __ldg(a.table + (size_t)in.b * a.max_pages + in.idx);
+  };
+  auto enter = [&]() {  // the place of unit in.c
+    in.key = in.s.base + (in.c * NW + w) * P::KEYS;
+    in.idx = in.key / a.P;
+    in.off = in.key - in.idx * a.P;
+    head_off = (size_t)(a.VG == 1 ? in.h : in.h / a.VG) * head_bytes;
+    lookup();
+  };
+  enter();
   auto issue = [&]() {
-    if (in_left > 0) {
-      const int key = in.key(w);
-      if (key < in.s.len) {
-        const bool ok = page >= 0 && page < a.num_pages;
-        if (!ok && lane == 0) flag_status(a.status, MOE_DEV_BAD_CACHE);
-        const size_t off = (size_t)(ok ? page : 0) * a.page_bytes +
-                           (size_t)(in.h / a.VG) * head_bytes + (size_t)(key % a.P) * (D * P::EB);
-        P::issue(ring + slot_in * P::STAGE_BYTES, a.kc + off, a.vc + off,
-                 ok ? in.s.first - key : P::KEYS, in.s.len - key, lane);
+    if (more) {
+      if (in.key < in.s.len) {
+        const bool ok = (unsigned)page < (unsigned)a.num_pages;
+        const size_t at = (size_t)(ok ? page : 0) * a.page_bytes + head_off + in.off * ROW;
+        const uint32_t dst = ring + slot_in * P::STAGE_BYTES;
+        if (ok && in.key >= in.s.first && in.key + P::KEYS <= in.s.len) {
+          P::template issue<false>(dst, k_lane + at, v_lane + at, 0, 0, lane);
+        } else {
+          if (!ok && lane == 0) flag_status(a.status, MOE_DEV_BAD_CACHE);
+          P::template issue<true>(dst, k_lane + at, v_lane + at,
+                                  ok ? in.s.first - in.key : P::KEYS, in.s.len - in.key, lane);
+        }
       }
       slot_in = slot_in + 1 == ST ? 0 : slot_in + 1;
-      if (--in_left > 0) {
-        in.next(a);
-        page = lookup();
+      if (++in.c < in_end) {
+        in.key += STRIDE;
+        in.idx += page_step;
+        in.off += off_step;
+        if (in.off >= a.P) in.off -= a.P, ++in.idx;
+        lookup();
+      } else {
+        in_S += in.s.units + kItemCost;
+        more = in_S < u1;
+        if (more) {
+          in.c = 0;
+          if (++in.h == HV) {
+            in.h = 0;
+            do {
+              in.s = seq_info<P, NW>(a, ++in.b);
+            } while (in.s.units == 0);
+          }
+          in_end = units_of(in_S, in.s.units);
+          enter();
+        }
       }
     }
     ptx::cp_async_commit();
@@ -702,120 +812,167 @@ __global__ void __launch_bounds__(NW * 32, NW == 8 ? 1 : 2) paged_attention_kern
 #pragma unroll 1
   for (int i = 0; i < ST - 1; ++i) issue();
 
+  // ---- the computing side, a segment (what the range holds of one item) at a time
   P st;
-  bool fresh = true;
-  int nh = 0, h0 = 0;
+  int b = b_first, h = h_first, c = c_first, slot = 0;
+  Seq sq = s_first;
+  int hk = 0, h0 = 0, nh = 0;
+  const Out *qrow = nullptr;
+  auto ask = [&]() {  // the item's queries
+    hk = a.VG == 1 ? h : h / a.VG;
+    h0 = hk * a.G + (h - hk * a.VG) * NH;
+    nh = min(NH, (hk + 1) * a.G - h0);
+    qrow = reinterpret_cast<const Out *>(a.q) + b * a.q_stride + (size_t)h0 * D;
+    st.fetch(qrow, nh, lane);
+  };
+  ask();
 #pragma unroll 1
-  while (left > 0) {
-    if (fresh) {
-      const int hk = cur.h / a.VG, vg = cur.h - hk * a.VG;
-      h0 = hk * a.G + vg * NH;
-      nh = min(NH, a.G - vg * NH);
-      const float sc = a.scale_log2 * (a.kscale ? __ldg(a.kscale + hk) : 1.f);
-      st.begin(reinterpret_cast<const Out *>(a.q) + cur.b * a.q_stride + (size_t)h0 * D, nh, sc,
-               lane, qs);
-      fresh = false;
-    }
-    issue();
-    ptx::cp_async_wait<ST - 1>();
-    const int key = cur.key(w);
-    if (key < cur.s.len)
-      st.step(ring + slot * P::STAGE_BYTES, cur.s.first - key, cur.s.len - key, nh, lane, qs);
-    slot = slot + 1 == ST ? 0 : slot + 1;
-    --left;
-    const bool end = cur.c + 1 == cur.s.units;
-    if (!end && left > 0) {
-      cur.c++;
-      ++u;
-      continue;
-    }
-    // ---- the segment ends: join the warps, then store the rows or the part
-    const long long F = u - cur.c, L = F + cur.s.units - 1;  // the item's units
-    const int wf = (int)(((F + 1) * W - 1) / T), wl = (int)(((L + 1) * W - 1) / T);
-    const bool whole = wf == wl;
-    const int part = 2 * (int)blockIdx.x + (F < u0 ? 0 : 1);
-    const int hk = cur.h / a.VG;
+  while (true) {
+    const float sc = a.scale_log2 * (a.kscale ? __ldg(a.kscale + hk) : 1.f);
     const float vs = a.vscale ? __ldg(a.vscale + hk) : 1.f;
-    Out *out = reinterpret_cast<Out *>(a.out) + ((size_t)cur.b * a.Hq + h0) * D;
-    float *lse = a.lse ? a.lse + (size_t)cur.b * a.Hq + h0 : nullptr;
-    st.stats(sm + w * NH, sl + w * NH, lane);
-    __syncthreads();
-    if (tid < nh) {  // warp factors; with them the sum, and the factor of a whole row
-      float top = -INFINITY, sum = 0.f;
-      for (int i = 0; i < NW; ++i) top = fmaxf(top, sm[i * NH + tid]);
-      for (int i = 0; i < NW; ++i) {
-        const float f = rescale(sm[i * NH + tid], top);
-        sum += sl[i * NH + tid] * f;
-        sf[i * NH + tid] = f;
-      }
-      if (whole) {
-        for (int i = 0; i < NW; ++i) sf[i * NH + tid] *= vs / sum;
-        if (lse) lse[tid] = (top + log2f(sum)) * kLn2;
-      } else {
-        __stcg(a.part_ml + (size_t)part * NH + tid, make_float2(top, sum));
-      }
-    }
-    __syncthreads();
+    st.begin(qrow, nh, sc, lane, qs);
+    const int n = units_of(S, sq.units) - c;
+    int key = sq.base + (c * NW + w) * P::KEYS;
 #pragma unroll 1
-    for (int i = 0; i < P::NCH; ++i) {
-      st.chunk(i, sf + w * NH, buf + w * NH * CH, lane);
-      __syncthreads();
-      for (int e = tid; e < nh * CH; e += NT) {
-        float x = 0.f;
-#pragma unroll
-        for (int k = 0; k < NW; ++k) x += buf[k * NH * CH + e];
-        const int at = (e / CH) * D + i * CH + e % CH;
-        if (whole)
-          store_out(out + at, x);
-        else
-          __stcg(a.part_o + (size_t)part * NH * D + at, x);
+    for (int i = 0; i < n; ++i, key += STRIDE) {
+      issue();
+      ptx::cp_async_wait<ST - 1>();
+      const uint32_t src = ring + slot * P::STAGE_BYTES;
+      if (key >= sq.first && key + P::KEYS <= sq.len)
+        st.template step<false>(src, 0, 0, nh, lane, qs);
+      else if (key < sq.len)
+        st.template step<true>(src, sq.first - key, sq.len - key, nh, lane, qs);
+      slot = slot + 1 == ST ? 0 : slot + 1;
+    }
+    // ---- the segment ends: join the warps, then store the rows or the part.
+    // Ranges k_lo - 1 .. k_hi hold parts of it: k_lo is the first whose
+    // beginning, floor(k T / W), is not moved to S or lies before it; those
+    // that begin in [S + kSnap, E - kSnap] begin inside.
+    const long long E = S + sq.units + kItemCost;
+    const int k_lo = (int)((min(S + kSnap, E) * W + T - 1) / T);
+    const int k_hi = (int)(((E - kSnap + 1) * W + T - 1) / T) - 1;
+    const int wf = k_lo - 1, wl = k_hi < k_lo ? wf : k_hi;
+    const bool whole = wf == wl;
+    const int me = (int)blockIdx.x;
+    const size_t part = 2 * me + (me == wf ? 1 : 0);  // the item begins in range wf
+    Out *out = reinterpret_cast<Out *>(a.out) + ((size_t)b * a.Hq + h0) * D;
+    float *lse = a.lse ? a.lse + (size_t)b * a.Hq + h0 : nullptr;
+    const int b_done = b, h_done = h, nh_done = nh;
+    S = E;
+    const bool last_item = S >= u1;
+    c = 0;
+    if (!last_item) {  // the next item's queries travel meanwhile
+      if (++h == HV) {
+        h = 0;
+        do {
+          sq = seq_info<P, NW>(a, ++b);
+        } while (sq.units == 0);
       }
+      ask();
+    }
+#pragma unroll 1
+    for (int i = 0; i < P::NCH; i += RC) {
+      __syncthreads();  // the exchange is free
+      if (i == 0) st.stats(sm + w * NH, sl + w * NH, lane);
+      st.template chunks<RC>(i, nh_done, buf + w * NH * CH, lane);
       __syncthreads();
+      if (i == 0) {
+        if (tid < nh_done) {  // warp factors; with them the sum, and the factor of a whole row
+          float top = -INFINITY, sum = 0.f;
+          for (int k = 0; k < NW; ++k) top = fmaxf(top, sm[k * NH + tid]);
+          for (int k = 0; k < NW; ++k) {
+            const float f = rescale(sm[k * NH + tid], top);
+            sum += sl[k * NH + tid] * f;
+            sf[k * NH + tid] = f;
+          }
+          if (whole) {
+            for (int k = 0; k < NW; ++k) sf[k * NH + tid] *= vs / sum;
+            if (lse) lse[tid] = (top + log2f(sum)) * kLn2;
+          } else {
+            __stcg(a.part_ml + part * NH + tid, make_float2(top, sum));
+          }
+        }
+        __syncthreads();
+      }
+      for (int e = tid * 2; e < nh_done * CH; e += NT * 2) {
+        const int head = e / CH, at = head * D + i * P::CH + e % CH;
+        float x = 0.f, y = 0.f;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) {
+          const float2 v = *reinterpret_cast<const float2 *>(buf + k * NH * CH + e);
+          const float f = sf[k * NH + head];
+          x = fmaf(v.x, f, x), y = fmaf(v.y, f, y);
+        }
+        if (whole)
+          store_out2(out + at, x, y);
+        else
+          __stcg(reinterpret_cast<float2 *>(a.part_o + part * NH * D + at), make_float2(x, y));
+      }
     }
     if (!whole) {
       __threadfence();
       __syncthreads();
       if (tid == 0) {
-        int32_t *cnt = a.counters + (size_t)cur.b * HV + cur.h;
-        const int n = atomicAdd(cnt, 1);
-        sh_last = n == wl - wf;
+        int32_t *cnt = a.counters + (size_t)b_done * HV + h_done;
+        sh_last = atomicAdd(cnt, 1) == wl - wf;
         if (sh_last) *cnt = 0;  // ready for the next call
         __threadfence();
       }
       __syncthreads();
       if (sh_last) {  // every part is there: join them in range order
-        auto part_of = [&](int k) { return 2 * k + (F < k * T / W ? 0 : 1); };
-        for (int e = tid; e < nh * D; e += NT) {
-          const int h = e / D;
-          float top = -INFINITY, sum = 0.f, x = 0.f;
-          for (int k0 = wf; k0 <= wl; k0 += 8) {
-            float2 ml[8];
-            float y[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              if (k0 + k > wl) continue;
-              const size_t p = part_of(k0 + k);
-              ml[k] = __ldcg(a.part_ml + p * NH + h);
-              y[k] = __ldcg(a.part_o + p * NH * D + e);
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              if (k0 + k > wl) continue;
-              const float t2 = fmaxf(top, ml[k].x);
-              const float f = rescale(top, t2), f2 = rescale(ml[k].x, t2);
-              sum = sum * f + ml[k].y * f2;
-              x = x * f + y[k] * f2;
-              top = t2;
-            }
+        auto part_of = [&](int k) { return (size_t)(2 * k + (k == wf ? 1 : 0)); };
+        const int np = wl - wf + 1;
+        // a warp per head: the maximum and the sum
+        for (int e = w; e < nh_done; e += NW) {
+          float top = -INFINITY, sum = 0.f;
+          for (int k = lane; k < np; k += 32)
+            top = fmaxf(top, __ldcg(a.part_ml + part_of(wf + k) * NH + e).x);
+          top = max_over_g(top);
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          for (int k = lane; k < np; k += 32) {
+            const float2 ml = __ldcg(a.part_ml + part_of(wf + k) * NH + e);
+            sum += ml.y * rescale(ml.x, top);
           }
-          store_out(out + e, x * (vs / sum));
-          if (lse && e % D == 0) lse[h] = (top + log2f(sum)) * kLn2;
+          sum = sum_over_g(sum);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          if (lane == 0) {
+            sm[e] = top;
+            sl[e] = vs / sum;
+            if (lse) lse[e] = (top + log2f(sum)) * kLn2;
+          }
         }
+        __syncthreads();
+        // 4 outputs a thread and pass, 8 parts in flight
+        for (int e = tid * 4; e < nh_done * D; e += NT * 4) {
+          const float top = sm[e / D], f = sl[e / D];
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int k0 = 0; k0 < np; k0 += 8) {
+            float mx[8];
+            float4 y[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (k0 + k < np) {
+                const size_t p = part_of(wf + k0 + k);
+                mx[k] = __ldcg(a.part_ml + p * NH + e / D).x;
+                y[k] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + p * NH * D + e));
+              }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (k0 + k < np) {
+                const float r = rescale(mx[k], top);
+                x.x = fmaf(y[k].x, r, x.x), x.y = fmaf(y[k].y, r, x.y);
+                x.z = fmaf(y[k].z, r, x.z), x.w = fmaf(y[k].w, r, x.w);
+              }
+          }
+          store_out2(out + e, x.x * f, x.y * f);
+          store_out2(out + e + 2, x.z * f, x.w * f);
+        }
+        __syncthreads();
       }
     }
-    fresh = true;
-    ++u;
-    if (left > 0) cur.next(a);
+    if (last_item) break;
   }
   ptx::cp_async_wait<0>();
 }
