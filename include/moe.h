@@ -569,14 +569,27 @@ moe_status_t moe_quantize_weights_w4(const moe_layer_desc_t *desc, int group, co
                                      void *w2_s, moe_stream_t stream);
 
 /*
+ * One-time layout of 4-bit weights for moe_experts_w4 (a pure permutation):
+ * every 16 weight rows x 128 reduction indices (8 gate and 8 up rows of w13;
+ * 16 rows of w2) become one contiguous record of their codes, in the order in
+ * which the lanes of a warp use them, and of their scales.  w13_t and w2_t:
+ * moe_w4_tiled_bytes(desc, group, 0 and 1) bytes, 16-byte aligned.  The
+ * codes and scales are not needed afterwards.  Enqueued on `stream`.
+ */
+size_t moe_w4_tiled_bytes(const moe_layer_desc_t *desc, int group, int which);
+moe_status_t moe_prepare_weights_w4(const moe_layer_desc_t *desc, int group, const int32_t *w13_q,
+                                    const void *w13_s, const int32_t *w2_q, const void *w2_s,
+                                    void *w13_t, void *w2_t, moe_stream_t stream);
+
+/*
  * The routed experts of a few tokens on 4-bit weights (bf16 layers):
  *   y[t] = sum_k topk_w[t,k] W2[e]^T h,  h = SiLU(W13[e]^T x[t], gate) * up,
  *   e = topk_idx[t,k]
- * (Algorithm 2 steps 4-11 with the weights above).  Each hit expert's weights
- * are read once for every 32 of its tokens; sums are float32, h is carried in
- * two bf16 parts (about 16 significant bits), y is rounded once.  Results are
- * bitwise reproducible.
+ * (Algorithm 2 steps 4-11 with the weights above).  Sums are float32, h is
+ * carried in two bf16 parts (about 16 significant bits), y is rounded once.
+ * Results are bitwise reproducible.
  *   x (n,H) bf16, topk_idx (n,K) int32, topk_w (n,K) float32, y (n,H) bf16;
+ *   w13_t, w2_t from moe_prepare_weights_w4 with the same group;
  *   n * K <= 4096 (else MOE_ERR_UNSUPPORTED): above that the bf16 grouped
  *   GEMMs are the better path.  An expert id outside [0, E) contributes
  *   nothing and sets MOE_DEV_BAD_ROUTING (status_word may be NULL).
@@ -585,9 +598,9 @@ moe_status_t moe_quantize_weights_w4(const moe_layer_desc_t *desc, int group, co
  */
 size_t moe_experts_w4_workspace_size(const moe_layer_desc_t *desc);
 moe_status_t moe_experts_w4(const moe_layer_desc_t *desc, int group, const void *x,
-                            const int32_t *topk_idx, const float *topk_w, const int32_t *w13_q,
-                            const void *w13_s, const int32_t *w2_q, const void *w2_s, void *y,
-                            void *ws, size_t ws_bytes, int32_t *status_word, moe_stream_t stream);
+                            const int32_t *topk_idx, const float *topk_w, const void *w13_t,
+                            const void *w2_t, void *y, void *ws, size_t ws_bytes,
+                            int32_t *status_word, moe_stream_t stream);
 
 /*
  * Test control for the device timeout path (failure detection without a

@@ -23,6 +23,7 @@ SYMBOLS = (
     "moe_prepare_router", "moe_set_gemm_tails",
     "moe_kv_append", "moe_paged_attention_workspace_size", "moe_paged_attention",
     "moe_quantize_weights_w4", "moe_experts_w4_workspace_size", "moe_experts_w4",
+    "moe_w4_tiled_bytes", "moe_prepare_weights_w4",
 )
 
 MOE_F32, MOE_BF16, MOE_E4M3 = 0, 1, 2
@@ -107,7 +108,9 @@ def _declare(lib):
                                       _vp, _sz, _vp, _vp]),
         "moe_quantize_weights_w4": (_st, [_desc_p, ctypes.c_int] + [_vp] * 7),
         "moe_experts_w4_workspace_size": (_sz, [_desc_p]),
-        "moe_experts_w4": (_st, [_desc_p, ctypes.c_int] + [_vp] * 9 + [_sz, _vp, _vp]),
+        "moe_w4_tiled_bytes": (_sz, [_desc_p, ctypes.c_int, ctypes.c_int]),
+        "moe_prepare_weights_w4": (_st, [_desc_p, ctypes.c_int] + [_vp] * 7),
+        "moe_experts_w4": (_st, [_desc_p, ctypes.c_int] + [_vp] * 7 + [_sz, _vp, _vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)

@@ -1,5 +1,6 @@
 // C ABI of the serving calls (paged cache append, paged attention, experts on
 // 4-bit weights): argument checks.  The kernels live in the other .cu files.
+#include "experts_w4.cuh"
 #include "kv_cache.cuh"
 
 using namespace moe;
@@ -130,24 +131,44 @@ size_t moe_experts_w4_workspace_size(const moe_layer_desc_t *desc) {
   return experts_w4_ws_bytes(d);
 }
 
+size_t moe_w4_tiled_bytes(const moe_layer_desc_t *desc, int group, int which) {
+  Desc d;
+  if (check_w4(desc, group, &d) != MOE_OK || which < 0 || which > 1) return 0;
+  return w4_tiled_bytes(d, group, which);
+}
+
+moe_status_t moe_prepare_weights_w4(const moe_layer_desc_t *desc, int group, const int32_t *w13_q,
+                                    const void *w13_s, const int32_t *w2_q, const void *w2_s,
+                                    void *w13_t, void *w2_t, moe_stream_t stream) {
+  Desc d;
+  moe_status_t st = check_w4(desc, group, &d);
+  if (st != MOE_OK) return st;
+  const void *ptrs[] = {w13_q, w13_s, w2_q, w2_s, w13_t, w2_t};
+  for (const void *p : ptrs)
+    if (!p || !aligned(p, 16)) return MOE_ERR_INVALID_ARG;
+  cudaError_t e = launch_prepare_w4(d, group, 0, w13_q, w13_s, w13_t, stream);
+  if (e == cudaSuccess) e = launch_prepare_w4(d, group, 1, w2_q, w2_s, w2_t, stream);
+  return cuda_status(e);
+}
+
 moe_status_t moe_experts_w4(const moe_layer_desc_t *desc, int group, const void *x,
-                            const int32_t *topk_idx, const float *topk_w, const int32_t *w13_q,
-                            const void *w13_s, const int32_t *w2_q, const void *w2_s, void *y,
-                            void *ws, size_t ws_bytes, int32_t *status_word, moe_stream_t stream) {
+                            const int32_t *topk_idx, const float *topk_w, const void *w13_t,
+                            const void *w2_t, void *y, void *ws, size_t ws_bytes,
+                            int32_t *status_word, moe_stream_t stream) {
   Desc d;
   moe_status_t st = check_w4(desc, group, &d);
   if (st != MOE_OK) return st;
   if (d.nK() > kW4MaxPairs) return MOE_ERR_UNSUPPORTED;
   if (d.n == 0) return MOE_OK;
-  const void *ptrs[] = {x, w13_q, w13_s, w2_q, w2_s, y};
+  const void *ptrs[] = {x, w13_t, w2_t, y};
   for (const void *p : ptrs)
     if (!p || !aligned(p, 16)) return MOE_ERR_INVALID_ARG;
   if (!topk_idx || !topk_w || !aligned(topk_idx, 4) || !aligned(topk_w, 4))
     return MOE_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
   if (ws_bytes < experts_w4_ws_bytes(d)) return MOE_ERR_WORKSPACE;
-  return cuda_status(launch_experts_w4(d, group, x, topk_idx, topk_w, w13_q, w13_s, w2_q, w2_s, y,
-                                       ws, status_word, stream));
+  return cuda_status(launch_experts_w4(d, group, x, topk_idx, topk_w, w13_t, w2_t, y, ws,
+                                       status_word, stream));
 }
 
 }  // extern "C"

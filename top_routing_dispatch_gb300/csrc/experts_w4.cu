@@ -5,10 +5,13 @@
 //
 // Bound: HBM, by the hit experts' weights (a weight meets the expert's one to
 // a few tens of tokens).  What the kernels do about it:
-//  - A warp owns 16 weight rows (output columns) over the whole reduction, so
-//    no sum crosses warps and no barrier is needed after the routing lists.
-//    Its weights stream through a shared-memory queue of its own, 1 KB (16
-//    rows x 128 codes) a step, which runs on across units.
+//  - The weights lie in records (moe_prepare_weights_w4): 16 rows x 128
+//    codes, 1 KB in the order in which a warp's lanes use them, and the
+//    records' scales.  A warp owns one or two tiles of 16 rows (output columns)
+//    over the whole reduction, so no sum crosses warps and no barrier is
+//    needed after the routing lists; its records stream through a
+//    shared-memory queue of its own, which runs on across units, and every
+//    lane reads back what it copied.
 //  - The weights are the 16-row operand of m16n8k16, tokens the 8 columns
 //    (1-4 column groups a pass).  A pair of codes becomes two bf16 (code - 8)
 //    / 4, exactly, by one and(-or) and one multiply-add (see quarter_codes);
@@ -21,23 +24,22 @@
 //    group; x is read in the same order, 16 bytes a lane, as it lies.
 #include <type_traits>
 
-#include "kv_cache.cuh"
+#include "experts_w4.cuh"
 #include "ptx.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int WT = 256, WW = WT / 32;  // threads and warps per CTA
-constexpr int TILE_BYTES = 1024 + 128;  // codes of 16 rows; their scales (8 bytes a row)
-template <int MT>
-constexpr int queue_steps() {  // of a warp
-  return MT == 1 ? 8 : 5;
+template <int GROUP>
+constexpr int record_bytes() {  // codes; 128 / GROUP bf16 scales a row
+  return 1024 + 16 * (128 / GROUP) * 2;
 }
-constexpr int kMaxEntries = kMaxE + kW4MaxPairs / 16;
+constexpr int kMaxEntries = kMaxE + kW4MaxPairs / 4;
+
 
 struct W4Args {
-  const int32_t *q;          // (E, C, R/8)
-  const __nv_bfloat16 *s;    // (E, C, R/group)
+  const uint8_t *rec;        // records (E, C/16, R/128)
   const int32_t *idx;        // (n K)
   const float *w;            // (n K)
   const __nv_bfloat16 *x;    // (n, H)
@@ -49,11 +51,6 @@ struct W4Args {
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N)
-               : "memory");
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
@@ -73,9 +70,12 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
   return v;
 }
+__device__ __forceinline__ uint32_t word(const uint4 &v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -85,7 +85,7 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ void mma_bf16_first(float (&c)[4], uint32_t a0, uint32_t a1,
                                                uint32_t a2, uint32_t a3, uint32_t b0,
                                                uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%10,%10,%10,%10};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
@@ -111,12 +111,19 @@ __device__ __forceinline__ uint32_t quarter_codes(uint32_t w) {
 // pairs <= ROWS) to compute.
 struct Lists {
   int start[kMaxE];
-  int entry_expert[kMaxEntries];
-  int entry_first[kMaxEntries];
-  int entry_n[kMaxEntries];
+  uint8_t entry_expert[kMaxEntries];
+  uint8_t entry_n[kMaxEntries];
+  uint16_t entry_first[kMaxEntries];
   int entries;
   uint16_t pair[kW4MaxPairs];
 };
+
+// Queue steps of a warp: what two CTAs of an SM can hold.
+template <int GROUP, int MT>
+constexpr int queue_steps() {
+  constexpr int fit = (int)((112 * 1024 - sizeof(Lists)) / (WW * MT * record_bytes<GROUP>()));
+  return fit > 8 ? 8 : fit;
+}
 
 // hist: (WW, kMaxE) scratch.  Each warp takes a contiguous slice of the pairs.
 template <int ROWS>
@@ -187,74 +194,52 @@ __device__ __forceinline__ void build_lists(Lists &L, int (*hist)[kMaxE], const 
   __syncthreads();
 }
 
-// DOWN false: gate and up rows of 8 MT columns of h, DOWN true: 16 MT columns
-// of y, a unit's MT tiles of 16 rows sharing each operand piece of x or h.
-// GROUP: reduction indices per scale.
-template <bool DOWN, int GROUP, int MT>
+// DOWN false: tiles of 8 gate and 8 up rows (8 columns of h), DOWN true: tiles
+// of 16 columns of y; a unit's MT tiles share each operand piece of x or h.
+// GROUP: reduction indices per scale.  NTM: column groups of an entry at most.
+template <bool DOWN, int GROUP, int MT, int NTM>
 __global__ void __launch_bounds__(WT, 2) w4_kernel(const W4Args a) {
-  constexpr int NS = 128 / GROUP;  // scales of a row in a step
-  constexpr int WPL = 4 / NS;      // a lane's words of a group: WPL t .. of the group's 4 WPL
-  constexpr int CR = DOWN ? 4 : 8;         // pairs of a column group
-  constexpr int ROWS = DOWN ? 16 : 32;     // pairs of an entry
-  constexpr int ST = queue_steps<MT>(), STEP_BYTES = MT * TILE_BYTES;
+  constexpr int NS = 128 / GROUP;   // scales of a row in a record
+  constexpr int WPL = 4 / NS;       // a lane's words of a group: WPL t .. of the group's 4 WPL
+  constexpr int CR = DOWN ? 4 : 8;  // pairs of a column group
+  constexpr int REC = record_bytes<GROUP>();
+  constexpr int ST = queue_steps<GROUP, MT>(), STEP_BYTES = MT * REC;
   extern __shared__ __align__(128) uint8_t smem[];
   Lists &L = *reinterpret_cast<Lists *>(smem + WW * ST * STEP_BYTES);
   pdl_enter();
-  build_lists<ROWS>(L, reinterpret_cast<int(*)[kMaxE]>(smem), a);  // the queue starts after it
+  // the queue's memory is scratch until the lists are ready
+  build_lists<CR * NTM>(L, reinterpret_cast<int(*)[kMaxE]>(smem), a);
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int tiles = (DOWN ? a.C / 16 : a.I / 8) / MT;
+  const int tiles = a.C / 16 / MT;  // units of an entry
   const int NB = a.R / 128;
   const int units = L.entries * tiles;
   const int step = gridDim.x * WW;
   const int u0 = w * gridDim.x + blockIdx.x;  // the first units go to different CTAs
   const uint32_t ring = ptx::smem_u32(smem) + w * (ST * STEP_BYTES);
-  // a row's four 16-byte pieces are permuted so that the reads below meet no
-  // bank twice
-  const int swz = GROUP == 32 ? (g >> 1) & 3 : GROUP == 64 ? g & 2 : 0;
-  const uint32_t put = ring + (uint32_t)(g * 4 + (t ^ swz)) * 16;
+  const size_t tile_bytes = (size_t)NB * REC;
 
-  // this lane's row of a unit: tile m, lower or upper eight rows
-  auto row_of = [&](int tile, int m, int half) {
-    return DOWN ? (tile * MT + m) * 16 + 8 * half + g : half * a.I + (tile * MT + m) * 8 + g;
-  };
-  int pu = u0, pb = 0, pslot = 0;
-  const int32_t *src[MT][2];
-  // t < 2: the first scale of the rows (lower, upper) whose scales this lane copies
-  const __nv_bfloat16 *scale[MT];
-  bool odd[MT] = {};  // NS == 1: that scale is the upper half of its 4 bytes
+  // the copying side
+  int pu = u0, pb = 0;
+  uint32_t put = ring + lane * 16;
+  const uint8_t *src = nullptr;
   auto locate = [&]() {
     if (pu >= units) return;
     const int ent = pu / tiles, tile = pu - ent * tiles;
-    const size_t e = L.entry_expert[ent];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const size_t ra = e * a.C + row_of(tile, m, 0), rb = e * a.C + row_of(tile, m, 1);
-      src[m][0] = a.q + ra * (a.R / 8) + t * 4;
-      src[m][1] = a.q + rb * (a.R / 8) + t * 4;
-      const size_t at = ((t & 1) ? rb : ra) * (a.R / GROUP);
-      scale[m] = a.s + at;
-      odd[m] = at & 1;
-    }
+    src = a.rec + ((size_t)L.entry_expert[ent] * (a.C / 16) + tile * MT) * tile_bytes + lane * 16;
   };
   auto issue = [&]() {
     if (pu < units) {
-      const uint32_t dst = pslot * STEP_BYTES;
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        cp_async16(put + dst + m * TILE_BYTES, src[m][0]);
-        cp_async16(put + dst + m * TILE_BYTES + 512, src[m][1]);
-        src[m][0] += 16, src[m][1] += 16;
-        if (t < 2) {
-          const uint32_t to = ring + dst + m * TILE_BYTES + 1024 + (t * 8 + g) * 8;
-          // a lone scale comes with its neighbour, from the 4-byte boundary
-          if constexpr (NS == 1)
-            cp_async_small<4>(to, scale[m] + pb - (odd[m] ^ (pb & 1)));
-          else
-            cp_async_small<2 * NS>(to, scale[m] + pb * NS);
-        }
+        const uint8_t *from = src + m * tile_bytes;
+        cp_async16(put + m * REC, from);
+        cp_async16(put + m * REC + 512, from + 512);
+        if (lane < 2 * NS) cp_async16(put + m * REC + 1024, from + 1024);
       }
-      pslot = pslot + 1 == ST ? 0 : pslot + 1;
+      src += REC;
+      put += STEP_BYTES;
+      if (put >= ring + ST * STEP_BYTES) put -= ST * STEP_BYTES;
       if (++pb == NB) {
         pb = 0;
         pu += step;
@@ -267,10 +252,10 @@ __global__ void __launch_bounds__(WT, 2) w4_kernel(const W4Args a) {
 #pragma unroll 1
   for (int i = 0; i < ST - 1; ++i) issue();
 
-  int slot = 0;
+  uint32_t get = ring + lane * 16;
 #pragma unroll 1
   for (int u = u0; u < units; u += step) {
-    const int ent = u / tiles, tile = u - ent * tiles;
+    const int ent = u / tiles, tile = (u - ent * tiles) * MT;
     const int rows = L.entry_n[ent], first = L.entry_first[ent];
     auto pass = [&](auto nt_c) {
       constexpr int NT = decltype(nt_c)::value;
@@ -292,64 +277,45 @@ __global__ void __launch_bounds__(WT, 2) w4_kernel(const W4Args a) {
 #pragma unroll
         for (int i = 0; i < NT; ++i)
           acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.f;
-      [[maybe_unused]] bool up[MT][2];
-      if constexpr (NS == 1)
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            up[m][h] = ((size_t)L.entry_expert[ent] * a.C + row_of(tile, m, h)) * NB & 1;
       uint4 xv[NT][4];  // the operand pieces of a step
-      auto load_x = [&](int b, int j) {
+      auto load_x = [&](int j) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-          xv[i][j] = __ldg(xr[i] + b * 16 + (j / WPL) * 4 * WPL + j % WPL);
+        for (int i = 0; i < NT; ++i) xv[i][j] = __ldg(xr[i] + (j / WPL) * 4 * WPL + j % WPL);
       };
       if constexpr (AHEAD)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) load_x(0, j);
+        for (int j = 0; j < 4; ++j) load_x(j);
 #pragma unroll 1
       for (int b = 0; b < NB; ++b) {
         ptx::cp_async_wait<ST - 2>();
-        __syncwarp();
+        __syncwarp();  // scales are read by lanes that did not copy them
         issue();
-        const uint32_t from = ring + slot * STEP_BYTES + g * 64;
-        const uint32_t sfrom = ring + slot * STEP_BYTES + 1024 + g * 8;
-        slot = slot + 1 == ST ? 0 : slot + 1;
-        uint2 sc[MT][2];
-        uint32_t wd[MT][2][4];
+        if (!AHEAD || b + 1 < NB) {  // the next pieces, or (not AHEAD) this step's
+          if (AHEAD || b > 0)
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+            for (int i = 0; i < NT; ++i) xr[i] += 16;
+        }
+        uint4 wd[MT][2], sc[MT];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t at = from + m * TILE_BYTES + h * 512;
-            if constexpr (GROUP == 128) {
-              const uint4 v = lds128(at + t * 16);
-              wd[m][h][0] = v.x, wd[m][h][1] = v.y, wd[m][h][2] = v.z, wd[m][h][3] = v.w;
-            } else if constexpr (GROUP == 64) {
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const uint2 v = lds64(at + ((2 * k + (t >> 1)) ^ swz) * 16 + (t & 1) * 8);
-                wd[m][h][2 * k] = v.x, wd[m][h][2 * k + 1] = v.y;
-              }
-            } else {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) wd[m][h][k] = lds32(at + (k ^ swz) * 16 + t * 4);
-            }
-            if constexpr (NS == 4)
-              sc[m][h] = lds64(sfrom + m * TILE_BYTES + h * 64);
-            else
-              sc[m][h].x = lds32(sfrom + m * TILE_BYTES + h * 64);
-            if constexpr (NS == 1) {
-              if (!(up[m][h] ^ (b & 1))) sc[m][h].x <<= 16;
-            }
+        for (int m = 0; m < MT; ++m) {
+          wd[m][0] = lds128(get + m * REC);
+          wd[m][1] = lds128(get + m * REC + 512);
+          const uint32_t at = get - lane * 16 + m * REC + 1024 + g * (4 * NS);
+          if constexpr (NS == 4) sc[m] = lds128(at);
+          if constexpr (NS == 2) {
+            const uint2 v = lds64(at);
+            sc[m].x = v.x, sc[m].y = v.y;
           }
+          if constexpr (NS == 1) sc[m].x = lds32(at);
+        }
+        get += STEP_BYTES;
+        if (get >= ring + ST * STEP_BYTES) get -= ST * STEP_BYTES;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if constexpr (!AHEAD) load_x(b, j);
+          if constexpr (!AHEAD) load_x(j);
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
-            const uint32_t wa = wd[m][0][j], wb = wd[m][1][j];
+            const uint32_t wa = word(wd[m][0], j), wb = word(wd[m][1], j);
             {
               const uint32_t a0 = quarter_codes<false>(wa), a1 = quarter_codes<false>(wb);
               const uint32_t a2 = quarter_codes<true>(wa), a3 = quarter_codes<true>(wb);
@@ -369,23 +335,22 @@ __global__ void __launch_bounds__(WT, 2) w4_kernel(const W4Args a) {
                 mma_bf16(part[m][i], a0, a1, a2, a3, xv[i][j].z, xv[i][j].w);
             }
             if (j % WPL == WPL - 1) {
-              const int k = j / WPL;  // this group's scale
-              float s[2];
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t p = k < 2 ? sc[m][h].x : sc[m][h].y;
-                s[h] = __uint_as_float(NS == 1 || (k & 1) ? p & 0xffff0000u : p << 16);
-              }
+              // this group's scales: rows g and g + 8 are NS scales apart
+              constexpr int K1 = NS;
+              const int k = j / WPL;
+              const uint32_t p0 = word(sc[m], k >> 1), p1 = word(sc[m], (K1 + k) >> 1);
+              const float s0 = __uint_as_float(k & 1 ? p0 & 0xffff0000u : p0 << 16);
+              const float s1 = __uint_as_float((K1 + k) & 1 ? p1 & 0xffff0000u : p1 << 16);
 #pragma unroll
               for (int i = 0; i < NT; ++i) {
-                acc[m][i][0] = fmaf(part[m][i][0], s[0], acc[m][i][0]);
-                acc[m][i][1] = fmaf(part[m][i][1], s[0], acc[m][i][1]);
-                acc[m][i][2] = fmaf(part[m][i][2], s[1], acc[m][i][2]);
-                acc[m][i][3] = fmaf(part[m][i][3], s[1], acc[m][i][3]);
+                acc[m][i][0] = fmaf(part[m][i][0], s0, acc[m][i][0]);
+                acc[m][i][1] = fmaf(part[m][i][1], s0, acc[m][i][1]);
+                acc[m][i][2] = fmaf(part[m][i][2], s1, acc[m][i][2]);
+                acc[m][i][3] = fmaf(part[m][i][3], s1, acc[m][i][3]);
               }
             }
           }
-          if constexpr (AHEAD) load_x(b + 1 < NB ? b + 1 : b, j);
+          if constexpr (AHEAD) load_x(j);
         }
       }
       // the sums are of quarter codes
@@ -398,7 +363,7 @@ __global__ void __launch_bounds__(WT, 2) w4_kernel(const W4Args a) {
           const float wt = 4.f * __ldg(a.w + f);
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
-            float *y = a.yslot + (size_t)f * a.C + (tile * MT + m) * 16 + g;
+            float *y = a.yslot + (size_t)f * a.C + (tile + m) * 16 + g;
             y[0] = (acc[m][i][0] + acc[m][i][1]) * wt;
             y[8] = (acc[m][i][2] + acc[m][i][3]) * wt;
           }
@@ -410,10 +375,10 @@ __global__ void __launch_bounds__(WT, 2) w4_kernel(const W4Args a) {
             const int f = L.pair[first + r];
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-              const float gate = 4.f * acc[m][i][c], up_ = 4.f * acc[m][i][2 + c];
-              const float h = gate / (1.f + __expf(-gate)) * up_;
+              const float gate = 4.f * acc[m][i][c], up = 4.f * acc[m][i][2 + c];
+              const float h = gate / (1.f + __expf(-gate)) * up;
               const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-              const size_t at = (size_t)f * a.I + (tile * MT + m) * 8 + g;
+              const size_t at = (size_t)f * a.I + (tile + m) * 8 + g;
               a.hhi[at] = hi;
               a.hlo[at] = __float2bfloat16_rn(h - __bfloat162float(hi));
             }
@@ -421,12 +386,14 @@ __global__ void __launch_bounds__(WT, 2) w4_kernel(const W4Args a) {
         }
       }
     };
-    if (rows <= CR)
+    if (NTM == 1 || rows <= CR) {
       pass(std::integral_constant<int, 1>());
-    else if (rows <= 2 * CR)
-      pass(std::integral_constant<int, 2>());
-    else
-      pass(std::integral_constant<int, 4>());
+    } else if constexpr (NTM >= 2) {
+      if (NTM == 2 || rows <= 2 * CR)
+        pass(std::integral_constant<int, 2>());
+      else if constexpr (NTM == 4)
+        pass(std::integral_constant<int, 4>());
+    }
   }
   ptx::cp_async_wait<0>();
 }
@@ -492,12 +459,49 @@ __global__ void __launch_bounds__(256) quantize_w4_kernel(const __nv_bfloat16 *_
   }
 }
 
+// Records of w13 (DOWN false) or w2: one thread writes 16 bytes.
+template <bool DOWN, int GROUP>
+__global__ void __launch_bounds__(256) prepare_w4_kernel(const uint32_t *__restrict__ q,
+                                                         const __nv_bfloat16 *__restrict__ s,
+                                                         uint8_t *__restrict__ rec,
+                                                         long long records, int C, int R) {
+  pdl_enter();
+  constexpr int NS = 128 / GROUP, WPL = 4 / NS, REC = record_bytes<GROUP>(), PIECES = REC / 16;
+  const int NB = R / 128, tiles = C / 16;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < records * PIECES;
+       i += (long long)gridDim.x * 256) {
+    const long long r = i / PIECES;
+    const int p = (int)(i - r * PIECES);
+    const int b = (int)(r % NB), tile = (int)(r / NB % tiles);
+    const size_t e = (size_t)(r / NB / tiles);
+    auto row = [&](int g, int half) {
+      return e * C + (DOWN ? tile * 16 + 8 * half + g : half * (C / 2) + tile * 8 + g);
+    };
+    uint4 v;
+    uint32_t *o = reinterpret_cast<uint32_t *>(&v);
+    if (p < 64) {  // plane p / 32, lane p % 32: the lane's four words of its row
+      const int g = (p & 31) >> 2, t = p & 3;
+      const uint32_t *from = q + row(g, p >> 5) * (R / 8) + b * 16 + t * WPL;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = __ldg(from + (j / WPL) * 4 * WPL + j % WPL);
+    } else {  // scales (g, half, NS), eight of them
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int k = (p - 64) * 8 + j, g = k / (2 * NS), half = k / NS % 2;
+        reinterpret_cast<__nv_bfloat16 *>(o)[j] = s[row(g, half) * (R / GROUP) + b * NS + k % NS];
+      }
+    }
+    reinterpret_cast<uint4 *>(rec + r * REC)[p] = v;
+  }
+}
+
 inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-template <bool DOWN, int GROUP, int MT>
+template <bool DOWN, int GROUP, int MT, int NTM>
 cudaError_t launch_mt(const W4Args &a, cudaStream_t s) {
-  constexpr size_t smem = (size_t)WW * queue_steps<MT>() * MT * TILE_BYTES + sizeof(Lists);
-  auto kernel = w4_kernel<DOWN, GROUP, MT>;
+  constexpr size_t smem =
+      (size_t)WW * queue_steps<GROUP, MT>() * MT * record_bytes<GROUP>() + sizeof(Lists);
+  auto kernel = w4_kernel<DOWN, GROUP, MT, NTM>;
   static bool ready[64] = {false};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -509,8 +513,8 @@ cudaError_t launch_mt(const W4Args &a, cudaStream_t s) {
     r = true;
   }
   // no more warps than the call can have units
-  const long long tiles = (DOWN ? a.C / 16 : a.I / 8) / MT;
-  const long long hit = a.nK < a.E ? a.nK : a.E + a.nK / 16;
+  const long long tiles = a.C / 16 / MT;
+  const long long hit = a.nK < a.E ? a.nK : a.E + a.nK / ((DOWN ? 4 : 8) * NTM);
   const long long full = 2ll * device_sm_count(), most = hit * tiles;
   const int grid = (int)(most < full ? most : full);
   return launch_pdl(kernel, dim3(grid), dim3(WT), smem, s, a);
@@ -520,20 +524,25 @@ template <bool DOWN, int GROUP>
 cudaError_t launch_stage(const W4Args &a, cudaStream_t s) {
   // two tiles a unit halve the operand loads; one tile while that leaves
   // warps without work
-  const long long tiles = DOWN ? a.C / 16 : a.I / 8;
+  const long long tiles = a.C / 16;
   const long long hit = a.nK < a.E ? a.nK : a.E;
-  if (hit * tiles <= 4ll * WW * device_sm_count()) return launch_mt<DOWN, GROUP, 1>(a, s);
-  return launch_mt<DOWN, GROUP, 2>(a, s);
+  if (hit * tiles <= 4ll * WW * device_sm_count()) return launch_mt<DOWN, GROUP, 1, 1>(a, s);
+  // column groups for nearly every expert's tokens at once (the mean and four
+  // deviations of their number); what exceeds them reads the weights again
+  const float mean = (float)a.nK / a.E, want = (mean + 4.f * sqrtf(mean)) / (DOWN ? 4 : 8);
+  if (want <= 1.f) return launch_mt<DOWN, GROUP, 2, 1>(a, s);
+  if (want <= 2.f) return launch_mt<DOWN, GROUP, 2, 2>(a, s);
+  return launch_mt<DOWN, GROUP, 2, 4>(a, s);
 }
 
 template <int GROUP>
-cudaError_t run(const Desc &d, W4Args a, const int32_t *w13_q, const void *w13_s,
-                const int32_t *w2_q, const void *w2_s, void *y, cudaStream_t s) {
-  a.q = w13_q, a.s = reinterpret_cast<const __nv_bfloat16 *>(w13_s);
+cudaError_t run(const Desc &d, W4Args a, const void *w13_t, const void *w2_t, void *y,
+                cudaStream_t s) {
+  a.rec = reinterpret_cast<const uint8_t *>(w13_t);
   a.C = 2 * d.I, a.R = d.H;
   cudaError_t e = launch_stage<false, GROUP>(a, s);
   if (e != cudaSuccess) return e;
-  a.q = w2_q, a.s = reinterpret_cast<const __nv_bfloat16 *>(w2_s);
+  a.rec = reinterpret_cast<const uint8_t *>(w2_t);
   a.C = d.H, a.R = d.I;
   e = launch_stage<true, GROUP>(a, s);
   if (e != cudaSuccess) return e;
@@ -544,6 +553,20 @@ cudaError_t run(const Desc &d, W4Args a, const int32_t *w13_q, const void *w13_s
                     reinterpret_cast<uint2 *>(y), d.n, d.K, d.E, V);
 }
 
+template <int GROUP>
+cudaError_t prepare(const Desc &d, int which, const int32_t *q, const void *scales, void *tiled,
+                    cudaStream_t s) {
+  const int C = which ? d.H : 2 * d.I, R = which ? d.I : d.H;
+  const long long records = (long long)d.E * (C / 16) * (R / 128);
+  const long long want = (records * (record_bytes<GROUP>() / 16) + 255) / 256;
+  const long long cap = 64ll * device_sm_count();
+  return launch_pdl(which ? prepare_w4_kernel<true, GROUP> : prepare_w4_kernel<false, GROUP>,
+                    dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0, s,
+                    reinterpret_cast<const uint32_t *>(q),
+                    reinterpret_cast<const __nv_bfloat16 *>(scales),
+                    reinterpret_cast<uint8_t *>(tiled), records, C, R);
+}
+
 }  // namespace
 
 size_t experts_w4_ws_bytes(const Desc &d) {
@@ -551,10 +574,21 @@ size_t experts_w4_ws_bytes(const Desc &d) {
   return 2 * align256(nK * d.I * 2) + align256(nK * d.H * 4);
 }
 
+size_t w4_tiled_bytes(const Desc &d, int group, int which) {
+  const size_t C = which ? d.H : 2 * d.I, R = which ? d.I : d.H;
+  return (size_t)d.E * (C / 16) * (R / 128) * (1024 + 32 * (128 / group));
+}
+
+cudaError_t launch_prepare_w4(const Desc &d, int group, int which, const int32_t *q,
+                              const void *scales, void *tiled, cudaStream_t s) {
+  if (group == 32) return prepare<32>(d, which, q, scales, tiled, s);
+  if (group == 64) return prepare<64>(d, which, q, scales, tiled, s);
+  return prepare<128>(d, which, q, scales, tiled, s);
+}
+
 cudaError_t launch_experts_w4(const Desc &d, int group, const void *x, const int32_t *topk_idx,
-                              const float *topk_w, const int32_t *w13_q, const void *w13_s,
-                              const int32_t *w2_q, const void *w2_s, void *y, void *ws,
-                              int32_t *status, cudaStream_t s) {
+                              const float *topk_w, const void *w13_t, const void *w2_t, void *y,
+                              void *ws, int32_t *status, cudaStream_t s) {
   if (d.n == 0) return cudaSuccess;
   W4Args a = {};
   a.idx = topk_idx, a.w = topk_w;
@@ -566,9 +600,9 @@ cudaError_t launch_experts_w4(const Desc &d, int group, const void *x, const int
   a.yslot = reinterpret_cast<float *>(p + 2 * hb);
   a.nK = (int)d.nK(), a.K = d.K, a.E = d.E, a.I = d.I;
   a.status = status;
-  if (group == 32) return run<32>(d, a, w13_q, w13_s, w2_q, w2_s, y, s);
-  if (group == 64) return run<64>(d, a, w13_q, w13_s, w2_q, w2_s, y, s);
-  return run<128>(d, a, w13_q, w13_s, w2_q, w2_s, y, s);
+  if (group == 32) return run<32>(d, a, w13_t, w2_t, y, s);
+  if (group == 64) return run<64>(d, a, w13_t, w2_t, y, s);
+  return run<128>(d, a, w13_t, w2_t, y, s);
 }
 
 cudaError_t launch_quantize_w4(int E, int rows, int cols, int group, const void *w, int32_t *q,

@@ -24,14 +24,4 @@ cudaError_t launch_paged_attention(const KVCache &c, const void *q, long long q_
                                    const int32_t *seq_lens, int window, float scale, void *out,
                                    float *lse, void *ws, int32_t *status, cudaStream_t s);
 
-// ---- experts_w4.cu
-constexpr int kW4MaxPairs = 4096;
-cudaError_t launch_quantize_w4(int E, int rows, int cols, int group, const void *w, int32_t *q,
-                               void *scales, cudaStream_t s);
-size_t experts_w4_ws_bytes(const Desc &d);
-cudaError_t launch_experts_w4(const Desc &d, int group, const void *x, const int32_t *topk_idx,
-                              const float *topk_w, const int32_t *w13_q, const void *w13_s,
-                              const int32_t *w2_q, const void *w2_s, void *y, void *ws,
-                              int32_t *status, cudaStream_t s);
-
 }  // namespace moe

@@ -189,6 +189,8 @@ def quantize_weights_w4(w13, w2, group=128, stream=None):
 
 class W4Experts:
     """The routed experts on 4-bit weights, for up to max_tokens tokens a call.
+    Keeps a copy of the weights in the kernels' own order; the tensors passed
+    are not needed afterwards.
 
     w13_q (E, 2I, H/8) and w2_q (E, H, I/8) int32 codes, w13_s (E, 2I,
     H/group) and w2_s (E, H, I/group) bfloat16 scales (quantize_weights_w4, or
@@ -210,19 +212,23 @@ class W4Experts:
               "w13_s (E, 2I, H/group) and w2_s (E, H, I/group)")
         dev = w13_q.device
         _want(all(t.device == dev for t in (w13_s, w2_q, w2_s)), "all tensors on one device")
-        self.weights = (w13_q, w13_s, w2_q, w2_s)
         self.H, self.I, self.E, self.K, self.group = H, I, E, int(K), group
         self.max_tokens, self.device = int(max_tokens), dev
         self.desc = make_desc(self.max_tokens, H, I, E, K, _BF16, False)
         self._ref = ctypes.byref(self.desc)
         lib = _lib.load()
         self._call = lib.moe_experts_w4
+        sizes = [lib.moe_w4_tiled_bytes(self._ref, group, i) for i in (0, 1)]
         nbytes = lib.moe_experts_w4_workspace_size(self._ref)
-        if nbytes == 0 and self.max_tokens > 0:  # the library's own reason
-            _check(self._call(self._ref, group, *[None] * 9, 0, None, None), "W4Experts")
+        if 0 in sizes or (nbytes == 0 and self.max_tokens > 0):  # the library's own reason
+            _check(self._call(self._ref, group, *[None] * 7, 0, None, None), "W4Experts")
+        self.w13_t, self.w2_t = (torch.empty(n, dtype=torch.uint8, device=dev) for n in sizes)
+        _check(lib.moe_prepare_weights_w4(
+            self._ref, group, _p(w13_q), _p(w13_s), _p(w2_q), _p(w2_s), _p(self.w13_t),
+            _p(self.w2_t), _handle(None, dev)), "moe_prepare_weights_w4")
         self.ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
         self.status = torch.zeros(1, dtype=_I32, device=dev)
-        self._w = tuple(t.data_ptr() for t in self.weights)
+        self._w = self.w13_t.data_ptr(), self.w2_t.data_ptr()
         self._tail = (self.ws.data_ptr(), nbytes, self.status.data_ptr())
 
     def __call__(self, x, topk_idx, topk_w, y=None, stream=None):
