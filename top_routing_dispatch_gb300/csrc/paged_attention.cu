@@ -18,10 +18,10 @@
 //    (no transposing loads): for K, lane (g, t) takes pieces t, t + 4, ... of
 //    row g; for V, pieces g, g + 8, ... of rows 2t, 2t+1, 2t+8, 2t+9, paired
 //    by byte permutes.
-//  - Those pieces travel through shared memory only as a queue: each lane
-//    copies its own pieces asynchronously into its own slots and reads them
-//    back, several steps later, itself.  No barrier and no bank conflict, and
-//    the queue runs on across the ends of sequences and heads.
+//  - The rows travel through shared memory in a queue of each warp's own
+//    (asynchronous copies of whole lines, pieces permuted against bank
+//    conflicts), which needs no barrier and runs on across the ends of
+//    sequences and heads.
 //  - The work of all sequences and kv heads is one row of units (a unit: the
 //    tokens that the CTA's warps take in one step), cut into equal ranges for
 //    one wave of CTAs.  A range may end inside a sequence: its part (maximum,
@@ -64,27 +64,16 @@ struct AttnArgs {
   int32_t *status;
 };
 
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool ok) {
-  const int n = ok ? 16 : 0;
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async8_zfill(uint32_t dst, const void *src, bool ok) {
-  const int n = ok ? 8 : 0;
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n)
-               : "memory");
-}
-// A piece of `bytes`; EDGE steps zero-fill what is not ok.
-template <int BYTES, bool EDGE>
+// 16 bytes global -> shared; EDGE: zeros unless ok (nothing is read then)
+template <bool EDGE>
 __device__ __forceinline__ void copy_piece(uint32_t dst, const uint8_t *src, bool ok) {
-  if constexpr (EDGE && BYTES == 16)
-    cp_async16_zfill(dst, src, ok);
-  else if constexpr (EDGE)
-    cp_async8_zfill(dst, src, ok);
-  else if constexpr (BYTES == 16)
+  if constexpr (EDGE) {
+    const int n = ok ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+                 : "memory");
+  } else {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+  }
 }
 // 2^x by the hardware's approximation (relative error 2^-22, tiny results 0)
 __device__ __forceinline__ float ex2(float x) {
@@ -100,6 +89,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
                : "memory");
   return v;
 }
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint32_t trans8x8(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -109,13 +103,13 @@ template <bool F16>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   if constexpr (F16)
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -139,6 +133,35 @@ __device__ __forceinline__ void store_out2(__nv_bfloat16 *p, float x, float y) {
 __device__ __forceinline__ void store_out2(float *p, float x, float y) {
   *reinterpret_cast<float2 *>(p) = make_float2(x, y);
 }
+
+// The rows of one step in the queue: KEYS rows of ROW bytes of K, then of V,
+// each as it lies in the cache (a head's tokens are contiguous), except that
+// the 16-byte pieces of a row are permuted: piece c of row r is in place
+// c ^ spread(r).  Copies write whole 128-byte lines, and no two of the eight
+// lanes that shared memory serves at a time read the same banks: for K those
+// are pieces t + 4j of rows 2p and 2p + 1, for V pieces 2p and 2p + 1 of rows
+// 0, 2, 4, 6 (or 1, 3, 5, 7).
+__device__ __forceinline__ int spread(int r) { return (r & 2) | ((((r >> 2) ^ r) & 1) << 2); }
+
+template <int KEYS, int ROW>
+struct Rows {
+  static constexpr int PIECES = ROW / 16;
+  static constexpr int TILE = KEYS * ROW, LOADS = TILE / 512;
+  static constexpr int MASK = PIECES < 8 ? PIECES - 1 : 7;  // of spread
+  static_assert(TILE % 512 == 0, "whole warps of copies");
+
+  // dst: the tile; lane: copies pieces lane, lane + 32, ...
+  template <bool EDGE>
+  __device__ __forceinline__ static void copy(uint32_t dst, const uint8_t *src, int lo, int hi,
+                                              int lane) {
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int x = i * 32 + lane, r = x / PIECES, c = x % PIECES;
+      copy_piece<EDGE>(dst + r * ROW + ((c ^ (spread(r) & MASK)) * 16), src + x * 16,
+                       r >= lo && r < hi);
+    }
+  }
+};
 
 // One lane's piece of a raise of the running maxima: the reduction over the
 // eight lanes that hold the same heads.
@@ -168,8 +191,8 @@ struct MmaPath {
   static constexpr int KJ = D / KE / 4;                 // K pieces per lane and row
   static constexpr int VE = E4M3 && D >= 128 ? 16 : 8;  // values of a V piece
   static constexpr int MI = D / (8 * VE), MJ = VE / 2;
-  static constexpr int LOADS = 2 * KJ + 4 * MI;
-  static constexpr int STAGE_BYTES = LOADS * 512;
+  using Tile = Rows<KEYS, D * EB>;
+  static constexpr int STAGE_BYTES = 2 * Tile::TILE;
   static constexpr int CH = 8 * VE;  // output values of a merge chunk
   static constexpr int NCH = MI;
   static constexpr int Q_SMEM = 0;
@@ -179,36 +202,6 @@ struct MmaPath {
   uint32_t qf[NT][KJ][E4M3 ? 8 : 4];
   float o[MI][MJ][NT][4];
   float m[NT][2], l[NT][2], mult[NT][2];
-
-  // a lane's first piece of K and of V within a step's rows
-  __device__ __forceinline__ static int k_lane(int lane) {
-    return (lane >> 2) * (D * EB) + (lane & 3) * 16;
-  }
-  __device__ __forceinline__ static int v_lane(int lane) {
-    return 2 * (lane & 3) * (D * EB) + (lane >> 2) * (VE * EB);
-  }
-  // k, v: this lane's first pieces; EDGE: only rows in [lo, hi), zeros elsewhere
-  template <bool EDGE>
-  __device__ __forceinline__ static void issue(uint32_t dst, const uint8_t *k, const uint8_t *v,
-                                               int lo, int hi, int lane) {
-    const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const bool ok = g + 8 * r >= lo && g + 8 * r < hi;
-#pragma unroll
-      for (int j = 0; j < KJ; ++j)
-        copy_piece<16, EDGE>(dst + (r * KJ + j) * 512, k + 8 * r * (D * EB) + j * 64, ok);
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = (r & 1) + 8 * (r >> 1);
-      const bool ok = 2 * t + row >= lo && 2 * t + row < hi;
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-        copy_piece<VE * EB, EDGE>(dst + (2 * KJ + r * MI + i) * 512,
-                                  v + row * (D * EB) + i * (8 * VE * EB), ok);
-    }
-  }
 
   // asks for nh query heads (head rows contiguous)
   __device__ __forceinline__ void fetch(const Out *q, int nh, int lane) {
@@ -278,11 +271,16 @@ struct MmaPath {
     }
   }
 
-  // the 16 keys of a slot (src: this lane's pieces); EDGE: only [lo, hi) count
+  // the 16 keys of a slot; EDGE: only [lo, hi) count
   template <bool EDGE>
-  __device__ __forceinline__ void step(uint32_t src, int lo, int hi, int nh, int lane,
+  __device__ __forceinline__ void step(uint32_t slot, int lo, int hi, int nh, int lane,
                                        const float *) {
-    const int g = lane >> 2;
+    constexpr int ROW = D * EB, MASK = Tile::MASK;
+    const int g = lane >> 2, t = lane & 3;
+    const int sk = spread(g) & MASK;  // the same for rows g and g + 8
+    // pieces t + 4j of row g: even j from k0, odd j from k1
+    const uint32_t k0 = slot + g * ROW + ((t ^ sk) & 7) * 16;
+    const uint32_t k1 = slot + g * ROW + (((t + 4) ^ sk) & 7) * 16;
     float s[NT][4], s2[NT][4];  // two chains of sums
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -290,7 +288,8 @@ struct MmaPath {
       for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
 #pragma unroll
     for (int j = 0; j < KJ; ++j) {
-      const uint4 a = lds128(src + j * 512), b = lds128(src + (KJ + j) * 512);
+      const uint32_t at = (j & 1 ? k1 : k0) + (j >> 1) * 128;
+      const uint4 a = lds128(at), b = lds128(at + 8 * ROW);
       if constexpr (!E4M3) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -310,7 +309,6 @@ struct MmaPath {
         }
       }
     }
-    src += 2 * KJ * 512;
     // scores in base 2; masked keys are -inf
     const bool in0 = !EDGE || (g >= lo && g < hi), in1 = !EDGE || (g + 8 >= lo && g + 8 < hi);
     bool high = false;
@@ -369,11 +367,27 @@ struct MmaPath {
         }
       }
     }
+    // rows 2t and 2t + 1 (+ 8): pieces g + 8i, or halves of piece g / 2
+    uint32_t vrow[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int sv = spread(2 * t + c) & MASK;
+      vrow[c] = slot + Tile::TILE + (2 * t + c) * ROW +
+                (VE * EB == 16 ? (g ^ sv) * 16 : ((g >> 1) ^ sv) * 16 + (g & 1) * 8);
+    }
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
       uint4 v[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = lds128(src + (r * MI + i) * 512);
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t at = vrow[r & 1] + (r >> 1) * 8 * ROW + i * 128;
+        if constexpr (VE * EB == 16) {
+          v[r] = lds128(at);
+        } else {
+          const uint2 h = lds64(at);
+          v[r].x = h.x, v[r].y = h.y;
+        }
+      }
 #pragma unroll
       for (int j = 0; j < MJ; ++j) {
         uint32_t a0, a1, a2, a3;
@@ -441,9 +455,8 @@ struct FmaPath {
   static constexpr int KJ = D / 16;            // K pieces per lane (row g, pieces t + 4j)
   static constexpr int VR = D >= 128 ? 1 : 2;  // rows of one V load of the warp
   static constexpr int VJ = D > 128 ? 2 : 1;   // V pieces per lane and row
-  static constexpr int VL = KEYS / VR * VJ;
-  static constexpr int LOADS = KJ + VL;
-  static constexpr int STAGE_BYTES = LOADS * 512;
+  using Tile = Rows<KEYS, D * EB>;
+  static constexpr int STAGE_BYTES = 2 * Tile::TILE;
   static constexpr int CH = D > 128 ? 128 : D;
   static constexpr int NCH = D / CH;
   static constexpr int Q_SMEM = NH * D;
@@ -451,28 +464,6 @@ struct FmaPath {
   float o[NH][VJ][4];
   float m[NH], l[NH];
   float mult;
-
-  __device__ __forceinline__ static int k_lane(int lane) {
-    return (lane >> 2) * (D * EB) + (lane & 3) * 16;
-  }
-  __device__ __forceinline__ static int v_lane(int lane) {
-    return VR == 2 ? (lane >> 4) * (D * EB) + (lane & 15) * 16 : lane * 16;
-  }
-  template <bool EDGE>
-  __device__ __forceinline__ static void issue(uint32_t dst, const uint8_t *k, const uint8_t *v,
-                                               int lo, int hi, int lane) {
-    const bool okk = (lane >> 2) >= lo && (lane >> 2) < hi;
-#pragma unroll
-    for (int j = 0; j < KJ; ++j) copy_piece<16, EDGE>(dst + j * 512, k + j * 64, okk);
-    const int sub = VR == 2 ? lane >> 4 : 0;
-#pragma unroll
-    for (int r = 0; r < KEYS / VR; ++r) {
-      const bool ok = r * VR + sub >= lo && r * VR + sub < hi;
-#pragma unroll
-      for (int j = 0; j < VJ; ++j)
-        copy_piece<16, EDGE>(dst + (KJ + r * VJ + j) * 512, v + r * VR * (D * EB) + j * 512, ok);
-    }
-  }
 
   __device__ __forceinline__ void fetch(const Out *, int, int) {}
 
@@ -492,13 +483,16 @@ struct FmaPath {
   }
 
   template <bool EDGE>
-  __device__ __forceinline__ void step(uint32_t src, int lo, int hi, int nh, int lane,
+  __device__ __forceinline__ void step(uint32_t slot, int lo, int hi, int nh, int lane,
                                        const float *qs) {
+    constexpr int ROW = D * EB;
     const int g = lane >> 2, t = lane & 3;
+    const uint32_t k0 = slot + g * ROW + (t ^ spread(g)) * 16;
+    const uint32_t k1 = slot + g * ROW + ((t + 4) ^ spread(g)) * 16;
     float4 k[KJ];
 #pragma unroll
     for (int j = 0; j < KJ; ++j) {
-      const uint4 x = lds128(src + j * 512);
+      const uint4 x = lds128((j & 1 ? k1 : k0) + (j >> 1) * 128);
       k[j] = make_float4(__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z),
                          __uint_as_float(x.w));
     }
@@ -542,13 +536,14 @@ struct FmaPath {
       p[h] = ex2(p[h] - (m[h] == -INFINITY ? 0.f : m[h]));
       l[h] += p[h];  // the key's four lanes hold the same sum
     }
-    const int sub = VR == 2 ? lane >> 4 : 0;
+    const int sub = VR == 2 ? lane >> 4 : 0, piece = VR == 2 ? lane & 15 : lane;
 #pragma unroll
     for (int r = 0; r < KEYS / VR; ++r) {
       float4 v[VJ];
 #pragma unroll
       for (int j = 0; j < VJ; ++j) {
-        const uint4 x = lds128(src + (KJ + r * VJ + j) * 512);
+        const int row = r * VR + sub;
+        const uint4 x = lds128(slot + Tile::TILE + row * ROW + (piece ^ spread(row)) * 16 + j * 512);
         v[j] = make_float4(__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z),
                            __uint_as_float(x.w));
       }
@@ -614,12 +609,22 @@ __device__ __forceinline__ Seq seq_info(const AttnArgs &a, int b) {
   return s;
 }
 
-// Output chunks that the warps exchange at a time, and the queue's depth: what
-// two CTAs of an SM (one of eight warps) can hold.
+// CTAs of an SM, the output chunks that the warps exchange at a time, and the
+// queue's depth: what the SM's shared memory and registers hold.
+template <class P>
+constexpr int ctas() {
+  return P::STAGE_BYTES > 8192 ? 1 : P::NH * P::D <= 1024 && P::Q_SMEM == 0 ? 3 : 2;
+}
+template <class P>
+constexpr int cta_bytes() {
+  return (227 / ctas<P>() - 1) * 1024;
+}
 template <class P, int NW>
 constexpr int round_chunks() {
-  constexpr int fit = (NW == 8 ? 32 : 16) * 1024 / (NW * P::NH * P::CH * 4);
-  return fit < 1 ? 1 : fit < P::NCH ? fit : P::NCH;
+  constexpr int fit = cta_bytes<P>() / 8 / (NW * P::NH * P::CH * 4);
+  int n = P::NCH;  // a power of two; the rounds are whole
+  while (n > 1 && n > fit) n /= 2;
+  return n;
 }
 template <class P, int NW>
 constexpr size_t merge_bytes() {
@@ -628,9 +633,10 @@ constexpr size_t merge_bytes() {
 }
 template <class P, int NW>
 constexpr int stages() {
-  constexpr int fit = (int)(((NW == 8 ? 226 : 112) * 1024 - merge_bytes<P, NW>()) /
-                            (NW * P::STAGE_BYTES));
-  return fit < 2 ? 2 : fit > 8 ? 8 : fit;
+  constexpr int fit = (int)((cta_bytes<P>() - merge_bytes<P, NW>()) / (NW * P::STAGE_BYTES));
+  static_assert(fit >= 2, "a queue of two steps");
+  static_assert(P::NCH % round_chunks<P, NW>() == 0, "whole rounds");
+  return fit > 8 ? 8 : fit;
 }
 
 template <class P, int NW>
@@ -639,7 +645,7 @@ constexpr size_t smem_bytes() {
 }
 
 template <class P, int NW>
-__global__ void __launch_bounds__(NW * 32, NW == 8 ? 1 : 2) paged_attention_kernel(
+__global__ void __launch_bounds__(NW * 32, ctas<P>()) paged_attention_kernel(
     const AttnArgs a) {
   pdl_enter();
   constexpr int NT = NW * 32, ST = stages<P, NW>();
@@ -733,7 +739,7 @@ __global__ void __launch_bounds__(NW * 32, NW == 8 ? 1 : 2) paged_attention_kern
     } while (s_first.units == 0);
   }
   long long S = sh_S;  // where the item begins in the row
-  const uint32_t ring = ptx::smem_u32(smem) + (uint32_t)w * (ST * P::STAGE_BYTES) + lane * 16;
+  const uint32_t ring = ptx::smem_u32(smem) + (uint32_t)w * (ST * P::STAGE_BYTES);
   constexpr int ROW = D * P::EB, STRIDE = NW * P::KEYS;
   const size_t head_bytes = (size_t)a.P * ROW;
   const int page_step = STRIDE / a.P, off_step = STRIDE - page_step * a.P;
@@ -756,7 +762,6 @@ __global__ void __launch_bounds__(NW * 32, NW == 8 ? 1 : 2) paged_attention_kern
   };
   int in_end = units_of(in_S, in.s.units);
   bool more = true;
-  const uint8_t *k_lane = a.kc + P::k_lane(lane), *v_lane = a.vc + P::v_lane(lane);
   int page = 0, slot_in = 0;
   size_t head_off = 0;
   auto lookup = [&]() {
@@ -777,11 +782,13 @@ __global__ void __launch_bounds__(NW * 32, NW == 8 ? 1 : 2) paged_attention_kern
         const size_t at = (size_t)(ok ? page : 0) * a.page_bytes + head_off + in.off * ROW;
         const uint32_t dst = ring + slot_in * P::STAGE_BYTES;
         if (ok && in.key >= in.s.first && in.key + P::KEYS <= in.s.len) {
-          P::template issue<false>(dst, k_lane + at, v_lane + at, 0, 0, lane);
+          P::Tile::template copy<false>(dst, a.kc + at, 0, 0, lane);
+          P::Tile::template copy<false>(dst + P::Tile::TILE, a.vc + at, 0, 0, lane);
         } else {
           if (!ok && lane == 0) flag_status(a.status, MOE_DEV_BAD_CACHE);
-          P::template issue<true>(dst, k_lane + at, v_lane + at,
-                                  ok ? in.s.first - in.key : P::KEYS, in.s.len - in.key, lane);
+          const int lo = ok ? in.s.first - in.key : P::KEYS, hi = in.s.len - in.key;
+          P::Tile::template copy<true>(dst, a.kc + at, lo, hi, lane);
+          P::Tile::template copy<true>(dst + P::Tile::TILE, a.vc + at, lo, hi, lane);
         }
       }
       slot_in = slot_in + 1 == ST ? 0 : slot_in + 1;
@@ -835,8 +842,10 @@ __global__ void __launch_bounds__(NW * 32, NW == 8 ? 1 : 2) paged_attention_kern
     int key = sq.base + (c * NW + w) * P::KEYS;
 #pragma unroll 1
     for (int i = 0; i < n; ++i, key += STRIDE) {
+      __syncwarp();  // the slot that is filled next has been read
       issue();
       ptx::cp_async_wait<ST - 1>();
+      __syncwarp();  // the other lanes' pieces have arrived too
       const uint32_t src = ring + slot * P::STAGE_BYTES;
       if (key >= sq.first && key + P::KEYS <= sq.len)
         st.template step<false>(src, 0, 0, nh, lane, qs);
