@@ -30,12 +30,12 @@
 namespace moe {
 namespace {
 
-constexpr int WT = 256, WW = WT / 32;  // threads and warps per CTA
+constexpr int WT = 256, WW = WT / 32;  // threads and warps of the kernel for few tokens
+constexpr float kFewGroups = 1.f;      // column groups up to which it is taken
 template <int GROUP>
 constexpr int record_bytes() {  // codes; 128 / GROUP bf16 scales a row
   return 1024 + 16 * (128 / GROUP) * 2;
 }
-constexpr int kMaxEntries = kMaxE + kW4MaxPairs / 4;
 
 
 struct W4Args {
@@ -105,50 +105,68 @@ __device__ __forceinline__ uint32_t quarter_codes(uint32_t w) {
   return r;
 }
 
-// The routing lists of the call, built by every CTA for itself: pairs sorted
-// by expert, in ascending order inside an expert (so that every CTA cuts an
-// expert's pairs into the same entries), and the entries (expert, first pair,
-// pairs <= ROWS) to compute.
+// The routing lists of the call, built by every CTA for itself in shared
+// memory: pairs sorted by expert, in ascending order inside an expert (so that
+// every CTA cuts an expert's pairs into the same entries), and the entries
+// (expert, first pair, pairs <= ROWS) to compute.
 struct Lists {
-  int start[kMaxE];
-  uint8_t entry_expert[kMaxEntries];
-  uint8_t entry_n[kMaxEntries];
-  uint16_t entry_first[kMaxEntries];
+  int *start;         // (E)
+  uint32_t *entry;    // expert | pairs - 1 << 8 | first << 16
+  uint16_t *pair;     // (nK)
   int entries;
-  uint16_t pair[kW4MaxPairs];
+  __device__ __forceinline__ int expert(int i) const { return entry[i] & 0xff; }
+  __device__ __forceinline__ int count(int i) const { return (entry[i] >> 8 & 0xff) + 1; }
+  __device__ __forceinline__ int first(int i) const { return entry[i] >> 16; }
 };
 
-// Queue steps of a warp: what two CTAs of an SM can hold.
-template <int GROUP, int MT>
-constexpr int queue_steps() {
-  constexpr int fit = (int)((112 * 1024 - sizeof(Lists)) / (WW * MT * record_bytes<GROUP>()));
-  return fit > 8 ? 8 : fit;
+__host__ __device__ inline int max_entries(int nK, int E, int rows) {
+  return (nK < E ? nK : E) + nK / rows;
+}
+__host__ __device__ inline int lists_bytes(int nK, int E, int rows) {
+  return (16 + 4 * E + 4 * max_entries(nK, E, rows) + 2 * nK + 15) & ~15;
 }
 
-// hist: (WW, kMaxE) scratch.  Each warp takes a contiguous slice of the pairs.
+// mem: lists_bytes; hist: (warps, E) scratch.  Each warp takes a contiguous
+// slice of the pairs.
 template <int ROWS>
-__device__ __forceinline__ void build_lists(Lists &L, int (*hist)[kMaxE], const W4Args &a) {
+__device__ __forceinline__ Lists build_lists(uint8_t *mem, int *hist, const W4Args &a) {
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int slice = (a.nK + 32 * WW - 1) / (32 * WW) * 32;
+  const int threads = blockDim.x, warps = threads >> 5;
+  Lists L;
+  int *total = reinterpret_cast<int *>(mem);
+  L.start = total + 4;
+  L.entry = reinterpret_cast<uint32_t *>(L.start + a.E);
+  L.pair = reinterpret_cast<uint16_t *>(L.entry + max_entries(a.nK, a.E, ROWS));
+  int *mine = hist + w * a.E;
+  const int slice = (a.nK + threads - 1) / threads * 32;
   const int f0 = w * slice, f1 = min(f0 + slice, a.nK);
-  for (int e = lane; e < a.E; e += 32) hist[w][e] = 0;
+  for (int e = lane; e < a.E; e += 32) mine[e] = 0;
   __syncwarp();
   bool bad = false;
-  for (int f = f0 + lane; f < f1; f += 32) {
-    const int e = __ldg(a.idx + f);
-    if ((unsigned)e < (unsigned)a.E)
-      atomicAdd(&hist[w][e], 1);
-    else
-      bad = true;
+  constexpr int BATCH = 8;  // ids in flight per lane
+  for (int fb = f0; fb < f1; fb += 32 * BATCH) {
+    int e[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int f = fb + 32 * i + lane;
+      e[i] = f < f1 ? __ldg(a.idx + f) : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      if (fb + 32 * i + lane >= f1) continue;
+      if ((unsigned)e[i] < (unsigned)a.E)
+        atomicAdd(&mine[e[i]], 1);
+      else
+        bad = true;
+    }
   }
   if (__syncthreads_or(bad) && tid == 0 && blockIdx.x == 0)
     flag_status(a.status, MOE_DEV_BAD_ROUTING);
-  for (int e = tid; e < a.E; e += WT) {  // counts; each warp's first rank
+  for (int e = tid; e < a.E; e += threads) {  // counts; each warp's first rank
     int run = 0;
-#pragma unroll
-    for (int i = 0; i < WW; ++i) {
-      const int h = hist[i][e];
-      hist[i][e] = run;
+    for (int i = 0; i < warps; ++i) {
+      const int h = hist[i * a.E + e];
+      hist[i * a.E + e] = run;
       run += h;
     }
     L.start[e] = run;
@@ -167,48 +185,167 @@ __device__ __forceinline__ void build_lists(Lists &L, int (*hist)[kMaxE], const 
       }
       const int first = pairs + ic - c;
       if (e0 + lane < a.E) L.start[e0 + lane] = first;
-      for (int i = 0; i < m; ++i) {
-        const int at = entries + im - m + i;
-        L.entry_expert[at] = e0 + lane;
-        L.entry_first[at] = first + ROWS * i;
-        L.entry_n[at] = min(ROWS, c - ROWS * i);
-      }
+      for (int i = 0; i < m; ++i)
+        L.entry[entries + im - m + i] = (uint32_t)(e0 + lane) |
+                                        (uint32_t)(min(ROWS, c - ROWS * i) - 1) << 8 |
+                                        (uint32_t)(first + ROWS * i) << 16;
       pairs += __shfl_sync(0xffffffffu, ic, 31);
       entries += __shfl_sync(0xffffffffu, im, 31);
     }
-    if (lane == 0) L.entries = entries;
+    if (lane == 0) *total = entries;
   }
   __syncthreads();
-  for (int fb = f0; fb < f1; fb += 32) {
-    const int f = fb + lane;
-    int e = f < f1 ? __ldg(a.idx + f) : -1;
-    const bool ok = (unsigned)e < (unsigned)a.E;
-    if (!ok) e = -1;
-    const unsigned peers = __match_any_sync(0xffffffffu, e);
-    const int rank = __popc(peers & ((1u << lane) - 1u));
-    if (ok) L.pair[L.start[e] + hist[w][e] + rank] = (uint16_t)f;
-    __syncwarp();
-    if (ok && rank == 0) hist[w][e] += __popc(peers);
-    __syncwarp();
+  for (int fb = f0; fb < f1; fb += 32 * BATCH) {
+    int e[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int f = fb + 32 * i + lane;
+      e[i] = f < f1 ? __ldg(a.idx + f) : -1;
+      if ((unsigned)e[i] >= (unsigned)a.E) e[i] = -1;
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      if (fb + 32 * i >= f1) break;  // the whole warp
+      const unsigned peers = __match_any_sync(0xffffffffu, e[i]);
+      const int rank = __popc(peers & ((1u << lane) - 1u));
+      if (e[i] >= 0) L.pair[L.start[e[i]] + mine[e[i]] + rank] = (uint16_t)(fb + 32 * i + lane);
+      __syncwarp();
+      if (e[i] >= 0 && rank == 0) mine[e[i]] += __popc(peers);
+      __syncwarp();
+    }
   }
+  L.entries = *total;
   __syncthreads();
+  return L;
 }
 
+// acc += one step (128 indices) of MT tiles: codes wd (two planes), scales sc;
+// x(i, j): the operand piece of column group i for words j.
+template <int GROUP, int MT, int NT, class X>
+__device__ __forceinline__ void step_product(const uint4 (&wd)[MT][2], const uint4 (&sc)[MT], X x,
+                                             float (&acc)[MT][NT][4]) {
+  constexpr int NS = 128 / GROUP, WPL = 4 / NS;
+  float part[MT][NT][4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint4 xv[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) xv[i] = x(i, j);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const uint32_t wa = word(wd[m][0], j), wb = word(wd[m][1], j);
+      {
+        const uint32_t a0 = quarter_codes<false>(wa), a1 = quarter_codes<false>(wb);
+        const uint32_t a2 = quarter_codes<true>(wa), a3 = quarter_codes<true>(wb);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          if (j % WPL == 0)
+            mma_bf16_first(part[m][i], a0, a1, a2, a3, xv[i].x, xv[i].y);
+          else
+            mma_bf16(part[m][i], a0, a1, a2, a3, xv[i].x, xv[i].y);
+        }
+      }
+      {
+        const uint32_t a0 = quarter_codes<false>(wa >> 8), a1 = quarter_codes<false>(wb >> 8);
+        const uint32_t a2 = quarter_codes<true>(wa >> 8), a3 = quarter_codes<true>(wb >> 8);
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          mma_bf16(part[m][i], a0, a1, a2, a3, xv[i].z, xv[i].w);
+      }
+      if (j % WPL == WPL - 1) {
+        // this group's scales: rows g and g + 8 are NS scales apart
+        const int k = j / WPL;
+        const uint32_t p0 = word(sc[m], k >> 1), p1 = word(sc[m], (NS + k) >> 1);
+        const float s0 = __uint_as_float(k & 1 ? p0 & 0xffff0000u : p0 << 16);
+        const float s1 = __uint_as_float((NS + k) & 1 ? p1 & 0xffff0000u : p1 << 16);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          acc[m][i][0] = fmaf(part[m][i][0], s0, acc[m][i][0]);
+          acc[m][i][1] = fmaf(part[m][i][1], s0, acc[m][i][1]);
+          acc[m][i][2] = fmaf(part[m][i][2], s1, acc[m][i][2]);
+          acc[m][i][3] = fmaf(part[m][i][3], s1, acc[m][i][3]);
+        }
+      }
+    }
+  }
+}
+
+// The scales of a record at `rec` for lane row g.
+template <int GROUP>
+__device__ __forceinline__ uint4 load_scales(uint32_t rec, int g) {
+  constexpr int NS = 128 / GROUP;
+  const uint32_t at = rec + 1024 + g * (4 * NS);
+  uint4 sc = make_uint4(0, 0, 0, 0);
+  if constexpr (NS == 4) sc = lds128(at);
+  if constexpr (NS == 2) {
+    const uint2 v = lds64(at);
+    sc.x = v.x, sc.y = v.y;
+  }
+  if constexpr (NS == 1) sc.x = lds32(at);
+  return sc;
+}
+
+// Stores the sums (of quarter codes) of tile `tile` for an entry's pairs.
+template <bool DOWN, int NT>
+__device__ __forceinline__ void store_tile(const W4Args &a, const Lists &L, const float (&acc)[NT][4],
+                                           int tile, int rows, int first, int lane) {
+  constexpr int CR = DOWN ? 4 : 8;
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    if constexpr (DOWN) {
+      const int r = CR * i + t;  // columns 2t and 2t+1: h's two parts
+      if (r >= rows) continue;
+      const int f = L.pair[first + r];
+      const float wt = 4.f * __ldg(a.w + f);
+      float *y = a.yslot + (size_t)f * a.C + tile * 16 + g;
+      y[0] = (acc[i][0] + acc[i][1]) * wt;
+      y[8] = (acc[i][2] + acc[i][3]) * wt;
+    } else {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int r = CR * i + 2 * t + c;
+        if (r >= rows) continue;
+        const int f = L.pair[first + r];
+        const float gate = 4.f * acc[i][c], up = 4.f * acc[i][2 + c];
+        const float h = gate / (1.f + __expf(-gate)) * up;
+        const __nv_bfloat16 hi = __float2bfloat16_rn(h);
+        const size_t at = (size_t)f * a.I + tile * 8 + g;
+        a.hhi[at] = hi;
+        a.hlo[at] = __float2bfloat16_rn(h - __bfloat162float(hi));
+      }
+    }
+  }
+}
+
+// Queue steps: what `ctas` CTAs of an SM can hold of `step` bytes beside 10 KB
+// of lists each (a call with longer lists gets fewer CTAs).
+constexpr int queue_steps(int ctas, int step) {
+  const int fit = ((227 / ctas - 1) * 1024 - 10 * 1024) / step;
+  return fit > 8 ? 8 : fit;
+}
+
+// Few tokens: up to CR pairs an entry (one column group), every warp by itself.
 // DOWN false: tiles of 8 gate and 8 up rows (8 columns of h), DOWN true: tiles
 // of 16 columns of y; a unit's MT tiles share each operand piece of x or h.
-// GROUP: reduction indices per scale.  NTM: column groups of an entry at most.
-template <bool DOWN, int GROUP, int MT, int NTM>
-__global__ void __launch_bounds__(WT, 2) w4_kernel(const W4Args a) {
-  constexpr int NS = 128 / GROUP;   // scales of a row in a record
-  constexpr int WPL = 4 / NS;       // a lane's words of a group: WPL t .. of the group's 4 WPL
+// GROUP: reduction indices per scale.
+template <bool DOWN, int GROUP, int MT>
+struct Few {
+  static constexpr int STEP = MT * record_bytes<GROUP>();
+  static constexpr int ST = queue_steps(2, WW * STEP);
+  static constexpr int QUEUE = WW * ST * STEP;
+};
+
+template <bool DOWN, int GROUP, int MT>
+__global__ void __launch_bounds__(WT, 2) w4_few_kernel(const W4Args a) {
+  using F = Few<DOWN, GROUP, MT>;
+  constexpr int WPL = GROUP / 32;   // a lane's words of a group: WPL t .. of the group's 4 WPL
   constexpr int CR = DOWN ? 4 : 8;  // pairs of a column group
-  constexpr int REC = record_bytes<GROUP>();
-  constexpr int ST = queue_steps<GROUP, MT>(), STEP_BYTES = MT * REC;
+  constexpr int REC = record_bytes<GROUP>(), ST = F::ST, STEP = F::STEP, NS = 128 / GROUP;
   extern __shared__ __align__(128) uint8_t smem[];
-  Lists &L = *reinterpret_cast<Lists *>(smem + WW * ST * STEP_BYTES);
-  pdl_enter();
+  if constexpr (!DOWN) pdl_enter();
   // the queue's memory is scratch until the lists are ready
-  build_lists<CR * NTM>(L, reinterpret_cast<int(*)[kMaxE]>(smem), a);
+  const Lists L = build_lists<CR>(smem + F::QUEUE, reinterpret_cast<int *>(smem), a);
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int tiles = a.C / 16 / MT;  // units of an entry
@@ -216,7 +353,7 @@ __global__ void __launch_bounds__(WT, 2) w4_kernel(const W4Args a) {
   const int units = L.entries * tiles;
   const int step = gridDim.x * WW;
   const int u0 = w * gridDim.x + blockIdx.x;  // the first units go to different CTAs
-  const uint32_t ring = ptx::smem_u32(smem) + w * (ST * STEP_BYTES);
+  const uint32_t ring = ptx::smem_u32(smem) + w * (ST * STEP);
   const size_t tile_bytes = (size_t)NB * REC;
 
   // the copying side
@@ -226,7 +363,7 @@ __global__ void __launch_bounds__(WT, 2) w4_kernel(const W4Args a) {
   auto locate = [&]() {
     if (pu >= units) return;
     const int ent = pu / tiles, tile = pu - ent * tiles;
-    src = a.rec + ((size_t)L.entry_expert[ent] * (a.C / 16) + tile * MT) * tile_bytes + lane * 16;
+    src = a.rec + ((size_t)L.expert(ent) * (a.C / 16) + tile * MT) * tile_bytes + lane * 16;
   };
   auto issue = [&]() {
     if (pu < units) {
@@ -238,8 +375,8 @@ __global__ void __launch_bounds__(WT, 2) w4_kernel(const W4Args a) {
         if (lane < 2 * NS) cp_async16(put + m * REC + 1024, from + 1024);
       }
       src += REC;
-      put += STEP_BYTES;
-      if (put >= ring + ST * STEP_BYTES) put -= ST * STEP_BYTES;
+      put += STEP;
+      if (put >= ring + ST * STEP) put -= ST * STEP;
       if (++pb == NB) {
         pb = 0;
         pu += step;
@@ -251,147 +388,222 @@ __global__ void __launch_bounds__(WT, 2) w4_kernel(const W4Args a) {
   locate();
 #pragma unroll 1
   for (int i = 0; i < ST - 1; ++i) issue();
+  if constexpr (DOWN) {  // weights are on their way before h is there
+    pdl_wait();
+    pdl_launch();
+  }
 
-  uint32_t get = ring + lane * 16;
+  uint32_t get = ring;
 #pragma unroll 1
   for (int u = u0; u < units; u += step) {
     const int ent = u / tiles, tile = (u - ent * tiles) * MT;
-    const int rows = L.entry_n[ent], first = L.entry_first[ent];
+    const int rows = L.count(ent), first = L.first(ent);
+    // the operand row of this lane's column: a pair's x, or in even columns
+    // the first, in odd the second part of its h (columns past the last pair
+    // repeat it; their sums are not stored)
+    const int f = L.pair[first + min(DOWN ? g >> 1 : g, rows - 1)];
+    const __nv_bfloat16 *p = DOWN ? (g & 1 ? a.hlo : a.hhi) + (size_t)f * a.R
+                                  : a.x + (size_t)(f / a.K) * a.R;
+    const uint4 *xr = reinterpret_cast<const uint4 *>(p) + t * WPL;
+    float acc[MT][1][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[m][0][0] = acc[m][0][1] = acc[m][0][2] = acc[m][0][3] = 0.f;
+    uint4 xv[4];  // the operand pieces of a step, asked for a step ahead
+#pragma unroll
+    for (int j = 0; j < 4; ++j) xv[j] = __ldg(xr + (j / WPL) * 4 * WPL + j % WPL);
+#pragma unroll 1
+    for (int b = 0; b < NB; ++b) {
+      ptx::cp_async_wait<ST - 2>();
+      __syncwarp();  // scales are read by lanes that did not copy them
+      issue();
+      if (b + 1 < NB) xr += 16;
+      uint4 wd[MT][2], sc[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        wd[m][0] = lds128(get + m * REC + lane * 16);
+        wd[m][1] = lds128(get + m * REC + 512 + lane * 16);
+        sc[m] = load_scales<GROUP>(get + m * REC, g);
+      }
+      get += STEP;
+      if (get >= ring + ST * STEP) get -= ST * STEP;
+      step_product<GROUP, MT, 1>(
+          wd, sc,
+          [&](int, int j) {
+            const uint4 v = xv[j];
+            xv[j] = __ldg(xr + (j / WPL) * 4 * WPL + j % WPL);
+            return v;
+          },
+          acc);
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+      store_tile<DOWN, 1>(a, L, acc[m], tile + m, rows, first, lane);
+  }
+  ptx::cp_async_wait<0>();
+}
+
+// More tokens: up to NTM column groups an entry.  The four warps of a CTA work
+// on eight tiles of one entry and share its operand rows, which travel in the
+// same queue as the weights: each step holds the 8 KB of codes of the eight
+// tiles and 128 indices of up to 8 NTM operand rows, pieces permuted so that
+// the reads meet no bank twice.
+constexpr int MW = 4, MT_MANY = 2;
+template <bool DOWN, int GROUP, int NTM>
+struct Many {
+  static constexpr int WEIGHTS = MW * MT_MANY * record_bytes<GROUP>();
+  static constexpr int STEP = WEIGHTS + NTM * 8 * 256;
+  static constexpr int ST = queue_steps(3, STEP);
+  static constexpr int QUEUE = ST * STEP;
+  static_assert(ST >= 3, "a queue of three steps");
+};
+
+// place of 16-byte piece c of operand row r
+template <int WPL>
+__device__ __forceinline__ int operand_place(int r, int c) {
+  return WPL == 1 ? c ^ ((r & 1) << 2) : WPL == 2 ? c ^ (r & 1) : c ^ ((c >> 3) & 1) ^ ((r & 1) << 1);
+}
+
+template <bool DOWN, int GROUP, int NTM>
+__global__ void __launch_bounds__(MW * 32, 3) w4_many_kernel(const W4Args a) {
+  using Q = Many<DOWN, GROUP, NTM>;
+  constexpr int WPL = GROUP / 32, MT = MT_MANY;
+  constexpr int CR = DOWN ? 4 : 8;  // pairs of a column group
+  constexpr int REC = record_bytes<GROUP>(), ST = Q::ST, STEP = Q::STEP, NS = 128 / GROUP;
+  extern __shared__ __align__(128) uint8_t smem[];
+  if constexpr (!DOWN) pdl_enter();
+  const Lists L = build_lists<CR * NTM>(smem + Q::QUEUE, reinterpret_cast<int *>(smem), a);
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int tiles = a.C / 16 / (MW * MT);  // units of an entry
+  const int NB = a.R / 128;
+  const int units = L.entries * tiles;
+  const uint32_t ring = ptx::smem_u32(smem);
+  const size_t tile_bytes = (size_t)NB * REC;
+
+  // the copying side: this warp's tiles, and one 16-byte piece of every
+  // eighth operand row
+  struct {
+    int u, b;
+    uint32_t put;
+  } pw{(int)blockIdx.x, 0, ring}, px = pw;
+  const uint8_t *src = nullptr;
+  const uint4 *xsrc[NTM];
+  int xrows = 0;
+  auto locate_weights = [&]() {
+    if (pw.u >= units) return;
+    const int ent = pw.u / tiles, tile = (pw.u - ent * tiles) * (MW * MT) + w * MT;
+    src = a.rec + ((size_t)L.expert(ent) * (a.C / 16) + tile) * tile_bytes + lane * 16;
+  };
+  auto locate_operand = [&]() {
+    if (px.u >= units) return;
+    const int ent = px.u / tiles, rows = L.count(ent), first = L.first(ent);
+    xrows = DOWN ? 2 * rows : rows;
+#pragma unroll
+    for (int i = 0; i < NTM; ++i) {
+      const int r = i * 8 + (tid >> 4);
+      const int f = L.pair[first + min(DOWN ? r >> 1 : r, rows - 1)];
+      const __nv_bfloat16 *p = DOWN ? (r & 1 ? a.hlo : a.hhi) + (size_t)f * a.R
+                                    : a.x + (size_t)(f / a.K) * a.R;
+      xsrc[i] = reinterpret_cast<const uint4 *>(p) + (tid & 15);
+    }
+  };
+  const uint32_t xput = Q::WEIGHTS + (tid >> 4) * 256 + operand_place<WPL>(tid >> 4, tid & 15) * 16;
+  auto advance = [&](auto &p, auto locate) {
+    p.put += STEP;
+    if (p.put == ring + ST * STEP) p.put = ring;
+    if (++p.b == NB) {
+      p.b = 0;
+      p.u += gridDim.x;
+      locate();
+    }
+  };
+  auto issue_weights = [&]() {
+    if (pw.u >= units) return;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const uint8_t *from = src + m * tile_bytes;
+      const uint32_t to = pw.put + (w * MT + m) * REC + lane * 16;
+      cp_async16(to, from);
+      cp_async16(to + 512, from + 512);
+      if (lane < 2 * NS) cp_async16(to + 1024, from + 1024);
+    }
+    src += REC;
+    advance(pw, locate_weights);
+  };
+  auto issue_operand = [&]() {
+    if (px.u >= units) return;
+#pragma unroll
+    for (int i = 0; i < NTM; ++i) {
+      if (i * 8 < xrows) cp_async16(px.put + xput + i * 8 * 256, xsrc[i]);
+      xsrc[i] += 16;
+    }
+    advance(px, locate_operand);
+  };
+  locate_weights();
+  locate_operand();
+#pragma unroll 1
+  for (int i = 0; i < ST - 1; ++i) issue_weights();
+  if constexpr (DOWN) {  // weights are on their way before h is there
+    pdl_wait();
+    pdl_launch();
+  }
+#pragma unroll 1
+  for (int i = 0; i < ST - 1; ++i) {
+    issue_operand();
+    ptx::cp_async_commit();
+  }
+
+  uint32_t get = ring;
+#pragma unroll 1
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    const int ent = u / tiles, tile = (u - ent * tiles) * (MW * MT) + w * MT;
+    const int rows = L.count(ent), first = L.first(ent);
     auto pass = [&](auto nt_c) {
       constexpr int NT = decltype(nt_c)::value;
-      constexpr bool AHEAD = NT <= 2;
-      // the operand row of this lane's column in each group: a pair's x, or in
-      // even columns the first, in odd the second part of its h (columns past
-      // the last pair repeat it; their sums are not stored)
-      const uint4 *xr[NT];
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const int f = L.pair[first + min(CR * i + (DOWN ? g >> 1 : g), rows - 1)];
-        const __nv_bfloat16 *p = DOWN ? (g & 1 ? a.hlo : a.hhi) + (size_t)f * a.R
-                                      : a.x + (size_t)(f / a.K) * a.R;
-        xr[i] = reinterpret_cast<const uint4 *>(p) + t * WPL;
-      }
-      float acc[MT][NT][4], part[MT][NT][4];
+      float acc[MT][NT][4];
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int i = 0; i < NT; ++i)
           acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.f;
-      uint4 xv[NT][4];  // the operand pieces of a step
-      auto load_x = [&](int j) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i) xv[i][j] = __ldg(xr[i] + (j / WPL) * 4 * WPL + j % WPL);
-      };
-      if constexpr (AHEAD)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) load_x(j);
 #pragma unroll 1
       for (int b = 0; b < NB; ++b) {
         ptx::cp_async_wait<ST - 2>();
-        __syncwarp();  // scales are read by lanes that did not copy them
-        issue();
-        if (!AHEAD || b + 1 < NB) {  // the next pieces, or (not AHEAD) this step's
-          if (AHEAD || b > 0)
-#pragma unroll
-            for (int i = 0; i < NT; ++i) xr[i] += 16;
-        }
+        __syncthreads();  // the step has arrived; the one before it has been used
+        issue_weights();
+        issue_operand();
+        ptx::cp_async_commit();
+        const uint32_t rec = get + w * MT * REC;
+        const uint32_t x = get + Q::WEIGHTS + g * 256;
         uint4 wd[MT][2], sc[MT];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          wd[m][0] = lds128(get + m * REC);
-          wd[m][1] = lds128(get + m * REC + 512);
-          const uint32_t at = get - lane * 16 + m * REC + 1024 + g * (4 * NS);
-          if constexpr (NS == 4) sc[m] = lds128(at);
-          if constexpr (NS == 2) {
-            const uint2 v = lds64(at);
-            sc[m].x = v.x, sc[m].y = v.y;
-          }
-          if constexpr (NS == 1) sc[m].x = lds32(at);
+          wd[m][0] = lds128(rec + m * REC + lane * 16);
+          wd[m][1] = lds128(rec + m * REC + 512 + lane * 16);
+          sc[m] = load_scales<GROUP>(rec + m * REC, g);
         }
-        get += STEP_BYTES;
-        if (get >= ring + ST * STEP_BYTES) get -= ST * STEP_BYTES;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (!AHEAD) load_x(j);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const uint32_t wa = word(wd[m][0], j), wb = word(wd[m][1], j);
-            {
-              const uint32_t a0 = quarter_codes<false>(wa), a1 = quarter_codes<false>(wb);
-              const uint32_t a2 = quarter_codes<true>(wa), a3 = quarter_codes<true>(wb);
-#pragma unroll
-              for (int i = 0; i < NT; ++i) {
-                if (j % WPL == 0)
-                  mma_bf16_first(part[m][i], a0, a1, a2, a3, xv[i][j].x, xv[i][j].y);
-                else
-                  mma_bf16(part[m][i], a0, a1, a2, a3, xv[i][j].x, xv[i][j].y);
-              }
-            }
-            {
-              const uint32_t a0 = quarter_codes<false>(wa >> 8), a1 = quarter_codes<false>(wb >> 8);
-              const uint32_t a2 = quarter_codes<true>(wa >> 8), a3 = quarter_codes<true>(wb >> 8);
-#pragma unroll
-              for (int i = 0; i < NT; ++i)
-                mma_bf16(part[m][i], a0, a1, a2, a3, xv[i][j].z, xv[i][j].w);
-            }
-            if (j % WPL == WPL - 1) {
-              // this group's scales: rows g and g + 8 are NS scales apart
-              constexpr int K1 = NS;
-              const int k = j / WPL;
-              const uint32_t p0 = word(sc[m], k >> 1), p1 = word(sc[m], (K1 + k) >> 1);
-              const float s0 = __uint_as_float(k & 1 ? p0 & 0xffff0000u : p0 << 16);
-              const float s1 = __uint_as_float((K1 + k) & 1 ? p1 & 0xffff0000u : p1 << 16);
-#pragma unroll
-              for (int i = 0; i < NT; ++i) {
-                acc[m][i][0] = fmaf(part[m][i][0], s0, acc[m][i][0]);
-                acc[m][i][1] = fmaf(part[m][i][1], s0, acc[m][i][1]);
-                acc[m][i][2] = fmaf(part[m][i][2], s1, acc[m][i][2]);
-                acc[m][i][3] = fmaf(part[m][i][3], s1, acc[m][i][3]);
-              }
-            }
-          }
-          if constexpr (AHEAD) load_x(j);
-        }
+        get += STEP;
+        if (get == ring + ST * STEP) get = ring;
+        step_product<GROUP, MT, NT>(
+            wd, sc,
+            [&](int i, int j) {
+              const int c = (j / WPL) * 4 * WPL + t * WPL + j % WPL;
+              return lds128(x + i * 8 * 256 + operand_place<WPL>(g, c) * 16);
+            },
+            acc);
       }
-      // the sums are of quarter codes
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        if constexpr (DOWN) {
-          const int r = CR * i + t;  // columns 2t and 2t+1: h's two parts
-          if (r >= rows) continue;
-          const int f = L.pair[first + r];
-          const float wt = 4.f * __ldg(a.w + f);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            float *y = a.yslot + (size_t)f * a.C + (tile + m) * 16 + g;
-            y[0] = (acc[m][i][0] + acc[m][i][1]) * wt;
-            y[8] = (acc[m][i][2] + acc[m][i][3]) * wt;
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int r = CR * i + 2 * t + c;
-            if (r >= rows) continue;
-            const int f = L.pair[first + r];
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              const float gate = 4.f * acc[m][i][c], up = 4.f * acc[m][i][2 + c];
-              const float h = gate / (1.f + __expf(-gate)) * up;
-              const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-              const size_t at = (size_t)f * a.I + (tile + m) * 8 + g;
-              a.hhi[at] = hi;
-              a.hlo[at] = __float2bfloat16_rn(h - __bfloat162float(hi));
-            }
-          }
-        }
-      }
+      for (int m = 0; m < MT; ++m)
+        store_tile<DOWN, NT>(a, L, acc[m], tile + m, rows, first, lane);
     };
-    if (NTM == 1 || rows <= CR) {
+    if (rows <= CR) {
       pass(std::integral_constant<int, 1>());
-    } else if constexpr (NTM >= 2) {
-      if (NTM == 2 || rows <= 2 * CR)
-        pass(std::integral_constant<int, 2>());
-      else if constexpr (NTM == 4)
+    } else if (NTM == 2 || rows <= 2 * CR) {
+      pass(std::integral_constant<int, 2>());
+    } else if constexpr (NTM == 4) {
+      if (rows <= 3 * CR)
+        pass(std::integral_constant<int, 3>());
+      else
         pass(std::integral_constant<int, 4>());
     }
   }
@@ -497,27 +709,42 @@ __global__ void __launch_bounds__(256) prepare_w4_kernel(const uint32_t *__restr
 
 inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-template <bool DOWN, int GROUP, int MT, int NTM>
-cudaError_t launch_mt(const W4Args &a, cudaStream_t s) {
-  constexpr size_t smem =
-      (size_t)WW * queue_steps<GROUP, MT>() * MT * record_bytes<GROUP>() + sizeof(Lists);
-  auto kernel = w4_kernel<DOWN, GROUP, MT, NTM>;
+// smem: the queue's bytes; the lists follow.  units: of the whole call at most.
+template <auto Kernel>
+cudaError_t launch_w4(const W4Args &a, int queue, int rows, int threads, int ctas,
+                      long long units, cudaStream_t s) {
+  // hist scratch of the lists fits the queue; the lists of the largest call
+  // (4096 pairs) are below 20 KB
+  const int smem = queue + lists_bytes(a.nK, a.E, rows);
   static bool ready[64] = {false};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   bool &r = ready[dev >= 0 && dev < 64 ? dev : 0];
   if (!r) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
     r = true;
   }
-  // no more warps than the call can have units
-  const long long tiles = a.C / 16 / MT;
-  const long long hit = a.nK < a.E ? a.nK : a.E + a.nK / ((DOWN ? 4 : 8) * NTM);
-  const long long full = 2ll * device_sm_count(), most = hit * tiles;
-  const int grid = (int)(most < full ? most : full);
-  return launch_pdl(kernel, dim3(grid), dim3(WT), smem, s, a);
+  const long long fit = 227 * 1024 / (smem + 1024);
+  const long long full = (fit < ctas ? fit : ctas) * device_sm_count();
+  return launch_pdl(Kernel, dim3((unsigned)(units < full ? units : full)), dim3(threads), smem, s,
+                    a);
+}
+
+template <bool DOWN, int GROUP, int MT>
+cudaError_t launch_few(const W4Args &a, cudaStream_t s) {
+  constexpr int rows = DOWN ? 4 : 8;
+  return launch_w4<w4_few_kernel<DOWN, GROUP, MT>>(a, Few<DOWN, GROUP, MT>::QUEUE, rows, WT, 2,
+                   (long long)max_entries(a.nK, a.E, rows) * (a.C / 16 / MT), s);
+}
+
+template <bool DOWN, int GROUP, int NTM>
+cudaError_t launch_many(const W4Args &a, cudaStream_t s) {
+  constexpr int rows = (DOWN ? 4 : 8) * NTM;
+  return launch_w4<w4_many_kernel<DOWN, GROUP, NTM>>(a, Many<DOWN, GROUP, NTM>::QUEUE, rows,
+                   MW * 32, 3,
+                   (long long)max_entries(a.nK, a.E, rows) * (a.C / 16 / (MW * MT_MANY)), s);
 }
 
 template <bool DOWN, int GROUP>
@@ -526,13 +753,13 @@ cudaError_t launch_stage(const W4Args &a, cudaStream_t s) {
   // warps without work
   const long long tiles = a.C / 16;
   const long long hit = a.nK < a.E ? a.nK : a.E;
-  if (hit * tiles <= 4ll * WW * device_sm_count()) return launch_mt<DOWN, GROUP, 1, 1>(a, s);
+  if (hit * tiles <= 4ll * WW * device_sm_count()) return launch_few<DOWN, GROUP, 1>(a, s);
   // column groups for nearly every expert's tokens at once (the mean and four
   // deviations of their number); what exceeds them reads the weights again
   const float mean = (float)a.nK / a.E, want = (mean + 4.f * sqrtf(mean)) / (DOWN ? 4 : 8);
-  if (want <= 1.f) return launch_mt<DOWN, GROUP, 2, 1>(a, s);
-  if (want <= 2.f) return launch_mt<DOWN, GROUP, 2, 2>(a, s);
-  return launch_mt<DOWN, GROUP, 2, 4>(a, s);
+  if (want <= kFewGroups) return launch_few<DOWN, GROUP, 2>(a, s);
+  if (want <= 2.f) return launch_many<DOWN, GROUP, 2>(a, s);
+  return launch_many<DOWN, GROUP, 4>(a, s);
 }
 
 template <int GROUP>
