@@ -31,7 +31,6 @@ namespace moe {
 namespace {
 
 constexpr int WT = 256, WW = WT / 32;  // threads and warps of the kernel for few tokens
-constexpr float kFewGroups = 1.f;      // column groups up to which it is taken
 template <int GROUP>
 constexpr int record_bytes() {  // codes; 128 / GROUP bf16 scales a row
   return 1024 + 16 * (128 / GROUP) * 2;
@@ -270,11 +269,10 @@ __device__ __forceinline__ void step_product(const uint4 (&wd)[MT][2], const uin
   }
 }
 
-// The scales of a record at `rec` for lane row g.
+// The scales of a record for a lane's two rows.
 template <int GROUP>
-__device__ __forceinline__ uint4 load_scales(uint32_t rec, int g) {
+__device__ __forceinline__ uint4 load_scales(uint32_t at) {
   constexpr int NS = 128 / GROUP;
-  const uint32_t at = rec + 1024 + g * (4 * NS);
   uint4 sc = make_uint4(0, 0, 0, 0);
   if constexpr (NS == 4) sc = lds128(at);
   if constexpr (NS == 2) {
@@ -318,10 +316,10 @@ __device__ __forceinline__ void store_tile(const W4Args &a, const Lists &L, cons
   }
 }
 
-// Queue steps: what `ctas` CTAs of an SM can hold of `step` bytes beside 10 KB
+// Queue steps: what `ctas` CTAs of an SM can hold of `step` bytes beside 4 KB
 // of lists each (a call with longer lists gets fewer CTAs).
 constexpr int queue_steps(int ctas, int step) {
-  const int fit = ((227 / ctas - 1) * 1024 - 10 * 1024) / step;
+  const int fit = ((227 / ctas - 1) * 1024 - 4 * 1024) / step;
   return fit > 8 ? 8 : fit;
 }
 
@@ -422,7 +420,7 @@ __global__ void __launch_bounds__(WT, 2) w4_few_kernel(const W4Args a) {
       for (int m = 0; m < MT; ++m) {
         wd[m][0] = lds128(get + m * REC + lane * 16);
         wd[m][1] = lds128(get + m * REC + 512 + lane * 16);
-        sc[m] = load_scales<GROUP>(get + m * REC, g);
+        sc[m] = load_scales<GROUP>(get + m * REC + 1024 + g * (4 * NS));
       }
       get += STEP;
       if (get >= ring + ST * STEP) get -= ST * STEP;
@@ -452,7 +450,8 @@ template <bool DOWN, int GROUP, int NTM>
 struct Many {
   static constexpr int WEIGHTS = MW * MT_MANY * record_bytes<GROUP>();
   static constexpr int STEP = WEIGHTS + NTM * 8 * 256;
-  static constexpr int ST = queue_steps(3, STEP);
+  static constexpr int CTAS = 3;  // of an SM
+  static constexpr int ST = queue_steps(CTAS, STEP);
   static constexpr int QUEUE = ST * STEP;
   static_assert(ST >= 3, "a queue of three steps");
 };
@@ -464,7 +463,7 @@ __device__ __forceinline__ int operand_place(int r, int c) {
 }
 
 template <bool DOWN, int GROUP, int NTM>
-__global__ void __launch_bounds__(MW * 32, 3) w4_many_kernel(const W4Args a) {
+__global__ void __launch_bounds__(MW * 32, Many<DOWN, GROUP, NTM>::CTAS) w4_many_kernel(const W4Args a) {
   using Q = Many<DOWN, GROUP, NTM>;
   constexpr int WPL = GROUP / 32, MT = MT_MANY;
   constexpr int CR = DOWN ? 4 : 8;  // pairs of a column group
@@ -477,27 +476,26 @@ __global__ void __launch_bounds__(MW * 32, 3) w4_many_kernel(const W4Args a) {
   const int tiles = a.C / 16 / (MW * MT);  // units of an entry
   const int NB = a.R / 128;
   const int units = L.entries * tiles;
-  const uint32_t ring = ptx::smem_u32(smem);
+  const uint32_t ring = ptx::smem_u32(smem), ring_end = ring + ST * STEP;
   const size_t tile_bytes = (size_t)NB * REC;
 
   // the copying side: this warp's tiles, and one 16-byte piece of every
   // eighth operand row
-  struct {
-    int u, b;
-    uint32_t put;
-  } pw{(int)blockIdx.x, 0, ring}, px = pw;
-  const uint8_t *src = nullptr;
+  const uint32_t wput = w * MT * REC + lane * 16;
+  const uint32_t xput = Q::WEIGHTS + (tid >> 4) * 256 + operand_place<WPL>(tid >> 4, tid & 15) * 16;
+  int pu = blockIdx.x, pb = NB;  // unit, steps of it to go
+  uint32_t put = ring;
+  const uint8_t *src[MT];
   const uint4 *xsrc[NTM];
-  int xrows = 0;
-  auto locate_weights = [&]() {
-    if (pw.u >= units) return;
-    const int ent = pw.u / tiles, tile = (pw.u - ent * tiles) * (MW * MT) + w * MT;
-    src = a.rec + ((size_t)L.expert(ent) * (a.C / 16) + tile) * tile_bytes + lane * 16;
-  };
-  auto locate_operand = [&]() {
-    if (px.u >= units) return;
-    const int ent = px.u / tiles, rows = L.count(ent), first = L.first(ent);
-    xrows = DOWN ? 2 * rows : rows;
+  int groups = 0;  // column groups in use
+  auto locate = [&]() {
+    if (pu >= units) return;
+    const int ent = pu / tiles, tile = (pu - ent * tiles) * (MW * MT) + w * MT;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+      src[m] = a.rec + ((size_t)L.expert(ent) * (a.C / 16) + tile + m) * tile_bytes + lane * 16;
+    const int rows = L.count(ent), first = L.first(ent);
+    groups = (rows + CR - 1) / CR;
 #pragma unroll
     for (int i = 0; i < NTM; ++i) {
       const int r = i * 8 + (tid >> 4);
@@ -507,53 +505,66 @@ __global__ void __launch_bounds__(MW * 32, 3) w4_many_kernel(const W4Args a) {
       xsrc[i] = reinterpret_cast<const uint4 *>(p) + (tid & 15);
     }
   };
-  const uint32_t xput = Q::WEIGHTS + (tid >> 4) * 256 + operand_place<WPL>(tid >> 4, tid & 15) * 16;
-  auto advance = [&](auto &p, auto locate) {
-    p.put += STEP;
-    if (p.put == ring + ST * STEP) p.put = ring;
-    if (++p.b == NB) {
-      p.b = 0;
-      p.u += gridDim.x;
+  auto copy_weights = [&]() {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const uint32_t to = put + wput;
+      cp_async16(to + m * REC, src[m]);
+      cp_async16(to + m * REC + 512, src[m] + 512);
+      if (lane < 2 * NS) cp_async16(to + m * REC + 1024, src[m] + 1024);
+      src[m] += REC;
+    }
+  };
+  auto copy_operand = [&]() {
+    const uint32_t to = put + xput;
+#pragma unroll
+    for (int i = 0; i < NTM; ++i) {
+      if (i == 0 || i < groups) cp_async16(to + i * 8 * 256, xsrc[i]);
+      xsrc[i] += 16;
+    }
+  };
+  auto advance = [&]() {
+    put += STEP;
+    if (put == ring_end) put = ring;
+    if (--pb == 0) {
+      pb = NB;
+      pu += gridDim.x;
       locate();
     }
   };
-  auto issue_weights = [&]() {
-    if (pw.u >= units) return;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const uint8_t *from = src + m * tile_bytes;
-      const uint32_t to = pw.put + (w * MT + m) * REC + lane * 16;
-      cp_async16(to, from);
-      cp_async16(to + 512, from + 512);
-      if (lane < 2 * NS) cp_async16(to + 1024, from + 1024);
-    }
-    src += REC;
-    advance(pw, locate_weights);
-  };
-  auto issue_operand = [&]() {
-    if (px.u >= units) return;
-#pragma unroll
-    for (int i = 0; i < NTM; ++i) {
-      if (i * 8 < xrows) cp_async16(px.put + xput + i * 8 * 256, xsrc[i]);
-      xsrc[i] += 16;
-    }
-    advance(px, locate_operand);
-  };
-  locate_weights();
-  locate_operand();
-#pragma unroll 1
-  for (int i = 0; i < ST - 1; ++i) issue_weights();
+  locate();
   if constexpr (DOWN) {  // weights are on their way before h is there
+#pragma unroll 1
+    for (int i = 0; i < ST - 1; ++i)
+      if (pu < units) {
+        copy_weights();
+        advance();
+      }
     pdl_wait();
     pdl_launch();
+    pu = blockIdx.x, pb = NB, put = ring;
+    locate();
   }
 #pragma unroll 1
   for (int i = 0; i < ST - 1; ++i) {
-    issue_operand();
+    if (pu < units) {
+      if constexpr (!DOWN) copy_weights();
+      if constexpr (DOWN)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) src[m] += REC;
+      copy_operand();
+      advance();
+    }
     ptx::cp_async_commit();
   }
 
   uint32_t get = ring;
+  const uint32_t sget = w * MT * REC + 1024 + g * (4 * NS);
+  uint32_t xget[4];  // this lane's operand pieces of a step, column group 0
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    xget[j] = Q::WEIGHTS + g * 256 +
+              operand_place<WPL>(g, (j / WPL) * 4 * WPL + t * WPL + j % WPL) * 16;
 #pragma unroll 1
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
     const int ent = u / tiles, tile = (u - ent * tiles) * (MW * MT) + w * MT;
@@ -567,44 +578,44 @@ __global__ void __launch_bounds__(MW * 32, 3) w4_many_kernel(const W4Args a) {
         for (int i = 0; i < NT; ++i)
           acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.f;
 #pragma unroll 1
-      for (int b = 0; b < NB; ++b) {
+      for (int b = NB; b > 0; --b) {
         ptx::cp_async_wait<ST - 2>();
         __syncthreads();  // the step has arrived; the one before it has been used
-        issue_weights();
-        issue_operand();
+        if (pu < units) {
+          copy_weights();
+          copy_operand();
+          advance();
+        }
         ptx::cp_async_commit();
-        const uint32_t rec = get + w * MT * REC;
-        const uint32_t x = get + Q::WEIGHTS + g * 256;
+        const uint32_t rec = get + wput;
         uint4 wd[MT][2], sc[MT];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          wd[m][0] = lds128(rec + m * REC + lane * 16);
-          wd[m][1] = lds128(rec + m * REC + 512 + lane * 16);
-          sc[m] = load_scales<GROUP>(rec + m * REC, g);
+          wd[m][0] = lds128(rec + m * REC);
+          wd[m][1] = lds128(rec + m * REC + 512);
+          sc[m] = load_scales<GROUP>(get + sget + m * REC);
         }
+        const uint32_t x = get;
         get += STEP;
-        if (get == ring + ST * STEP) get = ring;
+        if (get == ring_end) get = ring;
         step_product<GROUP, MT, NT>(
-            wd, sc,
-            [&](int i, int j) {
-              const int c = (j / WPL) * 4 * WPL + t * WPL + j % WPL;
-              return lds128(x + i * 8 * 256 + operand_place<WPL>(g, c) * 16);
-            },
-            acc);
+            wd, sc, [&](int i, int j) { return lds128(x + xget[j] + i * 8 * 256); }, acc);
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m)
         store_tile<DOWN, NT>(a, L, acc[m], tile + m, rows, first, lane);
     };
-    if (rows <= CR) {
+    if (NTM == 1 || rows <= CR) {
       pass(std::integral_constant<int, 1>());
-    } else if (NTM == 2 || rows <= 2 * CR) {
-      pass(std::integral_constant<int, 2>());
-    } else if constexpr (NTM == 4) {
-      if (rows <= 3 * CR)
-        pass(std::integral_constant<int, 3>());
-      else
-        pass(std::integral_constant<int, 4>());
+    } else if constexpr (NTM >= 2) {
+      if (NTM == 2 || rows <= 2 * CR) {
+        pass(std::integral_constant<int, 2>());
+      } else if constexpr (NTM == 4) {
+        if (rows <= 3 * CR)
+          pass(std::integral_constant<int, 3>());
+        else
+          pass(std::integral_constant<int, 4>());
+      }
     }
   }
   ptx::cp_async_wait<0>();
@@ -743,7 +754,7 @@ template <bool DOWN, int GROUP, int NTM>
 cudaError_t launch_many(const W4Args &a, cudaStream_t s) {
   constexpr int rows = (DOWN ? 4 : 8) * NTM;
   return launch_w4<w4_many_kernel<DOWN, GROUP, NTM>>(a, Many<DOWN, GROUP, NTM>::QUEUE, rows,
-                   MW * 32, 3,
+                   MW * 32, Many<DOWN, GROUP, NTM>::CTAS,
                    (long long)max_entries(a.nK, a.E, rows) * (a.C / 16 / (MW * MT_MANY)), s);
 }
 
@@ -757,7 +768,7 @@ cudaError_t launch_stage(const W4Args &a, cudaStream_t s) {
   // column groups for nearly every expert's tokens at once (the mean and four
   // deviations of their number); what exceeds them reads the weights again
   const float mean = (float)a.nK / a.E, want = (mean + 4.f * sqrtf(mean)) / (DOWN ? 4 : 8);
-  if (want <= kFewGroups) return launch_few<DOWN, GROUP, 2>(a, s);
+  if (want <= 1.f) return launch_many<DOWN, GROUP, 1>(a, s);
   if (want <= 2.f) return launch_many<DOWN, GROUP, 2>(a, s);
   return launch_many<DOWN, GROUP, 4>(a, s);
 }

@@ -45,6 +45,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 8.f;
 constexpr int kItemCost = 2;  // a new item's overhead, in units
+constexpr int kGroup = 12;    // parts joined at a time
 constexpr int kSnap = 4;      // a range's end this near an item's edge moves to it (> kItemCost)
 
 struct AttnArgs {
@@ -56,7 +57,8 @@ struct AttnArgs {
   const float *kscale, *vscale;
   void *out;
   float *lse;
-  int32_t *counters;  // one per (sequence, head group)
+  int32_t *counters;        // one per (sequence, head group)
+  int32_t *group_counters;  // one per part
   float2 *part_ml;    // (2 kMaxWorkers, NH): maximum and sum of a part
   float *part_o;      // (2 kMaxWorkers, NH, D)
   int B, Hq, Hkv, G, VG, P, num_pages, max_pages, window;
@@ -644,9 +646,92 @@ constexpr size_t smem_bytes() {
   return (size_t)NW * stages<P, NW>() * P::STAGE_BYTES + merge_bytes<P, NW>();
 }
 
+// Counts this CTA's arrival; true in the CTA that arrives last of n, which then
+// sees what the others stored.  Leaves the counter zero for the next call.
+__device__ __forceinline__ bool arrive(int32_t *counter, int n, int *sh) {
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    *sh = atomicAdd(counter, 1) == n - 1;
+    if (*sh) *counter = 0;
+    __threadfence();
+  }
+  __syncthreads();
+  return *sh;
+}
+
+// Joins np parts in order, by the whole CTA: those of ranges first, first + step,
+// ... of the item that begins in range wf; into the first one's part (out
+// nullptr), or into the rows of nh heads at out.
+template <class P, int NW>
+__device__ __forceinline__ void join_parts(const AttnArgs &a, int first, int step, int wf, int np,
+                                        int nh, float *sm, float *sl, float vs,
+                                        typename P::Out *out, float *lse) {
+  const bool to_part = out == nullptr;
+  auto part_of = [=](int k) {
+    return (size_t)(2 * (first + k * step) + (first + k * step == wf ? 1 : 0));
+  };
+  constexpr int D = P::D, NH = P::NH, AHEAD = 12;
+  const int tid = threadIdx.x, lane = tid & 31;
+  // a warp per head: the maximum and the sum
+  for (int e = tid >> 5; e < nh; e += NW) {
+    float top = -INFINITY, sum = 0.f;
+    for (int k = lane; k < np; k += 32) top = fmaxf(top, __ldcg(a.part_ml + part_of(k) * NH + e).x);
+    top = max_over_g(top);
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    for (int k = lane; k < np; k += 32) {
+      const float2 ml = __ldcg(a.part_ml + part_of(k) * NH + e);
+      sum += ml.y * rescale(ml.x, top);
+    }
+    sum = sum_over_g(sum);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    if (lane == 0) {
+      sm[e] = top;
+      sl[e] = to_part ? sum : vs / sum;
+      if (!to_part && lse) lse[e] = (top + log2f(sum)) * kLn2;
+    }
+  }
+  __syncthreads();
+  // 4 outputs a thread and pass
+  for (int e = tid * 4; e < nh * D; e += NW * 32 * 4) {
+    const int h = e / D;
+    const float top = sm[h];
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < np; k0 += AHEAD) {
+      float mx[AHEAD];
+      float4 y[AHEAD];
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k)
+        if (k0 + k < np) {
+          const size_t p = part_of(k0 + k);
+          mx[k] = __ldcg(a.part_ml + p * NH + h).x;
+          y[k] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + p * NH * D + e));
+        }
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k)
+        if (k0 + k < np) {
+          const float r = rescale(mx[k], top);
+          x.x = fmaf(y[k].x, r, x.x), x.y = fmaf(y[k].y, r, x.y);
+          x.z = fmaf(y[k].z, r, x.z), x.w = fmaf(y[k].w, r, x.w);
+        }
+    }
+    if (to_part) {
+      __stcg(reinterpret_cast<float4 *>(a.part_o + part_of(0) * NH * D + e), x);
+    } else {
+      const float f = sl[h];
+      store_out2(out + e, x.x * f, x.y * f);
+      store_out2(out + e + 2, x.z * f, x.w * f);
+    }
+  }
+  __syncthreads();  // every maximum of part 0 has been read
+  if (to_part && tid < nh) __stcg(a.part_ml + part_of(0) * NH + tid, make_float2(sm[tid], sl[tid]));
+}
+
 template <class P, int NW>
 __global__ void __launch_bounds__(NW * 32, ctas<P>()) paged_attention_kernel(
-    const AttnArgs a) {
+    const __grid_constant__ AttnArgs a) {
   pdl_enter();
   constexpr int NT = NW * 32, ST = stages<P, NW>();
   constexpr int D = P::D, NH = P::NH, RC = round_chunks<P, NW>(), CH = P::CH * RC;
@@ -657,6 +742,9 @@ __global__ void __launch_bounds__(NW * 32, ctas<P>()) paged_attention_kernel(
   float *qs = sf + NW * NH;
   __shared__ long long sh_sum[NW], sh_u[2], sh_S;
   __shared__ int sh_b, sh_h, sh_c, sh_last;
+  __shared__ struct Part {
+    int b, h, wf, wl;  // an item of which this range holds part 0 or 1
+  } sh_part[2];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int HV = a.Hkv * a.VG;
 
@@ -701,7 +789,10 @@ __global__ void __launch_bounds__(NW * 32, ctas<P>()) paged_attention_kernel(
   if ((long long)blockIdx.x >= W) return;
   // this CTA's range, its ends moved to the edges of items that they nearly meet
   const long long excl = (before + inc - mine) * HV;
-  if (tid == 0) sh_u[1] = T;
+  if (tid == 0) {
+    sh_u[1] = T;
+    sh_part[0].b = sh_part[1].b = -1;
+  }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -918,72 +1009,41 @@ __global__ void __launch_bounds__(NW * 32, ctas<P>()) paged_attention_kernel(
           __stcg(reinterpret_cast<float2 *>(a.part_o + part * NH * D + at), make_float2(x, y));
       }
     }
-    if (!whole) {
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        int32_t *cnt = a.counters + (size_t)b_done * HV + h_done;
-        sh_last = atomicAdd(cnt, 1) == wl - wf;
-        if (sh_last) *cnt = 0;  // ready for the next call
-        __threadfence();
-      }
-      __syncthreads();
-      if (sh_last) {  // every part is there: join them in range order
-        auto part_of = [&](int k) { return (size_t)(2 * k + (k == wf ? 1 : 0)); };
-        const int np = wl - wf + 1;
-        // a warp per head: the maximum and the sum
-        for (int e = w; e < nh_done; e += NW) {
-          float top = -INFINITY, sum = 0.f;
-          for (int k = lane; k < np; k += 32)
-            top = fmaxf(top, __ldcg(a.part_ml + part_of(wf + k) * NH + e).x);
-          top = max_over_g(top);
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          for (int k = lane; k < np; k += 32) {
-            const float2 ml = __ldcg(a.part_ml + part_of(wf + k) * NH + e);
-            sum += ml.y * rescale(ml.x, top);
-          }
-          sum = sum_over_g(sum);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          if (lane == 0) {
-            sm[e] = top;
-            sl[e] = vs / sum;
-            if (lse) lse[e] = (top + log2f(sum)) * kLn2;
-          }
-        }
-        __syncthreads();
-        // 4 outputs a thread and pass, 8 parts in flight
-        for (int e = tid * 4; e < nh_done * D; e += NT * 4) {
-          const float top = sm[e / D], f = sl[e / D];
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int k0 = 0; k0 < np; k0 += 8) {
-            float mx[8];
-            float4 y[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (k0 + k < np) {
-                const size_t p = part_of(wf + k0 + k);
-                mx[k] = __ldcg(a.part_ml + p * NH + e / D).x;
-                y[k] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + p * NH * D + e));
-              }
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (k0 + k < np) {
-                const float r = rescale(mx[k], top);
-                x.x = fmaf(y[k].x, r, x.x), x.y = fmaf(y[k].y, r, x.y);
-                x.z = fmaf(y[k].z, r, x.z), x.w = fmaf(y[k].w, r, x.w);
-              }
-          }
-          store_out2(out + e, x.x * f, x.y * f);
-          store_out2(out + e + 2, x.z * f, x.w * f);
-        }
-        __syncthreads();
-      }
+    if (!whole && tid == 0) {
+      Part &p = sh_part[me == wf ? 1 : 0];
+      p.b = b_done, p.h = h_done, p.wf = wf, p.wl = wl;
     }
     if (last_item) break;
   }
   ptx::cp_async_wait<0>();
+
+  // ---- the join of the items that the range shares with others (kept until
+  // the end: it would take registers from the steps).  Parts of more than
+  // kGroup ranges are joined in two levels, so that no CTA reads them all: the
+  // last of kGroup neighbouring ranges to arrive joins theirs into the first
+  // one's part, the last group joins the groups.
+  __threadfence();
+  __syncthreads();
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    const Part p = sh_part[i];
+    if (p.b < 0) continue;
+    const int me = (int)blockIdx.x, np = p.wl - p.wf + 1;
+    const int hk = p.h / a.VG, h0 = hk * a.G + (p.h - hk * a.VG) * NH;
+    const int nh = min(NH, (hk + 1) * a.G - h0);
+    const float vs = a.vscale ? __ldg(a.vscale + hk) : 1.f;
+    Out *out = reinterpret_cast<Out *>(a.out) + ((size_t)p.b * a.Hq + h0) * D;
+    float *lse = a.lse ? a.lse + (size_t)p.b * a.Hq + h0 : nullptr;
+    const int step = np > kGroup ? kGroup : 1, groups = (np + step - 1) / step;
+    bool last = true;
+    if (step > 1) {
+      const int first = p.wf + (me - p.wf) / kGroup * kGroup, n = min(kGroup, p.wl - first + 1);
+      last = arrive(a.group_counters + 2 * first + (first == p.wf ? 1 : 0), n, &sh_last);
+      if (last) join_parts<P, NW>(a, first, 1, p.wf, n, nh, sm, sl, vs, nullptr, nullptr);
+    }
+    if (last && arrive(a.counters + (size_t)p.b * HV + p.h, groups, &sh_last))
+      join_parts<P, NW>(a, p.wf, step, p.wf, groups, nh, sm, sl, vs, out, lse);
+  }
 }
 
 inline int head_groups(const KVCache &c, int nh) {
@@ -1033,7 +1093,8 @@ cudaError_t launch_mma(const AttnArgs &a, int D, cudaStream_t s) {
 size_t paged_attention_ws_bytes(const KVCache &c) {
   const int nh = item_heads(c);
   const size_t items = (size_t)c.num_seqs * c.kv_heads * head_groups(c, nh);
-  return align256(items * sizeof(int32_t)) + align256(2 * kMaxWorkers * nh * sizeof(float2)) +
+  return align256(items * sizeof(int32_t)) + align256(2 * kMaxWorkers * sizeof(int32_t)) +
+         align256(2 * kMaxWorkers * nh * sizeof(float2)) +
          align256((size_t)2 * kMaxWorkers * nh * c.head_dim * sizeof(float));
 }
 
@@ -1059,6 +1120,8 @@ cudaError_t launch_paged_attention(const KVCache &c, const void *q, long long q_
   uint8_t *w = reinterpret_cast<uint8_t *>(ws);
   a.counters = reinterpret_cast<int32_t *>(w);
   w += align256((size_t)a.B * a.Hkv * a.VG * sizeof(int32_t));
+  a.group_counters = reinterpret_cast<int32_t *>(w);
+  w += align256(2 * kMaxWorkers * sizeof(int32_t));
   a.part_ml = reinterpret_cast<float2 *>(w);
   w += align256(2 * kMaxWorkers * nh * sizeof(float2));
   a.part_o = reinterpret_cast<float *>(w);

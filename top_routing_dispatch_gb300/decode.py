@@ -27,11 +27,11 @@ def _want(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _handle(stream, device):
-    """The CUDA stream handle of `stream`, or of the device's current stream
-    (without building a Stream object, which costs 2 us a call)."""
+def _handle(stream, index):
+    """The CUDA stream handle of `stream`, or of device `index`'s current
+    stream (without building a Stream object, which costs 2 us a call)."""
     if stream is None:
-        return _raw_stream(device.index or 0)
+        return _raw_stream(index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -77,7 +77,8 @@ class PagedKVCache:
         self.k_cache, self.v_cache, self.page_table = k_cache, v_cache, page_table
         self.k_scale, self.v_scale, self.rope = k_scale, v_scale, rope
         self.dtype = _F32 if k_cache.dtype == _F32 else _BF16
-        self.device = dev
+        self.device, self._index = dev, dev.index or 0
+        self._scale = 1.0 / math.sqrt(dim)
         self.num_seqs, self.q_heads, self.kv_heads, self.head_dim = (
             page_table.shape[0], int(q_heads), kv_heads, dim)
         rows, rdim = rope.shape if rope is not None else (0, 0)
@@ -100,11 +101,19 @@ class PagedKVCache:
     def _heads(self, t, rows, heads, name):
         """Pointer and token stride of a (rows, heads, head_dim) tensor whose
         heads are contiguous."""
-        _want(t.dtype == self.dtype and t.device == self.device
-              and t.shape == (rows, heads, self.head_dim)
-              and (t.stride(2) == 1 and (heads == 1 or t.stride(1) == self.head_dim)),
-              f"{name}: ({rows}, {heads}, {self.head_dim}) {self.dtype}, a token's heads contiguous")
-        return t.data_ptr(), t.stride(0)
+        st = t.stride()
+        if (t.dtype is not self.dtype or t.shape != (rows, heads, self.head_dim) or st[2] != 1
+                or (st[1] != self.head_dim and heads != 1) or t.device != self.device):
+            raise ValueError(f"{name}: ({rows}, {heads}, {self.head_dim}) {self.dtype} on "
+                             f"{self.device}, a token's heads contiguous")
+        return t.data_ptr(), st[0]
+
+    def _ints(self, t, n, name):
+        """Pointer of a contiguous (n,) int32 tensor."""
+        if (t.dtype is not _I32 or t.shape != (n,) or not t.is_contiguous()
+                or t.device != self.device):
+            raise ValueError(f"{name}: contiguous ({n},) int32 on {self.device}")
+        return t.data_ptr()
 
     def append(self, q, k, v, seq_ids, positions, q_out=None, stream=None):
         """Rotates q and k by position, writes k and v into the cache, returns
@@ -115,21 +124,19 @@ class PagedKVCache:
         n = k.shape[0]
         kp, ks = self._heads(k, n, self.kv_heads, "k")
         vp, vs = self._heads(v, n, self.kv_heads, "v")
-        for name, t in (("seq_ids", seq_ids), ("positions", positions)):
-            _want(t.dtype == _I32 and t.shape == (n,) and t.device == self.device
-                  and t.is_contiguous(), f"{name}: ({n},) int32")
+        sp, pp = self._ints(seq_ids, n, "seq_ids"), self._ints(positions, n, "positions")
         qp, qs, op = None, 0, None
         if q is not None:
             qp, qs = self._heads(q, n, self.q_heads, "q")
             if q_out is None:
                 q_out = torch.empty((n, self.q_heads, self.head_dim), dtype=self.dtype,
                                     device=self.device)
-            op = self._heads(q_out, n, self.q_heads, "q_out")[0]
-            _want(q_out.is_contiguous(), "q_out: contiguous")
+            op, os = self._heads(q_out, n, self.q_heads, "q_out")
+            _want(n < 2 or os == self.q_heads * self.head_dim, "q_out: contiguous")
         else:
             _want(q_out is None, "q_out without q")
-        st = self._append(self._ref, n, qp, qs, kp, ks, vp, vs, seq_ids.data_ptr(),
-                          positions.data_ptr(), op, self._status, _handle(stream, self.device))
+        st = self._append(self._ref, n, qp, qs, kp, ks, vp, vs, sp, pp, op, self._status,
+                          _handle(stream, self._index))
         if st:
             raise MoEError(st, "moe_kv_append")
         return q_out
@@ -142,21 +149,18 @@ class PagedKVCache:
         scale: of the scores, 1/sqrt(head_dim) when None."""
         B = self.num_seqs
         qp, qs = self._heads(q, B, self.q_heads, "q")
-        _want(seq_lens.dtype == _I32 and seq_lens.shape == (B,) and seq_lens.is_contiguous()
-              and seq_lens.device == self.device, f"seq_lens: ({B},) int32")
+        lp = self._ints(seq_lens, B, "seq_lens")
         if out is None:
             out = torch.empty((B, self.q_heads, self.head_dim), dtype=self.dtype,
                               device=self.device)
-        else:
-            _want(out.dtype == self.dtype and out.is_contiguous() and out.device == self.device
-                  and out.shape == (B, self.q_heads, self.head_dim), "out: like q, contiguous")
-        _want(lse is None or (lse.dtype == _F32 and lse.is_contiguous()
-                              and lse.device == self.device and lse.shape == (B, self.q_heads)),
-              f"lse: ({B}, {self.q_heads}) float32")
-        st = self._attend(self._ref, qp, qs, seq_lens.data_ptr(), int(window),
-                          1.0 / math.sqrt(self.head_dim) if scale is None else float(scale),
-                          out.data_ptr(), None if lse is None else lse.data_ptr(), self._ws,
-                          self._nbytes, self._status, _handle(stream, self.device))
+        op, os = self._heads(out, B, self.q_heads, "out")
+        _want(B < 2 or os == self.q_heads * self.head_dim, "out: contiguous")
+        if lse is not None and (lse.dtype is not _F32 or lse.shape != (B, self.q_heads)
+                                or not lse.is_contiguous() or lse.device != self.device):
+            raise ValueError(f"lse: contiguous ({B}, {self.q_heads}) float32 on {self.device}")
+        st = self._attend(self._ref, qp, qs, lp, window, self._scale if scale is None else scale,
+                          op, None if lse is None else lse.data_ptr(), self._ws, self._nbytes,
+                          self._status, _handle(stream, self._index))
         if st:
             raise MoEError(st, "moe_paged_attention")
         return out
@@ -183,7 +187,7 @@ def quantize_weights_w4(w13, w2, group=128, stream=None):
     desc = make_desc(0, H, I, E, 1, _BF16, False)
     _check(_lib.load().moe_quantize_weights_w4(
         ctypes.byref(desc), int(group), _p(w13), _p(w2), *[_p(t) for t in out],
-        _handle(stream, w13.device)), "moe_quantize_weights_w4")
+        _handle(stream, w13.device.index or 0)), "moe_quantize_weights_w4")
     return out
 
 
@@ -213,7 +217,7 @@ class W4Experts:
         dev = w13_q.device
         _want(all(t.device == dev for t in (w13_s, w2_q, w2_s)), "all tensors on one device")
         self.H, self.I, self.E, self.K, self.group = H, I, E, int(K), group
-        self.max_tokens, self.device = int(max_tokens), dev
+        self.max_tokens, self.device, self._index = int(max_tokens), dev, dev.index or 0
         self.desc = make_desc(self.max_tokens, H, I, E, K, _BF16, False)
         self._ref = ctypes.byref(self.desc)
         lib = _lib.load()
@@ -225,7 +229,7 @@ class W4Experts:
         self.w13_t, self.w2_t = (torch.empty(n, dtype=torch.uint8, device=dev) for n in sizes)
         _check(lib.moe_prepare_weights_w4(
             self._ref, group, _p(w13_q), _p(w13_s), _p(w2_q), _p(w2_s), _p(self.w13_t),
-            _p(self.w2_t), _handle(None, dev)), "moe_prepare_weights_w4")
+            _p(self.w2_t), _handle(None, self._index)), "moe_prepare_weights_w4")
         self.ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
         self.status = torch.zeros(1, dtype=_I32, device=dev)
         self._w = self.w13_t.data_ptr(), self.w2_t.data_ptr()
@@ -235,23 +239,23 @@ class W4Experts:
         """y (n, H) bfloat16 (allocated when not given) for x (n, H) bfloat16
         and its routing topk_idx (n, K) int32, topk_w (n, K) float32."""
         n = x.shape[0]
-        _want(n <= self.max_tokens, f"{n} tokens, and {self.max_tokens} at most")
-        _want(x.dtype == _BF16 and x.shape == (n, self.H) and x.is_contiguous()
-              and x.device == self.device, f"x: contiguous ({n}, {self.H}) bfloat16")
-        _want(topk_idx.dtype == _I32 and topk_idx.shape == (n, self.K)
-              and topk_idx.is_contiguous() and topk_idx.device == self.device
-              and topk_w.dtype == _F32 and topk_w.shape == (n, self.K)
-              and topk_w.is_contiguous() and topk_w.device == self.device,
-              f"topk_idx and topk_w: contiguous ({n}, {self.K}) int32 and float32")
+        if (n > self.max_tokens or x.dtype is not _BF16 or x.shape != (n, self.H)
+                or not x.is_contiguous() or x.device != self.device):
+            raise ValueError(f"x: contiguous (up to {self.max_tokens}, {self.H}) bfloat16 on "
+                             f"{self.device}")
+        for t, dt, name in ((topk_idx, _I32, "topk_idx"), (topk_w, _F32, "topk_w")):
+            if (t.dtype is not dt or t.shape != (n, self.K) or not t.is_contiguous()
+                    or t.device != self.device):
+                raise ValueError(f"{name}: contiguous ({n}, {self.K}) {dt} on {self.device}")
         if y is None:
-            y = torch.empty((n, self.H), dtype=_BF16, device=self.device)
-        else:
-            _want(y.dtype == _BF16 and y.shape == x.shape and y.is_contiguous()
-                  and y.device == self.device, "y: like x")
+            y = torch.empty_like(x)
+        elif (y.dtype is not _BF16 or y.shape != x.shape or not y.is_contiguous()
+              or y.device != self.device):
+            raise ValueError("y: like x")
         self.desc.n = n
         st = self._call(self._ref, self.group, x.data_ptr(), topk_idx.data_ptr(),
                         topk_w.data_ptr(), *self._w, y.data_ptr(), *self._tail,
-                        _handle(stream, self.device))
+                        _handle(stream, self._index))
         if st:
             raise MoEError(st, "moe_experts_w4")
         return y
