@@ -44,6 +44,7 @@ struct W4Args {
   const __nv_bfloat16 *x;    // (n, H)
   __nv_bfloat16 *hhi, *hlo;  // (n K, I): h = hhi + hlo
   float *yslot;              // (n K, H), weighted
+  __nv_bfloat16 *y;          // (n, H)
   int nK, K, E, C, R, I;
   int32_t *status;
 };
@@ -283,6 +284,16 @@ __device__ __forceinline__ uint4 load_scales(uint32_t at) {
   return sc;
 }
 
+// h of pair f in column c from the sums (of quarter codes) of gate and up
+__device__ __forceinline__ void store_h(const W4Args &a, int f, int c, float gate, float up) {
+  gate *= 4.f, up *= 4.f;
+  const float h = gate / (1.f + __expf(-gate)) * up;
+  const __nv_bfloat16 hi = __float2bfloat16_rn(h);
+  const size_t at = (size_t)f * a.I + c;
+  a.hhi[at] = hi;
+  a.hlo[at] = __float2bfloat16_rn(h - __bfloat162float(hi));
+}
+
 // Stores the sums (of quarter codes) of tile `tile` for an entry's pairs.
 template <bool DOWN, int NT>
 __device__ __forceinline__ void store_tile(const W4Args &a, const Lists &L, const float (&acc)[NT][4],
@@ -304,13 +315,7 @@ __device__ __forceinline__ void store_tile(const W4Args &a, const Lists &L, cons
       for (int c = 0; c < 2; ++c) {
         const int r = CR * i + 2 * t + c;
         if (r >= rows) continue;
-        const int f = L.pair[first + r];
-        const float gate = 4.f * acc[i][c], up = 4.f * acc[i][2 + c];
-        const float h = gate / (1.f + __expf(-gate)) * up;
-        const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-        const size_t at = (size_t)f * a.I + tile * 8 + g;
-        a.hhi[at] = hi;
-        a.hlo[at] = __float2bfloat16_rn(h - __bfloat162float(hi));
+        store_h(a, L.pair[first + r], tile * 8 + g, acc[i][c], acc[i][2 + c]);
       }
     }
   }
@@ -323,61 +328,89 @@ constexpr int queue_steps(int ctas, int step) {
   return fit > 8 ? 8 : fit;
 }
 
-// Few tokens: up to CR pairs an entry (one column group), every warp by itself.
-// DOWN false: tiles of 8 gate and 8 up rows (8 columns of h), DOWN true: tiles
-// of 16 columns of y; a unit's MT tiles share each operand piece of x or h.
-// GROUP: reduction indices per scale.
-template <bool DOWN, int GROUP, int MT>
+// Few tokens: at most 32 pairs, each an entry of its own (an expert that two of
+// them share is read twice, mostly from L2); every warp works by itself on
+// (tile, pair) units.  DOWN false: the units of all pairs are dealt out over
+// the warps of the grid.  DOWN true: a CTA's warps share out the pairs of a
+// tile and the CTA then adds each token's rows in slot order, so that no
+// separate combine is needed.
+constexpr int kFewPairs = 32;
+template <int GROUP>
 struct Few {
-  static constexpr int STEP = MT * record_bytes<GROUP>();
-  static constexpr int ST = queue_steps(2, WW * STEP);
-  static constexpr int QUEUE = WW * ST * STEP;
+  static constexpr int REC = record_bytes<GROUP>(), ST = 8;
+  static constexpr int QUEUE = WW * ST * REC;
 };
 
-template <bool DOWN, int GROUP, int MT>
+template <bool DOWN, int GROUP>
 __global__ void __launch_bounds__(WT, 2) w4_few_kernel(const W4Args a) {
-  using F = Few<DOWN, GROUP, MT>;
+  using F = Few<GROUP>;
   constexpr int WPL = GROUP / 32;   // a lane's words of a group: WPL t .. of the group's 4 WPL
-  constexpr int CR = DOWN ? 4 : 8;  // pairs of a column group
-  constexpr int REC = record_bytes<GROUP>(), ST = F::ST, STEP = F::STEP, NS = 128 / GROUP;
+  constexpr int REC = F::REC, ST = F::ST, NS = 128 / GROUP;
   extern __shared__ __align__(128) uint8_t smem[];
-  if constexpr (!DOWN) pdl_enter();
-  // the queue's memory is scratch until the lists are ready
-  const Lists L = build_lists<CR>(smem + F::QUEUE, reinterpret_cast<int *>(smem), a);
+  __shared__ uint8_t sh_pair[WW][kFewPairs];    // the valid pairs, each warp's own copy
+  __shared__ uint8_t sh_expert[WW][kFewPairs];
+  __shared__ float sh_y[DOWN ? kFewPairs : 1][16];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int tiles = a.C / 16 / MT;  // units of an entry
-  const int NB = a.R / 128;
-  const int units = L.entries * tiles;
-  const int step = gridDim.x * WW;
-  const int u0 = w * gridDim.x + blockIdx.x;  // the first units go to different CTAs
-  const uint32_t ring = ptx::smem_u32(smem) + w * (ST * STEP);
+  if constexpr (!DOWN) pdl_enter();
+  const int e = lane < a.nK ? __ldg(a.idx + lane) : -1;
+  const bool ok = (unsigned)e < (unsigned)a.E;
+  const unsigned valid = __ballot_sync(0xffffffffu, ok);
+  if (ok) {
+    const int at = __popc(valid & ((1u << lane) - 1u));
+    sh_pair[w][at] = (uint8_t)lane;
+    sh_expert[w][at] = (uint8_t)e;
+  }
+  if (!DOWN && lane < a.nK && !ok && w == 0 && blockIdx.x == 0)
+    flag_status(a.status, MOE_DEV_BAD_ROUTING);
+  __syncwarp();
+  const int pairs = __popc(valid);
+  const int tiles = a.C / 16, NB = a.R / 128;
+  const uint32_t ring = ptx::smem_u32(smem) + w * (ST * REC), ring_end = ring + ST * REC;
   const size_t tile_bytes = (size_t)NB * REC;
 
+  // a warp's units in order: DOWN: pairs w, w + WW, ... of the CTA's tiles;
+  // else: every (warps of the grid)-th unit, a pair's tiles next to each other
+  struct Unit {
+    int tile, pair;  // pair: place in sh_pair
+  };
+  const int step = gridDim.x * WW;
+  auto first_unit = [&]() {
+    if constexpr (DOWN) return Unit{(int)blockIdx.x, w};
+    const int u = w * gridDim.x + blockIdx.x;
+    return Unit{u % tiles, u / tiles};
+  };
+  auto next_unit = [&](Unit &u) {
+    if constexpr (DOWN) {
+      u.pair += WW;
+      if (u.pair >= pairs) u.pair = w, u.tile += gridDim.x;
+    } else {
+      u.tile += step;
+      if (u.tile >= tiles) u.pair += u.tile / tiles, u.tile %= tiles;
+    }
+  };
+  auto more = [&](const Unit &u) { return u.pair < pairs && u.tile < tiles; };
+
   // the copying side
-  int pu = u0, pb = 0;
+  Unit in = first_unit();
+  int pb = NB;
   uint32_t put = ring + lane * 16;
   const uint8_t *src = nullptr;
   auto locate = [&]() {
-    if (pu >= units) return;
-    const int ent = pu / tiles, tile = pu - ent * tiles;
-    src = a.rec + ((size_t)L.expert(ent) * (a.C / 16) + tile * MT) * tile_bytes + lane * 16;
+    if (more(in))
+      src = a.rec + ((size_t)sh_expert[w][in.pair] * tiles + in.tile) * tile_bytes + lane * 16;
   };
   auto issue = [&]() {
-    if (pu < units) {
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const uint8_t *from = src + m * tile_bytes;
-        cp_async16(put + m * REC, from);
-        cp_async16(put + m * REC + 512, from + 512);
-        if (lane < 2 * NS) cp_async16(put + m * REC + 1024, from + 1024);
-      }
+    if (more(in)) {
+      cp_async16(put, src);
+      cp_async16(put + 512, src + 512);
+      if (lane < 2 * NS) cp_async16(put + 1024, src + 1024);
       src += REC;
-      put += STEP;
-      if (put >= ring + ST * STEP) put -= ST * STEP;
-      if (++pb == NB) {
-        pb = 0;
-        pu += step;
+      put += REC;
+      if (put >= ring_end) put -= ST * REC;
+      if (--pb == 0) {
+        pb = NB;
+        next_unit(in);
         locate();
       }
     }
@@ -392,39 +425,27 @@ __global__ void __launch_bounds__(WT, 2) w4_few_kernel(const W4Args a) {
   }
 
   uint32_t get = ring;
-#pragma unroll 1
-  for (int u = u0; u < units; u += step) {
-    const int ent = u / tiles, tile = (u - ent * tiles) * MT;
-    const int rows = L.count(ent), first = L.first(ent);
-    // the operand row of this lane's column: a pair's x, or in even columns
-    // the first, in odd the second part of its h (columns past the last pair
-    // repeat it; their sums are not stored)
-    const int f = L.pair[first + min(DOWN ? g >> 1 : g, rows - 1)];
+  auto product = [&](const Unit &u, float (&acc)[1][1][4]) {
+    // every column is the pair's x, or in turn the first and second part of h
+    const int f = sh_pair[w][u.pair];
     const __nv_bfloat16 *p = DOWN ? (g & 1 ? a.hlo : a.hhi) + (size_t)f * a.R
                                   : a.x + (size_t)(f / a.K) * a.R;
     const uint4 *xr = reinterpret_cast<const uint4 *>(p) + t * WPL;
-    float acc[MT][1][4];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[m][0][0] = acc[m][0][1] = acc[m][0][2] = acc[m][0][3] = 0.f;
+    acc[0][0][0] = acc[0][0][1] = acc[0][0][2] = acc[0][0][3] = 0.f;
     uint4 xv[4];  // the operand pieces of a step, asked for a step ahead
 #pragma unroll
     for (int j = 0; j < 4; ++j) xv[j] = __ldg(xr + (j / WPL) * 4 * WPL + j % WPL);
 #pragma unroll 1
-    for (int b = 0; b < NB; ++b) {
+    for (int b = NB; b > 0; --b) {
       ptx::cp_async_wait<ST - 2>();
       __syncwarp();  // scales are read by lanes that did not copy them
       issue();
-      if (b + 1 < NB) xr += 16;
-      uint4 wd[MT][2], sc[MT];
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        wd[m][0] = lds128(get + m * REC + lane * 16);
-        wd[m][1] = lds128(get + m * REC + 512 + lane * 16);
-        sc[m] = load_scales<GROUP>(get + m * REC + 1024 + g * (4 * NS));
-      }
-      get += STEP;
-      if (get >= ring + ST * STEP) get -= ST * STEP;
-      step_product<GROUP, MT, 1>(
+      if (b > 1) xr += 16;
+      const uint4 wd[1][2] = {{lds128(get + lane * 16), lds128(get + 512 + lane * 16)}};
+      const uint4 sc[1] = {load_scales<GROUP>(get + 1024 + g * (4 * NS))};
+      get += REC;
+      if (get == ring_end) get = ring;
+      step_product<GROUP, 1, 1>(
           wd, sc,
           [&](int, int j) {
             const uint4 v = xv[j];
@@ -433,9 +454,37 @@ __global__ void __launch_bounds__(WT, 2) w4_few_kernel(const W4Args a) {
           },
           acc);
     }
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-      store_tile<DOWN, 1>(a, L, acc[m], tile + m, rows, first, lane);
+  };
+  float acc[1][1][4];
+  if constexpr (DOWN) {
+    const int V = a.nK / a.K;  // tokens
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+      if (lane < 16)
+        for (int f = w; f < a.nK; f += WW)
+          if (!(valid >> f & 1u)) sh_y[f][lane] = 0.f;
+      for (int p = w; p < pairs; p += WW) {
+        product(Unit{tile, p}, acc);
+        if (t == 0) {
+          const int f = sh_pair[w][p];
+          const float wt = 4.f * __ldg(a.w + f);  // the sums are of quarter codes
+          sh_y[f][g] = (acc[0][0][0] + acc[0][0][1]) * wt;
+          sh_y[f][g + 8] = (acc[0][0][2] + acc[0][0][3]) * wt;
+        }
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < V * 16; i += WT) {
+        const int tok = i >> 4, c = i & 15;
+        float y = 0.f;
+        for (int k = 0; k < a.K; ++k) y += sh_y[tok * a.K + k][c];
+        a.y[(size_t)tok * a.C + tile * 16 + c] = __float2bfloat16_rn(y);
+      }
+      __syncthreads();
+    }
+  } else {
+    for (Unit u = first_unit(); more(u); next_unit(u)) {
+      product(u, acc);
+      if (t == 0) store_h(a, sh_pair[w][u.pair], u.tile * 8 + g, acc[0][0][0], acc[0][0][2]);
+    }
   }
   ptx::cp_async_wait<0>();
 }
@@ -724,16 +773,15 @@ inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 template <auto Kernel>
 cudaError_t launch_w4(const W4Args &a, int queue, int rows, int threads, int ctas,
                       long long units, cudaStream_t s) {
-  // hist scratch of the lists fits the queue; the lists of the largest call
-  // (4096 pairs) are below 20 KB
-  const int smem = queue + lists_bytes(a.nK, a.E, rows);
+  const int smem = queue + (rows ? lists_bytes(a.nK, a.E, rows) : 0);
   static bool ready[64] = {false};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   bool &r = ready[dev >= 0 && dev < 64 ? dev : 0];
   if (!r) {
-    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             queue + (rows ? lists_bytes(kW4MaxPairs, kMaxE, rows) : 0));
     if (e != cudaSuccess) return e;
     r = true;
   }
@@ -741,13 +789,6 @@ cudaError_t launch_w4(const W4Args &a, int queue, int rows, int threads, int cta
   const long long full = (fit < ctas ? fit : ctas) * device_sm_count();
   return launch_pdl(Kernel, dim3((unsigned)(units < full ? units : full)), dim3(threads), smem, s,
                     a);
-}
-
-template <bool DOWN, int GROUP, int MT>
-cudaError_t launch_few(const W4Args &a, cudaStream_t s) {
-  constexpr int rows = DOWN ? 4 : 8;
-  return launch_w4<w4_few_kernel<DOWN, GROUP, MT>>(a, Few<DOWN, GROUP, MT>::QUEUE, rows, WT, 2,
-                   (long long)max_entries(a.nK, a.E, rows) * (a.C / 16 / MT), s);
 }
 
 template <bool DOWN, int GROUP, int NTM>
@@ -758,13 +799,19 @@ cudaError_t launch_many(const W4Args &a, cudaStream_t s) {
                    (long long)max_entries(a.nK, a.E, rows) * (a.C / 16 / (MW * MT_MANY)), s);
 }
 
+inline bool few_pairs(const W4Args &a) {
+  return a.nK <= kFewPairs && a.nK * (a.I / 8) <= WW * device_sm_count();
+}
+
 template <bool DOWN, int GROUP>
 cudaError_t launch_stage(const W4Args &a, cudaStream_t s) {
-  // two tiles a unit halve the operand loads; one tile while that leaves
-  // warps without work
-  const long long tiles = a.C / 16;
-  const long long hit = a.nK < a.E ? a.nK : a.E;
-  if (hit * tiles <= 4ll * WW * device_sm_count()) return launch_few<DOWN, GROUP, 1>(a, s);
+  // few pairs, and at most one unit of the first product to two warps of the
+  // grid: beyond that the other kernel's larger steps pay (H = 2048, I = 1024:
+  // 13 us against 19 at one token, 23 against 22 at two)
+  if (few_pairs(a))
+    return launch_w4<w4_few_kernel<DOWN, GROUP>>(
+        a, Few<GROUP>::QUEUE, 0, WT, 2,
+        DOWN ? a.C / 16 : ((long long)a.nK * (a.C / 16) + WW - 1) / WW, s);
   // column groups for nearly every expert's tokens at once (the mean and four
   // deviations of their number); what exceeds them reads the weights again
   const float mean = (float)a.nK / a.E, want = (mean + 4.f * sqrtf(mean)) / (DOWN ? 4 : 8);
@@ -774,8 +821,7 @@ cudaError_t launch_stage(const W4Args &a, cudaStream_t s) {
 }
 
 template <int GROUP>
-cudaError_t run(const Desc &d, W4Args a, const void *w13_t, const void *w2_t, void *y,
-                cudaStream_t s) {
+cudaError_t run(const Desc &d, W4Args a, const void *w13_t, const void *w2_t, cudaStream_t s) {
   a.rec = reinterpret_cast<const uint8_t *>(w13_t);
   a.C = 2 * d.I, a.R = d.H;
   cudaError_t e = launch_stage<false, GROUP>(a, s);
@@ -783,12 +829,12 @@ cudaError_t run(const Desc &d, W4Args a, const void *w13_t, const void *w2_t, vo
   a.rec = reinterpret_cast<const uint8_t *>(w2_t);
   a.C = d.H, a.R = d.I;
   e = launch_stage<true, GROUP>(a, s);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || few_pairs(a)) return e;
   const int V = d.H / 4;
   const long long want = ((long long)d.n * V + 255) / 256, cap = 8ll * device_sm_count();
   return launch_pdl(w4_combine_kernel, dim3((int)(want < cap ? want : cap)), dim3(256), 0, s,
                     reinterpret_cast<const float4 *>(a.yslot), a.idx,
-                    reinterpret_cast<uint2 *>(y), d.n, d.K, d.E, V);
+                    reinterpret_cast<uint2 *>(a.y), d.n, d.K, d.E, V);
 }
 
 template <int GROUP>
@@ -831,6 +877,7 @@ cudaError_t launch_experts_w4(const Desc &d, int group, const void *x, const int
   W4Args a = {};
   a.idx = topk_idx, a.w = topk_w;
   a.x = reinterpret_cast<const __nv_bfloat16 *>(x);
+  a.y = reinterpret_cast<__nv_bfloat16 *>(y);
   uint8_t *p = reinterpret_cast<uint8_t *>(ws);
   const size_t hb = align256((size_t)d.nK() * d.I * 2);
   a.hhi = reinterpret_cast<__nv_bfloat16 *>(p);
@@ -838,9 +885,9 @@ cudaError_t launch_experts_w4(const Desc &d, int group, const void *x, const int
   a.yslot = reinterpret_cast<float *>(p + 2 * hb);
   a.nK = (int)d.nK(), a.K = d.K, a.E = d.E, a.I = d.I;
   a.status = status;
-  if (group == 32) return run<32>(d, a, w13_t, w2_t, y, s);
-  if (group == 64) return run<64>(d, a, w13_t, w2_t, y, s);
-  return run<128>(d, a, w13_t, w2_t, y, s);
+  if (group == 32) return run<32>(d, a, w13_t, w2_t, s);
+  if (group == 64) return run<64>(d, a, w13_t, w2_t, s);
+  return run<128>(d, a, w13_t, w2_t, s);
 }
 
 cudaError_t launch_quantize_w4(int E, int rows, int cols, int group, const void *w, int32_t *q,

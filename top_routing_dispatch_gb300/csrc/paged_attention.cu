@@ -188,6 +188,7 @@ __device__ __forceinline__ float rescale(float a, float b) {
 template <int D_, bool E4M3, int NT>
 struct MmaPath {
   using Out = __nv_bfloat16;
+  static constexpr int RANGE = 8;  // units of a range at least, unless there are more items
   static constexpr int D = D_, KEYS = 16, NH = 8 * NT, EB = E4M3 ? 1 : 2;
   static constexpr int KE = 16 / EB;                    // values of a K piece
   static constexpr int KJ = D / KE / 4;                 // K pieces per lane and row
@@ -453,6 +454,7 @@ struct MmaPath {
 template <int D_>
 struct FmaPath {
   using Out = float;
+  static constexpr int RANGE = 4;
   static constexpr int D = D_, KEYS = 8, NH = 8, EB = 4;
   static constexpr int KJ = D / 16;            // K pieces per lane (row g, pieces t + 4j)
   static constexpr int VR = D >= 128 ? 1 : 2;  // rows of one V load of the warp
@@ -594,6 +596,12 @@ struct FmaPath {
 
 // ---------------------------------------------------------------------------
 
+// a / b for a >= 0, b > 0, in 32 bits where they fit
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((unsigned long long)(a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
+  return a / b;
+}
+
 // What a sequence asks for: tokens [first, len), read from the KEYS-aligned
 // token `base` on, in `units` units.
 struct Seq {
@@ -671,62 +679,56 @@ __device__ __forceinline__ void join_parts(const AttnArgs &a, int first, int ste
   auto part_of = [=](int k) {
     return (size_t)(2 * (first + k * step) + (first + k * step == wf ? 1 : 0));
   };
-  constexpr int D = P::D, NH = P::NH, AHEAD = 12;
-  const int tid = threadIdx.x, lane = tid & 31;
-  // a warp per head: the maximum and the sum
-  for (int e = tid >> 5; e < nh; e += NW) {
-    float top = -INFINITY, sum = 0.f;
-    for (int k = lane; k < np; k += 32) top = fmaxf(top, __ldcg(a.part_ml + part_of(k) * NH + e).x);
-    top = max_over_g(top);
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    for (int k = lane; k < np; k += 32) {
-      const float2 ml = __ldcg(a.part_ml + part_of(k) * NH + e);
-      sum += ml.y * rescale(ml.x, top);
-    }
-    sum = sum_over_g(sum);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    if (lane == 0) {
-      sm[e] = top;
-      sl[e] = to_part ? sum : vs / sum;
-      if (!to_part && lse) lse[e] = (top + log2f(sum)) * kLn2;
-    }
-  }
-  __syncthreads();
-  // 4 outputs a thread and pass
-  for (int e = tid * 4; e < nh * D; e += NW * 32 * 4) {
+  constexpr int D = P::D, NH = P::NH;
+  // four outputs a thread and pass; each thread goes over the parts' maxima and
+  // sums itself, in one round of loads with the outputs
+  for (int e = threadIdx.x * 4; e < nh * D; e += NW * 32 * 4) {
     const int h = e / D;
-    const float top = sm[h];
+    float top = -INFINITY, sum = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < np; k0 += AHEAD) {
-      float mx[AHEAD];
-      float4 y[AHEAD];
+    for (int k0 = 0; k0 < np; k0 += kGroup) {
+      float2 ml[kGroup];
+      float4 y[kGroup];
 #pragma unroll
-      for (int k = 0; k < AHEAD; ++k)
+      for (int k = 0; k < kGroup; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.f);
         if (k0 + k < np) {
           const size_t p = part_of(k0 + k);
-          mx[k] = __ldcg(a.part_ml + p * NH + h).x;
+          ml[k] = __ldcg(a.part_ml + p * NH + h);
           y[k] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + p * NH * D + e));
         }
+      }
+      float t2 = top;
 #pragma unroll
-      for (int k = 0; k < AHEAD; ++k)
+      for (int k = 0; k < kGroup; ++k) t2 = fmaxf(t2, ml[k].x);
+      const float f = rescale(top, t2);
+      sum *= f, x.x *= f, x.y *= f, x.z *= f, x.w *= f;
+      top = t2;
+#pragma unroll
+      for (int k = 0; k < kGroup; ++k)
         if (k0 + k < np) {
-          const float r = rescale(mx[k], top);
+          const float r = rescale(ml[k].x, top);
+          sum = fmaf(ml[k].y, r, sum);
           x.x = fmaf(y[k].x, r, x.x), x.y = fmaf(y[k].y, r, x.y);
           x.z = fmaf(y[k].z, r, x.z), x.w = fmaf(y[k].w, r, x.w);
         }
     }
     if (to_part) {
+      // every thread of the head has to read part 0's maximum before it changes
       __stcg(reinterpret_cast<float4 *>(a.part_o + part_of(0) * NH * D + e), x);
+      if (e % D == 0) sm[h] = top, sl[h] = sum;
     } else {
-      const float f = sl[h];
+      const float f = vs / sum;
       store_out2(out + e, x.x * f, x.y * f);
       store_out2(out + e + 2, x.z * f, x.w * f);
+      if (lse && e % D == 0) lse[h] = (top + log2f(sum)) * kLn2;
     }
   }
-  __syncthreads();  // every maximum of part 0 has been read
-  if (to_part && tid < nh) __stcg(a.part_ml + part_of(0) * NH + tid, make_float2(sm[tid], sl[tid]));
+  if (to_part) {
+    __syncthreads();
+    if (threadIdx.x < nh)
+      __stcg(a.part_ml + part_of(0) * NH + threadIdx.x, make_float2(sm[threadIdx.x], sl[threadIdx.x]));
+  }
 }
 
 template <class P, int NW>
@@ -741,7 +743,7 @@ __global__ void __launch_bounds__(NW * 32, ctas<P>()) paged_attention_kernel(
   float *sm = buf + NW * NH * CH, *sl = sm + NW * NH, *sf = sl + NW * NH;
   float *qs = sf + NW * NH;
   __shared__ long long sh_sum[NW], sh_u[2], sh_S;
-  __shared__ int sh_b, sh_h, sh_c, sh_last;
+  __shared__ int sh_b, sh_h, sh_c, sh_last, sh_live[NW];
   __shared__ struct Part {
     int b, h, wf, wl;  // an item of which this range holds part 0 or 1
   } sh_part[2];
@@ -752,9 +754,11 @@ __global__ void __launch_bounds__(NW * 32, ctas<P>()) paged_attention_kernel(
   const int per = (a.B + NT - 1) / NT;
   const int b0 = tid * per, b1 = min(b0 + per, a.B);
   long long mine = 0;
+  int live = 0;
   for (int b = b0; b < b1; ++b) {
     const int n = seq_info<P, NW>(a, b).units;
     mine += n ? n + kItemCost : 0;
+    live += n != 0;
     const int len = __ldg(a.lens + b);
     if (blockIdx.x == 0 && (len < 0 || (long long)len > (long long)a.max_pages * a.P))
       flag_status(a.status, MOE_DEV_BAD_CACHE);
@@ -765,11 +769,13 @@ __global__ void __launch_bounds__(NW * 32, ctas<P>()) paged_attention_kernel(
     const long long y = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += y;
   }
-  if (lane == 31) sh_sum[w] = inc;
+  live = __reduce_add_sync(0xffffffffu, live);
+  if (lane == 31) sh_sum[w] = inc, sh_live[w] = live;
   __syncthreads();
-  long long before = 0, total = 0;
+  long long before = 0, total = 0, items = 0;
 #pragma unroll
   for (int i = 0; i < NW; ++i) {
+    items += sh_live[i];
     if (i < w) before += sh_sum[i];
     total += sh_sum[i];
   }
@@ -784,8 +790,8 @@ __global__ void __launch_bounds__(NW * 32, ctas<P>()) paged_attention_kernel(
     if (a.lse)
       for (int e = tid; e < a.Hq; e += NT) a.lse[(size_t)b * a.Hq + e] = -INFINITY;
   }
-  const long long want = (T + kSnap - 1) / kSnap;
-  const long long W = want < (long long)gridDim.x ? want : (long long)gridDim.x;
+  const long long want = max((T + P::RANGE - 1) / P::RANGE, items * HV);
+  const long long W = min(want, (long long)gridDim.x);
   if ((long long)blockIdx.x >= W) return;
   // this CTA's range, its ends moved to the edges of items that they nearly meet
   const long long excl = (before + inc - mine) * HV;
@@ -796,13 +802,13 @@ __global__ void __launch_bounds__(NW * 32, ctas<P>()) paged_attention_kernel(
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const long long x = ((long long)blockIdx.x + i) * T / W;
+    const long long x = quotient((blockIdx.x + i) * T, W);
     if (x < excl || x >= excl + mine * HV) continue;
     long long at = excl;
     for (int b = b0; b < b1; ++b) {
       const int units = seq_info<P, NW>(a, b).units, n = units ? units + kItemCost : 0;
       if (x < at + (long long)n * HV) {
-        int h = (int)((x - at) / n);
+        const int h = (int)quotient(x - at, n);
         long long S = at + (long long)h * n;
         long long to = x - S < kSnap ? S : S + n - x < kSnap ? S + n : x;
         sh_u[i] = to;
@@ -949,8 +955,8 @@ __global__ void __launch_bounds__(NW * 32, ctas<P>()) paged_attention_kernel(
     // beginning, floor(k T / W), is not moved to S or lies before it; those
     // that begin in [S + kSnap, E - kSnap] begin inside.
     const long long E = S + sq.units + kItemCost;
-    const int k_lo = (int)((min(S + kSnap, E) * W + T - 1) / T);
-    const int k_hi = (int)(((E - kSnap + 1) * W + T - 1) / T) - 1;
+    const int k_lo = (int)quotient(min(S + kSnap, E) * W + T - 1, T);
+    const int k_hi = (int)quotient((E - kSnap + 1) * W + T - 1, T) - 1;
     const int wf = k_lo - 1, wl = k_hi < k_lo ? wf : k_hi;
     const bool whole = wf == wl;
     const int me = (int)blockIdx.x;
