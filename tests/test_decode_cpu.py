@@ -1,0 +1,251 @@
+"""Refusals of the serving calls: every bad argument is answered before any
+CUDA call, through the C ABI (fake pointers, never dereferenced) and through
+the Python classes (CPU tensors).  No GPU needed."""
+import ctypes
+import math
+import os
+import shutil
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.skipif(
+    not (shutil.which("nvcc") or os.path.exists("/usr/local/cuda/bin/nvcc")),
+    reason="CUDA toolkit not installed")
+
+INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 3
+P = 1 << 20          # a fake, well aligned pointer
+BF16, F32, E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from top_routing_dispatch_gb300 import build as B
+    B.build()
+    from top_routing_dispatch_gb300 import _lib
+    return _lib.load()
+
+
+def cache(**kw):
+    from top_routing_dispatch_gb300._lib import KVCacheDesc
+    d = dict(num_seqs=4, q_heads=8, kv_heads=2, head_dim=128, page_size=16, num_pages=10,
+             max_pages=5, dtype=1, cache_dtype=1, rope_rows=0, rope_dim=0, rope_interleaved=0,
+             page_stride=2 * 16 * 128, k_cache=P, v_cache=P, page_table=P, k_scale=None,
+             v_scale=None, rope=None)
+    d.update(kw)
+    return KVCacheDesc(**d)
+
+
+BAD_CACHES = [
+    (dict(num_seqs=-1), INVALID), (dict(q_heads=0), INVALID), (dict(kv_heads=0), INVALID),
+    (dict(q_heads=7), INVALID), (dict(head_dim=0), INVALID), (dict(page_size=0), INVALID),
+    (dict(max_pages=0), INVALID), (dict(num_pages=-1), INVALID), (dict(dtype=2), INVALID),
+    (dict(dtype=5), INVALID), (dict(cache_dtype=0), INVALID),
+    (dict(dtype=0, cache_dtype=2), INVALID), (dict(k_scale=P), INVALID),
+    (dict(rope_dim=128), INVALID), (dict(rope=P, rope_rows=8), INVALID),
+    (dict(rope=P, rope_rows=8, rope_dim=144), INVALID), (dict(rope_rows=-1), INVALID),
+    (dict(page_stride=2 * 16 * 128 - 16), INVALID),
+    (dict(head_dim=96, page_stride=1 << 20), UNSUPPORTED), (dict(page_size=8), UNSUPPORTED),
+    (dict(page_size=24, page_stride=1 << 20), UNSUPPORTED),
+    (dict(rope=P, rope_rows=8, rope_dim=24), UNSUPPORTED),
+    (dict(page_stride=2 * 16 * 128 + 8), UNSUPPORTED), (dict(num_seqs=65537), UNSUPPORTED),
+]
+BAD_MEMORY = [dict(k_cache=None), dict(v_cache=None), dict(page_table=None), dict(k_cache=P + 8),
+              dict(v_cache=P + 4), dict(page_table=P + 2),
+              dict(rope=P + 4, rope_rows=8, rope_dim=64)]
+
+
+def append(lib, c=None, n=3, q=P, qs=1024, k=P, ks=256, v=P, vs=256, seq=P, pos=P, out=P):
+    c = cache() if c is None else c
+    return lib.moe_kv_append(ctypes.byref(c), n, q, qs, k, ks, v, vs, seq, pos, out, None, None)
+
+
+def attend(lib, c=None, q=P, qs=1024, lens=P, window=0, scale=1.0, out=P, lse=None, ws=P,
+           nbytes=1 << 40):
+    c = cache() if c is None else c
+    return lib.moe_paged_attention(ctypes.byref(c), q, qs, lens, window, scale, out, lse, ws,
+                                   nbytes, None, None)
+
+
+@pytest.mark.parametrize("bad,code", BAD_CACHES, ids=lambda v: str(v)[:40])
+def test_bad_cache_descriptions(lib, bad, code):
+    c = cache(**bad)
+    assert append(lib, c) == code and attend(lib, c) == code
+    assert append(lib, c, n=0) == code
+    assert lib.moe_paged_attention_workspace_size(ctypes.byref(c)) == 0
+
+
+@pytest.mark.parametrize("bad", BAD_MEMORY, ids=str)
+def test_bad_cache_memory(lib, bad):
+    assert append(lib, cache(**bad)) == INVALID
+    assert attend(lib, cache(**bad)) == INVALID
+
+
+def test_null_descriptions(lib):
+    null = ctypes.POINTER(type(cache()))()
+    assert lib.moe_kv_append(null, 1, P, 0, P, 0, P, 0, P, P, P, None, None) == INVALID
+    assert lib.moe_paged_attention(null, P, 0, P, 0, 1.0, P, None, P, 1, None, None) == INVALID
+    assert lib.moe_paged_attention_workspace_size(null) == 0
+    assert lib.moe_experts_w4_workspace_size(None) == 0
+    assert lib.moe_w4_tiled_bytes(None, 64, 0) == 0
+
+
+def test_append_refusals(lib):
+    assert append(lib, n=-1) == INVALID
+    assert append(lib, n=0, q=None, k=None, v=None, seq=None, pos=None, out=None) == 0
+    for kw in (dict(k=None), dict(v=None), dict(seq=None), dict(pos=None), dict(q=None),
+               dict(out=None), dict(q=P + 8), dict(k=P + 2), dict(v=P + 8), dict(out=P + 8),
+               dict(seq=P + 1), dict(pos=P + 2), dict(qs=1016), dict(qs=1028), dict(ks=128),
+               dict(vs=260), dict(q=P, out=P, qs=2048)):
+        assert append(lib, **kw) == INVALID, kw
+
+
+def test_attend_refusals(lib):
+    need = lib.moe_paged_attention_workspace_size(ctypes.byref(cache()))
+    assert need > 0 and need % 256 == 0
+    assert attend(lib, nbytes=need - 1) == WORKSPACE
+    assert attend(lib, cache(num_seqs=0), q=None, lens=None, out=None, ws=None) == 0
+    for kw in (dict(q=None), dict(lens=None), dict(out=None), dict(ws=None), dict(q=P + 8),
+               dict(out=P + 4), dict(lse=P + 2), dict(lens=P + 2), dict(ws=P + 128),
+               dict(window=-1), dict(scale=0.0), dict(scale=-1.0), dict(scale=math.nan),
+               dict(scale=math.inf), dict(qs=1000), dict(qs=1025)):
+        assert attend(lib, **kw) == INVALID, kw
+
+
+def desc(**kw):
+    import top_routing_dispatch_gb300 as M
+    d = dict(n=4, H=256, I=128, E=8, K=2, dtype="bf16", norm_topk_prob=False)
+    d.update(kw)
+    return M.make_desc(**d)
+
+
+def experts(lib, d=None, group=64, ptrs=(P,) * 6, ws=P, nbytes=1 << 40):
+    d = desc() if d is None else d
+    return lib.moe_experts_w4(ctypes.byref(d), group, *ptrs, ws, nbytes, None, None)
+
+
+def test_experts_refusals(lib):
+    d = desc()
+    need = lib.moe_experts_w4_workspace_size(ctypes.byref(d))
+    assert need > 0 and need % 256 == 0
+    assert experts(lib, nbytes=need - 1) == WORKSPACE
+    for g in (0, 16, 48, 256, -64):
+        assert experts(lib, group=g) == UNSUPPORTED
+        assert lib.moe_w4_tiled_bytes(ctypes.byref(d), g, 0) == 0
+        assert lib.moe_prepare_weights_w4(ctypes.byref(d), g, *[P] * 6, None) == UNSUPPORTED
+        assert lib.moe_quantize_weights_w4(ctypes.byref(d), g, *[P] * 6, None) == UNSUPPORTED
+    for kw in (dict(dtype="f32"), dict(H=192), dict(I=192), dict(n=2049), dict(E=300)):
+        assert experts(lib, desc(**kw)) == UNSUPPORTED, kw
+    for kw in (dict(n=-1), dict(K=9), dict(E=0)):
+        assert experts(lib, desc(**kw)) == INVALID, kw
+    for i in range(6):
+        for bad in (None, P + 2):
+            assert experts(lib, ptrs=[bad if j == i else P for j in range(6)]) == INVALID
+            if bad is None or i < 6:
+                args = [None if j == i else P for j in range(6)]
+                assert lib.moe_prepare_weights_w4(ctypes.byref(d), 64, *args, None) == INVALID
+                assert lib.moe_quantize_weights_w4(ctypes.byref(d), 64, *args, None) == INVALID
+    assert experts(lib, ws=None) == INVALID and experts(lib, ws=P + 16) == INVALID
+    assert experts(lib, desc(n=0), ptrs=(None,) * 6, ws=None) == 0
+    # 16 rows x 128 codes and their scales
+    assert lib.moe_w4_tiled_bytes(ctypes.byref(d), 64, 0) == 8 * 16 * 2 * (1024 + 64)
+    assert lib.moe_w4_tiled_bytes(ctypes.byref(d), 32, 1) == 8 * 16 * 1 * (1024 + 128)
+    assert lib.moe_w4_tiled_bytes(ctypes.byref(d), 64, 2) == 0
+
+
+def test_status_string(lib):
+    assert lib.moe_status_string(8) != b"unknown status"
+    assert lib.moe_status_string(9) == b"unknown status"
+
+
+# ------------------------------------------------------------ Python classes
+def kv(pages=6, heads=2, page=16, dim=64, dt=BF16):
+    return torch.zeros((pages, heads, page, dim)).to(dt)
+
+
+def make(**kw):
+    import top_routing_dispatch_gb300 as M
+    a = dict(k_cache=kv(), v_cache=kv(), page_table=torch.zeros((3, 2), dtype=torch.int32), q_heads=4)
+    a.update(kw)
+    return M.PagedKVCache(**a)
+
+
+def test_cache_constructor_refusals(lib):
+    import top_routing_dispatch_gb300 as M
+    make()
+    for kw in (dict(v_cache=kv(pages=7)), dict(v_cache=kv(dt=F32)), dict(k_cache=kv()[0]),
+               dict(k_cache=kv(dt=torch.float16), v_cache=kv(dt=torch.float16)),
+               dict(k_cache=kv(heads=4)[:, ::2], v_cache=kv(heads=4)[:, ::2]),
+               dict(k_cache=kv(heads=3)[:, :2]),  # further apart than v_cache's
+               dict(page_table=torch.zeros((3, 2))), dict(page_table=torch.zeros(3, dtype=torch.int32)),
+               dict(page_table=torch.zeros((3, 4), dtype=torch.int32)[:, ::2]),
+               dict(k_scale=torch.ones(3)), dict(rope=torch.zeros((8, 64), dtype=torch.float64)),
+               dict(rope=torch.zeros((8, 128))[:, ::2])):
+        with pytest.raises(ValueError):
+            make(**kw)
+    for kw in (dict(q_heads=3), dict(k_cache=kv(dim=96), v_cache=kv(dim=96)),
+               dict(k_cache=kv(page=8), v_cache=kv(page=8)), dict(k_scale=torch.ones(2)),
+               dict(rope=torch.zeros((8, 24)))):
+        with pytest.raises(M.MoEError):
+            make(**kw)
+
+
+def test_cache_call_refusals(lib):
+    c = make()
+    n = 3
+    good = dict(q=torch.zeros((n, 4, 64), dtype=BF16), k=torch.zeros((n, 2, 64), dtype=BF16),
+                v=torch.zeros((n, 2, 64), dtype=BF16), seq_ids=torch.zeros(n, dtype=torch.int32),
+                positions=torch.zeros(n, dtype=torch.int32))
+    wide = torch.zeros((n, 2, 128), dtype=BF16)
+    for kw in (dict(q=good["k"]), dict(k=good["q"]), dict(v=good["v"][:2]), dict(q=good["q"].float()),
+               dict(k=wide[:, :, ::2]), dict(v=torch.zeros((n, 4, 64), dtype=BF16)[:, ::2]),
+               dict(seq_ids=torch.zeros(n)), dict(positions=torch.zeros(n + 1, dtype=torch.int32)),
+               dict(positions=torch.zeros(2 * n, dtype=torch.int32)[::2]),
+               dict(q_out=good["q"].float()), dict(q=None, q_out=good["q"]),
+               dict(q_out=torch.zeros((n, 5, 64), dtype=BF16)[:, :4])):
+        with pytest.raises(ValueError):
+            c.append(**{**good, **kw})
+    q, lens = good["q"], torch.ones(3, dtype=torch.int32)
+    for kw in (dict(q=q[:2]), dict(q=q.float()), dict(seq_lens=lens.long()), dict(seq_lens=lens[:2]),
+               dict(out=q.float()), dict(out=torch.zeros((n, 5, 64), dtype=BF16)[:, :4]),
+               dict(lse=torch.zeros((3, 2))), dict(lse=torch.zeros((3, 4), dtype=BF16))):
+        with pytest.raises(ValueError):
+            c.attend(**{**dict(q=q, seq_lens=lens), **kw})
+
+
+def w4(E=2, H=128, I=128, g=64):
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    b = lambda *s: torch.zeros(s, dtype=BF16)  # noqa: E731
+    return [i(E, 2 * I, H // 8), b(E, 2 * I, H // g), i(E, H, I // 8), b(E, H, I // g)]
+
+
+def test_experts_constructor_refusals(lib):
+    import top_routing_dispatch_gb300 as M
+    for change in ({0: w4()[0].float()}, {1: w4()[1].float()}, {2: w4(I=256)[2]}, {3: w4(g=32)[3]},
+                   {0: w4()[0][0]}, {1: w4()[1][:, :, :0]}, {0: w4(H=256)[0][:, :, ::2]}):
+        t = w4()
+        for k, v in change.items():
+            t[k] = v
+        with pytest.raises(ValueError):
+            M.W4Experts(*t, K=1, max_tokens=4)
+    for t, kw in ((w4(g=16), {}), (w4(), dict(K=3)), (w4(H=64), {}), (w4(), dict(max_tokens=5000))):
+        with pytest.raises(M.MoEError):
+            M.W4Experts(*t, **{**dict(K=1, max_tokens=4), **kw})
+    with pytest.raises(ValueError):
+        M.quantize_weights_w4(torch.zeros((2, 128, 256)), torch.zeros((2, 128, 128)))
+    with pytest.raises(ValueError):
+        M.quantize_weights_w4(torch.zeros((2, 128, 256), dtype=BF16), torch.zeros((2, 64, 128), dtype=BF16))
+    with pytest.raises(M.MoEError):
+        M.quantize_weights_w4(torch.zeros((2, 128, 256), dtype=BF16),
+                              torch.zeros((2, 128, 128), dtype=BF16), group=48)
+
+
+def test_rope_table():
+    import top_routing_dispatch_gb300 as M
+    t = M.rope_table(50, 16, base=100.0, device="cpu")
+    assert t.shape == (50, 16) and t.dtype is F32
+    for p in (0, 1, 49):
+        for i in range(8):
+            a = p * 100.0 ** (-2 * i / 16)
+            assert abs(float(t[p, i]) - math.cos(a)) < 1e-6
+            assert abs(float(t[p, 8 + i]) - math.sin(a)) < 1e-6

@@ -181,13 +181,15 @@ def quantize_weights_w4(w13, w2, group=128, stream=None):
     E, H, I2 = w13.shape
     I = I2 // 2
     _want(w2.shape == (E, I, H) and I2 == 2 * I, "w13 (E, H, 2I) and w2 (E, I, H)")
+    _want(group > 0, "group: 32, 64 or 128")
     new = lambda shape, dt: torch.empty(shape, dtype=dt, device=w13.device)  # noqa: E731
-    out = (new((E, 2 * I, H // 8), _I32), new((E, 2 * I, max(H // group, 0)), _BF16),
-           new((E, H, I // 8), _I32), new((E, H, max(I // group, 0)), _BF16))
-    desc = make_desc(0, H, I, E, 1, _BF16, False)
-    _check(_lib.load().moe_quantize_weights_w4(
+    out = (new((E, 2 * I, H // 8), _I32), new((E, 2 * I, H // group), _BF16),
+           new((E, H, I // 8), _I32), new((E, H, I // group), _BF16))
+    lib, desc = _lib.load(), make_desc(0, H, I, E, 1, _BF16, False)
+    refused = lib.moe_w4_tiled_bytes(ctypes.byref(desc), int(group), 0) == 0
+    _check(lib.moe_quantize_weights_w4(
         ctypes.byref(desc), int(group), _p(w13), _p(w2), *[_p(t) for t in out],
-        _handle(stream, w13.device.index or 0)), "moe_quantize_weights_w4")
+        None if refused else _handle(stream, w13.device.index or 0)), "moe_quantize_weights_w4")
     return out
 
 
