@@ -508,7 +508,7 @@ typedef struct {
  *   q_out (n, q_heads, head_dim) contiguous; may be q itself when q is
  *   contiguous.  q and q_out may both be NULL (keys and values only).
  *   seq_ids (n), positions (n) int32.  A negative seq_ids[t] marks a padding
- *   token: nothing of it is read or written.
+ *   token: nothing is written for it.
  * Two tokens of one call must not share a sequence and position.  A token
  * whose sequence, position (also against rope_rows) or page is out of range
  * is skipped and sets MOE_DEV_BAD_CACHE.  status_word may be NULL.

@@ -46,6 +46,7 @@ struct W4Args {
   float *yslot;              // (n K, H), weighted
   __nv_bfloat16 *y;          // (n, H)
   int nK, K, E, C, R, I;
+  unsigned k_inv;            // f / K = f * k_inv >> 16 (f < 4096, K <= 16: checked for all)
   int32_t *status;
 };
 
@@ -284,12 +285,17 @@ __device__ __forceinline__ uint4 load_scales(uint32_t at) {
   return sc;
 }
 
+__device__ __forceinline__ size_t wide(unsigned a, unsigned b) {
+  return (unsigned long long)a * b;
+}
+
 // h of pair f in column c from the sums (of quarter codes) of gate and up
 __device__ __forceinline__ void store_h(const W4Args &a, int f, int c, float gate, float up) {
   gate *= 4.f, up *= 4.f;
-  const float h = gate / (1.f + __expf(-gate)) * up;
+  // the hardware's exp and reciprocal (errors 2^-21): h keeps 16 bits
+  const float h = __fdividef(gate, 1.f + __expf(-gate)) * up;
   const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-  const size_t at = (size_t)f * a.I + c;
+  const size_t at = wide((unsigned)f, (unsigned)a.I) + c;
   a.hhi[at] = hi;
   a.hlo[at] = __float2bfloat16_rn(h - __bfloat162float(hi));
 }
@@ -307,7 +313,7 @@ __device__ __forceinline__ void store_tile(const W4Args &a, const Lists &L, cons
       if (r >= rows) continue;
       const int f = L.pair[first + r];
       const float wt = 4.f * __ldg(a.w + f);
-      float *y = a.yslot + (size_t)f * a.C + tile * 16 + g;
+      float *y = a.yslot + wide((unsigned)f, (unsigned)a.C) + tile * 16 + g;
       y[0] = (acc[i][0] + acc[i][1]) * wt;
       y[8] = (acc[i][2] + acc[i][3]) * wt;
     } else {
@@ -524,7 +530,16 @@ __global__ void __launch_bounds__(MW * 32, Many<DOWN, GROUP, NTM>::CTAS) w4_many
   const int g = lane >> 2, t = lane & 3;
   const int tiles = a.C / 16 / (MW * MT);  // units of an entry
   const int NB = a.R / 128;
-  const int units = L.entries * tiles;
+  // unit = (entry, tile group); a CTA's units are gridDim.x apart
+  struct Unit {
+    int ent, grp;
+  };
+  const Unit stride{(int)gridDim.x / tiles, (int)gridDim.x % tiles};
+  auto next_unit = [&](Unit &u) {
+    u.ent += stride.ent, u.grp += stride.grp;
+    if (u.grp >= tiles) u.grp -= tiles, ++u.ent;
+  };
+  const Unit first_unit{(int)blockIdx.x / tiles, (int)blockIdx.x % tiles};
   const uint32_t ring = ptx::smem_u32(smem), ring_end = ring + ST * STEP;
   const size_t tile_bytes = (size_t)NB * REC;
 
@@ -532,25 +547,26 @@ __global__ void __launch_bounds__(MW * 32, Many<DOWN, GROUP, NTM>::CTAS) w4_many
   // eighth operand row
   const uint32_t wput = w * MT * REC + lane * 16;
   const uint32_t xput = Q::WEIGHTS + (tid >> 4) * 256 + operand_place<WPL>(tid >> 4, tid & 15) * 16;
-  int pu = blockIdx.x, pb = NB;  // unit, steps of it to go
+  Unit pu = first_unit;
+  int pb = NB;  // steps of it to go
   uint32_t put = ring;
   const uint8_t *src[MT];
   const uint4 *xsrc[NTM];
   int groups = 0;  // column groups in use
   auto locate = [&]() {
-    if (pu >= units) return;
-    const int ent = pu / tiles, tile = (pu - ent * tiles) * (MW * MT) + w * MT;
+    if (pu.ent >= L.entries) return;
+    const int tile = pu.grp * (MW * MT) + w * MT;
+    src[0] = a.rec + (size_t)(L.expert(pu.ent) * (a.C / 16) + tile) * tile_bytes + lane * 16;
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-      src[m] = a.rec + ((size_t)L.expert(ent) * (a.C / 16) + tile + m) * tile_bytes + lane * 16;
-    const int rows = L.count(ent), first = L.first(ent);
+    for (int m = 1; m < MT; ++m) src[m] = src[m - 1] + tile_bytes;
+    const int rows = L.count(pu.ent), first = L.first(pu.ent);
     groups = (rows + CR - 1) / CR;
 #pragma unroll
     for (int i = 0; i < NTM; ++i) {
       const int r = i * 8 + (tid >> 4);
-      const int f = L.pair[first + min(DOWN ? r >> 1 : r, rows - 1)];
-      const __nv_bfloat16 *p = DOWN ? (r & 1 ? a.hlo : a.hhi) + (size_t)f * a.R
-                                    : a.x + (size_t)(f / a.K) * a.R;
+      const unsigned f = L.pair[first + min(DOWN ? r >> 1 : r, rows - 1)];
+      const __nv_bfloat16 *p = DOWN ? (r & 1 ? a.hlo : a.hhi) + wide(f, (unsigned)a.R)
+                                    : a.x + wide(f * a.k_inv >> 16, (unsigned)a.R);
       xsrc[i] = reinterpret_cast<const uint4 *>(p) + (tid & 15);
     }
   };
@@ -577,7 +593,7 @@ __global__ void __launch_bounds__(MW * 32, Many<DOWN, GROUP, NTM>::CTAS) w4_many
     if (put == ring_end) put = ring;
     if (--pb == 0) {
       pb = NB;
-      pu += gridDim.x;
+      next_unit(pu);
       locate();
     }
   };
@@ -585,18 +601,18 @@ __global__ void __launch_bounds__(MW * 32, Many<DOWN, GROUP, NTM>::CTAS) w4_many
   if constexpr (DOWN) {  // weights are on their way before h is there
 #pragma unroll 1
     for (int i = 0; i < ST - 1; ++i)
-      if (pu < units) {
+      if (pu.ent < L.entries) {
         copy_weights();
         advance();
       }
     pdl_wait();
     pdl_launch();
-    pu = blockIdx.x, pb = NB, put = ring;
+    pu = first_unit, pb = NB, put = ring;
     locate();
   }
 #pragma unroll 1
   for (int i = 0; i < ST - 1; ++i) {
-    if (pu < units) {
+    if (pu.ent < L.entries) {
       if constexpr (!DOWN) copy_weights();
       if constexpr (DOWN)
 #pragma unroll
@@ -615,9 +631,9 @@ __global__ void __launch_bounds__(MW * 32, Many<DOWN, GROUP, NTM>::CTAS) w4_many
     xget[j] = Q::WEIGHTS + g * 256 +
               operand_place<WPL>(g, (j / WPL) * 4 * WPL + t * WPL + j % WPL) * 16;
 #pragma unroll 1
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    const int ent = u / tiles, tile = (u - ent * tiles) * (MW * MT) + w * MT;
-    const int rows = L.count(ent), first = L.first(ent);
+  for (Unit u = first_unit; u.ent < L.entries; next_unit(u)) {
+    const int tile = u.grp * (MW * MT) + w * MT;
+    const int rows = L.count(u.ent), first = L.first(u.ent);
     auto pass = [&](auto nt_c) {
       constexpr int NT = decltype(nt_c)::value;
       float acc[MT][NT][4];
@@ -630,7 +646,7 @@ __global__ void __launch_bounds__(MW * 32, Many<DOWN, GROUP, NTM>::CTAS) w4_many
       for (int b = NB; b > 0; --b) {
         ptx::cp_async_wait<ST - 2>();
         __syncthreads();  // the step has arrived; the one before it has been used
-        if (pu < units) {
+        if (pu.ent < L.entries) {
           copy_weights();
           copy_operand();
           advance();
@@ -884,6 +900,7 @@ cudaError_t launch_experts_w4(const Desc &d, int group, const void *x, const int
   a.hlo = reinterpret_cast<__nv_bfloat16 *>(p + hb);
   a.yslot = reinterpret_cast<float *>(p + 2 * hb);
   a.nK = (int)d.nK(), a.K = d.K, a.E = d.E, a.I = d.I;
+  a.k_inv = (65536u + d.K - 1) / d.K;
   a.status = status;
   if (group == 32) return run<32>(d, a, w13_t, w2_t, s);
   if (group == 64) return run<64>(d, a, w13_t, w2_t, s);

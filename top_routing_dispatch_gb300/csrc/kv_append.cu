@@ -134,8 +134,8 @@ __global__ void __launch_bounds__(AT) kv_append_kernel(const AppendArgs a) {
     }
   };
   // the rows do not depend on where the token goes: they are on their way
-  // while its page is looked up
-  if (seq >= 0) fetch(r0 + rl);
+  // while its sequence, position and page are looked up
+  fetch(r0 + rl);
   if (seq < 0) return;  // padding
   const int col = pos / a.P;
   bool ok = seq < a.num_seqs && pos >= 0 && col < a.max_pages && (a.R == 0 || pos < a.rope_rows);
