@@ -385,6 +385,15 @@ EXPERTS = [
     (33, 128, 256, 3, 1, 32),
     (64, 256, 128, 2, 1, 128),
 ]
+# reductions long enough for two warps a unit, few and many pairs, odd records
+EXPERTS_LONG = [
+    (1, 1024, 1024, 4, 2, 64),
+    (1, 1152, 1152, 5, 3, 128),
+    (2, 1024, 1152, 6, 4, 32),
+    (1, 2048, 128, 40, 8, 32),
+    (3, 1280, 1024, 64, 8, 128),
+    (70, 1152, 256, 2, 2, 32),
+]
 
 
 def make_w4(E, H, I, group, seed):
@@ -427,6 +436,24 @@ def test_experts(case):
     # a token's result does not depend on the others of the call
     t = n // 2
     assert torch.equal(y[t:t + 1], m(x[t:t + 1], idx[t:t + 1], tw[t:t + 1]))
+
+
+@pytest.mark.parametrize("case", EXPERTS_LONG, ids=str)
+def test_experts_long_reductions(case):
+    n, H, I, E, K, group = case
+    w = make_w4(E, H, I, group, 1)
+    x = torch.randn((n, H), generator=gen(2)).bfloat16().cuda()
+    idx, tw = routing(n, E, K, 3)
+    m = M().W4Experts(*w, K=K, max_tokens=n)
+    y = m(x, idx, tw)
+    m.check()
+    check_experts(y, x, idx, tw, w)
+    assert torch.equal(y, m(x, idx, tw))
+    bad = idx.clone()
+    bad[0, 0] = -3
+    y = m(x, bad, tw)
+    assert int(m.status.item()) == 1
+    check_experts(y, x, bad, tw, w)
 
 
 def test_experts_invalid_and_repeated_ids():

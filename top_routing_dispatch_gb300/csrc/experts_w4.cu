@@ -30,7 +30,6 @@
 namespace moe {
 namespace {
 
-constexpr int WT = 256, WW = WT / 32;  // threads and warps of the kernel for few tokens
 template <int GROUP>
 constexpr int record_bytes() {  // codes; 128 / GROUP bf16 scales a row
   return 1024 + 16 * (128 / GROUP) * 2;
@@ -339,23 +338,34 @@ constexpr int queue_steps(int ctas, int step) {
 // (tile, pair) units.  DOWN false: the units of all pairs are dealt out over
 // the warps of the grid.  DOWN true: a CTA's warps share out the pairs of a
 // tile and the CTA then adds each token's rows in slot order, so that no
-// separate combine is needed.
+// separate combine is needed.  KS = 2: two warps share a unit's reduction, the
+// first half's sum plus the second's, for calls that would leave most
+// warps without work (the codes' conversion keeps an SM's few warps busier
+// than the memory).
 constexpr int kFewPairs = 32;
-template <int GROUP>
+__device__ __forceinline__ void team_sync(int team) {  // the two warps of a team
+  asm volatile("bar.sync %0, 64;" ::"r"(team + 1) : "memory");
+}
+template <bool DOWN, int GROUP, int KS>
 struct Few {
-  static constexpr int REC = record_bytes<GROUP>(), ST = 8;
-  static constexpr int QUEUE = WW * ST * REC;
+  static constexpr int WW = DOWN ? 8 * KS : 8, WT = WW * 32;  // warps and threads of a CTA
+  static constexpr int CTAS = 16 / WW;                        // of an SM
+  static constexpr int REC = record_bytes<GROUP>(), ST = 8 / KS;
+  static constexpr int STEP = REC + 512;  // and 128 values of x, or of h's two parts
+  static constexpr int QUEUE = WW * ST * STEP;
 };
 
-template <bool DOWN, int GROUP>
-__global__ void __launch_bounds__(WT, 2) w4_few_kernel(const W4Args a) {
-  using F = Few<GROUP>;
+template <bool DOWN, int GROUP, int KS>
+__global__ void __launch_bounds__(Few<DOWN, GROUP, KS>::WT, Few<DOWN, GROUP, KS>::CTAS)
+    w4_few_kernel(const W4Args a) {
+  using F = Few<DOWN, GROUP, KS>;
+  constexpr int WW = F::WW, WT = F::WT;
   constexpr int WPL = GROUP / 32;   // a lane's words of a group: WPL t .. of the group's 4 WPL
-  constexpr int REC = F::REC, ST = F::ST, NS = 128 / GROUP;
+  constexpr int REC = F::REC, STEP = F::STEP, ST = F::ST, NS = 128 / GROUP;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint8_t sh_pair[WW][kFewPairs];    // the valid pairs, each warp's own copy
   __shared__ uint8_t sh_expert[WW][kFewPairs];
-  __shared__ float sh_y[DOWN ? kFewPairs : 1][16];
+  __shared__ float sh_y[KS][DOWN ? kFewPairs : WW / KS][16];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   if constexpr (!DOWN) pdl_enter();
@@ -372,24 +382,30 @@ __global__ void __launch_bounds__(WT, 2) w4_few_kernel(const W4Args a) {
   __syncwarp();
   const int pairs = __popc(valid);
   const int tiles = a.C / 16, NB = a.R / 128;
-  const uint32_t ring = ptx::smem_u32(smem) + w * (ST * REC), ring_end = ring + ST * REC;
+  const uint32_t ring = ptx::smem_u32(smem) + w * (ST * STEP), ring_end = ring + ST * STEP;
   const size_t tile_bytes = (size_t)NB * REC;
 
-  // a warp's units in order: DOWN: pairs w, w + WW, ... of the CTA's tiles;
-  // else: every (warps of the grid)-th unit, a pair's tiles next to each other
+  // blocks [b_first, b_first + b_count) of the reduction are this warp's
+  const int half = w % KS, team = w / KS;
+  constexpr int TEAMS = WW / KS;
+  const int b_first = half * NB / KS, b_count = (half + 1) * NB / KS - b_first;
+
+  // a team's units in order: DOWN: pairs team, team + TEAMS, ... of the CTA's
+  // tiles; else: every (teams of the grid)-th unit, a pair's tiles next to each
+  // other
   struct Unit {
     int tile, pair;  // pair: place in sh_pair
   };
-  const int step = gridDim.x * WW;
+  const int step = gridDim.x * TEAMS;
   auto first_unit = [&]() {
-    if constexpr (DOWN) return Unit{(int)blockIdx.x, w};
-    const int u = w * gridDim.x + blockIdx.x;
+    if constexpr (DOWN) return Unit{(int)blockIdx.x, team};
+    const int u = team * gridDim.x + blockIdx.x;
     return Unit{u % tiles, u / tiles};
   };
   auto next_unit = [&](Unit &u) {
     if constexpr (DOWN) {
-      u.pair += WW;
-      if (u.pair >= pairs) u.pair = w, u.tile += gridDim.x;
+      u.pair += TEAMS;
+      if (u.pair >= pairs) u.pair = team, u.tile += gridDim.x;
     } else {
       u.tile += step;
       if (u.tile >= tiles) u.pair += u.tile / tiles, u.tile %= tiles;
@@ -397,68 +413,90 @@ __global__ void __launch_bounds__(WT, 2) w4_few_kernel(const W4Args a) {
   };
   auto more = [&](const Unit &u) { return u.pair < pairs && u.tile < tiles; };
 
-  // the copying side
+  // the copying side: a record, and its 128 operand values (lanes 0-15: x or
+  // h's first part, lanes 16-31: h's second part)
   Unit in = first_unit();
-  int pb = NB;
+  int pb = b_count;  // steps of it to go
   uint32_t put = ring + lane * 16;
   const uint8_t *src = nullptr;
+  const uint4 *xsrc = nullptr;
   auto locate = [&]() {
-    if (more(in))
-      src = a.rec + ((size_t)sh_expert[w][in.pair] * tiles + in.tile) * tile_bytes + lane * 16;
+    if (!more(in)) return;
+    src = a.rec + ((size_t)sh_expert[w][in.pair] * tiles + in.tile) * tile_bytes +
+          (size_t)b_first * REC + lane * 16;
+    const unsigned f = sh_pair[w][in.pair];
+    const __nv_bfloat16 *p = DOWN ? (lane & 16 ? a.hlo : a.hhi) + wide(f, (unsigned)a.R)
+                                  : a.x + wide(f * a.k_inv >> 16, (unsigned)a.R);
+    xsrc = reinterpret_cast<const uint4 *>(p) + b_first * 16 + (lane & 15);
   };
-  auto issue = [&]() {
-    if (more(in)) {
-      cp_async16(put, src);
-      cp_async16(put + 512, src + 512);
-      if (lane < 2 * NS) cp_async16(put + 1024, src + 1024);
-      src += REC;
-      put += REC;
-      if (put >= ring_end) put -= ST * REC;
-      if (--pb == 0) {
-        pb = NB;
-        next_unit(in);
-        locate();
-      }
+  auto copy_weights = [&]() {
+    cp_async16(put, src);
+    cp_async16(put + 512, src + 512);
+    if (lane < 2 * NS) cp_async16(put + 1024, src + 1024);
+    src += REC;
+  };
+  auto copy_operand = [&]() {
+    if (DOWN || lane < 16) cp_async16(put + REC, xsrc);
+    xsrc += 16;
+  };
+  auto advance = [&]() {
+    put += STEP;
+    if (put >= ring_end) put -= ST * STEP;
+    if (--pb == 0) {
+      pb = b_count;
+      next_unit(in);
+      locate();
     }
-    ptx::cp_async_commit();
   };
   locate();
-#pragma unroll 1
-  for (int i = 0; i < ST - 1; ++i) issue();
   if constexpr (DOWN) {  // weights are on their way before h is there
+#pragma unroll 1
+    for (int i = 0; i < ST - 1; ++i)
+      if (more(in)) {
+        copy_weights();
+        advance();
+      }
     pdl_wait();
     pdl_launch();
+    in = first_unit(), pb = b_count, put = ring + lane * 16;
+    locate();
+  }
+#pragma unroll 1
+  for (int i = 0; i < ST - 1; ++i) {
+    if (more(in)) {
+      if constexpr (DOWN)
+        src += REC;
+      else
+        copy_weights();
+      copy_operand();
+      advance();
+    }
+    ptx::cp_async_commit();
   }
 
   uint32_t get = ring;
-  auto product = [&](const Unit &u, float (&acc)[1][1][4]) {
-    // every column is the pair's x, or in turn the first and second part of h
-    const int f = sh_pair[w][u.pair];
-    const __nv_bfloat16 *p = DOWN ? (g & 1 ? a.hlo : a.hhi) + (size_t)f * a.R
-                                  : a.x + (size_t)(f / a.K) * a.R;
-    const uint4 *xr = reinterpret_cast<const uint4 *>(p) + t * WPL;
+  // every column is the pair's x, or in turn the first and second part of h
+  const uint32_t xget = REC + (DOWN ? (g & 1) * 256 : 0) + t * WPL * 16;
+  auto product = [&](float (&acc)[1][1][4]) {
     acc[0][0][0] = acc[0][0][1] = acc[0][0][2] = acc[0][0][3] = 0.f;
-    uint4 xv[4];  // the operand pieces of a step, asked for a step ahead
-#pragma unroll
-    for (int j = 0; j < 4; ++j) xv[j] = __ldg(xr + (j / WPL) * 4 * WPL + j % WPL);
 #pragma unroll 1
-    for (int b = NB; b > 0; --b) {
+    for (int b = b_count; b > 0; --b) {
       ptx::cp_async_wait<ST - 2>();
-      __syncwarp();  // scales are read by lanes that did not copy them
-      issue();
-      if (b > 1) xr += 16;
+      __syncwarp();  // lanes read what others copied
+      if (more(in)) {
+        copy_weights();
+        copy_operand();
+        advance();
+      }
+      ptx::cp_async_commit();
       const uint4 wd[1][2] = {{lds128(get + lane * 16), lds128(get + 512 + lane * 16)}};
       const uint4 sc[1] = {load_scales<GROUP>(get + 1024 + g * (4 * NS))};
-      get += REC;
+      const uint32_t x = get + xget;
+      get += STEP;
       if (get == ring_end) get = ring;
       step_product<GROUP, 1, 1>(
           wd, sc,
-          [&](int, int j) {
-            const uint4 v = xv[j];
-            xv[j] = __ldg(xr + (j / WPL) * 4 * WPL + j % WPL);
-            return v;
-          },
-          acc);
+          [&](int, int j) { return lds128(x + ((j / WPL) * 4 * WPL + j % WPL) * 16); }, acc);
     }
   };
   float acc[1][1][4];
@@ -467,29 +505,47 @@ __global__ void __launch_bounds__(WT, 2) w4_few_kernel(const W4Args a) {
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
       if (lane < 16)
         for (int f = w; f < a.nK; f += WW)
-          if (!(valid >> f & 1u)) sh_y[f][lane] = 0.f;
-      for (int p = w; p < pairs; p += WW) {
-        product(Unit{tile, p}, acc);
+          if (!(valid >> f & 1u))
+#pragma unroll
+            for (int k = 0; k < KS; ++k) sh_y[k][f][lane] = 0.f;
+      for (int p = team; p < pairs; p += TEAMS) {
+        product(acc);
         if (t == 0) {
           const int f = sh_pair[w][p];
-          const float wt = 4.f * __ldg(a.w + f);  // the sums are of quarter codes
-          sh_y[f][g] = (acc[0][0][0] + acc[0][0][1]) * wt;
-          sh_y[f][g + 8] = (acc[0][0][2] + acc[0][0][3]) * wt;
+          sh_y[half][f][g] = acc[0][0][0] + acc[0][0][1];
+          sh_y[half][f][g + 8] = acc[0][0][2] + acc[0][0][3];
         }
       }
       __syncthreads();
       for (int i = threadIdx.x; i < V * 16; i += WT) {
         const int tok = i >> 4, c = i & 15;
         float y = 0.f;
-        for (int k = 0; k < a.K; ++k) y += sh_y[tok * a.K + k][c];
+        for (int k = 0; k < a.K; ++k) {
+          const int f = tok * a.K + k;
+          float z = sh_y[0][f][c];
+          if constexpr (KS == 2) z += sh_y[1][f][c];
+          if (valid >> f & 1u) y += z * (4.f * __ldg(a.w + f));  // the sums are of quarter codes
+        }
         a.y[(size_t)tok * a.C + tile * 16 + c] = __float2bfloat16_rn(y);
       }
       __syncthreads();
     }
   } else {
     for (Unit u = first_unit(); more(u); next_unit(u)) {
-      product(u, acc);
-      if (t == 0) store_h(a, sh_pair[w][u.pair], u.tile * 8 + g, acc[0][0][0], acc[0][0][2]);
+      product(acc);
+      if constexpr (KS == 2) {  // the second half's sums to the first half's warp
+        if (half == 1 && t == 0)
+          *reinterpret_cast<float2 *>(&sh_y[0][team][2 * g]) =
+              make_float2(acc[0][0][0], acc[0][0][2]);
+        team_sync(team);
+        if (half == 0 && t == 0) {
+          const float2 v = *reinterpret_cast<const float2 *>(&sh_y[0][team][2 * g]);
+          acc[0][0][0] += v.x, acc[0][0][2] += v.y;
+        }
+        team_sync(team);
+      }
+      if (half == 0 && t == 0)
+        store_h(a, sh_pair[w][u.pair], u.tile * 8 + g, acc[0][0][0], acc[0][0][2]);
     }
   }
   ptx::cp_async_wait<0>();
@@ -815,8 +871,19 @@ cudaError_t launch_many(const W4Args &a, cudaStream_t s) {
                    (long long)max_entries(a.nK, a.E, rows) * (a.C / 16 / (MW * MT_MANY)), s);
 }
 
+// tiles of the first product over all pairs
+inline long long few_units(const W4Args &a) { return (long long)a.nK * (a.I / 8); }
 inline bool few_pairs(const W4Args &a) {
-  return a.nK <= kFewPairs && a.nK * (a.I / 8) <= WW * device_sm_count();
+  return a.nK <= kFewPairs && few_units(a) <= 8 * device_sm_count();
+}
+
+template <bool DOWN, int GROUP, int KS>
+cudaError_t launch_few(const W4Args &a, cudaStream_t s) {
+  using F = Few<DOWN, GROUP, KS>;
+  constexpr int teams = F::WW / KS;
+  return launch_w4<w4_few_kernel<DOWN, GROUP, KS>>(
+      a, F::QUEUE, 0, F::WT, F::CTAS,
+      DOWN ? a.C / 16 : (few_units(a) + teams - 1) / teams, s);
 }
 
 template <bool DOWN, int GROUP>
@@ -825,9 +892,12 @@ cudaError_t launch_stage(const W4Args &a, cudaStream_t s) {
   // grid: beyond that the other kernel's larger steps pay (H = 2048, I = 1024:
   // 13 us against 19 at one token, 23 against 22 at two)
   if (few_pairs(a))
-    return launch_w4<w4_few_kernel<DOWN, GROUP>>(
-        a, Few<GROUP>::QUEUE, 0, WT, 2,
-        DOWN ? a.C / 16 : ((long long)a.nK * (a.C / 16) + WW - 1) / WW, s);
+    // two warps a unit when that still leaves half of the warps (one token, two
+    // experts of H = 4096, I = 1024: 12 us against 18; eight of H = 2048: 14.7
+    // against 14.0)
+    return 2 * few_units(a) <= 8 * device_sm_count() && a.R >= 1024
+               ? launch_few<DOWN, GROUP, 2>(a, s)
+               : launch_few<DOWN, GROUP, 1>(a, s);
   // column groups for nearly every expert's tokens at once (the mean and four
   // deviations of their number); what exceeds them reads the weights again
   const float mean = (float)a.nK / a.E, want = (mean + 4.f * sqrtf(mean)) / (DOWN ? 4 : 8);
