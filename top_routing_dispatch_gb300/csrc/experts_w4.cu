@@ -803,39 +803,46 @@ __global__ void __launch_bounds__(256) quantize_w4_kernel(const __nv_bfloat16 *_
   }
 }
 
-// Records of w13 (DOWN false) or w2: one thread writes 16 bytes.
+// Records of w13 (DOWN false) or w2: a warp writes a record, 16 bytes a lane and
+// turn.
 template <bool DOWN, int GROUP>
 __global__ void __launch_bounds__(256) prepare_w4_kernel(const uint32_t *__restrict__ q,
                                                          const __nv_bfloat16 *__restrict__ s,
                                                          uint8_t *__restrict__ rec,
                                                          long long records, int C, int R) {
   pdl_enter();
-  constexpr int NS = 128 / GROUP, WPL = 4 / NS, REC = record_bytes<GROUP>(), PIECES = REC / 16;
-  const int NB = R / 128, tiles = C / 16;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < records * PIECES;
-       i += (long long)gridDim.x * 256) {
-    const long long r = i / PIECES;
-    const int p = (int)(i - r * PIECES);
-    const int b = (int)(r % NB), tile = (int)(r / NB % tiles);
-    const size_t e = (size_t)(r / NB / tiles);
-    auto row = [&](int g, int half) {
-      return e * C + (DOWN ? tile * 16 + 8 * half + g : half * (C / 2) + tile * 8 + g);
+  constexpr int NS = 128 / GROUP, WPL = 4 / NS, REC = record_bytes<GROUP>();
+  const int NB = R / 128, tiles = C / 16, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  for (long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); r < records;
+       r += (long long)gridDim.x * 8) {
+    const long long rt = r / NB;
+    const int b = (int)(r - rt * NB);
+    const size_t e = (size_t)(rt / tiles);
+    const int tile = (int)(rt - (long long)e * tiles);
+    auto row = [&](int gg, int half) {
+      return e * C + (DOWN ? tile * 16 + 8 * half + gg : half * (C / 2) + tile * 8 + gg);
     };
-    uint4 v;
-    uint32_t *o = reinterpret_cast<uint32_t *>(&v);
-    if (p < 64) {  // plane p / 32, lane p % 32: the lane's four words of its row
-      const int g = (p & 31) >> 2, t = p & 3;
-      const uint32_t *from = q + row(g, p >> 5) * (R / 8) + b * 16 + t * WPL;
+    uint4 v[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // plane h: the lane's four words of its row
+      const uint32_t *from = q + row(g, h) * (R / 8) + b * 16 + t * WPL;
+      uint32_t *o = reinterpret_cast<uint32_t *>(&v[h]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[j] = __ldg(from + (j / WPL) * 4 * WPL + j % WPL);
-    } else {  // scales (g, half, NS), eight of them
+    }
+    uint4 *to = reinterpret_cast<uint4 *>(rec + r * REC);
+    to[lane] = v[0];
+    to[32 + lane] = v[1];
+    if (lane < 2 * NS) {  // scales (g, half, NS), eight of them
+      __align__(16) __nv_bfloat16 o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int k = (p - 64) * 8 + j, g = k / (2 * NS), half = k / NS % 2;
-        reinterpret_cast<__nv_bfloat16 *>(o)[j] = s[row(g, half) * (R / GROUP) + b * NS + k % NS];
+        const int k = lane * 8 + j, gg = k / (2 * NS), half = k / NS % 2;
+        o[j] = s[row(gg, half) * (R / GROUP) + b * NS + k % NS];
       }
+      to[64 + lane] = *reinterpret_cast<const uint4 *>(o);
     }
-    reinterpret_cast<uint4 *>(rec + r * REC)[p] = v;
   }
 }
 
@@ -928,8 +935,7 @@ cudaError_t prepare(const Desc &d, int which, const int32_t *q, const void *scal
                     cudaStream_t s) {
   const int C = which ? d.H : 2 * d.I, R = which ? d.I : d.H;
   const long long records = (long long)d.E * (C / 16) * (R / 128);
-  const long long want = (records * (record_bytes<GROUP>() / 16) + 255) / 256;
-  const long long cap = 64ll * device_sm_count();
+  const long long want = (records + 7) / 8, cap = 64ll * device_sm_count();
   return launch_pdl(which ? prepare_w4_kernel<true, GROUP> : prepare_w4_kernel<false, GROUP>,
                     dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0, s,
                     reinterpret_cast<const uint32_t *>(q),

@@ -46,7 +46,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 8.f;
 constexpr int kItemCost = 2;  // a new item's overhead, in units
 constexpr int kGroup = 12;    // parts joined at a time
-constexpr int kSnap = 4;      // a range's end this near an item's edge moves to it (> kItemCost)
+constexpr int kSnap = 4;      // a range's end this near an item's edge moves to it (> kItemCost);
+                              // ranges are no shorter unless there are more items than such ranges
 
 struct AttnArgs {
   const void *q;
@@ -188,7 +189,6 @@ __device__ __forceinline__ float rescale(float a, float b) {
 template <int D_, bool E4M3, int NT>
 struct MmaPath {
   using Out = __nv_bfloat16;
-  static constexpr int RANGE = 8;  // units of a range at least, unless there are more items
   static constexpr int D = D_, KEYS = 16, NH = 8 * NT, EB = E4M3 ? 1 : 2;
   static constexpr int KE = 16 / EB;                    // values of a K piece
   static constexpr int KJ = D / KE / 4;                 // K pieces per lane and row
@@ -454,7 +454,6 @@ struct MmaPath {
 template <int D_>
 struct FmaPath {
   using Out = float;
-  static constexpr int RANGE = 4;
   static constexpr int D = D_, KEYS = 8, NH = 8, EB = 4;
   static constexpr int KJ = D / 16;            // K pieces per lane (row g, pieces t + 4j)
   static constexpr int VR = D >= 128 ? 1 : 2;  // rows of one V load of the warp
@@ -465,16 +464,29 @@ struct FmaPath {
   static constexpr int NCH = D / CH;
   static constexpr int Q_SMEM = NH * D;
 
+  static constexpr int QR = NH * D / 4 / 128;
+  float4 qr[QR];  // the next item's queries, on their way
   float o[NH][VJ][4];
   float m[NH], l[NH];
   float mult;
 
-  __device__ __forceinline__ void fetch(const Out *, int, int) {}
+  // asks for nh query heads, shared out over the CTA's threads (128 of them)
+  __device__ __forceinline__ void fetch(const Out *q, int nh, int) {
+#pragma unroll
+    for (int i = 0; i < QR; ++i) {
+      const int e = threadIdx.x + i * 128;
+      if (e < nh * D / 4) qr[i] = __ldg(reinterpret_cast<const float4 *>(q) + e);
+    }
+  }
 
-  __device__ __forceinline__ void begin(const Out *q, int nh, float sc, int, float *qs) {
+  __device__ __forceinline__ void begin(const Out *, int nh, float sc, int, float *qs) {
     mult = sc;
     __syncthreads();  // qs is free
-    for (int e = threadIdx.x; e < nh * D; e += blockDim.x) qs[e] = __ldg(q + e);
+#pragma unroll
+    for (int i = 0; i < QR; ++i) {
+      const int e = threadIdx.x + i * 128;
+      if (e < nh * D / 4) reinterpret_cast<float4 *>(qs)[e] = qr[i];
+    }
     __syncthreads();
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
@@ -790,7 +802,7 @@ __global__ void __launch_bounds__(NW * 32, ctas<P>()) paged_attention_kernel(
     if (a.lse)
       for (int e = tid; e < a.Hq; e += NT) a.lse[(size_t)b * a.Hq + e] = -INFINITY;
   }
-  const long long want = max((T + P::RANGE - 1) / P::RANGE, items * HV);
+  const long long want = max((T + kSnap - 1) / kSnap, items * HV);
   const long long W = min(want, (long long)gridDim.x);
   if ((long long)blockIdx.x >= W) return;
   // this CTA's range, its ends moved to the edges of items that they nearly meet
