@@ -22,6 +22,7 @@
 //    own rounding to bf16 does again.
 //  - Words are handed to lanes so that one instruction's 16 indices lie in one
 //    group; x is read in the same order, 16 bytes a lane, as it lies.
+#include <cmath>
 #include <type_traits>
 
 #include "experts_w4.cuh"
@@ -557,12 +558,12 @@ __global__ void __launch_bounds__(Few<DOWN, GROUP, KS>::WT, Few<DOWN, GROUP, KS>
 // tiles and 128 indices of up to 8 NTM operand rows, pieces permuted so that
 // the reads meet no bank twice.
 constexpr int MW = 4, MT_MANY = 2;
-template <bool DOWN, int GROUP, int NTM>
+// CT: CTAs of an SM.
+template <bool DOWN, int GROUP, int NTM, int CT>
 struct Many {
   static constexpr int WEIGHTS = MW * MT_MANY * record_bytes<GROUP>();
   static constexpr int STEP = WEIGHTS + NTM * 8 * 256;
-  static constexpr int CTAS = 3;  // of an SM
-  static constexpr int ST = queue_steps(CTAS, STEP);
+  static constexpr int ST = queue_steps(CT, STEP);
   static constexpr int QUEUE = ST * STEP;
   static_assert(ST >= 3, "a queue of three steps");
 };
@@ -573,9 +574,9 @@ __device__ __forceinline__ int operand_place(int r, int c) {
   return WPL == 1 ? c ^ ((r & 1) << 2) : WPL == 2 ? c ^ (r & 1) : c ^ ((c >> 3) & 1) ^ ((r & 1) << 1);
 }
 
-template <bool DOWN, int GROUP, int NTM>
-__global__ void __launch_bounds__(MW * 32, Many<DOWN, GROUP, NTM>::CTAS) w4_many_kernel(const W4Args a) {
-  using Q = Many<DOWN, GROUP, NTM>;
+template <bool DOWN, int GROUP, int NTM, int CT>
+__global__ void __launch_bounds__(MW * 32, CT) w4_many_kernel(const W4Args a) {
+  using Q = Many<DOWN, GROUP, NTM, CT>;
   constexpr int WPL = GROUP / 32, MT = MT_MANY;
   constexpr int CR = DOWN ? 4 : 8;  // pairs of a column group
   constexpr int REC = record_bytes<GROUP>(), ST = Q::ST, STEP = Q::STEP, NS = 128 / GROUP;
@@ -870,12 +871,31 @@ cudaError_t launch_w4(const W4Args &a, int queue, int rows, int threads, int cta
                     a);
 }
 
-template <bool DOWN, int GROUP, int NTM>
+template <bool DOWN, int GROUP, int NTM, int CT>
 cudaError_t launch_many(const W4Args &a, cudaStream_t s) {
   constexpr int rows = (DOWN ? 4 : 8) * NTM;
-  return launch_w4<w4_many_kernel<DOWN, GROUP, NTM>>(a, Many<DOWN, GROUP, NTM>::QUEUE, rows,
-                   MW * 32, Many<DOWN, GROUP, NTM>::CTAS,
-                   (long long)max_entries(a.nK, a.E, rows) * (a.C / 16 / (MW * MT_MANY)), s);
+  return launch_w4<w4_many_kernel<DOWN, GROUP, NTM, CT>>(
+      a, Many<DOWN, GROUP, NTM, CT>::QUEUE, rows, MW * 32, CT,
+      (long long)max_entries(a.nK, a.E, rows) * (a.C / 16 / (MW * MT_MANY)), s);
+}
+
+// CTAs of an SM for `units` equal units: as few as hold them all at once (the
+// queues are deeper), else those whose last round is fullest; 4 are a little
+// faster in the long run (61 tokens at H = 7168, I = 2048, E = 256: 919, 901 and
+// 936 us with 3, 4 and 5), 5 where they make one round of two (3 tokens there:
+// 124, 132 and 112 us).
+inline int ctas_for(double units) {
+  const double sms = device_sm_count();
+  const double weight[] = {0.97, 1.0, 0.985};
+  int best = 3;
+  double top = 0.0;
+  for (int c = 3; c <= 5; ++c) {
+    const double rounds = units / (c * sms);
+    if (rounds <= 1.0) return c;
+    const double score = weight[c - 3] * rounds / ceil(rounds);
+    if (score > top) top = score, best = c;
+  }
+  return best;
 }
 
 // tiles of the first product over all pairs
@@ -908,9 +928,16 @@ cudaError_t launch_stage(const W4Args &a, cudaStream_t s) {
   // column groups for nearly every expert's tokens at once (the mean and four
   // deviations of their number); what exceeds them reads the weights again
   const float mean = (float)a.nK / a.E, want = (mean + 4.f * sqrtf(mean)) / (DOWN ? 4 : 8);
-  if (want <= 1.f) return launch_many<DOWN, GROUP, 1>(a, s);
-  if (want <= 2.f) return launch_many<DOWN, GROUP, 2>(a, s);
-  return launch_many<DOWN, GROUP, 4>(a, s);
+  if (want <= 1.f) {
+    // experts hit by tokens that choose theirs independently
+    const double hit = a.E * (1.0 - pow(1.0 - (double)a.K / a.E, (double)a.nK / a.K));
+    const int c = ctas_for(hit * (a.C / 16 / (MW * MT_MANY)));
+    return c == 3   ? launch_many<DOWN, GROUP, 1, 3>(a, s)
+           : c == 4 ? launch_many<DOWN, GROUP, 1, 4>(a, s)
+                    : launch_many<DOWN, GROUP, 1, 5>(a, s);
+  }
+  if (want <= 2.f) return launch_many<DOWN, GROUP, 2, 3>(a, s);
+  return launch_many<DOWN, GROUP, 4, 3>(a, s);
 }
 
 template <int GROUP>
