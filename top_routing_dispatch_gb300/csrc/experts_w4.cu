@@ -925,9 +925,12 @@ cudaError_t launch_stage(const W4Args &a, cudaStream_t s) {
     return 2 * few_units(a) <= 8 * device_sm_count() && a.R >= 1024
                ? launch_few<DOWN, GROUP, 2>(a, s)
                : launch_few<DOWN, GROUP, 1>(a, s);
-  // column groups for nearly every expert's tokens at once (the mean and four
-  // deviations of their number); what exceeds them reads the weights again
-  const float mean = (float)a.nK / a.E, want = (mean + 4.f * sqrtf(mean)) / (DOWN ? 4 : 8);
+  // column groups for most experts' tokens at once (the mean and one deviation
+  // of their number); what exceeds them reads the weights again, mostly from
+  // L2.  With four deviations, 30 and 45 tokens at H = 2048, I = 1024, E = 64
+  // take 60 and 65 us against 54 and 59, 128 at H = 7168, E = 256 1173 against
+  // 1127.
+  const float mean = (float)a.nK / a.E, want = (mean + sqrtf(mean)) / (DOWN ? 4 : 8);
   if (want <= 1.f) {
     // experts hit by tokens that choose theirs independently
     const double hit = a.E * (1.0 - pow(1.0 - (double)a.K / a.E, (double)a.nK / a.K));
