@@ -111,7 +111,6 @@ __device__ __forceinline__ uint32_t quarter_codes(uint32_t w) {
 // every CTA cuts an expert's pairs into the same entries), and the entries
 // (expert, first pair, pairs <= ROWS) to compute.
 struct Lists {
-  int *start;         // (E)
   uint32_t *entry;    // expert | pairs - 1 << 8 | first << 16
   uint16_t *pair;     // (nK)
   int entries;
@@ -124,98 +123,110 @@ __host__ __device__ inline int max_entries(int nK, int E, int rows) {
   return (nK < E ? nK : E) + nK / rows;
 }
 __host__ __device__ inline int lists_bytes(int nK, int E, int rows) {
-  return (16 + 4 * E + 4 * max_entries(nK, E, rows) + 2 * nK + 15) & ~15;
+  return (4 * max_entries(nK, E, rows) + 2 * nK + 15) & ~15;
 }
 
-// mem: lists_bytes; hist: (warps, E) scratch.  Each warp takes a contiguous
-// slice of the pairs.
+// mem: lists_bytes; scratch: build_bytes.  Each warp ranks a contiguous slice of
+// the pairs, 32 at a time; a thread then sums up the warps' counts of two
+// neighbouring experts and one scan gives their places.  The chain of
+// barriers and loads is what this costs, and every CTA waits for it: about 7500
+// cycles at 120 tokens, E = 64, K = 8 and 3000 at 3 tokens, E = 256 (a pass of
+// counts, a scan by one warp and a second pass for the ranks took 11000 and
+// 7700).
+constexpr int MW = 4;  // warps of a CTA
+static_assert(kMaxE <= 256 && kMaxE <= 2 * MW * 32, "8 bits, two experts a thread");
+constexpr int build_bytes(int nK) { return 4 * (MW * kMaxE + nK); }
+
 template <int ROWS>
-__device__ __forceinline__ Lists build_lists(uint8_t *mem, int *hist, const W4Args &a) {
+__device__ __forceinline__ Lists build_lists(uint8_t *mem, uint8_t *scratch, const W4Args &a) {
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int threads = blockDim.x, warps = threads >> 5;
+  __shared__ uint32_t sh_warp[MW];
   Lists L;
-  int *total = reinterpret_cast<int *>(mem);
-  L.start = total + 4;
-  L.entry = reinterpret_cast<uint32_t *>(L.start + a.E);
+  L.entry = reinterpret_cast<uint32_t *>(mem);
   L.pair = reinterpret_cast<uint16_t *>(L.entry + max_entries(a.nK, a.E, ROWS));
-  int *mine = hist + w * a.E;
-  const int slice = (a.nK + threads - 1) / threads * 32;
+  // (warps, kMaxE): pairs of an expert in a warp's slice, then the slice's place
+  int *hist = reinterpret_cast<int *>(scratch);
+  int *mine = hist + w * kMaxE;
+  uint32_t *rank = reinterpret_cast<uint32_t *>(hist + MW * kMaxE);  // (nK): expert | rank << 16
+  const int slice = (a.nK + MW * 32 - 1) / (MW * 32) * 32;
   const int f0 = w * slice, f1 = min(f0 + slice, a.nK);
-  for (int e = lane; e < a.E; e += 32) mine[e] = 0;
-  __syncwarp();
+#pragma unroll
+  for (int e = 0; e < kMaxE; e += 128)
+    *reinterpret_cast<int4 *>(mine + e + 4 * lane) = make_int4(0, 0, 0, 0);
   bool bad = false;
-  constexpr int BATCH = 8;  // ids in flight per lane
-  for (int fb = f0; fb < f1; fb += 32 * BATCH) {
-    int e[BATCH];
+#pragma unroll 8
+  for (int f = f0 + lane; f < f1; f += 32) {
+    const uint32_t e = (uint32_t)__ldg(a.idx + f);
+    bad |= e >= (uint32_t)a.E;
+    rank[f] = e < (uint32_t)a.E ? e : 0xffffu;
+  }
+  __syncwarp();
+#pragma unroll 2
+  for (int f = f0 + lane; f - lane < f1; f += 32) {
+    const uint32_t e = f < f1 ? rank[f] : 0xffffu;
+    const bool ok = e != 0xffffu;
+    // the lanes with the same expert, by the bits of its number: a ballot a
+    // bit, independent of each other (the instruction that compares all lanes
+    // at once takes several hundred cycles when most differ)
+    unsigned peers = __ballot_sync(0xffffffffu, ok);
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      const int f = fb + 32 * i + lane;
-      e[i] = f < f1 ? __ldg(a.idx + f) : 0;
+    for (int b = 0; b < 8; ++b) {
+      const unsigned m = __ballot_sync(0xffffffffu, e >> b & 1u);
+      peers &= e >> b & 1u ? m : ~m;
     }
-#pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      if (fb + 32 * i + lane >= f1) continue;
-      if ((unsigned)e[i] < (unsigned)a.E)
-        atomicAdd(&mine[e[i]], 1);
-      else
-        bad = true;
-    }
+    const unsigned below = peers & ((1u << lane) - 1u);
+    const int at = ok ? mine[e] : 0;
+    if (ok) rank[f] = e | (uint32_t)(at + __popc(below)) << 16;
+    __syncwarp();  // every peer has read the count
+    if (ok && below == 0) mine[e] = at + __popc(peers);
+    __syncwarp();
   }
   if (__syncthreads_or(bad) && tid == 0 && blockIdx.x == 0)
     flag_status(a.status, MOE_DEV_BAD_ROUTING);
-  for (int e = tid; e < a.E; e += threads) {  // counts; each warp's first rank
-    int run = 0;
-    for (int i = 0; i < warps; ++i) {
-      const int h = hist[i * a.E + e];
-      hist[i * a.E + e] = run;
-      run += h;
-    }
-    L.start[e] = run;
+  // experts 2 tid and 2 tid + 1
+  int2 run = make_int2(0, 0), at[MW];
+#pragma unroll
+  for (int i = 0; i < MW; ++i) {
+    at[i] = run;
+    const int2 h = *reinterpret_cast<const int2 *>(hist + i * kMaxE + 2 * tid);
+    run.x += h.x, run.y += h.y;
+  }
+  // pairs and, above them, entries
+  const uint32_t m0 = (run.x + ROWS - 1) / ROWS, m1 = (run.y + ROWS - 1) / ROWS;
+  const uint32_t own = (uint32_t)(run.x + run.y) | (m0 + m1) << 16;
+  uint32_t inc = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) sh_warp[w] = inc;
+  __syncthreads();
+  uint32_t before = inc - own, total = 0;
+#pragma unroll
+  for (int i = 0; i < MW; ++i) {
+    if (i < w) before += sh_warp[i];
+    total += sh_warp[i];
+  }
+  const uint32_t first = before & 0xffffu;
+#pragma unroll
+  for (int i = 0; i < MW; ++i)
+    *reinterpret_cast<int2 *>(hist + i * kMaxE + 2 * tid) =
+        make_int2(first + at[i].x, first + run.x + at[i].y);
+  uint32_t *entry = L.entry + (before >> 16);
+#pragma unroll 1
+  for (uint32_t i = 0; i < m0 + m1; ++i) {
+    const uint32_t second = i >= m0, k = (second ? i - m0 : i) * ROWS;
+    entry[i] = (2 * tid + second) | (min((uint32_t)ROWS, (second ? run.y : run.x) - k) - 1) << 8 |
+               (first + (second ? run.x : 0) + k) << 16;
   }
   __syncthreads();
-  if (w == 0) {  // starts, and the entries in expert order
-    int pairs = 0, entries = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-      const int c = e0 + lane < a.E ? L.start[e0 + lane] : 0;
-      const int m = (c + ROWS - 1) / ROWS;
-      int ic = c, im = m;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, ic, o), z = __shfl_up_sync(0xffffffffu, im, o);
-        if (lane >= o) ic += y, im += z;
-      }
-      const int first = pairs + ic - c;
-      if (e0 + lane < a.E) L.start[e0 + lane] = first;
-      for (int i = 0; i < m; ++i)
-        L.entry[entries + im - m + i] = (uint32_t)(e0 + lane) |
-                                        (uint32_t)(min(ROWS, c - ROWS * i) - 1) << 8 |
-                                        (uint32_t)(first + ROWS * i) << 16;
-      pairs += __shfl_sync(0xffffffffu, ic, 31);
-      entries += __shfl_sync(0xffffffffu, im, 31);
-    }
-    if (lane == 0) *total = entries;
+#pragma unroll 4
+  for (int f = f0 + lane; f < f1; f += 32) {
+    const uint32_t r = rank[f], e = r & 0xffffu;
+    if (e != 0xffffu) L.pair[mine[e] + (r >> 16)] = (uint16_t)f;
   }
-  __syncthreads();
-  for (int fb = f0; fb < f1; fb += 32 * BATCH) {
-    int e[BATCH];
-#pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      const int f = fb + 32 * i + lane;
-      e[i] = f < f1 ? __ldg(a.idx + f) : -1;
-      if ((unsigned)e[i] >= (unsigned)a.E) e[i] = -1;
-    }
-#pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      if (fb + 32 * i >= f1) break;  // the whole warp
-      const unsigned peers = __match_any_sync(0xffffffffu, e[i]);
-      const int rank = __popc(peers & ((1u << lane) - 1u));
-      if (e[i] >= 0) L.pair[L.start[e[i]] + mine[e[i]] + rank] = (uint16_t)(fb + 32 * i + lane);
-      __syncwarp();
-      if (e[i] >= 0 && rank == 0) mine[e[i]] += __popc(peers);
-      __syncwarp();
-    }
-  }
-  L.entries = *total;
+  L.entries = total >> 16;
   __syncthreads();
   return L;
 }
@@ -557,7 +568,7 @@ __global__ void __launch_bounds__(Few<DOWN, GROUP, KS>::WT, Few<DOWN, GROUP, KS>
 // same queue as the weights: each step holds the 8 KB of codes of the eight
 // tiles and 128 indices of up to 8 NTM operand rows, pieces permuted so that
 // the reads meet no bank twice.
-constexpr int MW = 4, MT_MANY = 2;
+constexpr int MT_MANY = 2;
 // CT: CTAs of an SM.
 template <bool DOWN, int GROUP, int NTM, int CT>
 struct Many {
@@ -566,6 +577,7 @@ struct Many {
   static constexpr int ST = queue_steps(CT, STEP);
   static constexpr int QUEUE = ST * STEP;
   static_assert(ST >= 3, "a queue of three steps");
+  static_assert(QUEUE >= build_bytes(kW4MaxPairs), "the lists' scratch lies in the queue");
 };
 
 // place of 16-byte piece c of operand row r
@@ -582,7 +594,7 @@ __global__ void __launch_bounds__(MW * 32, CT) w4_many_kernel(const W4Args a) {
   constexpr int REC = record_bytes<GROUP>(), ST = Q::ST, STEP = Q::STEP, NS = 128 / GROUP;
   extern __shared__ __align__(128) uint8_t smem[];
   if constexpr (!DOWN) pdl_enter();
-  const Lists L = build_lists<CR * NTM>(smem + Q::QUEUE, reinterpret_cast<int *>(smem), a);
+  const Lists L = build_lists<CR * NTM>(smem + Q::QUEUE, smem, a);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int tiles = a.C / 16 / (MW * MT);  // units of an entry
