@@ -12,6 +12,11 @@
 // row lane + lanes, ...  16 values are two vectors of 8 that rotate with each
 // other (i and i + rope_dim/2, or 16 neighbours when pairs are interleaved),
 // so no value is loaded twice and q may be rotated in place.
+//
+// Measured: 8191 tokens of 16 + 2 * 16 heads of 128, bf16 (206 MB): 37.5 us,
+// 5.5 TB/s, as long as a plain device copy of the same bytes takes; with the
+// rows asked for after the page is known 40 us.  61 tokens of 32 + 2 * 8 heads
+// into an e4m3 cache: 3 us.
 #include <cuda_fp8.h>
 
 #include "kv_cache.cuh"
@@ -203,10 +208,12 @@ template <int D, typename T, typename C>
 cudaError_t append_d(AppendArgs &a, int n, cudaStream_t s) {
   constexpr int RL = AT / (D / 16);
   const int rows = a.Hq + 2 * a.Hkv;
-  // few tokens: their head rows are spread over CTAs, one row per thread;
-  // many: one CTA per token
+  // few tokens: their head rows are spread over CTAs, one row per thread, so
+  // that a token is not the work of one SM; many: one CTA per token, which looks
+  // its place up once (48 rows of 128 a token: 61 tokens 2.34 us spread, 2.66
+  // not; 200 2.91 and 3.07; 300 4.06 and 3.10)
   const int parts = (rows + RL - 1) / RL;
-  const bool spread = (long long)n * parts <= 8ll * device_sm_count();
+  const bool spread = (long long)n * parts <= 4ll * device_sm_count();
   a.rows_per_cta = spread ? RL : rows;
   return launch_pdl(kv_append_kernel<D, T, C>, dim3(n, spread ? parts : 1), dim3(AT), 0, s, a);
 }
