@@ -53,7 +53,7 @@ struct W4Args {
   __nv_bfloat16 *hhi, *hlo;  // (n K, I): h = hhi + hlo
   float *yslot;              // (n K, H), weighted
   __nv_bfloat16 *y;          // (n, H)
-  int nK, K, E, C, R, I;
+  int nK, K, E, C, R, H, I;
   unsigned k_inv;            // f / K = f * k_inv >> 16 (f < 4096, K <= 16: checked for all)
   int32_t *status;
 };
@@ -923,10 +923,19 @@ inline int ctas_for(double units) {
   return best;
 }
 
-// tiles of the first product over all pairs
+// Few pairs, in units of the first product (tiles over all pairs): up to one to
+// four warps of the grid, two warps share a unit's reduction; up to one to two,
+// a warp takes a unit while its reduction is short.  Beyond that the other
+// kernel's larger steps pay.  One token, I = 1024, group 128, the kernel taken
+// and the next best: 512 units of H = 2048 10.0 us (other kernel 13.8), of 4096
+// 13.5 (20.4), of 7168 20.6 (28.5); 1024 units of H = 2048 13.8 (two warps a unit
+// 14.5, other kernel 16.3), of 4096 24.1 (two warps 24.6, one 30.5), of 7168 32.4
+// (37, 47.7); two tokens of H = 2048 22 (26).
 inline long long few_units(const W4Args &a) { return (long long)a.nK * (a.I / 8); }
+inline bool few_shared(const W4Args &a) { return few_units(a) <= 4 * device_sm_count(); }
 inline bool few_pairs(const W4Args &a) {
-  return a.nK <= kFewPairs && few_units(a) <= 8 * device_sm_count();
+  return a.nK <= kFewPairs &&
+         (few_shared(a) || (a.H <= 2048 && few_units(a) <= 8 * device_sm_count()));
 }
 
 template <bool DOWN, int GROUP, int KS>
@@ -940,16 +949,10 @@ cudaError_t launch_few(const W4Args &a, cudaStream_t s) {
 
 template <bool DOWN, int GROUP>
 cudaError_t launch_stage(const W4Args &a, cudaStream_t s) {
-  // few pairs, and at most one unit of the first product to two warps of the
-  // grid: beyond that the other kernel's larger steps pay (H = 2048, I = 1024:
-  // 13 us against 19 at one token, 23 against 22 at two)
   if (few_pairs(a))
-    // two warps a unit when that still leaves half of the warps (one token, two
-    // experts of H = 4096, I = 1024: 12 us against 18; eight of H = 2048: 14.7
-    // against 14.0)
-    return 2 * few_units(a) <= 8 * device_sm_count() && a.R >= 1024
-               ? launch_few<DOWN, GROUP, 2>(a, s)
-               : launch_few<DOWN, GROUP, 1>(a, s);
+    // (a reduction of less than eight steps is too short to share)
+    return few_shared(a) && a.R >= 1024 ? launch_few<DOWN, GROUP, 2>(a, s)
+                                        : launch_few<DOWN, GROUP, 1>(a, s);
   // column groups for most experts' tokens at once (the mean and one deviation
   // of their number); what exceeds them reads the weights again, mostly from
   // L2.  With four deviations, 30 and 45 tokens at H = 2048, I = 1024, E = 64
@@ -1030,7 +1033,7 @@ cudaError_t launch_experts_w4(const Desc &d, int group, const void *x, const int
   a.hhi = reinterpret_cast<__nv_bfloat16 *>(p);
   a.hlo = reinterpret_cast<__nv_bfloat16 *>(p + hb);
   a.yslot = reinterpret_cast<float *>(p + 2 * hb);
-  a.nK = (int)d.nK(), a.K = d.K, a.E = d.E, a.I = d.I;
+  a.nK = (int)d.nK(), a.K = d.K, a.E = d.E, a.H = d.H, a.I = d.I;
   a.k_inv = (65536u + d.K - 1) / d.K;
   a.status = status;
   if (group == 32) return run<32>(d, a, w13_t, w2_t, s);
