@@ -927,8 +927,8 @@ inline int ctas_for(double units) {
 // four warps of the grid, two warps share a unit's reduction; up to one to two,
 // a warp takes a unit while its reduction is short.  Beyond that the other
 // kernel's larger steps pay.  One token, I = 1024, group 128, the kernel taken
-// and the next best: 512 units of H = 2048 10.0 us (other kernel 13.8), of 4096
-// 13.5 (20.4), of 7168 20.6 (28.5); 1024 units of H = 2048 13.8 (two warps a unit
+// and the next best: 512 units of H = 2048 8.5 us (other kernel 13.8), of 4096
+// 13.3 (20.4), of 7168 20.6 (28.5); 1024 units of H = 2048 13.8 (two warps a unit
 // 14.5, other kernel 16.3), of 4096 24.1 (two warps 24.6, one 30.5), of 7168 32.4
 // (37, 47.7); two tokens of H = 2048 22 (26).
 inline long long few_units(const W4Args &a) { return (long long)a.nK * (a.I / 8); }
@@ -938,12 +938,22 @@ inline bool few_pairs(const W4Args &a) {
          (few_shared(a) || (a.H <= 2048 && few_units(a) <= 8 * device_sm_count()));
 }
 
+// The first product's CTAs with shared reductions are no more than the SMs, and ask
+// for half of an SM's shared memory so that no two share one: beside the CTAs of
+// a call before and of the second product they else settle in pairs, in some
+// runs for good (one token, I = 512, eight experts of H = 4096: 12 us against 19;
+// four of H = 2048, I = 1024: 8.5 against 9.8; not where a warp has a unit to
+// itself: eight of H = 2048 16.5 against 14).
+constexpr int kHalfSm = 114 * 1024;
+
 template <bool DOWN, int GROUP, int KS>
 cudaError_t launch_few(const W4Args &a, cudaStream_t s) {
   using F = Few<DOWN, GROUP, KS>;
   constexpr int teams = F::WW / KS;
+  constexpr int smem = !DOWN && KS == 2 ? kHalfSm : F::QUEUE;
+  static_assert(smem >= F::QUEUE, "the queue");
   return launch_w4<w4_few_kernel<DOWN, GROUP, KS>>(
-      a, F::QUEUE, 0, F::WT, F::CTAS,
+      a, smem, 0, F::WT, F::CTAS,
       DOWN ? a.C / 16 : (few_units(a) + teams - 1) / teams, s);
 }
 
