@@ -534,7 +534,9 @@ moe_status_t moe_kv_append(const moe_kv_cache_t *cache, int32_t n, const void *q
  *   It has to be zero-filled once before its first use; every call leaves the
  *   part that it needs zeroed that way.  Calls that may run at the same time
  *   need a workspace each.
- * Scores, the softmax's statistics and the sums are float32.  The work is
+ * Scores, the softmax's statistics and the sums are float32.  Over bf16 and
+ * 8-bit caches each probability multiplies V as two bf16 parts (within 2^-16
+ * of itself, however small it is beside the largest).  The work is
  * split over the tokens of long sequences and joined in a fixed order: results
  * are bitwise reproducible on one GPU.  A length outside
  * [0, max_pages * page_size] or a page outside [0, num_pages) sets

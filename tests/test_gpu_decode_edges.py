@@ -1,0 +1,73 @@
+"""Edges of the serving operators on the GPU, against their plain float64
+forms: steep softmaxes, shared workspaces, very long sequences and pages,
+values near the limits of their types, streams."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+from tests import decode_reference as R
+from tests import test_gpu_decode as T
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16, E4M3 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
+
+
+# ----------------------------------------------------- a steep softmax
+STEEP = [
+    # Hq, Hkv, D, P, lens
+    (2, 1, 64, 16, (300, 17)),
+    (4, 4, 128, 32, (3000,)),
+    (16, 2, 128, 64, (900, 2, 8192)),
+    (4, 1, 256, 16, (640,)),
+    (12, 1, 128, 16, (333, 64)),
+]
+
+
+@pytest.mark.parametrize("nats", [12, 17, 25, 60])
+@pytest.mark.parametrize("case", STEEP, ids=lambda c: "-".join(map(str, c[:4])))
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "f32"])
+def test_attend_keeps_the_tail_of_a_steep_softmax(kind, case, nats):
+    """The first token of a sequence stands `nats` above the others and its
+    value is zero, so that the result is the others' alone.
+
+    Bound: scores as in the reference's (their sums, and the roundings of
+    score and exponent), each probability rounded to no more than 2^-16 of
+    itself however small it is (float32: 2^-22), sums in float32."""
+    Hq, Hkv, D, P, lens = case
+    cache, q, n, window, _ = T.attend_case((kind, Hq, Hkv, D, P, 0, lens), q_std=1.0)
+    if kind == "e4m3":  # room for the first key below 448
+        cache.k_cache.copy_((cache.k_cache.float() / 8).to(E4M3))
+        cache.k_scale.mul_(8)
+    G = Hq // Hkv
+    for b in range(len(lens)):
+        page = int(cache.page_table[b, 0])
+        for h in range(Hkv):
+            sc = 1.0 if cache.k_scale is None else float(cache.k_scale[h])
+            u = q[b, h * G].float()
+            k = u * (nats * math.sqrt(D) / float(u.square().sum())) / sc
+            cache.k_cache[page, h, 0] = k.to(cache.k_cache.dtype)
+            cache.v_cache[page, h, 0] = torch.zeros(D, device="cuda").to(cache.v_cache.dtype)
+    lse = torch.empty(q.shape[:2], device="cuda")
+    out = cache.attend(q, n, lse=lse)
+    cache.check()
+    p_err = 2.0 ** -22 if kind == "f32" else 2.0 ** -16
+    scale = 1 / math.sqrt(D)
+    kc, vc = T.scaled(cache.k_cache, cache.k_scale), T.scaled(cache.v_cache, cache.v_scale)
+    assert torch.isfinite(kc).all()
+    table, qd = cache.page_table.cpu(), T.f64(q)
+    want, wl, bound = R.attend(qd, kc, vc, table, n.cpu(), 0, scale, p_err)
+    tol = bound + R.HALF[cache.dtype] * (want.abs() + bound) * (1 + 1e-6)
+    err = (T.f64(out) - want).abs()
+    assert (err <= tol).all(), float((err / tol.clamp(min=1e-30)).max())
+    # lse moves by no more than the scores, the sum's relative error, and its
+    # own rounding (in base 2, then by ln 2)
+    for b, ln in enumerate(lens):
+        k = R.gather(kc, table[b], 0, ln)
+        for h in range(Hq):
+            x = k[h // G] * qd[b, h] * scale
+            ds = D * R.U32 * float(x.abs().sum(1).max()) + 4 * R.U32 * float(x.sum(1).abs().max())
+            t = 2 * ds + 4 * (ln + 64) * R.U32 + 4 * R.U32 * abs(float(wl[b, h]))
+            assert abs(float(lse[b, h]) - float(wl[b, h])) <= t

@@ -133,6 +133,12 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t &lo, uint32_t
       : "=r"(lo), "=r"(hi)
       : "r"(x));
 }
+// a pair of halves that came from e4m3 as bf16, exactly: 4 significant bits, so
+// the lower half of their float32 form is empty (NaN stays NaN)
+__device__ __forceinline__ uint32_t f16_to_bf16(uint32_t x) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+  return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
+}
 __device__ __forceinline__ uint32_t word(const uint4 &v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
@@ -363,19 +369,14 @@ struct MmaPath {
       l[n][1] += p[1] + p[3];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        if constexpr (E4M3) {
-          // halves keep 11 significant bits of p next to e4m3's 4 of V
-          const __half2 h = __floats2half2_rn(p[2 * r], p[2 * r + 1]);
-          ph[n][r] = trans8x8(*reinterpret_cast<const uint32_t *>(&h));
-        } else {
-          // p in two bf16 parts: one alone would round the result as much as
-          // its own rounding to bf16 does again
-          const __nv_bfloat162 h = __floats2bfloat162_rn(p[2 * r], p[2 * r + 1]);
-          const float2 hf = __bfloat1622float2(h);
-          const __nv_bfloat162 w = __floats2bfloat162_rn(p[2 * r] - hf.x, p[2 * r + 1] - hf.y);
-          ph[n][r] = trans8x8(*reinterpret_cast<const uint32_t *>(&h));
-          pl[n][r] = trans8x8(*reinterpret_cast<const uint32_t *>(&w));
-        }
+        // p in two bf16 parts: one alone would round the result as much as its
+        // own rounding to bf16 does again, and halves end 2^-24 below the
+        // largest p, which loses the tail of a steep softmax
+        const __nv_bfloat162 h = __floats2bfloat162_rn(p[2 * r], p[2 * r + 1]);
+        const float2 hf = __bfloat1622float2(h);
+        const __nv_bfloat162 w = __floats2bfloat162_rn(p[2 * r] - hf.x, p[2 * r + 1] - hf.y);
+        ph[n][r] = trans8x8(*reinterpret_cast<const uint32_t *>(&h));
+        pl[n][r] = trans8x8(*reinterpret_cast<const uint32_t *>(&w));
       }
     }
     // rows 2t and 2t + 1 (+ 8): pieces g + 8i, or halves of piece g / 2
@@ -412,13 +413,12 @@ struct MmaPath {
           const uint32_t sel = j & 1 ? 0x7362 : 0x5140;
           e4m3x4_to_f16(__byte_perm(word(v[0], w), word(v[1], w), sel), a0, a1);
           e4m3x4_to_f16(__byte_perm(word(v[2], w), word(v[3], w), sel), a2, a3);
+          a0 = f16_to_bf16(a0), a1 = f16_to_bf16(a1), a2 = f16_to_bf16(a2), a3 = f16_to_bf16(a3);
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma16816<E4M3>(o[i][j][n], a0, a1, a2, a3, ph[n][0], ph[n][1]);
-        if constexpr (!E4M3)
+        for (int n = 0; n < NT; ++n) mma16816<false>(o[i][j][n], a0, a1, a2, a3, ph[n][0], ph[n][1]);
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            mma16816<false>(o[i][j][n], a0, a1, a2, a3, pl[n][0], pl[n][1]);
+        for (int n = 0; n < NT; ++n) mma16816<false>(o[i][j][n], a0, a1, a2, a3, pl[n][0], pl[n][1]);
       }
     }
   }
