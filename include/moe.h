@@ -536,7 +536,8 @@ moe_status_t moe_kv_append(const moe_kv_cache_t *cache, int32_t n, const void *q
  *   need a workspace each.
  * Scores, the softmax's statistics and the sums are float32.  Over bf16 and
  * 8-bit caches each probability multiplies V as two bf16 parts (within 2^-16
- * of itself, however small it is beside the largest).  The work is
+ * of itself, however small it is beside the largest); over 8-bit caches a
+ * query value keeps its 8 bits down to 2^-31 of its head's largest one.  The work is
  * split over the tokens of long sequences and joined in a fixed order: results
  * are bitwise reproducible on one GPU.  A length outside
  * [0, max_pages * page_size] or a page outside [0, num_pages) sets

@@ -71,3 +71,31 @@ def test_attend_keeps_the_tail_of_a_steep_softmax(kind, case, nats):
             ds = D * R.U32 * float(x.abs().sum(1).max()) + 4 * R.U32 * float(x.sum(1).abs().max())
             t = 2 * ds + 4 * (ln + 64) * R.U32 + 4 * R.U32 * abs(float(wl[b, h]))
             assert abs(float(lse[b, h]) - float(wl[b, h])) <= t
+
+
+# ------------------------------------------- queries of very unequal values
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("heads", [(2, 2), (12, 1)])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_attend_keeps_small_query_values(kind, heads, dim):
+    """One value of each query is 2^20 times the others' size, and the cache
+    holds zeros there: the scores are the others'.  The bound has nothing for
+    the large value's products, which are zero."""
+    cache, q, n, window, _ = T.attend_case((kind, *heads, dim, 16, 0, (150, 33)))
+    q[..., 5] = 2.0 ** 20
+    x = cache.k_cache.float()
+    x[..., 5] = 0
+    cache.k_cache.copy_(x.to(cache.k_cache.dtype))
+    out = cache.attend(q, n)
+    cache.check()
+    T.check_attend(cache, q, n, window, "bf16", out, None)
+
+
+@pytest.mark.parametrize("power", [-125, -100, 100, 120])
+def test_attend_queries_of_any_size_e4m3(power):
+    cache, q, n, window, _ = T.attend_case(("e4m3", 4, 2, 128, 16, 0, (150, 33)), q_std=1.0)
+    q = (q.float() * 2.0 ** power).to(BF16)
+    scale = 2.0 ** -power / math.sqrt(128) if power > -110 else 2.0 ** 120
+    out = cache.attend(q, n, scale=scale)
+    cache.check()
+    T.check_attend(cache, q, n, window, "bf16", out, None, scale=scale)

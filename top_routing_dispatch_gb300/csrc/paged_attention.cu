@@ -248,8 +248,10 @@ struct MmaPath {
         mult[n][0] = mult[n][1] = sc;
       } else {
         // e4m3 values are halves exactly; q as halves too, each head scaled by
-        // a power of two so that its largest value is in [1, 2): bf16's 8
-        // significant bits fit, and what falls under 2^-24 of the largest goes
+        // a power of two so that its largest value is in [2^14, 2^15) (its
+        // products with 448 are far from float32's limit): all 8 bits of the
+        // values down to 2^-31 of the largest are kept, less of smaller ones,
+        // which is beyond what float32 sums keep beside the largest
         float top = 0.f;
 #pragma unroll
         for (int j = 0; j < KJ; ++j)
@@ -262,9 +264,9 @@ struct MmaPath {
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         int ex = (int)(__float_as_uint(top) >> 23);
-        ex = ex < 1 ? 1 : ex > 253 ? 253 : ex;
-        const float down = __uint_as_float((uint32_t)(254 - ex) << 23);  // 2^(127 - ex)
-        const float up = __uint_as_float((uint32_t)ex << 23) * sc;       // 2^(ex - 127)
+        ex = ex < 15 ? 15 : ex > 253 ? 253 : ex;  // 2^127 is scaled to 2^15
+        const float down = __uint_as_float((uint32_t)(268 - ex) << 23);  // 2^(141 - ex)
+        const float up = __uint_as_float((uint32_t)(ex - 14) << 23) * sc;  // 2^(ex - 141)
 #pragma unroll
         for (int j = 0; j < KJ; ++j)
 #pragma unroll
