@@ -532,8 +532,9 @@ moe_status_t moe_kv_append(const moe_kv_cache_t *cache, int32_t n, const void *q
  *   they hold (infinities and NaN included).
  *   ws: moe_paged_attention_workspace_size(cache) bytes, 256-byte aligned.
  *   It has to be zero-filled once before its first use; every call leaves the
- *   part that it needs zeroed that way.  Calls that may run at the same time
- *   need a workspace each.
+ *   part that it needs zeroed that way.  Calls on any caches may follow one
+ *   another on one workspace of the largest of their sizes; calls that may run
+ *   at the same time need a workspace each.
  * Scores, the softmax's statistics and the sums are float32.  Over bf16 and
  * 8-bit caches each probability multiplies V as two bf16 parts (within 2^-16
  * of itself, however small it is beside the largest); over 8-bit caches a

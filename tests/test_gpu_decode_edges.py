@@ -99,3 +99,33 @@ def test_attend_queries_of_any_size_e4m3(power):
     out = cache.attend(q, n, scale=scale)
     cache.check()
     T.check_attend(cache, q, n, window, "bf16", out, None, scale=scale)
+
+
+# ------------------------------------------------------ shared workspaces
+def test_attend_calls_of_any_sizes_share_a_workspace():
+    """One workspace, zeroed once, for calls of other batches, head layouts and
+    types: each result is that of a workspace of its own, and the counters (the
+    first 6 KB) are left zero."""
+    cases = [
+        ("bf16", 16, 16, 64, 16, 0, tuple(300 + 7 * (i % 40) for i in range(200))),
+        ("bf16", 16, 16, 64, 16, 0, (700, 90, 4000)),
+        ("f32", 6, 1, 64, 16, 0, (3000, 2000)),
+        ("e4m3", 24, 2, 128, 32, 0, (9000, 100, 0, 5)),
+        ("bf16", 8, 1, 256, 16, 0, (20000,)),
+        ("f32", 20, 2, 64, 32, 100, (65, 700)),
+    ]
+    made = [T.attend_case(c, seed=i) for i, c in enumerate(cases)]
+    want = [cache.attend(q, n, window=w) for cache, q, n, w, _ in made]
+    ws = torch.zeros(max(c[0].ws.numel() for c in made), dtype=torch.uint8, device="cuda")
+    lib = T.M()._lib.load()
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    for i in (0, 1, 0, 2, 3, 0, 4, 5, 0, 4, 3, 0):
+        cache, q, n, w, _ = made[i]
+        out = torch.full_like(want[i], 7.0)
+        assert lib.moe_paged_attention(
+            ctypes.byref(cache.desc), q.data_ptr(), q.stride(0), n.data_ptr(), w,
+            1 / math.sqrt(cache.head_dim), out.data_ptr(), None, ws.data_ptr(), ws.numel(),
+            cache.status.data_ptr(), stream) == 0
+        cache.check()
+        assert torch.equal(out, want[i]), i
+    assert int(ws[:6144].sum()) == 0

@@ -66,7 +66,7 @@ struct AttnArgs {
   const float *kscale, *vscale;
   void *out;
   float *lse;
-  int32_t *counters;        // one per (sequence, head group)
+  int32_t *counters;        // of the item that begins in a range and goes on in the next: one per range
   int32_t *group_counters;  // one per part
   float2 *part_ml;    // (2 kMaxWorkers, NH): maximum and sum of a part
   float *part_o;      // (2 kMaxWorkers, NH, D)
@@ -1071,7 +1071,7 @@ __global__ void __launch_bounds__(NW * 32, ctas<P>()) paged_attention_kernel(
       last = arrive(a.group_counters + 2 * first + (first == p.wf ? 1 : 0), n, &sh_last);
       if (last) join_parts<P, NW>(a, first, 1, p.wf, n, nh, sm, sl, vs, nullptr, nullptr);
     }
-    if (last && arrive(a.counters + (size_t)p.b * HV + p.h, groups, &sh_last))
+    if (last && arrive(a.counters + p.wf, groups, &sh_last))
       join_parts<P, NW>(a, p.wf, step, p.wf, groups, nh, sm, sl, vs, out, lse);
   }
 }
@@ -1129,11 +1129,15 @@ cudaError_t launch_fma(const AttnArgs &a, int D, cudaStream_t s) {
 
 }  // namespace
 
+// The counters come first and in the same place whatever the call, so that
+// calls of any sizes may follow one another on one workspace.
+constexpr size_t kCounterBytes = kMaxWorkers * sizeof(int32_t);
+constexpr size_t kGroupCounterBytes = 2 * kMaxWorkers * sizeof(int32_t);
+static_assert(kCounterBytes % 256 == 0 && kGroupCounterBytes % 256 == 0, "alignment");
+
 size_t paged_attention_ws_bytes(const KVCache &c) {
   const int nh = item_heads(c);
-  const size_t items = (size_t)c.num_seqs * c.kv_heads * head_groups(c, nh);
-  return align256(items * sizeof(int32_t)) + align256(2 * kMaxWorkers * sizeof(int32_t)) +
-         align256(2 * kMaxWorkers * nh * sizeof(float2)) +
+  return kCounterBytes + kGroupCounterBytes + align256(2 * kMaxWorkers * nh * sizeof(float2)) +
          align256((size_t)2 * kMaxWorkers * nh * c.head_dim * sizeof(float));
 }
 
@@ -1158,9 +1162,9 @@ cudaError_t launch_paged_attention(const KVCache &c, const void *q, long long q_
   a.status = status;
   uint8_t *w = reinterpret_cast<uint8_t *>(ws);
   a.counters = reinterpret_cast<int32_t *>(w);
-  w += align256((size_t)a.B * a.Hkv * a.VG * sizeof(int32_t));
+  w += kCounterBytes;
   a.group_counters = reinterpret_cast<int32_t *>(w);
-  w += align256(2 * kMaxWorkers * sizeof(int32_t));
+  w += kGroupCounterBytes;
   a.part_ml = reinterpret_cast<float2 *>(w);
   w += align256(2 * kMaxWorkers * nh * sizeof(float2));
   a.part_o = reinterpret_cast<float *>(w);
