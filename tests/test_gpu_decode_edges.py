@@ -129,3 +129,25 @@ def test_attend_calls_of_any_sizes_share_a_workspace():
         cache.check()
         assert torch.equal(out, want[i]), i
     assert int(ws[:6144].sum()) == 0
+
+
+# --------------------------------------------------- very large pages, lengths
+def test_attend_and_append_in_pages_past_32_bit_offsets():
+    """A token's place inside its page lies beyond 2^31 bytes (the last tokens of
+    a page of 8.4 million, seen through a window)."""
+    P, D, w = 2 ** 23 + 16, 64, 30
+    n = P - 6
+    kc, vc = (torch.zeros((1, 1, P, D), device="cuda") for _ in range(2))
+    big = T.M().PagedKVCache(kc, vc, torch.zeros((1, 1), dtype=torch.int32, device="cuda"), 2)
+    k, v = (torch.randn((w, 1, D), generator=T.gen(i)).cuda() for i in (1, 2))
+    seq = torch.zeros(w, dtype=torch.int32, device="cuda")
+    big.append(None, k, v, seq, torch.arange(n - w, n, device="cuda").int())
+    assert torch.equal(kc[0, :, n - w:n], k.transpose(0, 1))
+    assert torch.equal(vc[0, :, n - w:n], v.transpose(0, 1))
+    q = torch.randn((1, 2, D), generator=T.gen(3)).cuda()
+    out = big.attend(q, torch.tensor([n], dtype=torch.int32, device="cuda"), window=w)
+    big.check()
+    small = T.M().PagedKVCache(*(torch.zeros((2, 1, 16, D), device="cuda") for _ in range(2)),
+                               torch.arange(2, dtype=torch.int32, device="cuda").view(1, 2), 2)
+    small.append(None, k, v, seq, torch.arange(w, device="cuda").int())
+    T.check_attend(small, q, torch.tensor([w], dtype=torch.int32), 0, "f32", out, None)

@@ -900,7 +900,7 @@ __global__ void __launch_bounds__(NW * 32, ctas<P>()) paged_attention_kernel(
     if (more) {
       if (in.key < in.s.len) {
         const bool ok = (unsigned)page < (unsigned)a.num_pages;
-        const size_t at = (size_t)(ok ? page : 0) * a.page_bytes + head_off + in.off * ROW;
+        const size_t at = (size_t)(ok ? page : 0) * a.page_bytes + head_off + (size_t)in.off * ROW;
         const uint32_t dst = ring + slot_in * P::STAGE_BYTES;
         if (ok && in.key >= in.s.first && in.key + P::KEYS <= in.s.len) {
           P::Tile::template copy<false>(dst, a.kc + at, 0, 0, lane);
