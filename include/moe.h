@@ -541,8 +541,8 @@ moe_status_t moe_kv_append(const moe_kv_cache_t *cache, int32_t n, const void *q
  * query value keeps its 8 bits down to 2^-31 of its head's largest one.  The work is
  * split over the tokens of long sequences and joined in a fixed order: results
  * are bitwise reproducible on one GPU.  A length outside
- * [0, max_pages * page_size] or a page outside [0, num_pages) sets
- * MOE_DEV_BAD_CACHE and leaves that sequence's row unspecified (status_word
+ * [0, max_pages * page_size] or above 2^31 - 1024, or a page outside
+ * [0, num_pages), sets MOE_DEV_BAD_CACHE and leaves that sequence's row unspecified (status_word
  * may be NULL).
  */
 size_t moe_paged_attention_workspace_size(const moe_kv_cache_t *cache);

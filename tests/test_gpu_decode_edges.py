@@ -151,3 +151,28 @@ def test_attend_and_append_in_pages_past_32_bit_offsets():
                                torch.arange(2, dtype=torch.int32, device="cuda").view(1, 2), 2)
     small.append(None, k, v, seq, torch.arange(w, device="cuda").int())
     T.check_attend(small, q, torch.tensor([w], dtype=torch.int32), 0, "f32", out, None)
+
+
+def test_attend_lengths_near_the_end_of_32_bits():
+    """The longest sequences (a page table may name one page many times), seen
+    through a window; longer ones are out of range."""
+    m, P, D, w, top = T.M(), 2 ** 24, 64, 100, 2 ** 31 - 1024
+    kc, vc = (torch.zeros((1, 1, P, D), dtype=BF16, device="cuda") for _ in range(2))
+    last = top % P
+    for i, c in enumerate((kc, vc)):
+        c[0, 0, last - w:last] = torch.randn((w, D), generator=T.gen(i)).cuda().to(BF16)
+    cache = m.PagedKVCache(kc, vc, torch.zeros((2, 128), dtype=torch.int32, device="cuda"), 4)
+    q = torch.randn((2, 4, D), generator=T.gen(3)).cuda().to(BF16)
+    out = cache.attend(q, torch.tensor([top, 7], dtype=torch.int32, device="cuda"), window=w)
+    cache.check()
+    small = m.PagedKVCache(
+        *(torch.nn.functional.pad(c[0, 0, last - w:last], (0, 0, 0, 12)).reshape(7, 1, 16, D)
+          for c in (kc, vc)), torch.arange(7, dtype=torch.int32, device="cuda").view(1, 7), 4)
+    T.check_attend(small, q[:1], torch.tensor([w], dtype=torch.int32), 0, "bf16", out[:1], None)
+    for length in (top + 1, 2 ** 31 - 1):
+        again = cache.attend(q, torch.tensor([length, 7], dtype=torch.int32, device="cuda"), window=w)
+        with pytest.raises(m.MoEError) as e:
+            cache.check()
+        assert e.value.status == 8
+        cache.status.zero_()
+        assert torch.equal(again[1], out[1])

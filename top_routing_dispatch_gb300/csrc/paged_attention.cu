@@ -626,6 +626,12 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
   return a / b;
 }
 
+// Tokens are counted in 32 bits, up to a few steps past a sequence's end.
+constexpr int kMaxLen = 0x7fffffff - 1023;
+__device__ __forceinline__ bool bad_length(const AttnArgs &a, int len) {
+  return len < 0 || len > kMaxLen || (long long)len > (long long)a.max_pages * a.P;
+}
+
 // What a sequence asks for: tokens [first, len), read from the KEYS-aligned
 // token `base` on, in `units` units.
 struct Seq {
@@ -636,7 +642,7 @@ template <class P, int NW>
 __device__ __forceinline__ Seq seq_info(const AttnArgs &a, int b) {
   Seq s;
   s.len = __ldg(a.lens + b);
-  if (s.len < 0 || (long long)s.len > (long long)a.max_pages * a.P) s.len = 0;  // flagged once
+  if (bad_length(a, s.len)) s.len = 0;  // flagged once
   s.first = a.window > 0 && s.len > a.window ? s.len - a.window : 0;
   s.base = s.first / P::KEYS * P::KEYS;
   s.units = (s.len - s.base + NW * P::KEYS - 1) / (NW * P::KEYS);
@@ -783,8 +789,7 @@ __global__ void __launch_bounds__(NW * 32, ctas<P>()) paged_attention_kernel(
     const int n = seq_info<P, NW>(a, b).units;
     mine += n ? n + kItemCost : 0;
     live += n != 0;
-    const int len = __ldg(a.lens + b);
-    if (blockIdx.x == 0 && (len < 0 || (long long)len > (long long)a.max_pages * a.P))
+    if (blockIdx.x == 0 && bad_length(a, __ldg(a.lens + b)))
       flag_status(a.status, MOE_DEV_BAD_CACHE);
   }
   long long inc = mine;
