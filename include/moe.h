@@ -590,7 +590,9 @@ moe_status_t moe_prepare_weights_w4(const moe_layer_desc_t *desc, int group, con
  *   y[t] = sum_k topk_w[t,k] W2[e]^T h,  h = SiLU(W13[e]^T x[t], gate) * up,
  *   e = topk_idx[t,k]
  * (Algorithm 2 steps 4-11 with the weights above).  Sums are float32, h is
- * carried in two bf16 parts (about 16 significant bits), y is rounded once.
+ * carried in two bf16 parts (about 16 significant bits; an infinity or NaN
+ * stays what it is), y is rounded once.  A group's sum is formed before its
+ * scale: it cannot overflow while x and h are below 2^120.
  * Results are bitwise reproducible.
  *   x (n,H) bf16, topk_idx (n,K) int32, topk_w (n,K) float32, y (n,H) bf16;
  *   w13_t, w2_t from moe_prepare_weights_w4 with the same group;

@@ -176,3 +176,61 @@ def test_attend_lengths_near_the_end_of_32_bits():
         assert e.value.status == 8
         cache.status.zero_()
         assert torch.equal(again[1], out[1])
+
+
+# ------------------------------------- experts: h at the ends of its range
+def one_hot_layer(gates, ups, group, w2_code, w2_scale, n):
+    """A layer of one expert (H = I = 128) in which every token's h[i] is
+    SiLU(gates[i]) * ups[i], each a bf16 value, for the first i and 0 beyond;
+    w2's codes are w2_code (H, I)."""
+    H = I = 128
+    codes = torch.full((1, 2 * I, H), 8)
+    s13 = torch.ones((1, 2 * I, H // group))
+    for base, values in ((0, gates), (I, ups)):
+        for i, v in enumerate(values):
+            codes[0, base + i, 0] = 9 if v >= 0 else 7
+            s13[0, base + i, 0] = abs(v)
+
+    def pack(c):
+        c = c.unflatten(-1, (-1, 8)).long()
+        w = sum(c[..., j] << (4 * (j // 2) + 16 * (j % 2)) for j in range(8))
+        return torch.where(w >= 2 ** 31, w - 2 ** 32, w).int().cuda()
+    w = [pack(codes), s13.bfloat16().cuda(), pack(w2_code[None]),
+         torch.full((1, H, I // group), w2_scale).bfloat16().cuda()]
+    assert R.unpack_w4(w[0].cpu(), w[1].cpu().float())[0, :len(gates), 0].tolist() == list(gates)
+    x = torch.zeros((n, H), dtype=BF16, device="cuda")
+    x[:, 0] = 1
+    idx = torch.zeros((n, 1), dtype=torch.int32, device="cuda")
+    return w, x, idx, torch.ones((n, 1), device="cuda")
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("group", [32, 128])
+def test_experts_h_beyond_bf16(n, group):
+    """Finite float32 h that rounds to an infinite bf16, of both signs."""
+    a = 181 / 128  # its square is 1.99957
+    code = torch.full((128, 128), 8)
+    code[:, 0], code[::2, 1], code[1::2, 2] = 9, 7, 9
+    w, x, idx, tw = one_hot_layer([a * 2.0 ** 63, a * 2.0 ** 60, a * 2.0 ** 63],
+                                  [a * 2.0 ** 64, a * 2.0 ** 60, -a * 2.0 ** 64], group, code, 2.0 ** -20, n)
+    ex = T.M().W4Experts(*w, K=1, max_tokens=n)
+    y = ex(x, idx, tw)
+    assert torch.isfinite(y.float()).all()
+    T.check_experts(y, x, idx, tw, w)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("group", [32, 128])
+def test_experts_infinite_h(n, group):
+    """An infinite h among finite ones gives infinities, as the sum does, where
+    no code is zero, and NaN where its own code is."""
+    code = torch.full((128, 128), 9)
+    code[1] = 7
+    code[2, 1] = 8
+    w, x, idx, tw = one_hot_layer([3.0, 2.0 ** 70], [1.0, 2.0 ** 70], group, code, 0.5, n)
+    y = T.M().W4Experts(*w, K=1, max_tokens=n)(x, idx, tw).float()
+    assert (y[:, 0] == math.inf).all() and (y[:, 1] == -math.inf).all()
+    assert torch.isnan(y[:, 2]).all() and (y[:, 3:] == math.inf).all()
+    w, x, idx, tw = one_hot_layer([3.0, 2.0 ** 70], [1.0, 2.0 ** 70], group, code, 0.5, n)
+    x[:, 0] = math.nan
+    assert torch.isnan(T.M().W4Experts(*w, K=1, max_tokens=n)(x, idx, tw).float()).all()

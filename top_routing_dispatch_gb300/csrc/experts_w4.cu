@@ -313,10 +313,14 @@ __device__ __forceinline__ void store_h(const W4Args &a, int f, int c, float gat
   gate *= 4.f, up *= 4.f;
   // the hardware's exp and reciprocal (errors 2^-21): h keeps 16 bits
   const float h = __fdividef(gate, 1.f + __expf(-gate)) * up;
-  const __nv_bfloat16 hi = __float2bfloat16_rn(h);
+  // a finite h beyond bf16's largest value has that as its first part; an
+  // infinite one or NaN has no second part (inf - inf is NaN)
+  constexpr float kTop = 0x1.fep127f;
+  const bool finite = fabsf(h) < INFINITY;
+  const __nv_bfloat16 hi = __float2bfloat16_rn(finite ? fminf(fmaxf(h, -kTop), kTop) : h);
   const size_t at = wide((unsigned)f, (unsigned)a.I) + c;
   a.hhi[at] = hi;
-  a.hlo[at] = __float2bfloat16_rn(h - __bfloat162float(hi));
+  a.hlo[at] = __float2bfloat16_rn(finite ? h - __bfloat162float(hi) : 0.f);
 }
 
 // Stores the sums (of quarter codes) of tile `tile` for an entry's pairs.
