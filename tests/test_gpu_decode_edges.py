@@ -234,3 +234,18 @@ def test_experts_infinite_h(n, group):
     w, x, idx, tw = one_hot_layer([3.0, 2.0 ** 70], [1.0, 2.0 ** 70], group, code, 0.5, n)
     x[:, 0] = math.nan
     assert torch.isnan(T.M().W4Experts(*w, K=1, max_tokens=n)(x, idx, tw).float()).all()
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_experts_strongly_negative_gates(n):
+    """SiLU far below zero, raised to ordinary size by a large `up`: exp(-88)
+    and exp(-90) are subnormal, within 2^-18 of themselves."""
+    gates = [-1.0, -20.0, -60.0, -80.0, -87.0, -88.0, -90.0, 90.0]
+    ups = [2.0 ** round(-g * math.log2(math.e) - math.log2(abs(g))) if g < 0 else 1 / 64 for g in gates]
+    code = torch.full((128, 128), 8)
+    for i in range(len(gates)):
+        code[i::16, i] = 9
+        code[8 + i::16, i] = 15
+    w, x, idx, tw = one_hot_layer(gates, ups, 32, code, 0.5, n)
+    y = T.M().W4Experts(*w, K=1, max_tokens=n)(x, idx, tw)
+    T.check_experts(y, x, idx, tw, w)

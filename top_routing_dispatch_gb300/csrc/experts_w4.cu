@@ -311,8 +311,11 @@ __device__ __forceinline__ size_t wide(unsigned a, unsigned b) {
 // h of pair f in column c from the sums (of quarter codes) of gate and up
 __device__ __forceinline__ void store_h(const W4Args &a, int f, int c, float gate, float up) {
   gate *= 4.f, up *= 4.f;
-  // the hardware's exp and reciprocal (errors 2^-21): h keeps 16 bits
-  const float h = __fdividef(gate, 1.f + __expf(-gate)) * up;
+  // SiLU by the full-precision exp of a number that is not positive: the fast
+  // one's error grows with the gate, and the fast division (2 ulp) wants a
+  // divisor below 2^126, here 1 to 2
+  const float e = expf(-fabsf(gate));
+  const float h = __fdividef(gate < 0.f ? gate * e : gate, 1.f + e) * up;
   // a finite h beyond bf16's largest value has that as its first part; an
   // infinite one or NaN has no second part (inf - inf is NaN)
   constexpr float kTop = 0x1.fep127f;
