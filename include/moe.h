@@ -565,7 +565,8 @@ moe_status_t moe_paged_attention(const moe_kv_cache_t *cache, const void *q, int
  *
  * moe_quantize_weights_w4 makes them from row-major bf16 w13 (E,H,2I) and w2
  * (E,I,H): scale = bf16(max |w| of the group / 7), code = 8 + w / scale
- * rounded to nearest even and limited to 0..15 (a group of zeros: scale 0, codes 8).
+ * rounded to nearest even and limited to 0..15 (a group of zeros: scale 0, codes 8;
+ * a group that holds an infinity or NaN: scale NaN, codes 8).
  * The descriptor's n, K and weight_layout are not used.
  */
 moe_status_t moe_quantize_weights_w4(const moe_layer_desc_t *desc, int group, const void *w13,

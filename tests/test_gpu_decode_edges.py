@@ -249,3 +249,24 @@ def test_experts_strongly_negative_gates(n):
     w, x, idx, tw = one_hot_layer(gates, ups, 32, code, 0.5, n)
     y = T.M().W4Experts(*w, K=1, max_tokens=n)(x, idx, tw)
     T.check_experts(y, x, idx, tw, w)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_quantize_keeps_non_finite_weights_visible(bad):
+    """A group with an infinite or NaN weight gets a NaN scale and codes 8; the
+    other groups are as without it."""
+    m, E, H, I, group = T.M(), 2, 256, 128, 64
+    w13 = (torch.randn((E, H, 2 * I), generator=T.gen(1)) / 16).bfloat16().cuda()
+    w2 = (torch.randn((E, I, H), generator=T.gen(2)) / 11).bfloat16().cuda()
+    want = m.quantize_weights_w4(w13, w2, group)
+    w13[1, 70, 9], w2[0, 3, 200] = bad, bad
+    got = m.quantize_weights_w4(w13, w2, group)
+    for (q, s, q0, s0), at in (((*got[:2], *want[:2]), (1, 9, 1)), ((*got[2:], *want[2:]), (0, 200, 0))):
+        e, c, g = at
+        words = group // 8
+        assert torch.isnan(s[at].float())
+        assert (q[e, c, g * words:(g + 1) * words] == 0x88888888 - 2 ** 32).all()
+        q, s = q.clone(), s.clone()
+        s[at] = s0[at]
+        q[e, c, g * words:(g + 1) * words] = q0[e, c, g * words:(g + 1) * words]
+        assert torch.equal(q, q0) and torch.equal(s, s0)

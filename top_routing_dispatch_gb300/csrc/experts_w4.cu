@@ -815,9 +815,12 @@ __global__ void __launch_bounds__(256) quantize_w4_kernel(const __nv_bfloat16 *_
     const int gr = (int)(rest % groups);
     const long long e = rest / groups;
     const __nv_bfloat16 *src = w + ((size_t)e * R + (size_t)gr * GROUP) * C + c;
-    float top = 0.f;
+    // magnitudes compare as their bits do, infinity and NaN above all others
+    unsigned bits = 0;
 #pragma unroll 8
-    for (int r = 0; r < GROUP; ++r) top = fmaxf(top, fabsf(__bfloat162float(src[(size_t)r * C])));
+    for (int r = 0; r < GROUP; ++r)
+      bits = max(bits, __bfloat16_as_ushort(src[(size_t)r * C]) & 0x7fffu);
+    const float top = bits < 0x7f80u ? __uint_as_float(bits << 16) : NAN;
     const __nv_bfloat16 sb = __float2bfloat16_rn(top / 7.f);
     const float sc = __bfloat162float(sb);
     s[((size_t)e * C + c) * groups + gr] = sb;
