@@ -560,7 +560,7 @@ moe_status_t moe_paged_attention(const moe_kv_cache_t *cache, const void *q, int
  *   W[r][c] = (code - 8) * scale[c][r / group],  code in 0..15.
  *   w13_q (E, 2I, H/8) int32, w13_s (E, 2I, H/group) bf16,
  *   w2_q (E, H, I/8) int32,   w2_s (E, H, I/group) bf16.
- * group 32, 64 or 128; H % 128 == 0 and I % 128 == 0 (else
+ * group 32, 64 or 128; H % 128 == 0 and I % 128 == 0; I below 2^30 (else
  * MOE_ERR_UNSUPPORTED).
  *
  * moe_quantize_weights_w4 makes them from row-major bf16 w13 (E,H,2I) and w2

@@ -249,3 +249,16 @@ def test_rope_table():
             a = p * 100.0 ** (-2 * i / 16)
             assert abs(float(t[p, i]) - math.cos(a)) < 1e-6
             assert abs(float(t[p, 8 + i]) - math.sin(a)) < 1e-6
+
+
+def test_experts_refuse_sizes_past_32_bits(lib):
+    """2 I columns are counted in 32 bits."""
+    d = desc(H=128, I=1 << 30, E=1, K=1, n=1)
+    for which in (0, 1):
+        assert lib.moe_w4_tiled_bytes(ctypes.byref(d), 128, which) == 0
+    assert lib.moe_experts_w4_workspace_size(ctypes.byref(d)) == 0
+    assert experts(lib, d, group=128) == UNSUPPORTED
+    assert lib.moe_prepare_weights_w4(ctypes.byref(d), 128, *[P] * 6, None) == UNSUPPORTED
+    assert lib.moe_quantize_weights_w4(ctypes.byref(d), 128, *[P] * 6, None) == UNSUPPORTED
+    d = desc(H=128, I=(1 << 30) - 128, E=1, K=1, n=1)
+    assert lib.moe_w4_tiled_bytes(ctypes.byref(d), 128, 0) == ((1 << 31) - 256) // 16 * 1056

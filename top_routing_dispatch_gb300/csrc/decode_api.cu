@@ -51,6 +51,7 @@ moe_status_t check_w4(const moe_layer_desc_t *desc, int group, Desc *d) {
   if (st != MOE_OK) return st;
   if (group != 32 && group != 64 && group != 128) return MOE_ERR_UNSUPPORTED;
   if (!d->bf16 || d->H % 128 || d->I % 128) return MOE_ERR_UNSUPPORTED;
+  if (d->I > 0x7fffffff / 2) return MOE_ERR_UNSUPPORTED;  // w13's 2 I columns are an int
   return MOE_OK;
 }
 
