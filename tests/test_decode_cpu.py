@@ -262,3 +262,59 @@ def test_experts_refuse_sizes_past_32_bits(lib):
     assert lib.moe_quantize_weights_w4(ctypes.byref(d), 128, *[P] * 6, None) == UNSUPPORTED
     d = desc(H=128, I=(1 << 30) - 128, E=1, K=1, n=1)
     assert lib.moe_w4_tiled_bytes(ctypes.byref(d), 128, 0) == ((1 << 31) - 256) // 16 * 1056
+
+
+# ------------------------------------------------------------------ devices
+def calls():
+    """Every Python call that launches, on CPU tensors that are right otherwise."""
+    import top_routing_dispatch_gb300 as M
+    n, c = 3, make()
+    q, kv3 = torch.zeros((n, 4, 64), dtype=BF16), torch.zeros((n, 2, 64), dtype=BF16)
+    ints = torch.zeros(n, dtype=torch.int32)
+    return {
+        "append": lambda: c.append(q, kv3, kv3, ints, ints, q_out=q.clone()),
+        "attend": lambda: c.attend(q, ints, out=q.clone()),
+        "check": lambda: c.check(),
+        "experts": lambda: M.W4Experts(*w4(), K=1, max_tokens=4),
+        "quantize": lambda: M.quantize_weights_w4(torch.zeros((2, 128, 256), dtype=BF16),
+                                                  torch.zeros((2, 128, 128), dtype=BF16), group=64),
+    }
+
+
+@pytest.mark.parametrize("name", ["append", "attend", "check", "experts", "quantize"])
+def test_calls_refuse_tensors_that_are_not_on_a_gpu(lib, name):
+    with pytest.raises(ValueError, match="CUDA"):
+        calls()[name]()
+
+
+def test_calls_refuse_a_device_that_is_not_current(lib, monkeypatch):
+    """The library launches on the current device."""
+    from top_routing_dispatch_gb300 import decode
+    monkeypatch.setattr(decode, "_current_device", lambda: 0)
+    decode._ready(torch.device("cuda", 0))
+    with pytest.raises(ValueError, match="current"):
+        decode._ready(torch.device("cuda", 1))
+    seen = []
+
+    class Reached(Exception):
+        pass
+
+    def ready(device):
+        seen.append(device)
+        raise Reached
+    monkeypatch.setattr(decode, "_ready", ready)
+    for call in calls().values():
+        with pytest.raises(Reached):
+            call()
+    assert len(seen) == 5
+
+
+def test_an_experts_call_asks_for_its_device(lib, monkeypatch):
+    from top_routing_dispatch_gb300 import decode
+    ex = object.__new__(decode.W4Experts)
+    ex.H, ex.K, ex.max_tokens, ex.device, ex._index = 128, 1, 4, torch.device("cpu"), None
+    x = torch.zeros((2, 128), dtype=BF16)
+    idx, tw = torch.zeros((2, 1), dtype=torch.int32), torch.zeros((2, 1))
+    for call in (lambda: ex(x, idx, tw, y=torch.zeros_like(x)), ex.check):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()

@@ -3,7 +3,8 @@ decoder layer.
 
 PagedKVCache holds a paged key-value cache (append, attend); W4Experts holds
 4-bit expert weights.  As in api.py the work is done by the library's kernels;
-here arguments are checked and turned into pointers.
+here arguments are checked and turned into pointers.  Tensors are on the
+current CUDA device, where the library launches.
 """
 from __future__ import annotations
 
@@ -20,11 +21,27 @@ _DT = {torch.float32: _lib.MOE_F32, torch.bfloat16: _lib.MOE_BF16,
 _I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _want(ok: bool, what: str):
     if not ok:
         raise ValueError(what)
+
+
+def _ready(device):
+    """Refuses what the library cannot run on: it launches on the current
+    device, and takes every pointer for that device's memory."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors on a CUDA device wanted, these are on {device}")
+    if device.index != _current_device():
+        raise ValueError(f"the tensors are on {device}, which is not the current CUDA device "
+                         "(torch.cuda.set_device, or with torch.cuda.device)")
+
+
+def _index(device):
+    """A CUDA device's number, None for other devices."""
+    return device.index if device.type == "cuda" else None
 
 
 def _handle(stream, index):
@@ -77,7 +94,7 @@ class PagedKVCache:
         self.k_cache, self.v_cache, self.page_table = k_cache, v_cache, page_table
         self.k_scale, self.v_scale, self.rope = k_scale, v_scale, rope
         self.dtype = _F32 if k_cache.dtype == _F32 else _BF16
-        self.device, self._index = dev, dev.index or 0
+        self.device, self._index = dev, _index(dev)
         self._scale = 1.0 / math.sqrt(dim)
         self.num_seqs, self.q_heads, self.kv_heads, self.head_dim = (
             page_table.shape[0], int(q_heads), kv_heads, dim)
@@ -135,6 +152,8 @@ class PagedKVCache:
             _want(n < 2 or os == self.q_heads * self.head_dim, "q_out: contiguous")
         else:
             _want(q_out is None, "q_out without q")
+        if self._index is None or self._index != _current_device():
+            _ready(self.device)
         st = self._append(self._ref, n, qp, qs, kp, ks, vp, vs, sp, pp, op, self._status,
                           _handle(stream, self._index))
         if st:
@@ -158,6 +177,8 @@ class PagedKVCache:
         if lse is not None and (lse.dtype is not _F32 or lse.shape != (B, self.q_heads)
                                 or not lse.is_contiguous() or lse.device != self.device):
             raise ValueError(f"lse: contiguous ({B}, {self.q_heads}) float32 on {self.device}")
+        if self._index is None or self._index != _current_device():
+            _ready(self.device)
         st = self._attend(self._ref, qp, qs, lp, window, self._scale if scale is None else scale,
                           op, None if lse is None else lse.data_ptr(), self._ws, self._nbytes,
                           self._status, _handle(stream, self._index))
@@ -168,6 +189,7 @@ class PagedKVCache:
     def check(self, stream=None):
         """Waits for the stream and raises MoEError if a call met a sequence,
         position or page out of range."""
+        _ready(self.device)
         _check(int(_lib.load().moe_check_status(_p(self.status), _stream(stream))),
                "device status")
 
@@ -187,9 +209,11 @@ def quantize_weights_w4(w13, w2, group=128, stream=None):
            new((E, H, I // 8), _I32), new((E, H, I // group), _BF16))
     lib, desc = _lib.load(), make_desc(0, H, I, E, 1, _BF16, False)
     refused = lib.moe_w4_tiled_bytes(ctypes.byref(desc), int(group), 0) == 0
+    if not refused:
+        _ready(w13.device)
     _check(lib.moe_quantize_weights_w4(
         ctypes.byref(desc), int(group), _p(w13), _p(w2), *[_p(t) for t in out],
-        None if refused else _handle(stream, w13.device.index or 0)), "moe_quantize_weights_w4")
+        None if refused else _handle(stream, w13.device.index)), "moe_quantize_weights_w4")
     return out
 
 
@@ -219,7 +243,7 @@ class W4Experts:
         dev = w13_q.device
         _want(all(t.device == dev for t in (w13_s, w2_q, w2_s)), "all tensors on one device")
         self.H, self.I, self.E, self.K, self.group = H, I, E, int(K), group
-        self.max_tokens, self.device, self._index = int(max_tokens), dev, dev.index or 0
+        self.max_tokens, self.device, self._index = int(max_tokens), dev, _index(dev)
         self.desc = make_desc(self.max_tokens, H, I, E, K, _BF16, False)
         self._ref = ctypes.byref(self.desc)
         lib = _lib.load()
@@ -228,6 +252,7 @@ class W4Experts:
         nbytes = lib.moe_experts_w4_workspace_size(self._ref)
         if 0 in sizes or (nbytes == 0 and self.max_tokens > 0):  # the library's own reason
             _check(self._call(self._ref, group, *[None] * 7, 0, None, None), "W4Experts")
+        _ready(dev)
         self.w13_t, self.w2_t = (torch.empty(n, dtype=torch.uint8, device=dev) for n in sizes)
         _check(lib.moe_prepare_weights_w4(
             self._ref, group, _p(w13_q), _p(w13_s), _p(w2_q), _p(w2_s), _p(self.w13_t),
@@ -254,6 +279,8 @@ class W4Experts:
         elif (y.dtype is not _BF16 or y.shape != x.shape or not y.is_contiguous()
               or y.device != self.device):
             raise ValueError("y: like x")
+        if self._index is None or self._index != _current_device():
+            _ready(self.device)
         self.desc.n = n
         st = self._call(self._ref, self.group, x.data_ptr(), topk_idx.data_ptr(),
                         topk_w.data_ptr(), *self._w, y.data_ptr(), *self._tail,
@@ -265,5 +292,6 @@ class W4Experts:
     def check(self, stream=None):
         """Waits for the stream and raises MoEError if a call met an expert id
         out of range."""
+        _ready(self.device)
         _check(int(_lib.load().moe_check_status(_p(self.status), _stream(stream))),
                "device status")
