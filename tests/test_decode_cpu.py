@@ -5,6 +5,8 @@ import ctypes
 import math
 import os
 import shutil
+import threading
+import types
 
 import pytest
 import torch
@@ -318,3 +320,43 @@ def test_an_experts_call_asks_for_its_device(lib, monkeypatch):
     for call in (lambda: ex(x, idx, tw, y=torch.zeros_like(x)), ex.check):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+# ------------------------------------------------------- threads and streams
+def host_experts(monkeypatch, call):
+    """A W4Experts whose launches go to `call`, for up to 8 tokens."""
+    from top_routing_dispatch_gb300 import decode
+    lib = types.SimpleNamespace(
+        moe_w4_tiled_bytes=lambda *a: 64, moe_experts_w4_workspace_size=lambda *a: 256,
+        moe_prepare_weights_w4=lambda *a: 0, moe_experts_w4=call)
+    monkeypatch.setattr(decode._lib, "load", lambda: lib)
+    monkeypatch.setattr(decode, "_ready", lambda device: None)
+    monkeypatch.setattr(decode, "_handle", lambda stream, index: stream or 0)
+    return decode.W4Experts(*w4(), K=1, max_tokens=8)
+
+
+def expert_inputs(n):
+    x = torch.zeros((n, 128), dtype=BF16)
+    return dict(x=x, topk_idx=torch.zeros((n, 1), dtype=torch.int32), topk_w=torch.zeros((n, 1)),
+                y=torch.zeros_like(x))
+
+
+def test_two_threads_keep_their_token_counts(lib, monkeypatch):
+    """A call's token count is its own, whatever other calls of the object do
+    between its start and the library's reading of it."""
+    seen, other, threads = {}, expert_inputs(7), []
+
+    def call(ref, group, x, *rest):
+        first = not seen
+        seen.setdefault(x, None)
+        if first:  # another call has begun meanwhile, as far as it gets
+            threads.append(threading.Thread(target=lambda: ex(**other)))
+            threads[0].start()
+            threads[0].join(0.3)
+        seen[x] = ref._obj.n
+        return 0
+    ex = host_experts(monkeypatch, call)
+    mine = expert_inputs(2)
+    ex(**mine)
+    threads[0].join()
+    assert seen[mine["x"].data_ptr()] == 2 and seen[other["x"].data_ptr()] == 7

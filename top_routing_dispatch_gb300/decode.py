@@ -261,6 +261,16 @@ class W4Experts:
         self.status = torch.zeros(1, dtype=_I32, device=dev)
         self._w = self.w13_t.data_ptr(), self.w2_t.data_ptr()
         self._tail = (self.ws.data_ptr(), nbytes, self.status.data_ptr())
+        self._refs = {}  # descriptions by token count
+
+    def _ref_for(self, n):
+        """The layer's description for n tokens, which no other call changes."""
+        ref = self._refs.get(n)
+        if ref is None:
+            desc = _lib.LayerDesc.from_buffer_copy(self.desc)
+            desc.n = n
+            ref = self._refs[n] = ctypes.byref(desc)
+        return ref
 
     def __call__(self, x, topk_idx, topk_w, y=None, stream=None):
         """y (n, H) bfloat16 (allocated when not given) for x (n, H) bfloat16
@@ -281,8 +291,7 @@ class W4Experts:
             raise ValueError("y: like x")
         if self._index is None or self._index != _current_device():
             _ready(self.device)
-        self.desc.n = n
-        st = self._call(self._ref, self.group, x.data_ptr(), topk_idx.data_ptr(),
+        st = self._call(self._ref_for(n), self.group, x.data_ptr(), topk_idx.data_ptr(),
                         topk_w.data_ptr(), *self._w, y.data_ptr(), *self._tail,
                         _handle(stream, self._index))
         if st:
