@@ -601,7 +601,9 @@ moe_status_t moe_prepare_weights_w4(const moe_layer_desc_t *desc, int group, con
  *   GEMMs are the better path.  An expert id outside [0, E) contributes
  *   nothing and sets MOE_DEV_BAD_ROUTING (status_word may be NULL).
  *   ws: moe_experts_w4_workspace_size(desc) bytes, 256-byte aligned, contents
- *   need no initialisation.
+ *   need no initialisation.  A call is two or three kernels that hand results
+ *   on in ws: calls that may run at the same time, or that host threads may
+ *   enqueue at the same time, need a workspace each.
  */
 size_t moe_experts_w4_workspace_size(const moe_layer_desc_t *desc);
 moe_status_t moe_experts_w4(const moe_layer_desc_t *desc, int group, const void *x,

@@ -360,3 +360,23 @@ def test_two_threads_keep_their_token_counts(lib, monkeypatch):
     ex(**mine)
     threads[0].join()
     assert seen[mine["x"].data_ptr()] == 2 and seen[other["x"].data_ptr()] == 7
+
+
+def test_expert_calls_of_two_threads_do_not_interleave(lib, monkeypatch):
+    """A call is two or three kernels on one workspace: another thread's must not
+    come between them."""
+    inside, most, gate = [0], [0], threading.Event()
+
+    def call(*a):
+        inside[0] += 1
+        most[0] = max(most[0], inside[0])
+        gate.wait(0.1)
+        inside[0] -= 1
+        return 0
+    ex = host_experts(monkeypatch, call)
+    threads = [threading.Thread(target=lambda: ex(**expert_inputs(3))) for _ in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert most[0] == 1

@@ -3,6 +3,7 @@ forms: steep softmaxes, shared workspaces, very long sequences and pages,
 values near the limits of their types, streams."""
 import ctypes
 import math
+import threading
 
 import pytest
 import torch
@@ -270,3 +271,29 @@ def test_quantize_keeps_non_finite_weights_visible(bad):
         s[at] = s0[at]
         q[e, c, g * words:(g + 1) * words] = q0[e, c, g * words:(g + 1) * words]
         assert torch.equal(q, q0) and torch.equal(s, s0)
+
+
+# ------------------------------------------------------- threads and streams
+def test_experts_object_shared_by_threads():
+    """Threads with token counts of their own call one object on one stream."""
+    H, I, E, K = 256, 128, 8, 2
+    ex = T.M().W4Experts(*T.make_w4(E, H, I, 64, 1), K=K, max_tokens=64)
+    work = []
+    for i, n in enumerate((1, 3, 40, 64)):
+        x = torch.randn((n, H), generator=T.gen(i)).bfloat16().cuda()
+        idx, tw = T.routing(n, E, K, 10 + i)
+        work.append((x, idx, tw, ex(x, idx, tw).clone(), []))
+    torch.cuda.synchronize()
+
+    def calls(x, idx, tw, want, got):
+        for _ in range(30):
+            got.append(ex(x, idx, tw))
+    threads = [threading.Thread(target=calls, args=w) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    ex.check()
+    for *_, want, got in work:
+        assert len(got) == 30 and all(torch.equal(want, g) for g in got)

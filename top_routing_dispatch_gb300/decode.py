@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import threading
 
 import torch
 
@@ -262,6 +263,9 @@ class W4Experts:
         self._w = self.w13_t.data_ptr(), self.w2_t.data_ptr()
         self._tail = (self.ws.data_ptr(), nbytes, self.status.data_ptr())
         self._refs = {}  # descriptions by token count
+        # a call is two or three kernels on one workspace: threads' calls enter the
+        # stream one after another
+        self._lock = threading.Lock()
 
     def _ref_for(self, n):
         """The layer's description for n tokens, which no other call changes."""
@@ -291,9 +295,10 @@ class W4Experts:
             raise ValueError("y: like x")
         if self._index is None or self._index != _current_device():
             _ready(self.device)
-        st = self._call(self._ref_for(n), self.group, x.data_ptr(), topk_idx.data_ptr(),
-                        topk_w.data_ptr(), *self._w, y.data_ptr(), *self._tail,
-                        _handle(stream, self._index))
+        with self._lock:
+            st = self._call(self._ref_for(n), self.group, x.data_ptr(), topk_idx.data_ptr(),
+                            topk_w.data_ptr(), *self._w, y.data_ptr(), *self._tail,
+                            _handle(stream, self._index))
         if st:
             raise MoEError(st, "moe_experts_w4")
         return y
