@@ -1,6 +1,7 @@
 """Refusals of the serving calls: every bad argument is answered before any
 CUDA call, through the C ABI (fake pointers, never dereferenced) and through
 the Python classes (CPU tensors).  No GPU needed."""
+import contextlib
 import ctypes
 import math
 import os
@@ -380,3 +381,74 @@ def test_expert_calls_of_two_threads_do_not_interleave(lib, monkeypatch):
     for t in threads:
         t.join()
     assert most[0] == 1
+
+
+class FakeStream:
+    """Stands for torch's stream objects where there is no GPU."""
+    waits, recorded, capturing, inside = [], [], False, []
+
+    def __init__(self, handle, device=None):
+        self.cuda_stream = handle
+
+    def wait_event(self, event):
+        FakeStream.waits.append((self.cuda_stream, event))
+
+
+@pytest.fixture
+def fake_streams(monkeypatch):
+    from top_routing_dispatch_gb300 import decode
+    FakeStream.waits, FakeStream.recorded, FakeStream.capturing = [], [], False
+
+    @contextlib.contextmanager
+    def use(stream):
+        FakeStream.inside.append(stream.cuda_stream)
+        yield
+        FakeStream.inside.pop()
+    monkeypatch.setattr(torch.cuda, "ExternalStream", FakeStream)
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: FakeStream(0))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: FakeStream.capturing)
+    monkeypatch.setattr(torch.Tensor, "record_stream",
+                        lambda t, s: FakeStream.recorded.append((t.data_ptr(), s.cuda_stream)))
+    monkeypatch.setattr(decode, "_ready", lambda device: None)
+    monkeypatch.setattr(decode, "_handle", lambda stream, index: stream or 0)
+
+
+def test_each_stream_has_a_workspace_of_its_own(lib, monkeypatch, fake_streams):
+    """Two calls on two streams may run at the same time, and a stream's first
+    call waits for what the constructor enqueued."""
+    c = make()
+    q, lens = torch.zeros((3, 4, 64), dtype=BF16), torch.ones(3, dtype=torch.int32)
+    used = []
+    c._attend = lambda *a: used.append((a[-1], a[8])) or 0
+    for s in (None, 5, 6, 5, None, 6):
+        c.attend(q, lens, out=q.clone(), stream=s)
+    by = dict(used)
+    assert len(set(by.values())) == 3 and used == [(s, by[s]) for s in (0, 5, 6, 5, 0, 6)]
+    assert [s for s, _ in FakeStream.waits] == [5, 6]
+    ints, kv3 = torch.zeros(3, dtype=torch.int32), torch.zeros((3, 2, 64), dtype=BF16)
+    c._append = lambda *a: 0
+    c.append(None, kv3, kv3, ints, ints, stream=7)  # its status word is the constructor's
+    assert [s for s, _ in FakeStream.waits] == [5, 6, 7]
+    assert (c.status.data_ptr(), 7) in FakeStream.recorded
+
+    used.clear()
+    ex = host_experts(monkeypatch, lambda *a: used.append((a[-1], a[8])) or 0)
+    for s in (None, 5, 6, 5, None, 6):
+        ex(**expert_inputs(3), stream=s)
+    by = dict(used)
+    assert len(set(by.values())) == 3 and used == [(s, by[s]) for s in (0, 5, 6, 5, 0, 6)]
+    assert (ex.w13_t.data_ptr(), 5) in FakeStream.recorded
+
+
+def test_a_capture_uses_the_first_workspace(lib, fake_streams):
+    c = make()
+    q, lens = torch.zeros((3, 4, 64), dtype=BF16), torch.ones(3, dtype=torch.int32)
+    used = []
+    c._attend = lambda *a: used.append(a[8]) or 0
+    FakeStream.capturing = True
+    c.attend(q, lens, out=q.clone(), stream=9)
+    assert used == [c.ws.data_ptr()] and FakeStream.waits == []
+    FakeStream.capturing = False
+    c.attend(q, lens, out=q.clone(), stream=9)
+    assert used[1] != used[0]

@@ -297,3 +297,61 @@ def test_experts_object_shared_by_threads():
     ex.check()
     for *_, want, got in work:
         assert len(got) == 30 and all(torch.equal(want, g) for g in got)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "f32"])
+def test_attend_on_two_streams_at_once(kind):
+    """Calls of one cache on two streams, with lengths of their own."""
+    cache, q, n, _, _ = T.attend_case((kind, 8, 4, 128, 16, 0, (3000, 40, 7000)))
+    cases = [(q, n), (q + 1, torch.tensor([500, 0, 6001], dtype=torch.int32, device="cuda"))]
+    want = [cache.attend(*c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    outs = [[torch.empty_like(q) for _ in range(25)] for _ in cases]
+    for i in range(25):
+        for c, s, o in zip(cases, streams, outs):
+            cache.attend(*c, out=o[i], stream=s)
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(w, x) for x in o)
+    assert torch.equal(cache.attend(*cases[0]), want[0])
+    cache.check()
+
+
+def test_experts_on_two_streams_at_once():
+    H, I, E, K = 1024, 512, 16, 4
+    ex = T.M().W4Experts(*T.make_w4(E, H, I, 64, 1), K=K, max_tokens=60)
+    cases = []
+    for i, n in enumerate((60, 5)):
+        x = torch.randn((n, H), generator=T.gen(i)).bfloat16().cuda()
+        cases.append((x, *T.routing(n, E, K, 10 + i)))
+    want = [ex(*c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    outs = [[torch.empty_like(c[0]) for _ in range(25)] for c in cases]
+    for i in range(25):
+        for c, s, o in zip(cases, streams, outs):
+            ex(*c, y=o[i], stream=s)
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(w, x) for x in o)
+    ex.check()
+
+
+def test_first_call_on_another_stream_waits_for_the_constructor():
+    H, I, E, K, n = 2048, 1024, 64, 8, 2
+    w = T.make_w4(E, H, I, 128, 1)
+    x = torch.randn((n, H), generator=T.gen(2)).bfloat16().cuda()
+    idx, tw = T.routing(n, E, K, 3)
+    want = T.M().W4Experts(*w, K=K, max_tokens=n)(x, idx, tw)
+    cache, q, lens, _, _ = T.attend_case(("bf16", 16, 16, 128, 16, 0, (5000,)))
+    rows = cache.attend(q, lens)
+    table = cache.page_table
+    for _ in range(3):
+        s, y, o = torch.cuda.Stream(), torch.empty_like(x), torch.empty_like(q)
+        torch.cuda.synchronize()
+        T.M().W4Experts(*w, K=K, max_tokens=n)(x, idx, tw, y=y, stream=s)
+        T.M().PagedKVCache(cache.k_cache, cache.v_cache, table, 16).attend(q, lens, out=o, stream=s)
+        s.synchronize()
+        assert torch.equal(y, want) and torch.equal(o, rows)
+        torch.cuda.synchronize()

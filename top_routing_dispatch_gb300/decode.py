@@ -53,6 +53,39 @@ def _handle(stream, index):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+class _Workspaces:
+    """A workspace for each stream that an object's calls run on, so that calls
+    on several streams may run at the same time.
+
+    make() allocates one on the current stream; `kept` are the object's other
+    tensors, filled on the stream that is current now.  Another stream's first
+    call waits for that.  A call under stream capture on a stream that has no
+    workspace yet uses the first one (memory allocated by a capture belongs to
+    its graph)."""
+
+    def __init__(self, device, make, kept):
+        self._device, self._make, self._kept = device, make, kept
+        self.all = [make()]
+        self._made, handle = None, 0
+        if device.type == "cuda":
+            stream = torch.cuda.current_stream(device)
+            self._made, handle = stream.record_event(), stream.cuda_stream
+        self.pointers = {handle: self.all[0].data_ptr()}  # by stream handle
+
+    def add(self, handle):
+        """The workspace of a stream's first call."""
+        stream = torch.cuda.ExternalStream(handle, device=self._device)
+        with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return self.all[0].data_ptr()
+            stream.wait_event(self._made)
+            ws = self._make()
+        for t in self._kept:
+            t.record_stream(stream)
+        self.all.append(ws)
+        return self.pointers.setdefault(handle, ws.data_ptr())
+
+
 def rope_table(rows: int, dim: int, base: float = 10000.0, device="cuda"):
     """(rows, dim) float32: for each position the cosines and then the sines of
     its dim/2 angles position * base^(-2i/dim), evaluated in float64."""
@@ -71,6 +104,11 @@ class PagedKVCache:
     rope_table, or None.  All are the caller's and are kept alive here; the
     page table may be changed in place between calls.  Queries, keys, values
     and results are bfloat16 (float32 for a float32 cache).
+
+    Calls run on `stream`, or the current stream; each stream has a workspace
+    of its own.  Calls captured in graphs share the workspace of the stream on
+    which the object was made: replays are ordered with each other and with
+    that stream's calls by the caller.
     """
 
     def __init__(self, k_cache, v_cache, page_table, q_heads, k_scale=None, v_scale=None,
@@ -112,9 +150,12 @@ class PagedKVCache:
         if nbytes == 0:  # the library's own reason
             _check(self._attend(self._ref, None, 0, None, 0, 1.0, None, None, None, 0, None, None),
                    "PagedKVCache")
-        self.ws = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
         self.status = torch.zeros(1, dtype=_I32, device=dev)
-        self._ws, self._nbytes, self._status = self.ws.data_ptr(), nbytes, self.status.data_ptr()
+        self._nbytes, self._status = nbytes, self.status.data_ptr()
+        self._streams = _Workspaces(
+            dev, lambda: torch.zeros(nbytes, dtype=torch.uint8, device=dev), [self.status])
+        self.ws = self._streams.all[0]
+        self._pointers = self._streams.pointers
 
     def _heads(self, t, rows, heads, name):
         """Pointer and token stride of a (rows, heads, head_dim) tensor whose
@@ -155,8 +196,10 @@ class PagedKVCache:
             _want(q_out is None, "q_out without q")
         if self._index is None or self._index != _current_device():
             _ready(self.device)
-        st = self._append(self._ref, n, qp, qs, kp, ks, vp, vs, sp, pp, op, self._status,
-                          _handle(stream, self._index))
+        handle = _handle(stream, self._index)
+        if handle not in self._pointers:
+            self._streams.add(handle)  # for the status word
+        st = self._append(self._ref, n, qp, qs, kp, ks, vp, vs, sp, pp, op, self._status, handle)
         if st:
             raise MoEError(st, "moe_kv_append")
         return q_out
@@ -180,16 +223,18 @@ class PagedKVCache:
             raise ValueError(f"lse: contiguous ({B}, {self.q_heads}) float32 on {self.device}")
         if self._index is None or self._index != _current_device():
             _ready(self.device)
+        handle = _handle(stream, self._index)
         st = self._attend(self._ref, qp, qs, lp, window, self._scale if scale is None else scale,
-                          op, None if lse is None else lse.data_ptr(), self._ws, self._nbytes,
-                          self._status, _handle(stream, self._index))
+                          op, None if lse is None else lse.data_ptr(),
+                          self._pointers.get(handle) or self._streams.add(handle), self._nbytes,
+                          self._status, handle)
         if st:
             raise MoEError(st, "moe_paged_attention")
         return out
 
     def check(self, stream=None):
-        """Waits for the stream and raises MoEError if a call met a sequence,
-        position or page out of range."""
+        """Waits for the stream (the calls' one) and raises MoEError if a call
+        met a sequence, position or page out of range."""
         _ready(self.device)
         _check(int(_lib.load().moe_check_status(_p(self.status), _stream(stream))),
                "device status")
@@ -226,7 +271,12 @@ class W4Experts:
     w13_q (E, 2I, H/8) and w2_q (E, H, I/8) int32 codes, w13_s (E, 2I,
     H/group) and w2_s (E, H, I/group) bfloat16 scales (quantize_weights_w4, or
     a checkpoint's own codes in the packing that include/moe.h gives).
-    K: experts per token."""
+    K: experts per token.
+
+    Calls run on `stream`, or the current stream; each stream has a workspace
+    of its own.  Calls captured in graphs share the workspace of the stream on
+    which the object was made: replays are ordered with each other and with
+    that stream's calls by the caller."""
 
     def __init__(self, w13_q, w13_s, w2_q, w2_s, K, max_tokens):
         _want(all(t.dim() == 3 and t.is_contiguous() for t in (w13_q, w13_s, w2_q, w2_s)),
@@ -258,10 +308,14 @@ class W4Experts:
         _check(lib.moe_prepare_weights_w4(
             self._ref, group, _p(w13_q), _p(w13_s), _p(w2_q), _p(w2_s), _p(self.w13_t),
             _p(self.w2_t), _handle(None, self._index)), "moe_prepare_weights_w4")
-        self.ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
         self.status = torch.zeros(1, dtype=_I32, device=dev)
+        self._streams = _Workspaces(
+            dev, lambda: torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev),
+            [self.w13_t, self.w2_t, self.status])
+        self.ws = self._streams.all[0]
+        self._pointers = self._streams.pointers
         self._w = self.w13_t.data_ptr(), self.w2_t.data_ptr()
-        self._tail = (self.ws.data_ptr(), nbytes, self.status.data_ptr())
+        self._nbytes, self._status = nbytes, self.status.data_ptr()
         self._refs = {}  # descriptions by token count
         # a call is two or three kernels on one workspace: threads' calls enter the
         # stream one after another
@@ -295,17 +349,19 @@ class W4Experts:
             raise ValueError("y: like x")
         if self._index is None or self._index != _current_device():
             _ready(self.device)
+        handle = _handle(stream, self._index)
+        ws = self._pointers.get(handle) or self._streams.add(handle)
         with self._lock:
             st = self._call(self._ref_for(n), self.group, x.data_ptr(), topk_idx.data_ptr(),
-                            topk_w.data_ptr(), *self._w, y.data_ptr(), *self._tail,
-                            _handle(stream, self._index))
+                            topk_w.data_ptr(), *self._w, y.data_ptr(), ws, self._nbytes,
+                            self._status, handle)
         if st:
             raise MoEError(st, "moe_experts_w4")
         return y
 
     def check(self, stream=None):
-        """Waits for the stream and raises MoEError if a call met an expert id
-        out of range."""
+        """Waits for the stream (the calls' one) and raises MoEError if a call
+        met an expert id out of range."""
         _ready(self.device)
         _check(int(_lib.load().moe_check_status(_p(self.status), _stream(stream))),
                "device status")
