@@ -452,3 +452,18 @@ def test_a_capture_uses_the_first_workspace(lib, fake_streams):
     FakeStream.capturing = False
     c.attend(q, lens, out=q.clone(), stream=9)
     assert used[1] != used[0]
+
+
+def test_results_are_allocated_on_the_calls_stream(lib, monkeypatch, fake_streams):
+    made = []
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: made.append(list(FakeStream.inside)) or empty(*a, **k))
+    c = make()
+    q, lens = torch.zeros((3, 4, 64), dtype=BF16), torch.ones(3, dtype=torch.int32)
+    ints, kv3 = torch.zeros(3, dtype=torch.int32), torch.zeros((3, 2, 64), dtype=BF16)
+    c._attend = c._append = lambda *a: 0
+    for call in (lambda: c.attend(q, lens, stream=5),
+                 lambda: c.append(q, kv3, kv3, ints, ints, stream=5)):
+        made.clear()
+        t = call()
+        assert made == [[5]] and (t.data_ptr(), 0) in FakeStream.recorded

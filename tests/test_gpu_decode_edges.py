@@ -355,3 +355,32 @@ def test_first_call_on_another_stream_waits_for_the_constructor():
         s.synchronize()
         assert torch.equal(y, want) and torch.equal(o, rows)
         torch.cuda.synchronize()
+
+
+def test_results_of_a_side_stream_spare_the_current_streams_memory():
+    """A result that a call on another stream allocates is not in memory that
+    the current stream's work still uses."""
+    cache, q, n, _, _ = T.attend_case(("bf16", 8, 4, 128, 16, 0, (90, 300, 7)))
+    want = cache.attend(q, n)
+    s = torch.cuda.Stream()
+    big = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(5):
+        old = torch.full_like(want, 3.0)
+        for _ in range(20):
+            big.add_(1)  # holds the current stream up
+        kept = old + 1
+        del old          # free for the current stream, which has yet to read it
+        out = cache.attend(q, n, stream=s)
+        torch.cuda.synchronize()
+        assert (kept == 4).all() and torch.equal(out, want)
+    codes = T.M().quantize_weights_w4(*(torch.randn((2, 128, m), generator=T.gen(1)).bfloat16().cuda()
+                                        for m in (256, 128)), group=64)
+    ex = T.M().W4Experts(*codes, K=1, max_tokens=4)
+    x = torch.randn((4, 128), generator=T.gen(2)).bfloat16().cuda()
+    idx, tw = T.routing(4, 2, 1, 3)
+    want = ex(x, idx, tw)
+    torch.cuda.synchronize()
+    got = ex(x, idx, tw, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)

@@ -53,6 +53,19 @@ def _handle(stream, index):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory for a result that a call on `stream` (None: the current one) writes:
+    the allocator's reuse of it is ordered on that stream, and waits for the
+    current one, where the result is used."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(_handle(stream, None), device=device)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
+
+
 class _Workspaces:
     """A workspace for each stream that an object's calls run on, so that calls
     on several streams may run at the same time.
@@ -106,7 +119,8 @@ class PagedKVCache:
     and results are bfloat16 (float32 for a float32 cache).
 
     Calls run on `stream`, or the current stream; each stream has a workspace
-    of its own.  Calls captured in graphs share the workspace of the stream on
+    of its own, and a result allocated by a call is ready for that stream's
+    next work.  Calls captured in graphs share the workspace of the stream on
     which the object was made: replays are ordered with each other and with
     that stream's calls by the caller.
     """
@@ -174,6 +188,11 @@ class PagedKVCache:
             raise ValueError(f"{name}: contiguous ({n},) int32 on {self.device}")
         return t.data_ptr()
 
+    def _result(self, rows, stream):
+        if self._index is None or self._index != _current_device():
+            _ready(self.device)
+        return _empty((rows, self.q_heads, self.head_dim), self.dtype, self.device, stream)
+
     def append(self, q, k, v, seq_ids, positions, q_out=None, stream=None):
         """Rotates q and k by position, writes k and v into the cache, returns
         the rotated q (in q_out, allocated when not given; q_out may be q).
@@ -188,8 +207,7 @@ class PagedKVCache:
         if q is not None:
             qp, qs = self._heads(q, n, self.q_heads, "q")
             if q_out is None:
-                q_out = torch.empty((n, self.q_heads, self.head_dim), dtype=self.dtype,
-                                    device=self.device)
+                q_out = self._result(n, stream)
             op, os = self._heads(q_out, n, self.q_heads, "q_out")
             _want(n < 2 or os == self.q_heads * self.head_dim, "q_out: contiguous")
         else:
@@ -214,8 +232,7 @@ class PagedKVCache:
         qp, qs = self._heads(q, B, self.q_heads, "q")
         lp = self._ints(seq_lens, B, "seq_lens")
         if out is None:
-            out = torch.empty((B, self.q_heads, self.head_dim), dtype=self.dtype,
-                              device=self.device)
+            out = self._result(B, stream)
         op, os = self._heads(out, B, self.q_heads, "out")
         _want(B < 2 or os == self.q_heads * self.head_dim, "out: contiguous")
         if lse is not None and (lse.dtype is not _F32 or lse.shape != (B, self.q_heads)
@@ -250,13 +267,13 @@ def quantize_weights_w4(w13, w2, group=128, stream=None):
     I = I2 // 2
     _want(w2.shape == (E, I, H) and I2 == 2 * I, "w13 (E, H, 2I) and w2 (E, I, H)")
     _want(group > 0, "group: 32, 64 or 128")
-    new = lambda shape, dt: torch.empty(shape, dtype=dt, device=w13.device)  # noqa: E731
-    out = (new((E, 2 * I, H // 8), _I32), new((E, 2 * I, H // group), _BF16),
-           new((E, H, I // 8), _I32), new((E, H, I // group), _BF16))
     lib, desc = _lib.load(), make_desc(0, H, I, E, 1, _BF16, False)
     refused = lib.moe_w4_tiled_bytes(ctypes.byref(desc), int(group), 0) == 0
     if not refused:
         _ready(w13.device)
+    new = lambda shape, dt: _empty(shape, dt, w13.device, None if refused else stream)  # noqa: E731
+    out = (new((E, 2 * I, H // 8), _I32), new((E, 2 * I, H // group), _BF16),
+           new((E, H, I // 8), _I32), new((E, H, I // group), _BF16))
     _check(lib.moe_quantize_weights_w4(
         ctypes.byref(desc), int(group), _p(w13), _p(w2), *[_p(t) for t in out],
         None if refused else _handle(stream, w13.device.index)), "moe_quantize_weights_w4")
@@ -274,7 +291,8 @@ class W4Experts:
     K: experts per token.
 
     Calls run on `stream`, or the current stream; each stream has a workspace
-    of its own.  Calls captured in graphs share the workspace of the stream on
+    of its own, and a result allocated by a call is ready for that stream's
+    next work.  Calls captured in graphs share the workspace of the stream on
     which the object was made: replays are ordered with each other and with
     that stream's calls by the caller."""
 
@@ -343,7 +361,9 @@ class W4Experts:
                     or t.device != self.device):
                 raise ValueError(f"{name}: contiguous ({n}, {self.K}) {dt} on {self.device}")
         if y is None:
-            y = torch.empty_like(x)
+            if self._index is None or self._index != _current_device():
+                _ready(self.device)
+            y = _empty(x.shape, _BF16, self.device, stream)
         elif (y.dtype is not _BF16 or y.shape != x.shape or not y.is_contiguous()
               or y.device != self.device):
             raise ValueError("y: like x")
