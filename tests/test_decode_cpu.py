@@ -467,3 +467,11 @@ def test_results_are_allocated_on_the_calls_stream(lib, monkeypatch, fake_stream
         made.clear()
         t = call()
         assert made == [[5]] and (t.data_ptr(), 0) in FakeStream.recorded
+
+
+@pytest.mark.parametrize("bad", [None, P + 2, P + 8])
+@pytest.mark.parametrize("i", range(6))
+def test_weight_preparation_refuses_null_and_misaligned_pointers(lib, i, bad):
+    d, args = desc(), [bad if j == i else P for j in range(6)]
+    assert lib.moe_prepare_weights_w4(ctypes.byref(d), 64, *args, None) == INVALID
+    assert lib.moe_quantize_weights_w4(ctypes.byref(d), 64, *args, None) == INVALID
