@@ -384,3 +384,21 @@ def test_results_of_a_side_stream_spare_the_current_streams_memory():
     got = ex(x, idx, tw, stream=s)
     s.synchronize()
     assert torch.equal(got, want)
+
+
+def test_objects_made_on_a_side_stream_serve_the_default_one():
+    _, q, n, _, _ = made = T.attend_case(("bf16", 8, 4, 128, 16, 0, (90, 3000, 7)))
+    w = T.make_w4(4, 256, 128, 64, 1)
+    x = torch.randn((3, 256), generator=T.gen(1)).bfloat16().cuda()
+    idx, tw = T.routing(3, 4, 2, 3)
+    rows, y = made[0].attend(q, n), T.M().W4Experts(*w, K=2, max_tokens=3)(x, idx, tw)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        cache = T.M().PagedKVCache(made[0].k_cache, made[0].v_cache, made[0].page_table, 8)
+        ex = T.M().W4Experts(*w, K=2, max_tokens=3)
+    for stream in (None, 0, torch.cuda.default_stream()):
+        assert torch.equal(cache.attend(q, n, stream=stream), rows)
+        assert torch.equal(ex(x, idx, tw, stream=stream), y)
+    assert len(cache._pointers) == 2 and len(ex._pointers) == 2
+    cache.check()
+    ex.check()
