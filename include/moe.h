@@ -597,9 +597,8 @@ moe_status_t moe_prepare_weights_w4(const moe_layer_desc_t *desc, int group, con
  * Results are bitwise reproducible.
  *   x (n,H) bf16, topk_idx (n,K) int32, topk_w (n,K) float32, y (n,H) bf16;
  *   w13_t, w2_t from moe_prepare_weights_w4 with the same group;
- *   n * K <= 4096 (else MOE_ERR_UNSUPPORTED): above that the bf16 grouped
- *   GEMMs are the better path.  An expert id outside [0, E) contributes
- *   nothing and sets MOE_DEV_BAD_ROUTING (status_word may be NULL).
+ *   n * K <= 4096 (else MOE_ERR_UNSUPPORTED).  An expert id outside [0, E)
+ *   contributes nothing and sets MOE_DEV_BAD_ROUTING (status_word may be NULL).
  *   ws: moe_experts_w4_workspace_size(desc) bytes, 256-byte aligned, contents
  *   need no initialisation.  A call is two or three kernels that hand results
  *   on in ws: calls that may run at the same time, or that host threads may

@@ -36,10 +36,11 @@
 //
 // Measured (cached bytes read once, of a copy rate of 6.7 TB/s): 62 sequences of
 // 17 to 8191 tokens, 16/16 heads of 128, bf16: 111 us, 6.3 TB/s, 93 %; 128 of
-// 500 to 12001, 64/8 heads, e4m3: 157 us, 6.1 TB/s; one of 131071, 32/4 heads,
+// 500 to 12001, 64/8 heads, e4m3: 156 us, 6.1 TB/s (issue slots 57 % busy: the
+// conversions of K and V and V's second product); one of 131071, 32/4 heads,
 // bf16: 53 us, 5.0 TB/s, of which start and join take 11; one of 137 tokens: 7 us,
 // the chain length, page, rows, exchange; a window of 2000 over 11 sequences,
-// float32, 12/4 heads of 64: 14 us (bf16: 10).
+// float32, 12/4 heads of 64: 15 us (bf16: 11).
 #include <cuda_fp16.h>
 
 #include "kv_cache.cuh"
@@ -463,7 +464,8 @@ struct MmaPath {
 // of them computed (those beyond the item's are of zeros), so that the heads'
 // chains overlap and a call fetches no more code than its heads need (24
 // sequences of 6500 tokens, 12/4 heads of 64: 46 us, against 65 with code for 8
-// that left at the item's last head; 10/2 heads: 42 against 50).
+// that left at the item's last head; 10/2 heads: 42 against 50; one set of inputs,
+// part of which stays in L2: three sets in turn take 58 and 51).
 // ---------------------------------------------------------------------------
 template <int D_, int NH_>
 struct FmaPath {
