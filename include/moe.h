@@ -76,7 +76,7 @@ typedef enum {
 #define MOE_DEV_BAD_CACHE 0x8
 
 /* MOE_E4M3 (8-bit float, 4 exponent bits, largest value 448) is a type of
- * key-value caches only. */
+ * key-value caches and of optimizer states only. */
 typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_E4M3 = 2 } moe_dtype_t;
 
 /*
@@ -609,6 +609,155 @@ moe_status_t moe_experts_w4(const moe_layer_desc_t *desc, int group, const void 
                             const int32_t *topk_idx, const float *topk_w, const void *w13_t,
                             const void *w2_t, void *y, void *ws, size_t ws_bytes,
                             int32_t *status_word, moe_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Training: what stands around moe_backward in a training step.
+ *
+ * The norm before the layer with its gradients, the global norm of all
+ * gradients, and the AdamW step that takes them.  Pointers of these calls need
+ * the alignment of their element type only; 16-byte aligned rows and tensors
+ * are read in wide pieces.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Layer norm of n rows of H values.
+ *   dtype: of the rows (MOE_F32 or MOE_BF16); weight_dtype: of weight and bias,
+ *   MOE_F32 or dtype.  rms nonzero: the root mean square form, in which the
+ *   mean is taken as 0.  eps finite and at least 0.  H at most 2^20 (else
+ *   MOE_ERR_UNSUPPORTED).
+ */
+typedef struct {
+  int32_t n;            /* rows (may be 0) */
+  int32_t H;            /* values of a row */
+  int32_t dtype;        /* moe_dtype_t */
+  int32_t weight_dtype; /* moe_dtype_t */
+  int32_t rms;
+  float eps;
+} moe_norm_t;
+
+/*
+ * For each row, in float32:
+ *   s = x + residual, rounded to dtype (s = x where residual is NULL)
+ *   mu = sum s / H (0 if rms);  r = 1 / sqrt(sum (s - mu)^2 / H + eps)
+ *   y = (s - mu) r weight + bias, rounded once
+ * The mean is subtracted before the squares are summed.  A row whose squares
+ * pass float32 gives y = bias; a NaN or infinity stays in its row.
+ *   x, residual (n, H): rows x_stride and residual_stride elements apart (at
+ *   least H; not looked at where n < 2); s, y (n, H) contiguous; weight (H),
+ *   bias (H) or NULL; s is written where residual is given, and NULL
+ *   otherwise; stats (2, n) float32 or NULL: the means (0 if rms), then the r.
+ * Outputs must not overlap inputs or each other.
+ */
+moe_status_t moe_layer_norm(const moe_norm_t *desc, const void *x, int64_t x_stride,
+                            const void *residual, int64_t residual_stride, const void *weight,
+                            const void *bias, void *s, void *y, float *stats,
+                            moe_stream_t stream);
+
+/*
+ * Gradients of moe_layer_norm for dy = dL/dy, from the rows s that it
+ * normalised and their stats:
+ *   xh = (s - mu) r;  t = dy weight
+ *   dx = r (t - sum t / H (0 if rms) - xh sum(t xh) / H) + ds, rounded once
+ *   dweight = sum over the rows of dy xh;  dbias = sum over the rows of dy
+ * dx is the gradient of x and of residual alike; ds, where not NULL, is the
+ * gradient that reaches s by other ways (the residual stream).
+ *   dy, s, ds (n, H): rows a stride apart as above; dx (n, H) contiguous;
+ *   dweight, dbias (H) float32, overwritten (dbias may be NULL); n = 0 gives
+ *   zeros.  ws: moe_layer_norm_backward_workspace_size(desc) bytes, 16-byte
+ *   aligned, contents need no initialisation; calls that may run at the same
+ *   time need a workspace each.
+ * Every sum has a fixed order: results are bitwise reproducible on one GPU.
+ * Outputs must not overlap inputs or each other.
+ */
+size_t moe_layer_norm_backward_workspace_size(const moe_norm_t *desc);
+moe_status_t moe_layer_norm_backward(const moe_norm_t *desc, const void *dy, int64_t dy_stride,
+                                     const void *s, int64_t s_stride, const float *stats,
+                                     const void *weight, const void *ds, int64_t ds_stride,
+                                     void *dx, float *dweight, float *dbias, void *ws,
+                                     size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * Global norm of gradients: norm = sqrt(sum of g^2 over all values of all
+ * tensors), factor = min(1, max_norm / (norm + 1e-6)).  Squares are float32
+ * (a value beyond 1.8e19 makes the norm infinite and the factor 0), their sum
+ * double in a fixed order.  A NaN gives NaN for both.
+ *   tensors: host array of `count` descriptions, read during the call; data
+ *   numel contiguous values of dtype (MOE_F32 or MOE_BF16; NULL where numel is
+ *   0).  At most 65536 tensors of 2^40 values in all (else
+ *   MOE_ERR_UNSUPPORTED).  max_norm above 0, may be infinite.
+ *   norm, factor: one float32 each (device).  ws:
+ *   moe_grad_norm_workspace_size(count) bytes, 256-byte aligned, contents need
+ *   no initialisation; calls that may run at the same time need one each.
+ */
+typedef struct {
+  const void *data;
+  int64_t numel;
+  int32_t dtype; /* moe_dtype_t */
+} moe_tensor_t;
+
+size_t moe_grad_norm_workspace_size(int32_t count);
+moe_status_t moe_grad_norm(const moe_tensor_t *tensors, int32_t count, float max_norm,
+                           float *norm, float *factor, void *ws, size_t ws_bytes,
+                           moe_stream_t stream);
+
+/*
+ * One AdamW step over many tensors.  For every value, with g = grad times
+ * *grad_scale (where given) and t the number of this step, counted from 1:
+ *   m = beta1 m + (1 - beta1) g;  v = beta2 v + ((1 - beta2) g) g
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in float32; each product and sum of m and v is rounded by itself.  p is the
+ * master where there is one (param becomes its rounding), else param.
+ *
+ * state_dtype MOE_F32: m and v are numel float32.  MOE_E4M3: m and v are numel
+ * e4m3 codes, and m_scale, v_scale ceil(numel / 256) float32; 256 neighbouring
+ * values share a scale:
+ *   m = code * m_scale;  sqrt(v) = code * v_scale
+ *   scale = (1/448) * max(largest finite magnitude of the 256, 2^-100)
+ *   code = value * (1 / scale) rounded to nearest even; a positive sqrt(v) has
+ *   at least the smallest positive code; an infinity or NaN has the NaN code.
+ * The step is taken with m and v before that rounding.  New states are zeros
+ * (codes and scales too).
+ */
+typedef struct {
+  void *param;        /* numel values of dtype */
+  float *master;      /* numel float32, or NULL */
+  const void *grad;   /* numel values of grad_dtype */
+  void *m, *v;
+  float *m_scale, *v_scale; /* MOE_E4M3 states only, else NULL */
+  int64_t numel;
+  int32_t dtype;      /* MOE_F32 or MOE_BF16 */
+  int32_t grad_dtype; /* MOE_F32 or MOE_BF16 */
+  float weight_decay;
+} moe_adamw_tensor_t;
+
+typedef struct {
+  int32_t state_dtype;     /* MOE_F32 or MOE_E4M3 */
+  float lr;
+  const float *lr_device;  /* one float32 (device) that replaces lr, or NULL */
+  const float *grad_scale; /* one float32 (device), or NULL: 1 */
+  double beta1, beta2;     /* at least 0, below 1 */
+  float eps;               /* above 0 */
+} moe_adamw_t;
+
+/*
+ * step_state: MOE_ADAMW_STATE_BYTES of device memory, 16-byte aligned, that
+ * holds the number of steps taken.  moe_adamw_set_steps writes it (steps 0 for
+ * new states) for the betas that the steps will have; moe_adamw_step advances
+ * it on the device, so that a step captured in a CUDA graph counts on when it
+ * is replayed.  Its first 8 bytes are the number, an int64.
+ *   tensors: host array of `count` descriptions, read during the call; no two
+ *   may share memory that the step writes.  At most 65536 tensors of 2^40
+ *   values in all (else MOE_ERR_UNSUPPORTED).  Steps on one step_state or on
+ *   one tensor are ordered by the caller.
+ */
+#define MOE_ADAMW_STATE_BYTES 64
+moe_status_t moe_adamw_set_steps(double beta1, double beta2, int64_t steps, void *step_state,
+                                 moe_stream_t stream);
+moe_status_t moe_adamw_step(const moe_adamw_t *opt, const moe_adamw_tensor_t *tensors,
+                            int32_t count, void *step_state, moe_stream_t stream);
 
 /*
  * Test control for the device timeout path (failure detection without a

@@ -24,6 +24,8 @@ SYMBOLS = (
     "moe_kv_append", "moe_paged_attention_workspace_size", "moe_paged_attention",
     "moe_quantize_weights_w4", "moe_experts_w4_workspace_size", "moe_experts_w4",
     "moe_w4_tiled_bytes", "moe_prepare_weights_w4",
+    "moe_layer_norm", "moe_layer_norm_backward_workspace_size", "moe_layer_norm_backward",
+    "moe_grad_norm_workspace_size", "moe_grad_norm", "moe_adamw_set_steps", "moe_adamw_step",
 )
 
 MOE_F32, MOE_BF16, MOE_E4M3 = 0, 1, 2
@@ -34,6 +36,7 @@ STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "M
 DEV_BAD_ROUTING, DEV_BAD_LAYOUT, DEV_TIMEOUT, DEV_BAD_CACHE = 0x1, 0x2, 0x4, 0x8
 W4_MAX_PAIRS = 4096  # largest n * K of moe_experts_w4
 NOALLOC_MAX_PAIRS = 524288  # MOE_NOALLOC_MAX_PAIRS
+ADAMW_STATE_BYTES = 64  # MOE_ADAMW_STATE_BYTES
 
 # workspace slots of moe_workspace_slot
 SLOT = dict(logits=0, topk_idx=1, topk_w=2, counts=3, offsets=4, perm=5, inv_perm=6,
@@ -56,9 +59,36 @@ class KVCacheDesc(ctypes.Structure):
             "k_cache", "v_cache", "page_table", "k_scale", "v_scale", "rope")]
 
 
+class NormDesc(ctypes.Structure):
+    """moe_norm_t"""
+    _fields_ = [(name, ctypes.c_int32) for name in ("n", "H", "dtype", "weight_dtype", "rms")] + [
+        ("eps", ctypes.c_float)]
+
+
+class TensorDesc(ctypes.Structure):
+    """moe_tensor_t"""
+    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+class AdamWTensor(ctypes.Structure):
+    """moe_adamw_tensor_t"""
+    _fields_ = [(name, ctypes.c_void_p) for name in (
+        "param", "master", "grad", "m", "v", "m_scale", "v_scale")] + [
+        ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+        ("weight_decay", ctypes.c_float)]
+
+
+class AdamWDesc(ctypes.Structure):
+    """moe_adamw_t"""
+    _fields_ = [("state_dtype", ctypes.c_int32), ("lr", ctypes.c_float),
+                ("lr_device", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p),
+                ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_float)]
+
+
 _vp = ctypes.c_void_p
 _desc_p = ctypes.POINTER(LayerDesc)
 _cache_p = ctypes.POINTER(KVCacheDesc)
+_norm_p = ctypes.POINTER(NormDesc)
 _st = ctypes.c_int
 _i32, _i64, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 
@@ -111,6 +141,16 @@ def _declare(lib):
         "moe_w4_tiled_bytes": (_sz, [_desc_p, ctypes.c_int, ctypes.c_int]),
         "moe_prepare_weights_w4": (_st, [_desc_p, ctypes.c_int] + [_vp] * 7),
         "moe_experts_w4": (_st, [_desc_p, ctypes.c_int] + [_vp] * 7 + [_sz, _vp, _vp]),
+        "moe_layer_norm": (_st, [_norm_p, _vp, _i64, _vp, _i64] + [_vp] * 6),
+        "moe_layer_norm_backward_workspace_size": (_sz, [_norm_p]),
+        "moe_layer_norm_backward": (_st, [_norm_p, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64]
+                                    + [_vp] * 4 + [_sz, _vp]),
+        "moe_grad_norm_workspace_size": (_sz, [_i32]),
+        "moe_grad_norm": (_st, [ctypes.POINTER(TensorDesc), _i32, ctypes.c_float, _vp, _vp, _vp,
+                                _sz, _vp]),
+        "moe_adamw_set_steps": (_st, [ctypes.c_double, ctypes.c_double, _i64, _vp, _vp]),
+        "moe_adamw_step": (_st, [ctypes.POINTER(AdamWDesc), ctypes.POINTER(AdamWTensor), _i32,
+                                 _vp, _vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)

@@ -1,0 +1,30 @@
+// Internal declarations of the training operators (layer norm, gradient norm,
+// AdamW): norm.cu, adamw.cu, train_api.cu.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+// ---- norm.cu
+constexpr int kNormMaxH = 1 << 20;  // longest row
+size_t norm_backward_ws_bytes(const moe_norm_t &d);
+cudaError_t launch_norm(const moe_norm_t &d, const void *x, long long x_stride,
+                        const void *residual, long long residual_stride, const void *weight,
+                        const void *bias, void *s, void *y, float *stats, cudaStream_t st);
+cudaError_t launch_norm_backward(const moe_norm_t &d, const void *dy, long long dy_stride,
+                                 const void *s, long long s_stride, const float *stats,
+                                 const void *weight, const void *ds, long long ds_stride, void *dx,
+                                 float *dweight, float *dbias, void *ws, cudaStream_t st);
+
+// ---- adamw.cu
+constexpr int kAdamBlock = 256;  // values of a tensor that share a scale
+size_t grad_norm_ws_bytes(int count);
+cudaError_t launch_grad_norm(const moe_tensor_t *t, int count, float max_norm, float *norm,
+                             float *factor, void *ws, cudaStream_t s);
+cudaError_t launch_adamw_set_steps(double beta1, double beta2, long long steps, void *state,
+                                   cudaStream_t s);
+cudaError_t launch_adamw(const moe_adamw_t &o, const moe_adamw_tensor_t *t, int count, void *state,
+                         cudaStream_t s);
+
+}  // namespace moe

@@ -1,0 +1,320 @@
+"""Python face of the training calls around the layer's backward pass.
+
+LayerNorm is the norm before the layer with its gradients, GradNorm the global
+norm of all gradients, AdamW the step that takes them.  As in api.py the work
+is done by the library's kernels; here arguments are checked and turned into
+pointers.  Tensors are on the current CUDA device, where the library launches.
+
+Calls run on `stream`, or the current stream.  What a call allocates is
+allocated on its stream, scratch included, so calls of one LayerNorm or GradNorm
+may run on several streams at the same time.
+"""
+from __future__ import annotations
+
+import ctypes
+import itertools
+import math
+
+import torch
+
+from . import _lib, decode
+from .api import MoEError, _check, _p
+from .decode import _BF16, _F32, _DT, _empty, _handle, _index, _want, _Workspaces
+
+_E4M3 = torch.float8_e4m3fn
+BLOCK = 256  # values of a tensor that share a scale where states are held in 8 bits
+
+
+def _here(device, index):
+    if index is None or index != decode._current_device():
+        decode._ready(device)
+
+
+class LayerNorm:
+    """Layer norm of rows: y = (s - mean) / sqrt(variance + eps) * weight + bias,
+    or its root mean square form (rms: the mean taken as 0).
+
+    weight, bias: (H,), float32 or of the rows' type; bias may be None.
+    dtype: of the rows, float32 or bfloat16 (weight's type when None).  Both
+    tensors are the caller's and are kept alive here; they may be changed in
+    place between calls."""
+
+    def __init__(self, weight, bias=None, eps=1e-5, rms=False, dtype=None):
+        _want(weight.dim() == 1 and weight.is_contiguous() and weight.dtype in (_F32, _BF16),
+              "weight: contiguous (H,) float32 or bfloat16")
+        _want(bias is None or (bias.shape == weight.shape and bias.dtype == weight.dtype
+                               and bias.is_contiguous() and bias.device == weight.device),
+              "bias: like weight")
+        dtype = weight.dtype if dtype is None else dtype
+        _want(dtype in (_F32, _BF16), "dtype: float32 or bfloat16")
+        self.weight, self.bias, self.dtype, self.H = weight, bias, dtype, weight.shape[0]
+        self.device, self._index = weight.device, _index(weight.device)
+        self._form = (self.H, _DT[dtype], _DT[weight.dtype], int(bool(rms)), float(eps))
+        self._w, self._b = weight.data_ptr(), None if bias is None else bias.data_ptr()
+        lib = _lib.load()
+        self._forward, self._backward = lib.moe_layer_norm, lib.moe_layer_norm_backward
+        self._ws_size = lib.moe_layer_norm_backward_workspace_size
+        if self._ws_size(ctypes.byref(_lib.NormDesc(1, *self._form))) == 0:  # the library's reason
+            _check(self._forward(ctypes.byref(_lib.NormDesc(0, *self._form)), None, 0, None, 0,
+                                 *[None] * 6), "LayerNorm")
+
+    def _rows(self, t, n, name):
+        """Pointer and row stride of a (n, H) tensor whose rows are contiguous."""
+        if (t.dtype is not self.dtype or t.shape != (n, self.H) or t.device != self.device
+                or (t.stride(1) != 1 and self.H != 1)):
+            raise ValueError(f"{name}: ({n}, {self.H}) {self.dtype} on {self.device}, "
+                             "rows contiguous")
+        return t.data_ptr(), t.stride(0)
+
+    def _out(self, t, shape, dtype, name, stream):
+        if t is None:
+            return _empty(shape, dtype, self.device, stream)
+        if (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
+                or t.device != self.device):
+            raise ValueError(f"{name}: contiguous {tuple(shape)} {dtype} on {self.device}")
+        return t
+
+    def __call__(self, x, residual=None, y=None, s=None, stats=None, stream=None):
+        """y (n, H) of the rows x (n, H); with residual (n, H), of s = x +
+        residual, and (y, s) is returned.  y and s are allocated when not
+        given.  stats: (2, n) float32 to fill with means and reciprocal
+        deviations for backward, or None."""
+        _want(x.dim() == 2, "x: (n, H)")
+        n = x.shape[0]
+        xp, xs = self._rows(x, n, "x")
+        rp, rs, sp = None, 0, None
+        _here(self.device, self._index)
+        if residual is not None:
+            rp, rs = self._rows(residual, n, "residual")
+            s = self._out(s, x.shape, self.dtype, "s", stream)
+            sp = s.data_ptr()
+        else:
+            _want(s is None, "s without residual")
+        y = self._out(y, x.shape, self.dtype, "y", stream)
+        tp = None
+        if stats is not None:
+            tp = self._out(stats, (2, n), _F32, "stats", stream).data_ptr()
+        st = self._forward(ctypes.byref(_lib.NormDesc(n, *self._form)), xp, xs, rp, rs, self._w,
+                           self._b, sp, y.data_ptr(), tp, _handle(stream, self._index))
+        if st:
+            raise MoEError(st, "moe_layer_norm")
+        return y if residual is None else (y, s)
+
+    def backward(self, dy, s, stats, ds=None, dx=None, dweight=None, dbias=None, stream=None):
+        """(dx, dweight, dbias) for dy (n, H), from the rows s that were
+        normalised (x, or the sum with the residual) and their stats.  ds (n,
+        H): a gradient that reaches s by other ways, added to dx.  dx is of the
+        rows' type, dweight and dbias (H,) float32 (None without a bias); they
+        are allocated when not given and overwritten."""
+        _want(dy.dim() == 2, "dy: (n, H)")
+        n = dy.shape[0]
+        dp, dst = self._rows(dy, n, "dy")
+        sp, sst = self._rows(s, n, "s")
+        ep, est = (None, 0) if ds is None else self._rows(ds, n, "ds")
+        _here(self.device, self._index)
+        tp = self._out(stats, (2, n), _F32, "stats", stream).data_ptr()
+        dx = self._out(dx, dy.shape, self.dtype, "dx", stream)
+        dweight = self._out(dweight, (self.H,), _F32, "dweight", stream)
+        if self._b is not None:
+            dbias = self._out(dbias, (self.H,), _F32, "dbias", stream)
+        else:
+            _want(dbias is None, "dbias without a bias")
+        ref = ctypes.byref(_lib.NormDesc(n, *self._form))
+        ws, nbytes = None, 0
+        if n:
+            nbytes = self._ws_size(ref)
+            ws = _empty((nbytes,), torch.uint8, self.device, stream)
+        st = self._backward(ref, dp, dst, sp, sst, tp, self._w, ep, est, dx.data_ptr(),
+                            dweight.data_ptr(), None if dbias is None else dbias.data_ptr(),
+                            None if ws is None else ws.data_ptr(), nbytes,
+                            _handle(stream, self._index))
+        if st:
+            raise MoEError(st, "moe_layer_norm_backward")
+        return dx, dweight, dbias
+
+
+def _tensors(ts, name, types=(_F32, _BF16)):
+    """A list of contiguous tensors of one device."""
+    ts = list(ts)
+    _want(len(ts) > 0, f"{name}: at least one tensor")
+    for t in ts:
+        _want(t.dtype in types and t.is_contiguous() and t.device == ts[0].device,
+              f"{name}: contiguous {' or '.join(str(d) for d in types)}, all on one device")
+    return ts
+
+
+def _scalar(t, device, name):
+    """Pointer of one float32 on the device, None for None."""
+    if t is None:
+        return None
+    if t.dtype is not _F32 or t.numel() != 1 or t.device != device:
+        raise ValueError(f"{name}: one float32 on {device}")
+    return t.data_ptr()
+
+
+class GradNorm:
+    """The global norm of a list of gradients, and the factor that clips it.
+
+    grads: contiguous float32 or bfloat16 tensors of one device.  They are the
+    caller's and are kept alive here; a call reads what they hold then."""
+
+    def __init__(self, grads):
+        self.grads = _tensors(grads, "grads")
+        self.device = self.grads[0].device
+        self._index = _index(self.device)
+        self._list = (_lib.TensorDesc * len(self.grads))(
+            *[_lib.TensorDesc(t.data_ptr(), t.numel(), _DT[t.dtype]) for t in self.grads])
+        lib = _lib.load()
+        self._call = lib.moe_grad_norm
+        self._nbytes = lib.moe_grad_norm_workspace_size(len(self.grads))
+
+    def __call__(self, max_norm=float("inf"), norm=None, factor=None, stream=None):
+        """(norm, factor), one float32 each on the device (allocated when not
+        given): the root of the sum of all squares, and min(1, max_norm / (norm
+        + 1e-6)), the grad_scale of a clipped AdamW step."""
+        _here(self.device, self._index)
+        norm = _empty((1,), _F32, self.device, stream) if norm is None else norm
+        factor = _empty((1,), _F32, self.device, stream) if factor is None else factor
+        np_, fp = _scalar(norm, self.device, "norm"), _scalar(factor, self.device, "factor")
+        ws = _empty((max(self._nbytes, 1),), torch.uint8, self.device, stream)
+        st = self._call(self._list, len(self.grads), max_norm, np_, fp, ws.data_ptr(),
+                        self._nbytes, _handle(stream, self._index))
+        if st:
+            raise MoEError(st, "moe_grad_norm")
+        return norm, factor
+
+
+class AdamW:
+    """AdamW over a list of parameters, one launch a step.
+
+    params, grads: contiguous float32 or bfloat16 tensors of one device, a
+    gradient of the same size for every parameter (its type may differ).  They
+    are the caller's and are kept alive here: a step reads the gradients that
+    the buffers hold then, and writes the parameters in place.
+    masters: None; True, for a float32 copy of every bfloat16 parameter, made
+    here; or a list of float32 tensors (entries may be None).  Where there is a
+    master the step updates it, and the parameter becomes its rounding.
+    state: float32, or float8_e4m3fn for 8-bit states with a scale for every
+    256 values (the layout is moe_adamw_step's in include/moe.h).
+    weight_decay: one number, or one for every parameter.
+
+    m, v: (blocks, 256) of the state type, the parameters' states one behind
+    the other, each beginning a block (offsets: their first blocks; what lies
+    behind a parameter's end is never read or written); m_scale, v_scale:
+    (blocks,) float32 or None.  8-bit v holds the root of the second moment.
+
+    Steps on one object, and steps that are captured in graphs, are ordered by
+    the caller.  The number of steps is kept on the device: a captured step
+    counts on at each replay.
+    """
+
+    def __init__(self, params, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
+                 state=_F32, masters=None):
+        self.params, self.grads = _tensors(params, "params"), _tensors(grads, "grads")
+        n, dev = len(self.params), self.params[0].device
+        _want(len(self.grads) == n and self.grads[0].device == dev
+              and all(g.shape == p.shape for p, g in zip(self.params, self.grads)),
+              "grads: one of the same shape for every parameter, on their device")
+        _want(state in (_F32, _E4M3), "state: float32 or float8_e4m3fn")
+        decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else [
+            float(d) for d in weight_decay]
+        _want(len(decay) == n, "weight_decay: a number, or one for every parameter")
+        if masters is None or masters is True:
+            masters = [p.float() if masters and p.dtype == _BF16 else None for p in self.params]
+        self.masters = list(masters)
+        _want(len(self.masters) == n and all(
+            w is None or (w.dtype == _F32 and w.shape == p.shape and w.is_contiguous()
+                          and w.device == dev) for p, w in zip(self.params, self.masters)),
+              "masters: a contiguous float32 tensor of its shape, or None, for every parameter")
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+                       for t in self.params + [w for w in self.masters if w is not None]
+                       if t.numel())
+        _want(all(a[1] <= b[0] for a, b in zip(spans, spans[1:])),
+              "params and masters: no two may share memory")
+        self.lr, self.betas, self.eps = float(lr), (float(betas[0]), float(betas[1])), float(eps)
+        _want(all(0 <= b < 1 for b in self.betas) and 0 < self.eps < math.inf
+              and all(0 <= d < math.inf for d in [self.lr] + decay),
+              "betas in [0, 1), eps above 0, lr and weight_decay at least 0, all finite")
+        self.state, self.device, self._index = state, dev, _index(dev)
+        blocks = [-(-p.numel() // BLOCK) for p in self.params]
+        *self.offsets, total = itertools.accumulate(blocks, initial=0)
+        zeros = lambda *shape: torch.zeros(shape, dtype=_F32 if state == _F32 else torch.uint8,  # noqa: E731
+                                           device=dev).view(state)
+        self.m, self.v = zeros(total, BLOCK), zeros(total, BLOCK)
+        self.m_scale = self.v_scale = None
+        if state != _F32:
+            self.m_scale, self.v_scale = (torch.zeros(total, device=dev) for _ in range(2))
+        size, e = BLOCK * self.m.element_size(), state != _F32
+        self._list = (_lib.AdamWTensor * n)(*[
+            _lib.AdamWTensor(p.data_ptr(), _p(w), g.data_ptr(), self.m.data_ptr() + b * size,
+                             self.v.data_ptr() + b * size,
+                             self.m_scale.data_ptr() + 4 * b if e else None,
+                             self.v_scale.data_ptr() + 4 * b if e else None, p.numel(),
+                             _DT[p.dtype], _DT[g.dtype], d)
+            for p, w, g, b, d in zip(self.params, self.masters, self.grads, self.offsets, decay)])
+        self._step = _lib.load().moe_adamw_step
+        self.step_state = torch.zeros(_lib.ADAMW_STATE_BYTES, dtype=torch.uint8, device=dev)
+        self._set_steps(0)
+
+    def _desc(self, lr, lr_device, scale):
+        return _lib.AdamWDesc(_DT[self.state], lr, lr_device, scale, *self.betas, self.eps)
+
+    def _set_steps(self, steps):
+        decode._ready(self.device)
+        _check(_lib.load().moe_adamw_set_steps(*self.betas, steps, _p(self.step_state),
+                                               _handle(None, self._index)), "moe_adamw_set_steps")
+        kept = [t for t in (self.m, self.v, self.m_scale, self.v_scale, self.step_state)
+                if t is not None] + [w for w in self.masters if w is not None]
+        # a stream's first step waits for what was enqueued here
+        self._streams = _Workspaces(self.device, lambda: self.step_state, kept)
+
+    def step(self, lr=None, grad_scale=None, stream=None):
+        """One step with the gradients that the buffers hold.  lr: a number, or
+        one float32 on the device (read when the step runs, so a captured step
+        may be replayed with another), the constructor's when None.
+        grad_scale: one float32 on the device that multiplies the gradients
+        (GradNorm's factor), or None."""
+        lp = None
+        if lr is None:
+            lr = self.lr
+        elif isinstance(lr, torch.Tensor):
+            lp, lr = _scalar(lr, self.device, "lr"), 0.0
+        gp = _scalar(grad_scale, self.device, "grad_scale")
+        _here(self.device, self._index)
+        handle = _handle(stream, self._index)
+        if handle not in self._streams.pointers:
+            self._streams.add(handle)
+        st = self._step(ctypes.byref(self._desc(lr, lp, gp)), self._list, len(self.params),
+                        self.step_state.data_ptr(), handle)
+        if st:
+            raise MoEError(st, "moe_adamw_step")
+
+    @property
+    def steps(self):
+        """Steps taken (waits for the device)."""
+        return int(self.step_state[:8].view(torch.int64).item())
+
+    def state_dict(self):
+        """The states (the object's own tensors), the number of steps (waits for
+        the device) and the masters."""
+        return {"steps": self.steps, "m": self.m, "v": self.v, "m_scale": self.m_scale,
+                "v_scale": self.v_scale, "masters": self.masters}
+
+    def load_state_dict(self, d):
+        """Copies states and the number of steps, and masters where d has them,
+        on the current stream."""
+        for name in ("m", "v", "m_scale", "v_scale"):
+            to, src = getattr(self, name), d[name]
+            _want((to is None) == (src is None) and (to is None or (
+                src.dtype == to.dtype and src.shape == to.shape)), f"{name}: another shape or type")
+        masters = d.get("masters")
+        _want(masters is None or (len(masters) == len(self.masters) and all(
+            (a is None) == (b is None) and (a is None or a.shape == b.shape)
+            for a, b in zip(masters, self.masters))), "masters: other shapes")
+        for name in ("m", "v", "m_scale", "v_scale"):
+            if d[name] is not None:
+                getattr(self, name).view(torch.uint8).copy_(d[name].view(torch.uint8))
+        for to, src in zip(self.masters, masters or []):
+            if to is not None:
+                to.copy_(src)
+        self._set_steps(int(d["steps"]))
