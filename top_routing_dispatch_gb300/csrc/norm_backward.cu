@@ -1,0 +1,292 @@
+// Gradients of the layer norm: xh = (s - mu) r, t = dy w,
+//   dx = r (t - sum t / H - xh sum(t xh) / H) + ds,
+//   dw = sum over rows of dy xh, db = sum over rows of dy.
+//
+// Bound: HBM, every value read once and written once.  A group of threads
+// keeps its columns' sums for dw and db in registers over all its rows; the
+// groups of a CTA join them in shared memory, the CTAs through one float32 row
+// each in the workspace, added in a fixed order by a second kernel.
+#include "norm.cuh"
+
+namespace moe {
+namespace {
+
+struct BackArgs {
+  const void *dy, *s, *w, *ds;
+  long long dys, ss, dss;  // elements between rows
+  const float *stats;
+  void *dx;
+  float *part;  // (2, parts, H) sums for dweight and dbias
+  int n, H, parts;
+  bool wide, rms, bias;
+};
+
+// N: tensors read (dy and s; and ds)
+template <typename T, bool VEC, int GS, int VALS, int N, int D>
+__global__ void __launch_bounds__(kNormThreads) norm_back_kernel(const BackArgs a) {
+  using IO = RowIO<T, VEC, GS, VALS>;
+  pdl_enter();
+  extern __shared__ __align__(16) char ring[];
+  __shared__ __align__(16) float2 parts[2][kNormThreads / 32];
+  const int t = threadIdx.x % GS, group = threadIdx.x / GS, groups = blockDim.x / GS;
+  const int H = a.H, first = threadIdx.x / GS * GS / 32;
+  char *mine = ring + group * (D * N * IO::BYTES);
+  const uint32_t mine32 = ptx::smem_u32(mine);
+  const long long step = (long long)gridDim.x * groups;
+  long long row = blockIdx.x + (long long)gridDim.x * group, ahead = row;
+  auto issue = [&](int slot) {
+    if (ahead < a.n) {
+      const uint32_t to = mine32 + slot * N * IO::BYTES;
+      IO::issue(to, static_cast<const T *>(a.dy) + ahead * a.dys, H, t);
+      IO::issue(to + IO::BYTES, static_cast<const T *>(a.s) + ahead * a.ss, H, t);
+      if (N == 3)
+        IO::issue(to + 2 * IO::BYTES, static_cast<const T *>(a.ds) + ahead * a.dss, H, t);
+    }
+    ptx::cp_async_commit();
+    ahead += step;
+  };
+#pragma unroll
+  for (int i = 0; i < D - 1; ++i) issue(i);
+  constexpr bool HOLD = VALS <= 16;  // a row's values in registers over its sum
+  float w[VALS], dw[VALS], db[VALS];
+  if (HOLD) IO::param(a.w, a.wide, H, t, w);
+#pragma unroll
+  for (int k = 0; k < VALS; ++k) dw[k] = db[k] = 0.f;
+  const float inv = 1.f / (float)H;
+  const int turns = (int)((a.n - blockIdx.x + step - 1) / step);
+  for (int i = 0; i < turns; ++i, row += step) {
+    const bool on = row < a.n;
+    const float mu = on && !a.rms ? __ldg(a.stats + row) : 0.f;
+    const float r = on ? __ldg(a.stats + a.n + row) : 0.f;
+    issue((i + D - 1) % D);
+    ptx::cp_async_wait<D - 1>();
+    if (IO::SHARED) group_sync<GS>(group);
+    const T *pd = static_cast<const T *>(a.dy) + row * a.dys;
+    const T *ps = static_cast<const T *>(a.s) + row * a.ss;
+    const char *slot = mine + i % D * (N * IO::BYTES);
+    float g[VALS], xh[VALS];
+    auto fetch = [&]() {
+      IO::read(slot, pd, H, t, g);
+      IO::read(slot + IO::BYTES, ps, H, t, xh);
+#pragma unroll
+      for (int k = 0; k < VALS; ++k) xh[k] = (xh[k] - mu) * r;
+    };
+    fetch();
+    float2 sum = make_float2(0.f, 0.f);
+    if (on) {
+      if (!HOLD) IO::param(a.w, a.wide, H, t, w);
+#pragma unroll
+      for (int k = 0; k < VALS; ++k) {
+        if (IO::at(k, t) < H) {  // dy is 0 behind the row's end, xh need not be finite
+          const float v = g[k] * w[k];
+          sum.x += v;
+          sum.y = fmaf(v, xh[k], sum.y);
+          dw[k] = fmaf(g[k], xh[k], dw[k]);
+          db[k] += g[k];
+        }
+      }
+    }
+    sum = group_sum<GS>(sum, parts[i & 1] + first, group);
+    const float c1 = a.rms ? 0.f : sum.x * inv, c2 = sum.y * inv;
+    if (on) {
+      if (!HOLD) {
+        fetch();
+        IO::param(a.w, a.wide, H, t, w);
+      }
+#pragma unroll
+      for (int k = 0; k < VALS; ++k) g[k] = r * (g[k] * w[k] - c1 - xh[k] * c2);
+      if (N == 3) {
+        IO::read(slot + 2 * IO::BYTES, static_cast<const T *>(a.ds) + row * a.dss, H, t, xh);
+#pragma unroll
+        for (int k = 0; k < VALS; ++k) g[k] += xh[k];
+      }
+      IO::store(static_cast<T *>(a.dx) + row * H, H, t, g);
+    }
+    if (IO::SHARED) group_sync<GS>(group);  // the slot may be filled again
+  }
+  // the CTA's sums, group by group
+  float *out = a.part + (size_t)blockIdx.x * H;
+  if (groups > 1) {
+    ptx::cp_async_wait<0>();
+    __syncthreads();
+    float *all = reinterpret_cast<float *>(ring);
+    for (int pass = 0; pass < (a.bias ? 2 : 1); ++pass, out += (size_t)a.parts * H) {
+#pragma unroll
+      for (int k = 0; k < VALS; ++k)
+        if (IO::at(k, t) < H) all[group * H + IO::at(k, t)] = pass ? db[k] : dw[k];
+      __syncthreads();
+      for (int c = threadIdx.x; c < H; c += blockDim.x) {
+        float v = all[c];
+        for (int q = 1; q < groups; ++q) v += all[q * H + c];
+        out[c] = v;
+      }
+      __syncthreads();
+    }
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < VALS; ++k) {
+    if (IO::at(k, t) < H) {
+      out[IO::at(k, t)] = dw[k];
+      if (a.bias) out[(size_t)a.parts * H + IO::at(k, t)] = db[k];
+    }
+  }
+}
+
+// Rows of any length and alignment, first part: dx, a CTA a row.
+template <typename T>
+__global__ void __launch_bounds__(1024) norm_back_long_kernel(const BackArgs a) {
+  pdl_enter();
+  __shared__ __align__(16) float2 parts[32];
+  const long long row = blockIdx.x;
+  const T *dy = static_cast<const T *>(a.dy) + row * a.dys;
+  const T *s = static_cast<const T *>(a.s) + row * a.ss;
+  const T *ds = a.ds ? static_cast<const T *>(a.ds) + row * a.dss : nullptr;
+  T *dx = static_cast<T *>(a.dx) + row * a.H;
+  const float mu = a.rms ? 0.f : a.stats[row], r = a.stats[(size_t)a.n + row];
+  const float inv = 1.f / (float)a.H;
+  auto weight = [&](int i) {
+    return a.wide ? static_cast<const float *>(a.w)[i] : to_f(static_cast<const T *>(a.w)[i]);
+  };
+  float2 sum = make_float2(0.f, 0.f);
+  for (int i = threadIdx.x; i < a.H; i += 1024) {
+    const float v = to_f(dy[i]) * weight(i);
+    sum.x += v;
+    sum.y = fmaf(v, (to_f(s[i]) - mu) * r, sum.y);
+  }
+  sum = group_sum<1024>(sum, parts, 0);
+  const float c1 = a.rms ? 0.f : sum.x * inv, c2 = sum.y * inv;
+  for (int i = threadIdx.x; i < a.H; i += 1024) {
+    const float v = r * (to_f(dy[i]) * weight(i) - c1 - (to_f(s[i]) - mu) * r * c2);
+    dx[i] = from_f<T>(ds ? v + to_f(ds[i]) : v);
+  }
+}
+
+constexpr int kWarps = 8;  // of a column kernel's CTA
+
+// Second part: sums of dy xh and of dy over a range of rows, 32 columns a CTA
+template <typename T>
+__global__ void __launch_bounds__(32 * kWarps) norm_columns_kernel(const BackArgs a) {
+  pdl_enter();
+  __shared__ float sw[kWarps][32], sb[kWarps][32];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int col = blockIdx.x * 32 + lane;
+  const int r0 = (int)((long long)a.n * blockIdx.y / a.parts);
+  const int r1 = (int)((long long)a.n * (blockIdx.y + 1) / a.parts);
+  float dw = 0.f, db = 0.f;
+  if (col < a.H) {
+    for (int row = r0 + warp; row < r1; row += kWarps) {
+      const float mu = a.rms ? 0.f : a.stats[row], r = a.stats[(size_t)a.n + row];
+      const float x = to_f(static_cast<const T *>(a.s)[row * a.ss + col]);
+      const float dy = to_f(static_cast<const T *>(a.dy)[row * a.dys + col]);
+      dw = fmaf(dy, (x - mu) * r, dw);
+      db += dy;
+    }
+  }
+  sw[warp][lane] = dw, sb[warp][lane] = db;
+  __syncthreads();
+  if (warp || col >= a.H) return;
+#pragma unroll
+  for (int i = 1; i < kWarps; ++i) dw += sw[i][lane], db += sb[i][lane];
+  a.part[(size_t)blockIdx.y * a.H + col] = dw;
+  if (a.bias) a.part[((size_t)a.parts + blockIdx.y) * a.H + col] = db;
+}
+
+// dweight (blockIdx.y 0) and dbias (1): the parts in a fixed order
+__global__ void __launch_bounds__(32 * kWarps)
+    norm_join_kernel(const float *part, int parts, int H, float *dweight, float *dbias) {
+  pdl_enter();
+  __shared__ float acc[kWarps][32];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int col = blockIdx.x * 32 + lane;
+  float *out = blockIdx.y ? dbias : dweight;
+  const float *p = part + (size_t)blockIdx.y * parts * H + col;
+  float v = 0.f;
+  if (col < H) {
+#pragma unroll 8
+    for (int i = warp; i < parts; i += kWarps) v += p[(size_t)i * H];
+  }
+  acc[warp][lane] = v;
+  __syncthreads();
+  if (warp || col >= H) return;
+#pragma unroll
+  for (int i = 1; i < kWarps; ++i) v += acc[i][lane];
+  out[col] = v;
+}
+
+template <typename T, bool VEC, int GS, int VALS>
+struct Backward {
+  template <int N>
+  static bool with(const BackArgs &a, cudaStream_t s, cudaError_t *e) {
+    constexpr int D = ring_slots<T, VALS, N>();
+    if constexpr (D == 0) {
+      return false;
+    } else {
+      BackArgs b = a;
+      const int sms = device_sm_count();
+      const NormGrid g = norm_grid<GS>(a.n, sms < kNormParts ? sms : kNormParts);
+      b.parts = g.ctas;
+      constexpr int one = D * N * RowIO<T, VEC, GS, VALS>::BYTES;
+      // the groups' sums are joined in the ring
+      static_assert(one >= GS * VALS * 4, "ring");
+      auto kernel = norm_back_kernel<T, VEC, GS, VALS, N, D>;
+      static bool ready[64] = {false};
+      *e = allow_smem(kernel, one * (kNormThreads / GS), ready);
+      if (*e == cudaSuccess)
+        *e = launch_pdl(kernel, dim3(g.ctas), dim3(g.groups * GS), one * g.groups, s, b);
+      return true;
+    }
+  }
+  static bool go(const BackArgs &a, cudaStream_t s, cudaError_t *e) {
+    return a.ds ? with<3>(a, s, e) : with<2>(a, s, e);
+  }
+};
+
+template <typename T>
+cudaError_t backward(const BackArgs &a, float *dweight, float *dbias, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  constexpr int per = kPer<T>;
+  const bool vec = a.H % per == 0 && a.dys % per == 0 && a.ss % per == 0 && on_bytes(a.dy, 16) &&
+                   on_bytes(a.s, 16) && on_bytes(a.dx, 16) && on_bytes(a.w, 16) &&
+                   (!a.ds || (a.dss % per == 0 && on_bytes(a.ds, 16)));
+  int parts = device_sm_count();
+  parts = parts < kNormParts ? parts : kNormParts;
+  const bool ring = vec ? by_length<T, true, Backward>(a, s, &e)
+                        : on_bytes(a.dy, 4) && on_bytes(a.s, 4) && on_bytes(a.ds, 4) &&
+                              by_length<T, false, Backward>(a, s, &e);
+  if (!ring) {
+    parts = kNormParts;
+    e = launch_pdl(norm_back_long_kernel<T>, dim3(a.n), dim3(1024), 0, s, a);
+    if (e == cudaSuccess)
+      e = launch_pdl(norm_columns_kernel<T>, dim3((a.H + 31) / 32, a.parts), dim3(32 * kWarps), 0,
+                     s, a);
+  }
+  if (e != cudaSuccess) return e;
+  return launch_pdl(norm_join_kernel, dim3((a.H + 31) / 32, dbias ? 2 : 1), dim3(32 * kWarps), 0,
+                    s, (const float *)a.part, a.n < parts ? a.n : parts, a.H, dweight, dbias);
+}
+
+}  // namespace
+
+size_t norm_backward_ws_bytes(const moe_norm_t &d) {
+  const int parts = d.n < 1 ? 1 : d.n < kNormParts ? d.n : kNormParts;
+  return 2 * sizeof(float) * (size_t)parts * d.H;
+}
+
+cudaError_t launch_norm_backward(const moe_norm_t &d, const void *dy, long long dy_stride,
+                                 const void *s, long long s_stride, const float *stats,
+                                 const void *weight, const void *ds, long long ds_stride, void *dx,
+                                 float *dweight, float *dbias, void *ws, cudaStream_t st) {
+  if (d.n == 0) {
+    cudaError_t e = cudaMemsetAsync(dweight, 0, sizeof(float) * d.H, st);
+    if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, sizeof(float) * d.H, st);
+    return e;
+  }
+  const BackArgs a = {dy, s, weight, ds, dy_stride, s_stride, ds_stride, stats, dx,
+                      static_cast<float *>(ws), d.n, d.H, d.n < kNormParts ? d.n : kNormParts,
+                      d.weight_dtype == MOE_F32, d.rms != 0, dbias != nullptr};
+  return d.dtype == MOE_F32 ? backward<float>(a, dweight, dbias, st)
+                            : backward<__nv_bfloat16>(a, dweight, dbias, st);
+}
+
+}  // namespace moe
