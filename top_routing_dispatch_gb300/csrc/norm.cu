@@ -34,20 +34,23 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs a) {
   const uint32_t mine32 = ptx::smem_u32(mine);
   const long long step = (long long)gridDim.x * groups;
   long long row = blockIdx.x + (long long)gridDim.x * group, ahead = row;
+  const T *x = static_cast<const T *>(a.x) + row * a.xs, *x_in = x;
+  const T *res = static_cast<const T *>(a.res) + (N == 2 ? row * a.rs : 0), *res_in = res;
+  T *y = static_cast<T *>(a.y) + row * H, *s = static_cast<T *>(a.s) + (N == 2 ? row * H : 0);
   auto issue = [&](int slot) {
     if (ahead < a.n) {
-      IO::issue(mine32 + slot * N * IO::BYTES, static_cast<const T *>(a.x) + ahead * a.xs, H, t);
-      if (N == 2)
-        IO::issue(mine32 + (slot * N + 1) * IO::BYTES,
-                  static_cast<const T *>(a.res) + ahead * a.rs, H, t);
+      const uint32_t to = mine32 + slot * (N * IO::BYTES);
+      IO::issue(to, x_in, H, t);
+      if (N == 2) IO::issue(to + IO::BYTES, res_in, H, t);
     }
     ptx::cp_async_commit();
-    ahead += step;
+    ahead += step, x_in += step * a.xs, res_in += N == 2 ? step * a.rs : 0;
   };
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < D - 1; ++i) issue(i);
-  float w[VALS], b[VALS];
-  if (VALS <= 16) {
+  float2 w[IO::P], b[IO::P];
+  constexpr bool KEEP = VALS <= 16;  // weight and bias in registers over all rows
+  if (KEEP) {
     IO::param(a.w, a.wide, H, t, w);
     if (a.b) IO::param(a.b, a.wide, H, t, b);
   }
@@ -55,64 +58,75 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs a) {
   // all groups of a CTA take the same number of turns: those of a warp share
   // its shuffles
   const int turns = (int)((a.n - blockIdx.x + step - 1) / step);
-  for (int i = 0; i < turns; ++i, row += step) {
+#pragma unroll 1
+  for (int i = 0; i < turns; ++i) {
     issue((i + D - 1) % D);
     ptx::cp_async_wait<D - 1>();
     if (IO::SHARED) group_sync<GS>(group);
     const bool on = row < a.n;
-    const T *x = static_cast<const T *>(a.x) + row * a.xs;
     const char *slot = mine + i % D * (N * IO::BYTES);
-    float f[VALS];
-    IO::read(slot, x, H, t, f);
+    float2 f[IO::P];
+    IO::read(slot, IO::odd(x), H, t, f);
     if (N == 2) {
-      float g[VALS];
-      IO::read(slot + IO::BYTES, static_cast<const T *>(a.res) + row * a.rs, H, t, g);
+      float2 g[IO::P];
+      IO::read(slot + IO::BYTES, IO::odd(res), H, t, g);
 #pragma unroll
-      for (int k = 0; k < VALS; ++k) f[k] = to_f(from_f<T>(f[k] + g[k]));
-      if (on) IO::store(static_cast<T *>(a.s) + row * H, H, t, f);
+      for (int k = 0; k < IO::P; ++k) f[k] = add2(f[k], g[k]);
+      IO::round(f);
+      if (on) IO::store(s, H, t, f);
     }
-    float mu = 0.f, off = 0.f;
+    float mu = 0.f, off = 0.f, var;
     if (!a.rms) {
-      float2 sum = make_float2(0.f, 0.f);
+      float2 sum = f[0];
 #pragma unroll
-      for (int k = 0; k < VALS; ++k) sum.x += f[k];
-      mu = group_sum<GS>(sum, parts[0] + first, group).x * inv;
-    }
-    // squares of the deviations from the mean; the deviations' own sum takes
-    // out what rounding left in it
-    float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < VALS; ++k) {
-      const float d = IO::at(k, t) < H ? f[k] - mu : 0.f;
-      sum.x += d;
-      sum.y = fmaf(d, d, sum.y);
-    }
-    // the root mean square form has one sum a row: places in turn
-    sum = group_sum<GS>(sum, parts[a.rms ? i & 1 : 1] + first, group);
-    float var = sum.y * inv;
-    if (!a.rms) {
-      off = sum.x * inv;
-      var = fmaf(-off, off, var);
+      for (int k = 1; k < IO::P; ++k) sum = add2(sum, f[k]);
+      mu = group_sum<GS>(sum.x + sum.y, parts[0] + first, group) * inv;
+      // squares of the deviations from the mean; the deviations' own sum takes
+      // out what rounding left in it
+      float2 d = make_float2(0.f, 0.f), q = d;
+      const float2 m = both(-mu);
+      IO::each(H, t, [&](int k) {
+        f[k] = add2(f[k], m);
+        if (!IO::whole(k, H, t)) f[k].y = 0.f;
+        d = add2(d, f[k]);
+        q = fma2(f[k], f[k], q);
+      });
+      const float2 v = group_sum<GS>(make_float2(d.x + d.y, q.x + q.y), parts[1] + first, group);
+      off = v.x * inv;
+      var = fmaf(-off, off, v.y * inv);
       var = var < 0.f ? 0.f : var;  // a NaN stays one
       mu += off;
-    }
-    const float r = 1.f / sqrtf(var + a.eps);
-    if (VALS > 16) {
-      IO::param(a.w, a.wide, H, t, w);
-      if (a.b) IO::param(a.b, a.wide, H, t, b);
-    }
+    } else {
+      float2 q = mul2(f[0], f[0]);
 #pragma unroll
-    for (int k = 0; k < VALS; ++k) {
-      const float xh = (f[k] - mu) * r;
-      f[k] = a.b ? fmaf(xh, w[k], b[k]) : xh * w[k];
+      for (int k = 1; k < IO::P; ++k) q = fma2(f[k], f[k], q);
+      // one sum a row: places in turn
+      var = group_sum<GS>(q.x + q.y, parts[i & 1] + first, group) * inv;
     }
+    const float r = rsqrt_of(var + a.eps);
     if (on) {
-      IO::store(static_cast<T *>(a.y) + row * H, H, t, f);
+      if (!KEEP) {
+        IO::param(a.w, a.wide, H, t, w);
+        if (a.b) IO::param(a.b, a.wide, H, t, b);
+      }
+      const float2 r2 = both(r), o2 = both(-off);
+#pragma unroll
+      for (int k = 0; k < IO::P; ++k) f[k] = mul2(a.rms ? f[k] : add2(f[k], o2), r2);
+      if (a.b) {
+#pragma unroll
+        for (int k = 0; k < IO::P; ++k) f[k] = fma2(f[k], w[k], b[k]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < IO::P; ++k) f[k] = mul2(f[k], w[k]);
+      }
+      IO::store(y, H, t, f);
       if (a.stats && t == 0) {
         a.stats[row] = mu;
         a.stats[(size_t)a.n + row] = r;
       }
     }
+    row += step, x += step * a.xs, y += step * H;
+    if (N == 2) res += step * a.rs, s += step * H;
     if (IO::SHARED && GS <= 32) __syncwarp();  // larger groups have had a barrier since
   }
 }
@@ -140,7 +154,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
     sum.x += f;
   }
   const T *in = res ? s : x;  // a thread's own values
-  float mu = group_sum<1024>(sum, parts[0], 0).x * inv;
+  float mu = group_sum<1024>(sum.x, parts[0], 0) * inv;
   if (a.rms) mu = 0.f;
   sum = make_float2(0.f, 0.f);
   for (int i = threadIdx.x; i < a.H; i += 1024) {
@@ -156,7 +170,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
     var = var < 0.f ? 0.f : var;
     mu += off;
   }
-  const float r = 1.f / sqrtf(var + a.eps);
+  const float r = rsqrt_of(var + a.eps);
   auto param = [&](const void *p, int i) {
     return a.wide ? static_cast<const float *>(p)[i] : to_f(static_cast<const T *>(p)[i]);
   };

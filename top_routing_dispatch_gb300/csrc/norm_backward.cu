@@ -34,74 +34,82 @@ __global__ void __launch_bounds__(kNormThreads) norm_back_kernel(const BackArgs 
   const uint32_t mine32 = ptx::smem_u32(mine);
   const long long step = (long long)gridDim.x * groups;
   long long row = blockIdx.x + (long long)gridDim.x * group, ahead = row;
+  const T *dy = static_cast<const T *>(a.dy) + row * a.dys, *dy_in = dy;
+  const T *sp = static_cast<const T *>(a.s) + row * a.ss, *sp_in = sp;
+  const T *ds = static_cast<const T *>(a.ds) + (N == 3 ? row * a.dss : 0), *ds_in = ds;
+  T *dx = static_cast<T *>(a.dx) + row * H;
   auto issue = [&](int slot) {
     if (ahead < a.n) {
-      const uint32_t to = mine32 + slot * N * IO::BYTES;
-      IO::issue(to, static_cast<const T *>(a.dy) + ahead * a.dys, H, t);
-      IO::issue(to + IO::BYTES, static_cast<const T *>(a.s) + ahead * a.ss, H, t);
-      if (N == 3)
-        IO::issue(to + 2 * IO::BYTES, static_cast<const T *>(a.ds) + ahead * a.dss, H, t);
+      const uint32_t to = mine32 + slot * (N * IO::BYTES);
+      IO::issue(to, dy_in, H, t);
+      IO::issue(to + IO::BYTES, sp_in, H, t);
+      if (N == 3) IO::issue(to + 2 * IO::BYTES, ds_in, H, t);
     }
     ptx::cp_async_commit();
-    ahead += step;
+    ahead += step, dy_in += step * a.dys, sp_in += step * a.ss;
+    if (N == 3) ds_in += step * a.dss;
   };
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < D - 1; ++i) issue(i);
   constexpr bool HOLD = VALS <= 16;  // a row's values in registers over its sum
-  float w[VALS], dw[VALS], db[VALS];
+  float2 w[IO::P], dw[IO::P], db[IO::P];
   if (HOLD) IO::param(a.w, a.wide, H, t, w);
 #pragma unroll
-  for (int k = 0; k < VALS; ++k) dw[k] = db[k] = 0.f;
+  for (int k = 0; k < IO::P; ++k) dw[k] = db[k] = make_float2(0.f, 0.f);
   const float inv = 1.f / (float)H;
   const int turns = (int)((a.n - blockIdx.x + step - 1) / step);
-  for (int i = 0; i < turns; ++i, row += step) {
+  // the statistics of the next row are on their way during a row
+  float mu_in = 0.f, r_in = 0.f;
+  auto stats = [&](long long at) {
+    if (at < a.n) {
+      if (!a.rms) mu_in = __ldg(a.stats + at);
+      r_in = __ldg(a.stats + a.n + at);
+    }
+  };
+  stats(row);
+#pragma unroll 1
+  for (int i = 0; i < turns; ++i) {
     const bool on = row < a.n;
-    const float mu = on && !a.rms ? __ldg(a.stats + row) : 0.f;
-    const float r = on ? __ldg(a.stats + a.n + row) : 0.f;
+    const float2 mu = both(-mu_in), r = both(r_in);
+    stats(row + step);
     issue((i + D - 1) % D);
     ptx::cp_async_wait<D - 1>();
     if (IO::SHARED) group_sync<GS>(group);
-    const T *pd = static_cast<const T *>(a.dy) + row * a.dys;
-    const T *ps = static_cast<const T *>(a.s) + row * a.ss;
     const char *slot = mine + i % D * (N * IO::BYTES);
-    float g[VALS], xh[VALS];
-    auto fetch = [&]() {
-      IO::read(slot, pd, H, t, g);
-      IO::read(slot + IO::BYTES, ps, H, t, xh);
-#pragma unroll
-      for (int k = 0; k < VALS; ++k) xh[k] = (xh[k] - mu) * r;
-    };
-    fetch();
-    float2 sum = make_float2(0.f, 0.f);
-    if (on) {
+    // with d = s - mu and g = dy r: r t = g w, and the sums of r t and r t d
+    // give r c1 and c2
+    float2 g[IO::P], d[IO::P];
+    float2 s1 = make_float2(0.f, 0.f), s2 = s1;
+    auto fetch = [&](bool sums) {
+      IO::read(slot, IO::odd(dy), H, t, g);
+      IO::read(slot + IO::BYTES, IO::odd(sp), H, t, d);
       if (!HOLD) IO::param(a.w, a.wide, H, t, w);
-#pragma unroll
-      for (int k = 0; k < VALS; ++k) {
-        if (IO::at(k, t) < H) {  // dy is 0 behind the row's end, xh need not be finite
-          const float v = g[k] * w[k];
-          sum.x += v;
-          sum.y = fmaf(v, xh[k], sum.y);
-          dw[k] = fmaf(g[k], xh[k], dw[k]);
-          db[k] += g[k];
-        }
-      }
-    }
-    sum = group_sum<GS>(sum, parts[i & 1] + first, group);
-    const float c1 = a.rms ? 0.f : sum.x * inv, c2 = sum.y * inv;
+      IO::each(H, t, [&](int k) {  // g is 0 behind the row's end
+        d[k] = add2(d[k], mu);
+        if (sums) db[k] = add2(db[k], g[k]);
+        g[k] = mul2(g[k], r);
+        if (!IO::whole(k, H, t)) d[k].y = 0.f;
+        if (sums) dw[k] = fma2(g[k], d[k], dw[k]);
+        g[k] = mul2(g[k], w[k]);
+        if (sums) s1 = add2(s1, g[k]), s2 = fma2(g[k], d[k], s2);
+      });
+    };
+    if (on) fetch(true);
+    s1 = group_sum<GS>(make_float2(s1.x + s1.y, s2.x + s2.y), parts[i & 1] + first, group);
     if (on) {
-      if (!HOLD) {
-        fetch();
-        IO::param(a.w, a.wide, H, t, w);
-      }
+      const float2 c1 = both(a.rms ? 0.f : -s1.x * inv), c2 = both(-s1.y * inv * r.x * r.x);
+      if (!HOLD) fetch(false);
 #pragma unroll
-      for (int k = 0; k < VALS; ++k) g[k] = r * (g[k] * w[k] - c1 - xh[k] * c2);
+      for (int k = 0; k < IO::P; ++k) g[k] = fma2(d[k], c2, add2(g[k], c1));
       if (N == 3) {
-        IO::read(slot + 2 * IO::BYTES, static_cast<const T *>(a.ds) + row * a.dss, H, t, xh);
+        IO::read(slot + 2 * IO::BYTES, IO::odd(ds), H, t, d);
 #pragma unroll
-        for (int k = 0; k < VALS; ++k) g[k] += xh[k];
+        for (int k = 0; k < IO::P; ++k) g[k] = add2(g[k], d[k]);
       }
-      IO::store(static_cast<T *>(a.dx) + row * H, H, t, g);
+      IO::store(dx, H, t, g);
     }
+    row += step, dy += step * a.dys, sp += step * a.ss, dx += step * H;
+    if (N == 3) ds += step * a.dss;
     if (IO::SHARED) group_sync<GS>(group);  // the slot may be filled again
   }
   // the CTA's sums, group by group
@@ -113,7 +121,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_back_kernel(const BackArgs 
     for (int pass = 0; pass < (a.bias ? 2 : 1); ++pass, out += (size_t)a.parts * H) {
 #pragma unroll
       for (int k = 0; k < VALS; ++k)
-        if (IO::at(k, t) < H) all[group * H + IO::at(k, t)] = pass ? db[k] : dw[k];
+        if (IO::at(k, t) < H)
+          all[group * H + IO::at(k, t)] = k % 2 ? (pass ? db : dw)[k / 2].y : (pass ? db : dw)[k / 2].x;
       __syncthreads();
       for (int c = threadIdx.x; c < H; c += blockDim.x) {
         float v = all[c];
@@ -127,8 +136,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_back_kernel(const BackArgs 
 #pragma unroll
   for (int k = 0; k < VALS; ++k) {
     if (IO::at(k, t) < H) {
-      out[IO::at(k, t)] = dw[k];
-      if (a.bias) out[(size_t)a.parts * H + IO::at(k, t)] = db[k];
+      out[IO::at(k, t)] = k % 2 ? dw[k / 2].y : dw[k / 2].x;
+      if (a.bias) out[(size_t)a.parts * H + IO::at(k, t)] = k % 2 ? db[k / 2].y : db[k / 2].x;
     }
   }
 }
