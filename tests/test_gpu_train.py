@@ -602,3 +602,36 @@ def test_c_calls_with_plain_pointers():
     assert torch.equal(y, layer(x))
     got = layer.backward(y, x, stats)
     assert torch.equal(dx, got[0]) and torch.equal(dw, got[1])
+
+
+# ------------------------------------------------- rows of every phase
+@pytest.mark.parametrize("T", [F32, BF16])
+@pytest.mark.parametrize("n,H", [(1, 3), (2, 1), (9, 5), (400, 7), (1300, 9), (153, 121), (1217, 127), (1200, 130),
+                                 (161, 1025), (305, 2050), (160, 4093), (310, 8186), (153, 8189), (155, 16379)])
+def test_norm_odd_rows_in_many_rounds(n, H, T):
+    """Rows that begin at every place within 16 bytes, several to a group, in a
+    buffer with nothing behind its last row."""
+    layer, x, res, w, b, eps = norm_case(n, H, T, F32, False, True, True, seed=40)
+    x, res = x.cuda(), res.cuda()
+    stats = torch.empty((2, n), device="cuda")
+    y, s = layer(x, res, stats=stats)
+    check_norm(layer, x.cpu(), res.cpu(), w, b, eps, False, y, s, stats)
+    y, s = layer(x, res[:, :].clone(), stats=stats)
+    dy = rand(41, n, H).to(T).cuda()
+    out = layer.backward(dy, s, stats, ds=res)
+    check_backward(layer, dy.cpu(), s.cpu(), stats, w, res.cpu(), False, out, True)
+
+
+def test_norm_row_strides_of_unequal_phase():
+    """x in a buffer of odd row stride, the result contiguous; and strides of
+    one odd phase that are not the length."""
+    for T in (F32, BF16):
+        for H, strides in ((40, (41, 41)), (40, (41, 48)), (41, (49, 57)), (41, (41, 49)), (33, (35, 35))):
+            n = 700
+            x, res = (rand(i, n, st).to(T).cuda()[:, :H] for i, st in enumerate(strides))
+            layer, _, _, w, b, eps = norm_case(2, H, T, F32, False, True, True)
+            stats = torch.empty((2, n), device="cuda")
+            y, s = layer(x, res, stats=stats)
+            check_norm(layer, x.cpu(), res.cpu(), w, b, eps, False, y, s, stats)
+            out = layer.backward(x, s, stats, ds=res)
+            check_backward(layer, x.cpu(), s.cpu(), stats, w, res.cpu(), False, out, True)

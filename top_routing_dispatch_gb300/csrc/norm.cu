@@ -19,12 +19,14 @@ struct NormArgs {
   int n, H;
   bool wide, rms;  // float32 weight; no mean
   float eps;
+  int phase;  // values from a row's beginning within 16 bytes to the next row's
+  bool vec;   // weight and bias on 16 bytes
 };
 
 // N: tensors read (x; x and residual)
-template <typename T, bool VEC, int GS, int VALS, int N, int D>
+template <typename T, int GS, int VALS, bool SHIFT, int N, int D>
 __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs a) {
-  using IO = RowIO<T, VEC, GS, VALS>;
+  using IO = RowIO<T, GS, VALS, SHIFT>;
   pdl_enter();
   extern __shared__ __align__(16) char ring[];
   __shared__ __align__(16) float2 parts[2][kNormThreads / 32];
@@ -34,14 +36,15 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs a) {
   const uint32_t mine32 = ptx::smem_u32(mine);
   const long long step = (long long)gridDim.x * groups;
   long long row = blockIdx.x + (long long)gridDim.x * group, ahead = row;
-  const T *x = static_cast<const T *>(a.x) + row * a.xs, *x_in = x;
-  const T *res = static_cast<const T *>(a.res) + (N == 2 ? row * a.rs : 0), *res_in = res;
+  const T *x_in = static_cast<const T *>(a.x) + row * a.xs;
+  const T *res_in = static_cast<const T *>(a.res) + (N == 2 ? row * a.rs : 0);
   T *y = static_cast<T *>(a.y) + row * H, *s = static_cast<T *>(a.s) + (N == 2 ? row * H : 0);
+  const IO io(H, t, (int)(row * a.phase % IO::V));
   auto issue = [&](int slot) {
     if (ahead < a.n) {
       const uint32_t to = mine32 + slot * (N * IO::BYTES);
-      IO::issue(to, x_in, H, t);
-      if (N == 2) IO::issue(to + IO::BYTES, res_in, H, t);
+      io.issue(to, x_in, a.xs, a.n - 1 - ahead);
+      if (N == 2) io.issue(to + IO::BYTES, res_in, a.rs, a.n - 1 - ahead);
     }
     ptx::cp_async_commit();
     ahead += step, x_in += step * a.xs, res_in += N == 2 ? step * a.rs : 0;
@@ -51,8 +54,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs a) {
   float2 w[IO::P], b[IO::P];
   constexpr bool KEEP = VALS <= 16;  // weight and bias in registers over all rows
   if (KEEP) {
-    IO::param(a.w, a.wide, H, t, w);
-    if (a.b) IO::param(a.b, a.wide, H, t, b);
+    io.param(a.w, a.wide, a.vec, w);
+    if (a.b) io.param(a.b, a.wide, a.vec, b);
   }
   const float inv = 1.f / (float)H;
   // all groups of a CTA take the same number of turns: those of a warp share
@@ -62,18 +65,17 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs a) {
   for (int i = 0; i < turns; ++i) {
     issue((i + D - 1) % D);
     ptx::cp_async_wait<D - 1>();
-    if (IO::SHARED) group_sync<GS>(group);
     const bool on = row < a.n;
     const char *slot = mine + i % D * (N * IO::BYTES);
     float2 f[IO::P];
-    IO::read(slot, IO::odd(x), H, t, f);
+    io.read(slot, f);
     if (N == 2) {
       float2 g[IO::P];
-      IO::read(slot + IO::BYTES, IO::odd(res), H, t, g);
+      io.read(slot + IO::BYTES, g);
 #pragma unroll
       for (int k = 0; k < IO::P; ++k) f[k] = add2(f[k], g[k]);
       IO::round(f);
-      if (on) IO::store(s, H, t, f);
+      if (on) io.store(s, f);
     }
     float mu = 0.f, off = 0.f, var;
     if (!a.rms) {
@@ -85,9 +87,11 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs a) {
       // out what rounding left in it
       float2 d = make_float2(0.f, 0.f), q = d;
       const float2 m = both(-mu);
-      IO::each(H, t, [&](int k) {
-        f[k] = add2(f[k], m);
-        if (!IO::whole(k, H, t)) f[k].y = 0.f;
+#pragma unroll
+      for (int k = 0; k < IO::P; ++k) f[k] = add2(f[k], m);
+#pragma unroll
+      for (int c = 0; c < IO::PIECES; ++c) io.mask(c, f);
+      io.each([&](int, int k) {
         d = add2(d, f[k]);
         q = fma2(f[k], f[k], q);
       });
@@ -106,8 +110,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs a) {
     const float r = rsqrt_of(var + a.eps);
     if (on) {
       if (!KEEP) {
-        IO::param(a.w, a.wide, H, t, w);
-        if (a.b) IO::param(a.b, a.wide, H, t, b);
+        io.param(a.w, a.wide, a.vec, w);
+        if (a.b) io.param(a.b, a.wide, a.vec, b);
       }
       const float2 r2 = both(r), o2 = both(-off);
 #pragma unroll
@@ -119,15 +123,14 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs a) {
 #pragma unroll
         for (int k = 0; k < IO::P; ++k) f[k] = mul2(f[k], w[k]);
       }
-      IO::store(y, H, t, f);
+      io.store(y, f);
       if (a.stats && t == 0) {
         a.stats[row] = mu;
         a.stats[(size_t)a.n + row] = r;
       }
     }
-    row += step, x += step * a.xs, y += step * H;
-    if (N == 2) res += step * a.rs, s += step * H;
-    if (IO::SHARED && GS <= 32) __syncwarp();  // larger groups have had a barrier since
+    row += step, y += step * H;
+    if (N == 2) s += step * H;
   }
 }
 
@@ -184,7 +187,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
   }
 }
 
-template <typename T, bool VEC, int GS, int VALS>
+template <typename T, int GS, int VALS, bool SHIFT>
 struct Forward {
   template <int N>
   static bool with(const NormArgs &a, cudaStream_t s, cudaError_t *e) {
@@ -193,8 +196,8 @@ struct Forward {
       return false;
     } else {
       const NormGrid g = norm_grid<GS>(a.n, device_sm_count());
-      constexpr int one = D * N * RowIO<T, VEC, GS, VALS>::BYTES;
-      auto kernel = norm_kernel<T, VEC, GS, VALS, N, D>;
+      constexpr int one = D * N * RowIO<T, GS, VALS, SHIFT>::BYTES;
+      auto kernel = norm_kernel<T, GS, VALS, SHIFT, N, D>;
       static bool ready[64] = {false};
       *e = allow_smem(kernel, one * (kNormThreads / GS), ready);
       if (*e == cudaSuccess)
@@ -208,15 +211,14 @@ struct Forward {
 };
 
 template <typename T>
-cudaError_t forward(const NormArgs &a, cudaStream_t s) {
+cudaError_t forward(NormArgs &a, cudaStream_t s) {
+  Phases ph(kPer<T>);
+  ph.add(a.x, a.xs), ph.add(a.res, a.rs), ph.add(a.s, a.H), ph.add(a.y, a.H);
+  a.phase = ph.step;
+  a.vec = on_bytes(a.w, 16) && on_bytes(a.b, 16);
   cudaError_t e = cudaSuccess;
-  constexpr int per = kPer<T>;
-  const bool vec = a.H % per == 0 && a.xs % per == 0 && on_bytes(a.x, 16) && on_bytes(a.y, 16) &&
-                   on_bytes(a.w, 16) && on_bytes(a.b, 16) &&
-                   (!a.res || (a.rs % per == 0 && on_bytes(a.res, 16) && on_bytes(a.s, 16)));
-  if (vec ? by_length<T, true, Forward>(a, s, &e)
-          : on_bytes(a.x, 4) && on_bytes(a.res, 4) && by_length<T, false, Forward>(a, s, &e))
-    return e;
+  if (ph.one && (ph.step || a.H % kPer<T> ? by_length<T, true, Forward>(a, s, &e)
+                                      : by_length<T, false, Forward>(a, s, &e))) return e;
   return launch_pdl(norm_long_kernel<T>, dim3(a.n), dim3(1024), 0, s, a);
 }
 
@@ -226,8 +228,8 @@ cudaError_t launch_norm(const moe_norm_t &d, const void *x, long long x_stride,
                         const void *residual, long long residual_stride, const void *weight,
                         const void *bias, void *s, void *y, float *stats, cudaStream_t st) {
   if (d.n == 0) return cudaSuccess;
-  const NormArgs a = {x, residual, weight, bias, x_stride, residual_stride, s, y, stats, d.n, d.H,
-                      d.weight_dtype == MOE_F32, d.rms != 0, d.eps};
+  NormArgs a = {x, residual, weight, bias, x_stride, residual_stride, s, y, stats, d.n, d.H,
+                d.weight_dtype == MOE_F32, d.rms != 0, d.eps, 0, false};
   return d.dtype == MOE_F32 ? forward<float>(a, st) : forward<__nv_bfloat16>(a, st);
 }
 

@@ -4,13 +4,13 @@
 // VALS values to a thread.  A persistent CTA holds several groups; each copies
 // its next rows asynchronously into a ring of D slots of its own in shared
 // memory, so the loads of D - 1 rows are on their way while one row's sums go
-// through the group.  Three ways into the ring:
-//   VEC            16 bytes a copy; a thread copies what it will read itself,
-//                  so no barrier is needed.
-//   words, float   4 bytes a copy, likewise.
-//   words, bf16    rows that do not start on 16 bytes, perhaps not even on 4:
-//                  the 4-byte words that cover the row, one barrier a row, and
-//                  values read at the row's offset in its first word.
+// through the group.  A thread copies the 16-byte pieces that it will read
+// itself, so the ring needs no barrier.
+//
+// Rows of odd length do not begin on 16 bytes.  A group's rows are a multiple
+// of 8 apart, so they all begin at the same place within 16 bytes (the phase):
+// the group works on the aligned pieces that cover a row, its columns shifted
+// by the phase, and masks the row's ends.
 #pragma once
 
 #include "ptx.cuh"
@@ -37,8 +37,9 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
 }
 
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+// 16 bytes, of which `bytes` are read and the rest are zeros
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
 
@@ -67,73 +68,64 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// A thread's VALS values of a row, in pairs.
-template <typename T, bool VEC, int GS, int VALS>
+// A thread's VALS values of a row, in pairs: pieces of V values, GS apart.
+// SHIFT: rows have phases; else every piece lies inside the row or outside.
+template <typename T, int GS, int VALS, bool SHIFT>
 struct RowIO {
-  static constexpr int V = VEC ? kPer<T> : 1;
-  static constexpr bool SHARED = !VEC && sizeof(T) == 2;  // slots are read by other threads
+  static constexpr int V = kPer<T>, PIECES = VALS / V, P = VALS / 2;
   static constexpr int BYTES = GS * VALS * (int)sizeof(T);
-  static constexpr int P = VALS / 2;       // pairs
-  static constexpr int RUN = VEC ? V / 2 : 1;  // pairs that lie inside the row or outside together
-  // column of the k-th value of the group's thread t
-  static __device__ __forceinline__ int at(int k, int t) {
-    return VEC ? (k / V * GS + t) * V + k % V : k * GS + t;
+  int H, t, o;       // row length, thread of the group, phase
+  bool full[PIECES]; // all of the piece lies inside the row
+  bool live[PIECES]; // some of it does
+
+  __device__ __forceinline__ RowIO(int H_, int t_, int o_) : H(H_), t(t_), o(SHIFT ? o_ : 0) {
+#pragma unroll
+    for (int c = 0; c < PIECES; ++c) {
+      live[c] = first(c) < H;  // begins less than a piece before the row
+      full[c] = SHIFT ? first(c) >= 0 && first(c) + V <= H : live[c];
+    }
   }
-  static __device__ __forceinline__ int odd(const T *row) {
-    return SHARED ? (int)(reinterpret_cast<uintptr_t>(row) >> 1) & 1 : 0;
-  }
-  static __device__ __forceinline__ void issue(uint32_t slot, const T *row, int H, int t) {
-    if (SHARED) {
-      const int o = odd(row), end = H + o;
+  // column of a piece's first value
+  __device__ __forceinline__ int first(int c) const { return (c * GS + t) * V - (SHIFT ? o : 0); }
+  // column of value k, and whether the row has it
+  __device__ __forceinline__ int at(int k) const { return first(k / V) + k % V; }
+  __device__ __forceinline__ bool has(int k) const { return (unsigned)at(k) < (unsigned)H; }
+
+  // Asks for a row with `behind` rows behind it in the tensor.  A piece may begin
+  // before the row, inside the rows before it (the first row has phase 0), and
+  // may end behind it, but not behind the tensor.
+  __device__ __forceinline__ void issue(uint32_t slot, const T *row, long long stride,
+                                        long long behind) const {
+    if (!SHIFT) {
 #pragma unroll
-      for (int k = 0; k < VALS / 2; ++k) {
-        const int j = k * GS + t;  // word; the last may hold one value of the row
-        if (2 * j < end) cp_async4(slot + 4 * j, row - o + 2 * j, 2 * j + 2 <= end ? 4 : 2);
-      }
-    } else if (VEC) {
+      for (int c = 0; c < PIECES; ++c)
+        if (live[c]) ptx::cp_async_cg16(slot + (c * GS + t) * 16, row + first(c));
+      return;
+    }
+    const int room = behind >= V || behind * stride >= V ? V : (int)(behind * stride);
 #pragma unroll
-      for (int k = 0; k < VALS; k += V)
-        if (at(k, t) < H) ptx::cp_async_cg16(slot + at(k, t) * (int)sizeof(T), row + at(k, t));
-    } else {
-#pragma unroll
-      for (int k = 0; k < VALS; ++k)
-        if (at(k, t) < H) cp_async4(slot + 4 * at(k, t), row + at(k, t), 4);
+    for (int c = 0; c < PIECES; ++c) {
+      if (!live[c]) continue;
+      const uint32_t to = slot + (c * GS + t) * 16;
+      const int left = H + room - first(c);
+      cp_async16(to, row + first(c), left < V ? left * (int)sizeof(T) : 16);
     }
   }
   static __device__ __forceinline__ float2 pair(uint32_t u) {  // of bf16
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
   }
-  // 16 bytes as pairs, from pair i of f on
+  // 16 bytes as pairs
   static __device__ __forceinline__ void widen(uint4 u, float2 *f) {
-    if (sizeof(T) == 2) {
+    if constexpr (sizeof(T) == 2) {
       f[0] = pair(u.x), f[1] = pair(u.y), f[2] = pair(u.z), f[3] = pair(u.w);
     } else {
       f[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
       f[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
     }
   }
-  // values behind the row's end are 0
-  static __device__ __forceinline__ void read(const char *slot, int o, int H, int t,
-                                              float2 (&f)[P]) {
-    const T *p = reinterpret_cast<const T *>(slot) + (SHARED ? o : 0);
-    if (VEC) {
-#pragma unroll
-      for (int k = 0; k < VALS; k += V) {
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (at(k, t) < H) u = *reinterpret_cast<const uint4 *>(p + at(k, t));
-        widen(u, f + k / 2);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < P; ++k) {
-        f[k].x = at(2 * k, t) < H ? to_f(p[at(2 * k, t)]) : 0.f;
-        f[k].y = at(2 * k + 1, t) < H ? to_f(p[at(2 * k + 1, t)]) : 0.f;
-      }
-    }
-  }
   static __device__ __forceinline__ uint4 narrow(const float2 *f) {
     uint4 u;
-    if (sizeof(T) == 2) {
+    if constexpr (sizeof(T) == 2) {
       __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&u);
 #pragma unroll
       for (int i = 0; i < 4; ++i) h[i] = __float22bfloat162_rn(f[i]);
@@ -142,6 +134,22 @@ struct RowIO {
                      __float_as_uint(f[1].y));
     }
     return u;
+  }
+  // zeros for the values of piece c that the row does not have
+  __device__ __forceinline__ void mask(int c, float2 (&f)[P]) const {
+    if (!SHIFT || full[c]) return;
+#pragma unroll
+    for (int k = c * V; k < (c + 1) * V; ++k)
+      if (!has(k)) (k % 2 ? f[k / 2].y : f[k / 2].x) = 0.f;
+  }
+  __device__ __forceinline__ void read(const char *slot, float2 (&f)[P]) const {
+#pragma unroll
+    for (int c = 0; c < PIECES; ++c) {
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (live[c]) u = *reinterpret_cast<const uint4 *>(slot + (c * GS + t) * 16);
+      widen(u, f + c * V / 2);
+      if (live[c]) mask(c, f);
+    }
   }
   // the values rounded to T
   static __device__ __forceinline__ void round(float2 (&f)[P]) {
@@ -153,63 +161,66 @@ struct RowIO {
       }
     }
   }
-  static __device__ __forceinline__ void store(T *row, int H, int t, const float2 (&f)[P]) {
-    if (VEC) {
+  __device__ __forceinline__ void store(T *row, const float2 (&f)[P]) const {
 #pragma unroll
-      for (int k = 0; k < VALS; k += V)
-        if (at(k, t) < H) *reinterpret_cast<uint4 *>(row + at(k, t)) = narrow(f + k / 2);
-    } else {
+    for (int c = 0; c < PIECES; ++c) {
+      if (full[c]) {
+        *reinterpret_cast<uint4 *>(row + first(c)) = narrow(f + c * V / 2);
+      } else if (SHIFT && live[c]) {
 #pragma unroll
-      for (int k = 0; k < P; ++k) {
-        if (at(2 * k, t) < H) row[at(2 * k, t)] = from_f<T>(f[k].x);
-        if (at(2 * k + 1, t) < H) row[at(2 * k + 1, t)] = from_f<T>(f[k].y);
+        for (int k = c * V; k < (c + 1) * V; ++k)
+          if (has(k)) row[at(k)] = from_f<T>(k % 2 ? f[k / 2].y : f[k / 2].x);
       }
     }
   }
-  // weight or bias at the same columns, from global memory
-  static __device__ __forceinline__ void param(const void *w, bool wide, int H, int t,
-                                               float2 (&f)[P]) {
-    if (VEC) {
+  // weight or bias at the same columns, from global memory; wide: float32
+  __device__ __forceinline__ void param(const void *w, bool wide, bool aligned,
+                                        float2 (&f)[P]) const {
 #pragma unroll
-      for (int k = 0; k < VALS; k += V) {
-        const int i = at(k, t);
-        if (i >= H) {
-#pragma unroll
-          for (int j = 0; j < V / 2; ++j) f[k / 2 + j] = make_float2(0.f, 0.f);
-        } else if (wide) {
+    for (int c = 0; c < PIECES; ++c) {
+      if (aligned && (!SHIFT || o == 0) && full[c]) {
+        if (wide) {
 #pragma unroll
           for (int j = 0; j < V; j += 4)
-            *reinterpret_cast<float4 *>(&f[(k + j) / 2]) =
-                __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(w) + i + j));
+            *reinterpret_cast<float4 *>(&f[(c * V + j) / 2]) = __ldg(
+                reinterpret_cast<const float4 *>(static_cast<const float *>(w) + first(c) + j));
         } else {
-          widen(__ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(w) + i)), f + k / 2);
+          widen(__ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(w) + first(c))),
+                f + c * V / 2);
         }
+        continue;
       }
-    } else {
 #pragma unroll
-      for (int k = 0; k < VALS; ++k) {
-        const int i = at(k, t);
-        (k % 2 ? f[k / 2].y : f[k / 2].x) = i >= H ? 0.f
-                                            : wide ? __ldg(static_cast<const float *>(w) + i)
-                                                   : to_f(static_cast<const T *>(w)[i]);
-      }
+      for (int k = c * V; k < (c + 1) * V; ++k)
+        (k % 2 ? f[k / 2].y : f[k / 2].x) =
+            !has(k) ? 0.f
+            : wide  ? __ldg(static_cast<const float *>(w) + at(k))
+                    : to_f(static_cast<const T *>(w)[at(k)]);
     }
   }
-  // f(k) for every pair k with values inside the row; of the strided forms
-  // the second value of a pair may lie behind the row's end
+  // f(c, k) for the pairs k of every piece c that the row has some of
   template <typename F>
-  static __device__ __forceinline__ void each(int H, int t, F f) {
+  __device__ __forceinline__ void each(F f) const {
 #pragma unroll
-    for (int k = 0; k < P; k += RUN) {
-      if (at(2 * k, t) < H) {
+    for (int c = 0; c < PIECES; ++c) {
+      if (live[c]) {
 #pragma unroll
-        for (int j = 0; j < RUN; ++j) f(k + j);
+        for (int k = c * V / 2; k < (c + 1) * V / 2; ++k) f(c, k);
       }
     }
   }
-  // whether both values of pair k lie inside the row
-  static __device__ __forceinline__ bool whole(int k, int H, int t) {
-    return VEC || at(2 * k + 1, t) < H;
+};
+
+// Whether rows of the given strides keep one phase: 16-byte aligned, and
+// strides equal modulo the values of 16 bytes.
+struct Phases {
+  int per, step;
+  bool one = true, first = true;
+  explicit Phases(int per_) : per(per_), step(0) {}
+  void add(const void *p, long long stride) {
+    if (!p) return;
+    if (first) step = (int)(stride % per), first = false;
+    one = one && (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % per == step;
   }
 };
 
@@ -268,28 +279,30 @@ constexpr int ring_slots() {
 }
 
 // The group for rows of H values: the smallest of which a thread takes 16, or
-// 512 threads of 32 values; G<...>::go, or false where rows are longer.
-template <typename T, bool VEC, template <typename, bool, int, int> class G, typename A>
-bool by_length(const A &a, cudaStream_t s, cudaError_t *e) {
-  const int H = a.H + (!VEC && sizeof(T) == 2);  // a word may begin one value early
-  if (H <= 8 * 16) return G<T, VEC, 8, 16>::go(a, s, e);
-  if (H <= 32 * 16) return G<T, VEC, 32, 16>::go(a, s, e);
-  if (H <= 64 * 16) return G<T, VEC, 64, 16>::go(a, s, e);
-  if (H <= 128 * 16) return G<T, VEC, 128, 16>::go(a, s, e);
-  if (H <= 256 * 16) return G<T, VEC, 256, 16>::go(a, s, e);
-  if (H <= 512 * 16) return G<T, VEC, 512, 16>::go(a, s, e);
-  if (H <= 512 * 32) return G<T, VEC, 512, 32>::go(a, s, e);
+// 512 threads of 32 values.  False where rows are longer.
+template <typename T, bool SHIFT, template <typename, int, int, bool> class G, typename A>
+bool by_length(A &a, cudaStream_t s, cudaError_t *e) {
+  const int H = a.H + (SHIFT ? kPer<T> - 1 : 0);
+  if (H <= 8 * 16) return G<T, 8, 16, SHIFT>::go(a, s, e);
+  if (H <= 32 * 16) return G<T, 32, 16, SHIFT>::go(a, s, e);
+  if (H <= 64 * 16) return G<T, 64, 16, SHIFT>::go(a, s, e);
+  if (H <= 128 * 16) return G<T, 128, 16, SHIFT>::go(a, s, e);
+  if (H <= 256 * 16) return G<T, 256, 16, SHIFT>::go(a, s, e);
+  if (H <= 512 * 16) return G<T, 512, 16, SHIFT>::go(a, s, e);
+  if (H <= 512 * 32) return G<T, 512, 32, SHIFT>::go(a, s, e);
   return false;
 }
 
 // CTAs and groups of a launch over n rows: the rows of a round lie beside each
-// other over the CTAs, so that few rows use many SMs.
+// other over the CTAs, so that few rows use many SMs.  A group's next row is a
+// multiple of 8 on.
 struct NormGrid {
   int ctas, groups;
 };
 template <int GS>
 inline NormGrid norm_grid(int n, int most) {
   NormGrid g;
+  most = most < 8 ? 8 : most - most % 8;
   g.ctas = n < most ? n : most;
   const int rows = (int)(((long long)n + g.ctas - 1) / g.ctas), all = kNormThreads / GS;
   constexpr int warp = GS < 32 ? 32 / GS : 1;  // whole warps

@@ -19,12 +19,14 @@ struct BackArgs {
   float *part;  // (2, parts, H) sums for dweight and dbias
   int n, H, parts;
   bool wide, rms, bias;
+  int phase;  // as in the forward
+  bool vec;   // weight on 16 bytes
 };
 
 // N: tensors read (dy and s; and ds)
-template <typename T, bool VEC, int GS, int VALS, int N, int D>
+template <typename T, int GS, int VALS, bool SHIFT, int N, int D>
 __global__ void __launch_bounds__(kNormThreads) norm_back_kernel(const BackArgs a) {
-  using IO = RowIO<T, VEC, GS, VALS>;
+  using IO = RowIO<T, GS, VALS, SHIFT>;
   pdl_enter();
   extern __shared__ __align__(16) char ring[];
   __shared__ __align__(16) float2 parts[2][kNormThreads / 32];
@@ -34,26 +36,28 @@ __global__ void __launch_bounds__(kNormThreads) norm_back_kernel(const BackArgs 
   const uint32_t mine32 = ptx::smem_u32(mine);
   const long long step = (long long)gridDim.x * groups;
   long long row = blockIdx.x + (long long)gridDim.x * group, ahead = row;
-  const T *dy = static_cast<const T *>(a.dy) + row * a.dys, *dy_in = dy;
-  const T *sp = static_cast<const T *>(a.s) + row * a.ss, *sp_in = sp;
-  const T *ds = static_cast<const T *>(a.ds) + (N == 3 ? row * a.dss : 0), *ds_in = ds;
+  const T *dy_in = static_cast<const T *>(a.dy) + row * a.dys;
+  const T *s_in = static_cast<const T *>(a.s) + row * a.ss;
+  const T *ds_in = static_cast<const T *>(a.ds) + (N == 3 ? row * a.dss : 0);
+  const IO io(H, t, (int)(row * a.phase % IO::V));
   T *dx = static_cast<T *>(a.dx) + row * H;
   auto issue = [&](int slot) {
     if (ahead < a.n) {
       const uint32_t to = mine32 + slot * (N * IO::BYTES);
-      IO::issue(to, dy_in, H, t);
-      IO::issue(to + IO::BYTES, sp_in, H, t);
-      if (N == 3) IO::issue(to + 2 * IO::BYTES, ds_in, H, t);
+      const long long behind = a.n - 1 - ahead;
+      io.issue(to, dy_in, a.dys, behind);
+      io.issue(to + IO::BYTES, s_in, a.ss, behind);
+      if (N == 3) io.issue(to + 2 * IO::BYTES, ds_in, a.dss, behind);
     }
     ptx::cp_async_commit();
-    ahead += step, dy_in += step * a.dys, sp_in += step * a.ss;
+    ahead += step, dy_in += step * a.dys, s_in += step * a.ss;
     if (N == 3) ds_in += step * a.dss;
   };
 #pragma unroll 1
   for (int i = 0; i < D - 1; ++i) issue(i);
   constexpr bool HOLD = VALS <= 16;  // a row's values in registers over its sum
   float2 w[IO::P], dw[IO::P], db[IO::P];
-  if (HOLD) IO::param(a.w, a.wide, H, t, w);
+  if (HOLD) io.param(a.w, a.wide, a.vec, w);
 #pragma unroll
   for (int k = 0; k < IO::P; ++k) dw[k] = db[k] = make_float2(0.f, 0.f);
   const float inv = 1.f / (float)H;
@@ -74,21 +78,22 @@ __global__ void __launch_bounds__(kNormThreads) norm_back_kernel(const BackArgs 
     stats(row + step);
     issue((i + D - 1) % D);
     ptx::cp_async_wait<D - 1>();
-    if (IO::SHARED) group_sync<GS>(group);
     const char *slot = mine + i % D * (N * IO::BYTES);
     // with d = s - mu and g = dy r: r t = g w, and the sums of r t and r t d
     // give r c1 and c2
     float2 g[IO::P], d[IO::P];
     float2 s1 = make_float2(0.f, 0.f), s2 = s1;
     auto fetch = [&](bool sums) {
-      IO::read(slot, IO::odd(dy), H, t, g);
-      IO::read(slot + IO::BYTES, IO::odd(sp), H, t, d);
-      if (!HOLD) IO::param(a.w, a.wide, H, t, w);
-      IO::each(H, t, [&](int k) {  // g is 0 behind the row's end
-        d[k] = add2(d[k], mu);
+      io.read(slot, g);
+      io.read(slot + IO::BYTES, d);
+      if (!HOLD) io.param(a.w, a.wide, a.vec, w);
+#pragma unroll
+      for (int k = 0; k < IO::P; ++k) d[k] = add2(d[k], mu);
+#pragma unroll
+      for (int c = 0; c < IO::PIECES; ++c) io.mask(c, d);
+      io.each([&](int, int k) {
         if (sums) db[k] = add2(db[k], g[k]);
         g[k] = mul2(g[k], r);
-        if (!IO::whole(k, H, t)) d[k].y = 0.f;
         if (sums) dw[k] = fma2(g[k], d[k], dw[k]);
         g[k] = mul2(g[k], w[k]);
         if (sums) s1 = add2(s1, g[k]), s2 = fma2(g[k], d[k], s2);
@@ -102,15 +107,13 @@ __global__ void __launch_bounds__(kNormThreads) norm_back_kernel(const BackArgs 
 #pragma unroll
       for (int k = 0; k < IO::P; ++k) g[k] = fma2(d[k], c2, add2(g[k], c1));
       if (N == 3) {
-        IO::read(slot + 2 * IO::BYTES, IO::odd(ds), H, t, d);
+        io.read(slot + 2 * IO::BYTES, d);
 #pragma unroll
         for (int k = 0; k < IO::P; ++k) g[k] = add2(g[k], d[k]);
       }
-      IO::store(dx, H, t, g);
+      io.store(dx, g);
     }
-    row += step, dy += step * a.dys, sp += step * a.ss, dx += step * H;
-    if (N == 3) ds += step * a.dss;
-    if (IO::SHARED) group_sync<GS>(group);  // the slot may be filled again
+    row += step, dx += step * H;
   }
   // the CTA's sums, group by group
   float *out = a.part + (size_t)blockIdx.x * H;
@@ -120,9 +123,10 @@ __global__ void __launch_bounds__(kNormThreads) norm_back_kernel(const BackArgs 
     float *all = reinterpret_cast<float *>(ring);
     for (int pass = 0; pass < (a.bias ? 2 : 1); ++pass, out += (size_t)a.parts * H) {
 #pragma unroll
-      for (int k = 0; k < VALS; ++k)
-        if (IO::at(k, t) < H)
-          all[group * H + IO::at(k, t)] = k % 2 ? (pass ? db : dw)[k / 2].y : (pass ? db : dw)[k / 2].x;
+      for (int k = 0; k < VALS; ++k) {
+        const float2 v = (pass ? db : dw)[k / 2];
+        if (io.has(k)) all[group * H + io.at(k)] = k % 2 ? v.y : v.x;
+      }
       __syncthreads();
       for (int c = threadIdx.x; c < H; c += blockDim.x) {
         float v = all[c];
@@ -135,9 +139,9 @@ __global__ void __launch_bounds__(kNormThreads) norm_back_kernel(const BackArgs 
   }
 #pragma unroll
   for (int k = 0; k < VALS; ++k) {
-    if (IO::at(k, t) < H) {
-      out[IO::at(k, t)] = k % 2 ? dw[k / 2].y : dw[k / 2].x;
-      if (a.bias) out[(size_t)a.parts * H + IO::at(k, t)] = k % 2 ? db[k / 2].y : db[k / 2].x;
+    if (io.has(k)) {
+      out[io.at(k)] = k % 2 ? dw[k / 2].y : dw[k / 2].x;
+      if (a.bias) out[(size_t)a.parts * H + io.at(k)] = k % 2 ? db[k / 2].y : db[k / 2].x;
     }
   }
 }
@@ -223,48 +227,42 @@ __global__ void __launch_bounds__(32 * kWarps)
   out[col] = v;
 }
 
-template <typename T, bool VEC, int GS, int VALS>
+template <typename T, int GS, int VALS, bool SHIFT>
 struct Backward {
   template <int N>
-  static bool with(const BackArgs &a, cudaStream_t s, cudaError_t *e) {
+  static bool with(BackArgs &a, cudaStream_t s, cudaError_t *e) {
     constexpr int D = ring_slots<T, VALS, N>();
     if constexpr (D == 0) {
       return false;
     } else {
-      BackArgs b = a;
       const int sms = device_sm_count();
       const NormGrid g = norm_grid<GS>(a.n, sms < kNormParts ? sms : kNormParts);
-      b.parts = g.ctas;
-      constexpr int one = D * N * RowIO<T, VEC, GS, VALS>::BYTES;
+      a.parts = g.ctas;
+      constexpr int one = D * N * RowIO<T, GS, VALS, SHIFT>::BYTES;
       // the groups' sums are joined in the ring
       static_assert(one >= GS * VALS * 4, "ring");
-      auto kernel = norm_back_kernel<T, VEC, GS, VALS, N, D>;
+      auto kernel = norm_back_kernel<T, GS, VALS, SHIFT, N, D>;
       static bool ready[64] = {false};
       *e = allow_smem(kernel, one * (kNormThreads / GS), ready);
       if (*e == cudaSuccess)
-        *e = launch_pdl(kernel, dim3(g.ctas), dim3(g.groups * GS), one * g.groups, s, b);
+        *e = launch_pdl(kernel, dim3(g.ctas), dim3(g.groups * GS), one * g.groups, s, a);
       return true;
     }
   }
-  static bool go(const BackArgs &a, cudaStream_t s, cudaError_t *e) {
+  static bool go(BackArgs &a, cudaStream_t s, cudaError_t *e) {
     return a.ds ? with<3>(a, s, e) : with<2>(a, s, e);
   }
 };
 
 template <typename T>
-cudaError_t backward(const BackArgs &a, float *dweight, float *dbias, cudaStream_t s) {
+cudaError_t backward(BackArgs &a, float *dweight, float *dbias, cudaStream_t s) {
+  Phases ph(kPer<T>);
+  ph.add(a.dy, a.dys), ph.add(a.s, a.ss), ph.add(a.ds, a.dss), ph.add(a.dx, a.H);
+  a.phase = ph.step;
+  a.vec = on_bytes(a.w, 16);
   cudaError_t e = cudaSuccess;
-  constexpr int per = kPer<T>;
-  const bool vec = a.H % per == 0 && a.dys % per == 0 && a.ss % per == 0 && on_bytes(a.dy, 16) &&
-                   on_bytes(a.s, 16) && on_bytes(a.dx, 16) && on_bytes(a.w, 16) &&
-                   (!a.ds || (a.dss % per == 0 && on_bytes(a.ds, 16)));
-  int parts = device_sm_count();
-  parts = parts < kNormParts ? parts : kNormParts;
-  const bool ring = vec ? by_length<T, true, Backward>(a, s, &e)
-                        : on_bytes(a.dy, 4) && on_bytes(a.s, 4) && on_bytes(a.ds, 4) &&
-                              by_length<T, false, Backward>(a, s, &e);
-  if (!ring) {
-    parts = kNormParts;
+  if (!ph.one || !(ph.step || a.H % kPer<T> ? by_length<T, true, Backward>(a, s, &e)
+                                          : by_length<T, false, Backward>(a, s, &e))) {
     e = launch_pdl(norm_back_long_kernel<T>, dim3(a.n), dim3(1024), 0, s, a);
     if (e == cudaSuccess)
       e = launch_pdl(norm_columns_kernel<T>, dim3((a.H + 31) / 32, a.parts), dim3(32 * kWarps), 0,
@@ -272,7 +270,7 @@ cudaError_t backward(const BackArgs &a, float *dweight, float *dbias, cudaStream
   }
   if (e != cudaSuccess) return e;
   return launch_pdl(norm_join_kernel, dim3((a.H + 31) / 32, dbias ? 2 : 1), dim3(32 * kWarps), 0,
-                    s, (const float *)a.part, a.n < parts ? a.n : parts, a.H, dweight, dbias);
+                    s, (const float *)a.part, a.parts, a.H, dweight, dbias);
 }
 
 }  // namespace
@@ -291,9 +289,9 @@ cudaError_t launch_norm_backward(const moe_norm_t &d, const void *dy, long long 
     if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, sizeof(float) * d.H, st);
     return e;
   }
-  const BackArgs a = {dy, s, weight, ds, dy_stride, s_stride, ds_stride, stats, dx,
-                      static_cast<float *>(ws), d.n, d.H, d.n < kNormParts ? d.n : kNormParts,
-                      d.weight_dtype == MOE_F32, d.rms != 0, dbias != nullptr};
+  BackArgs a = {dy, s, weight, ds, dy_stride, s_stride, ds_stride, stats, dx,
+                static_cast<float *>(ws), d.n, d.H, d.n < kNormParts ? d.n : kNormParts,
+                d.weight_dtype == MOE_F32, d.rms != 0, dbias != nullptr, 0, false};
   return d.dtype == MOE_F32 ? backward<float>(a, dweight, dbias, st)
                             : backward<__nv_bfloat16>(a, dweight, dbias, st);
 }

@@ -49,53 +49,72 @@ class LayerNorm:
         _want(dtype in (_F32, _BF16), "dtype: float32 or bfloat16")
         self.weight, self.bias, self.dtype, self.H = weight, bias, dtype, weight.shape[0]
         self.device, self._index = weight.device, _index(weight.device)
+        self._dev = weight.get_device()
         self._form = (self.H, _DT[dtype], _DT[weight.dtype], int(bool(rms)), float(eps))
         self._w, self._b = weight.data_ptr(), None if bias is None else bias.data_ptr()
+        self._refs = {}  # descriptions by number of rows
         lib = _lib.load()
         self._forward, self._backward = lib.moe_layer_norm, lib.moe_layer_norm_backward
         self._ws_size = lib.moe_layer_norm_backward_workspace_size
-        if self._ws_size(ctypes.byref(_lib.NormDesc(1, *self._form))) == 0:  # the library's reason
-            _check(self._forward(ctypes.byref(_lib.NormDesc(0, *self._form)), None, 0, None, 0,
-                                 *[None] * 6), "LayerNorm")
+        if self._ws_size(self._ref_for(1)[0]) == 0:  # the library's own reason
+            _check(self._forward(self._ref_for(0)[0], None, 0, None, 0, *[None] * 6), "LayerNorm")
 
-    def _rows(self, t, n, name):
+    def _ref_for(self, n):
+        """The description of n rows, which no other call changes, and the bytes
+        of scratch that its backward needs."""
+        ref = self._refs.get(n)
+        if ref is None:
+            if len(self._refs) > 1000:
+                self._refs = {}
+            ref = ctypes.byref(_lib.NormDesc(n, *self._form))
+            ref = self._refs[n] = (ref, self._ws_size(ref))
+        return ref
+
+    def _rows(self, t, shape, name):
         """Pointer and row stride of a (n, H) tensor whose rows are contiguous."""
-        if (t.dtype is not self.dtype or t.shape != (n, self.H) or t.device != self.device
-                or (t.stride(1) != 1 and self.H != 1)):
-            raise ValueError(f"{name}: ({n}, {self.H}) {self.dtype} on {self.device}, "
+        st = t.stride()
+        if (t.dtype is not self.dtype or t.shape != shape or t.get_device() != self._dev
+                or (st[1] != 1 and self.H != 1)):
+            raise ValueError(f"{name}: {tuple(shape)} {self.dtype} on {self.device}, "
                              "rows contiguous")
-        return t.data_ptr(), t.stride(0)
+        return t.data_ptr(), st[0]
 
-    def _out(self, t, shape, dtype, name, stream):
-        if t is None:
-            return _empty(shape, dtype, self.device, stream)
+    def _first(self, t, name):
+        """Shape, pointer and row stride of the tensor that says how many rows there are."""
+        shape = t.shape
+        _want(len(shape) == 2 and shape[1] == self.H, f"{name}: (n, {self.H})")
+        return shape, *self._rows(t, shape, name)
+
+    def _out(self, t, shape, dtype, name):
+        """Pointer of a given contiguous tensor."""
         if (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
-                or t.device != self.device):
+                or t.get_device() != self._dev):
             raise ValueError(f"{name}: contiguous {tuple(shape)} {dtype} on {self.device}")
-        return t
+        return t.data_ptr()
 
     def __call__(self, x, residual=None, y=None, s=None, stats=None, stream=None):
         """y (n, H) of the rows x (n, H); with residual (n, H), of s = x +
         residual, and (y, s) is returned.  y and s are allocated when not
         given.  stats: (2, n) float32 to fill with means and reciprocal
         deviations for backward, or None."""
-        _want(x.dim() == 2, "x: (n, H)")
-        n = x.shape[0]
-        xp, xs = self._rows(x, n, "x")
-        rp, rs, sp = None, 0, None
+        shape, xp, xs = self._first(x, "x")
+        n = shape[0]
+        rp, rs, sp, tp = None, 0, None, None
         _here(self.device, self._index)
         if residual is not None:
-            rp, rs = self._rows(residual, n, "residual")
-            s = self._out(s, x.shape, self.dtype, "s", stream)
-            sp = s.data_ptr()
-        else:
-            _want(s is None, "s without residual")
-        y = self._out(y, x.shape, self.dtype, "y", stream)
-        tp = None
+            rp, rs = self._rows(residual, shape, "residual")
+            if s is None:
+                s = _empty(shape, self.dtype, self.device, stream)
+            sp = self._out(s, shape, self.dtype, "s")
+        elif s is not None:
+            raise ValueError("s without residual")
+        if y is None:
+            y = _empty(shape, self.dtype, self.device, stream)
+        yp = self._out(y, shape, self.dtype, "y")
         if stats is not None:
-            tp = self._out(stats, (2, n), _F32, "stats", stream).data_ptr()
-        st = self._forward(ctypes.byref(_lib.NormDesc(n, *self._form)), xp, xs, rp, rs, self._w,
-                           self._b, sp, y.data_ptr(), tp, _handle(stream, self._index))
+            tp = self._out(stats, (2, n), _F32, "stats")
+        st = self._forward(self._ref_for(n)[0], xp, xs, rp, rs, self._w, self._b, sp, yp, tp,
+                           _handle(stream, self._index))
         if st:
             raise MoEError(st, "moe_layer_norm")
         return y if residual is None else (y, s)
@@ -106,27 +125,28 @@ class LayerNorm:
         H): a gradient that reaches s by other ways, added to dx.  dx is of the
         rows' type, dweight and dbias (H,) float32 (None without a bias); they
         are allocated when not given and overwritten."""
-        _want(dy.dim() == 2, "dy: (n, H)")
-        n = dy.shape[0]
-        dp, dst = self._rows(dy, n, "dy")
-        sp, sst = self._rows(s, n, "s")
-        ep, est = (None, 0) if ds is None else self._rows(ds, n, "ds")
+        shape, dp, dst = self._first(dy, "dy")
+        n, vec = shape[0], (self.H,)
+        sp, sst = self._rows(s, shape, "s")
+        ep, est = (None, 0) if ds is None else self._rows(ds, shape, "ds")
         _here(self.device, self._index)
-        tp = self._out(stats, (2, n), _F32, "stats", stream).data_ptr()
-        dx = self._out(dx, dy.shape, self.dtype, "dx", stream)
-        dweight = self._out(dweight, (self.H,), _F32, "dweight", stream)
+        tp = self._out(stats, (2, n), _F32, "stats")
+        if dx is None:
+            dx = _empty(shape, self.dtype, self.device, stream)
+        if dweight is None:
+            dweight = _empty(vec, _F32, self.device, stream)
+        bp = None
         if self._b is not None:
-            dbias = self._out(dbias, (self.H,), _F32, "dbias", stream)
-        else:
-            _want(dbias is None, "dbias without a bias")
-        ref = ctypes.byref(_lib.NormDesc(n, *self._form))
-        ws, nbytes = None, 0
-        if n:
-            nbytes = self._ws_size(ref)
-            ws = _empty((nbytes,), torch.uint8, self.device, stream)
-        st = self._backward(ref, dp, dst, sp, sst, tp, self._w, ep, est, dx.data_ptr(),
-                            dweight.data_ptr(), None if dbias is None else dbias.data_ptr(),
-                            None if ws is None else ws.data_ptr(), nbytes,
+            if dbias is None:
+                dbias = _empty(vec, _F32, self.device, stream)
+            bp = self._out(dbias, vec, _F32, "dbias")
+        elif dbias is not None:
+            raise ValueError("dbias without a bias")
+        ref, nbytes = self._ref_for(n)
+        ws = _empty(nbytes, torch.uint8, self.device, stream)
+        st = self._backward(ref, dp, dst, sp, sst, tp, self._w, ep, est,
+                            self._out(dx, shape, self.dtype, "dx"),
+                            self._out(dweight, vec, _F32, "dweight"), bp, ws.data_ptr(), nbytes,
                             _handle(stream, self._index))
         if st:
             raise MoEError(st, "moe_layer_norm_backward")
@@ -173,10 +193,10 @@ class GradNorm:
         given): the root of the sum of all squares, and min(1, max_norm / (norm
         + 1e-6)), the grad_scale of a clipped AdamW step."""
         _here(self.device, self._index)
-        norm = _empty((1,), _F32, self.device, stream) if norm is None else norm
-        factor = _empty((1,), _F32, self.device, stream) if factor is None else factor
+        norm = _empty(1, _F32, self.device, stream) if norm is None else norm
+        factor = _empty(1, _F32, self.device, stream) if factor is None else factor
         np_, fp = _scalar(norm, self.device, "norm"), _scalar(factor, self.device, "factor")
-        ws = _empty((max(self._nbytes, 1),), torch.uint8, self.device, stream)
+        ws = _empty(self._nbytes, torch.uint8, self.device, stream)
         st = self._call(self._list, len(self.grads), max_norm, np_, fp, ws.data_ptr(),
                         self._nbytes, _handle(stream, self._index))
         if st:
