@@ -708,8 +708,9 @@ moe_status_t moe_grad_norm(const moe_tensor_t *tensors, int32_t count, float max
  *   m = beta1 m + (1 - beta1) g;  v = beta2 v + ((1 - beta2) g) g
  *   p = p (1 - lr weight_decay)
  *       - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
- * in float32; each product and sum of m and v is rounded by itself.  p is the
- * master where there is one (param becomes its rounding), else param.
+ * in float32.  The products (1 - beta1) g and ((1 - beta2) g) g are rounded,
+ * beta m and beta v are added to them fused (one rounding).  p is the master
+ * where there is one (param becomes its rounding), else param.
  *
  * state_dtype MOE_F32: m and v are numel float32.  MOE_E4M3: m and v are numel
  * e4m3 codes, and m_scale, v_scale ceil(numel / 256) float32; 256 neighbouring

@@ -291,7 +291,8 @@ B1, B2, EPS, LR, WD = 0.9, 0.95, 1e-8, 3e-3, 0.1
 
 
 class Plain:
-    """The same step on CPU copies: moments in float32, operation by operation;
+    """The same step on CPU copies: moments in float32, in the
+    interface's operations;
     parameters in float64 with their bound."""
 
     def __init__(self, opt, state):

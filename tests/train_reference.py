@@ -104,10 +104,12 @@ def encode(x, positive):
 
 
 def adamw_moments(g, m, v, b1, b2):
-    """m, v and sqrt(v) in float32, each product and sum rounded by itself."""
+    """m, v and sqrt(v) in float32: the gradient's terms rounded, the rest fused
+    (a product of two float32 values is exact in float64)."""
     f = lambda x: torch.tensor(x, dtype=torch.float32)  # noqa: E731
-    m = m * f(b1) + g * f(1 - b1)
-    v = v * f(b2) + (g * f(1 - b2)) * g
+    fma = lambda a, b, c: (a.double() * b.double() + c.double()).float()  # noqa: E731
+    m = fma(m, f(b1), g * f(1 - b1))
+    v = fma(v, f(b2), (g * f(1 - b2)) * g)
     return m, v, v.sqrt()
 
 

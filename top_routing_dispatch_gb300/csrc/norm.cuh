@@ -13,6 +13,7 @@
 // by the phase, and masks the row's ends.
 #pragma once
 
+#include "pairs.cuh"
 #include "ptx.cuh"
 #include "train.cuh"
 
@@ -43,31 +44,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int by
                : "memory");
 }
 
-// Two float32 operations in one instruction, each rounded as its single form
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<unsigned long long &>(d))
-      : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
-  return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<unsigned long long &>(d))
-      : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
-  return d;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<unsigned long long &>(d))
-      : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)),
-        "l"(reinterpret_cast<unsigned long long &>(c)));
-  return d;
-}
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-
 // A thread's VALS values of a row, in pairs: pieces of V values, GS apart.
 // SHIFT: rows have phases; else every piece lies inside the row or outside.
 template <typename T, int GS, int VALS, bool SHIFT>
@@ -96,19 +72,16 @@ struct RowIO {
   // may end behind it, but not behind the tensor.
   __device__ __forceinline__ void issue(uint32_t slot, const T *row, long long stride,
                                         long long behind) const {
-    if (!SHIFT) {
-#pragma unroll
-      for (int c = 0; c < PIECES; ++c)
-        if (live[c]) ptx::cp_async_cg16(slot + (c * GS + t) * 16, row + first(c));
-      return;
-    }
     const int room = behind >= V || behind * stride >= V ? V : (int)(behind * stride);
 #pragma unroll
     for (int c = 0; c < PIECES; ++c) {
       if (!live[c]) continue;
       const uint32_t to = slot + (c * GS + t) * 16;
       const int left = H + room - first(c);
-      cp_async16(to, row + first(c), left < V ? left * (int)sizeof(T) : 16);
+      if (!SHIFT || left >= V)
+        ptx::cp_async_cg16(to, row + first(c));
+      else
+        cp_async16(to, row + first(c), left * (int)sizeof(T));
     }
   }
   static __device__ __forceinline__ float2 pair(uint32_t u) {  // of bf16
@@ -137,10 +110,12 @@ struct RowIO {
   }
   // zeros for the values of piece c that the row does not have
   __device__ __forceinline__ void mask(int c, float2 (&f)[P]) const {
-    if (!SHIFT || full[c]) return;
+    if constexpr (SHIFT) {
+      if (full[c]) return;
 #pragma unroll
-    for (int k = c * V; k < (c + 1) * V; ++k)
-      if (!has(k)) (k % 2 ? f[k / 2].y : f[k / 2].x) = 0.f;
+      for (int k = c * V; k < (c + 1) * V; ++k)
+        if (!has(k)) (k % 2 ? f[k / 2].y : f[k / 2].x) = 0.f;
+    }
   }
   __device__ __forceinline__ void read(const char *slot, float2 (&f)[P]) const {
 #pragma unroll
