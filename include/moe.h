@@ -740,7 +740,7 @@ typedef struct {
   const float *lr_device;  /* one float32 (device) that replaces lr, or NULL */
   const float *grad_scale; /* one float32 (device), or NULL: 1 */
   double beta1, beta2;     /* at least 0, below 1 */
-  float eps;               /* above 0 */
+  float eps;               /* at least 2^-126 */
 } moe_adamw_t;
 
 /*

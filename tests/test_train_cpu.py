@@ -142,7 +142,7 @@ def step(lib, o=None, t=None, count=1, state=P):
 def test_adamw_refusals(lib):
     for kw in (dict(state_dtype=1), dict(state_dtype=3), dict(lr=-1e-3), dict(lr=math.nan),
                dict(lr=math.inf), dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=1.0),
-               dict(beta2=math.nan), dict(eps=0.0), dict(eps=-1e-8), dict(eps=math.inf),
+               dict(beta2=math.nan), dict(eps=0.0), dict(eps=1e-39), dict(eps=-1e-8), dict(eps=math.inf),
                dict(lr_device=P + 2), dict(grad_scale=P + 1)):
         assert step(lib, opt(**kw)) == INVALID, kw
     for kw in (dict(param=None), dict(grad=None), dict(m=None), dict(v=None), dict(numel=-1),

@@ -25,6 +25,8 @@
 // NaN, a tiny v or a zero code needs stands apart behind one test.
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "pairs.cuh"
 #include "train.cuh"
 
@@ -32,7 +34,8 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kMostBlocks = 8;  // of a warp's turn
+constexpr int kCtas = 3;         // of an SM
+constexpr int kMostBlocks = 16;  // of a warp's turn
 constexpr float kInvMax = (float)(1.0 / 448.0);
 constexpr float kTiny = 0x1p-100f;  // the least largest value that a scale is made for
 constexpr uint32_t kInfBits = 0x7f800000u;
@@ -81,96 +84,116 @@ struct StepArgs {
   bool last;                 // launch of the step
 };
 
-// sqrt(v), rounded to nearest: one Newton step with a fused residual (Markstein)
-// from the approximate reciprocal root; below 2^-96 the residual would
-// underflow.  Equal to __fsqrt_rn for every float32 from 2^-102 up (tried).
+// The tensor that a turn belongs to, from k on: the last that does not begin
+// behind it.
+template <typename A>
+__device__ __forceinline__ int tensor_of(const A &a, int turn, int k) {
+  if (k + 1 >= a.count || turn < a.t[k + 1].first) return k;
+  int lo = k + 1, hi = a.count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    (turn < a.t[mid].first ? hi : lo) = mid;
+  }
+  return lo;
+}
+
+// Roots and reciprocals rounded to nearest, by one Newton step with a fused
+// residual (Markstein) from the hardware's approximations.  Compared with
+// __fsqrt_rn and __frcp_rn on every float32: equal from 2^-102 up (below, the
+// residual underflows), and from 2^-126 to 2^126.
+__device__ __forceinline__ float approx_rsqrt(float v) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
+  return y;
+}
+__device__ __forceinline__ float approx_rcp(float x) {  // within 2 u
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float2 root2(float2 v) {
-  const float2 y = make_float2(rsqrtf(v.x), rsqrtf(v.y));
+  const float2 y = make_float2(approx_rsqrt(v.x), approx_rsqrt(v.y));
   const float2 s = mul2(v, y);
   return fma2(fma2(mul2(s, both(-1.f)), s, v), mul2(y, both(0.5f)), s);
 }
 __device__ __forceinline__ bool plain_root(uint32_t bits) {
   return bits >= 0x0f800000u && bits < kInfBits;  // 2^-96 to the largest finite
 }
-
-__device__ __forceinline__ float reciprocal(float x) {  // within 2 u
-  float y;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+__device__ __forceinline__ float reciprocal(float x) {
+  const float y = approx_rcp(x);
+  return fmaf(fmaf(-x, y, 1.f), y, y);
 }
 
-// 4 neighbouring values from `at` as two pairs; those past `left` are 0
-template <typename T, bool FULL>
-__device__ __forceinline__ void load4(const void *p, long long at, int left, float2 *f) {
-  const T *q = static_cast<const T *>(p) + at;
-  if constexpr (FULL && sizeof(T) == 2) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(q);
-    f[0] = make_float2(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u));
-    f[1] = make_float2(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-  } else if constexpr (FULL) {
-    const float4 u = *reinterpret_cast<const float4 *>(q);
-    f[0] = make_float2(u.x, u.y), f[1] = make_float2(u.z, u.w);
-  } else {
-    float e[4];
+// 4 neighbouring values as they lie in memory; those past `left` are 0
+template <typename T>
+struct Raw4 {
+  static constexpr int W = (int)sizeof(T);  // words
+  uint32_t w[W];
+  template <bool FULL>
+  __device__ __forceinline__ void load(const T *q, int left) {
+    if constexpr (FULL && sizeof(T) == 4) {
+      const uint4 u = *reinterpret_cast<const uint4 *>(q);
+      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    } else if constexpr (FULL && sizeof(T) == 2) {
+      const uint2 u = *reinterpret_cast<const uint2 *>(q);
+      w[0] = u.x, w[1] = u.y;
+    } else if constexpr (FULL) {
+      w[0] = *reinterpret_cast<const uint32_t *>(q);
+    } else {
+      T e[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) e[i] = i < left ? (float)q[i] : 0.f;
-    f[0] = make_float2(e[0], e[1]), f[1] = make_float2(e[2], e[3]);
-  }
-}
-
-template <typename T, bool FULL>
-__device__ __forceinline__ void store4(void *p, long long at, int left, const float2 *f) {
-  T *q = static_cast<T *>(p) + at;
-  if constexpr (FULL && sizeof(T) == 2) {
-    uint2 u;
-    reinterpret_cast<__nv_bfloat162 *>(&u)[0] = __float22bfloat162_rn(f[0]);
-    reinterpret_cast<__nv_bfloat162 *>(&u)[1] = __float22bfloat162_rn(f[1]);
-    *reinterpret_cast<uint2 *>(q) = u;
-  } else if constexpr (FULL) {
-    *reinterpret_cast<float4 *>(q) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-  } else {
-    const float e[4] = {f[0].x, f[0].y, f[1].x, f[1].y};
+      for (int i = 0; i < 4; ++i) e[i] = i < left ? q[i] : T{};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < left) q[i] = (T)e[i];
+      for (int i = 0; i < W; ++i) w[i] = reinterpret_cast<const uint32_t *>(e)[i];
+    }
   }
-}
-
-template <bool FULL>
-__device__ __forceinline__ uint32_t load_codes(const void *p, long long at, int left) {
-  const uint8_t *q = static_cast<const uint8_t *>(p) + at;
-  uint32_t u = 0;
-  if constexpr (FULL) {
-    u = *reinterpret_cast<const uint32_t *>(q);
-  } else {
+  template <bool FULL>
+  __device__ __forceinline__ void store(T *q, int left) const {
+    if constexpr (FULL && sizeof(T) == 4) {
+      *reinterpret_cast<uint4 *>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else if constexpr (FULL && sizeof(T) == 2) {
+      *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
+    } else if constexpr (FULL) {
+      *reinterpret_cast<uint32_t *>(q) = w[0];
+    } else {
+      const T *e = reinterpret_cast<const T *>(w);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < left) u |= (uint32_t)q[i] << (8 * i);
+      for (int i = 0; i < 4; ++i)
+        if (i < left) q[i] = e[i];
+    }
   }
-  return u;
-}
-template <bool FULL>
-__device__ __forceinline__ void store_codes(void *p, long long at, int left, uint32_t u) {
-  uint8_t *q = static_cast<uint8_t *>(p) + at;
-  if constexpr (FULL) {
-    *reinterpret_cast<uint32_t *>(q) = u;
-  } else {
+  __device__ __forceinline__ void get(float2 *f) const {
+    if constexpr (sizeof(T) == 4) {
+      f[0] = make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+      f[1] = make_float2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+    } else if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < left) q[i] = (uint8_t)(u >> (8 * i));
+      for (int i = 0; i < 2; ++i)
+        f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+            (__nv_fp8x2_storage_t)(w[0] >> (16 * i) & 0xffff), __NV_E4M3);
+        f[i] = __half22float2(__half2(h));
+      }
+    }
   }
-}
-
-__device__ __forceinline__ void decode4(uint32_t u, float2 *f) {
-  const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u & 0xffff), __NV_E4M3);
-  const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u >> 16), __NV_E4M3);
-  f[0] = __half22float2(__half2(a)), f[1] = __half22float2(__half2(b));
-}
-__device__ __forceinline__ uint32_t encode4(const float2 *f) {
-  const uint32_t a = __nv_cvt_float2_to_fp8x2(f[0], __NV_SATFINITE, __NV_E4M3);
-  const uint32_t b = __nv_cvt_float2_to_fp8x2(f[1], __NV_SATFINITE, __NV_E4M3);
-  return a | b << 16;
-}
+  __device__ __forceinline__ void set(const float2 *f) {
+    if constexpr (sizeof(T) == 4) {
+      w[0] = __float_as_uint(f[0].x), w[1] = __float_as_uint(f[0].y);
+      w[2] = __float_as_uint(f[1].x), w[3] = __float_as_uint(f[1].y);
+    } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        reinterpret_cast<__nv_bfloat162 *>(w)[i] = __float22bfloat162_rn(f[i]);
+    } else {
+      const uint32_t x = __nv_cvt_float2_to_fp8x2(f[0], __NV_SATFINITE, __NV_E4M3);
+      const uint32_t y = __nv_cvt_float2_to_fp8x2(f[1], __NV_SATFINITE, __NV_E4M3);
+      w[0] = x | y << 16;
+    }
+  }
+};
 
 // Magnitude that counts for a scale: that of a finite value
 __device__ __forceinline__ uint32_t finite_bits(float v) {
@@ -186,137 +209,178 @@ struct Step {
   bool scaled;
 };
 
-// One block of 256 values.  PT, GT: types of parameter and gradient; MASTER:
-// a float32 master of a bf16 parameter (a float32 parameter's is a copy).
-template <bool E4M3, typename PT, typename GT, bool MASTER, bool FULL>
-__device__ __forceinline__ void step_block(const Tensor &t, const Step &c, long long block,
-                                           int lane) {
-  const long long base = block * kAdamBlock;
-  float2 g[4], p[4], m[4], v[4], root[4];
-  float ms = 0.f, vs = 0.f;
-  int left[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const long long at = base + 128 * h + 4 * lane;
-    left[h] = FULL ? 4 : (int)(t.numel - at < 4 ? t.numel - at : 4);
-    load4<GT, FULL>(t.grad, at, left[h], g + 2 * h);
-    if (MASTER || t.master)
-      load4<float, FULL>(t.master, at, left[h], p + 2 * h);
-    else
-      load4<PT, FULL>(t.param, at, left[h], p + 2 * h);
-    if (E4M3) {
-      decode4(load_codes<FULL>(t.m, at, left[h]), m + 2 * h);
-      decode4(load_codes<FULL>(t.v, at, left[h]), v + 2 * h);
-    } else {
-      load4<float, FULL>(t.m, at, left[h], m + 2 * h);
-      load4<float, FULL>(t.v, at, left[h], v + 2 * h);
+// A lane's part of a block of 256 values.  PT, GT: types of parameter and
+// gradient; MASTER: a bf16 parameter's float32 master (a float32 parameter's
+// is a copy, written where there is one).
+template <bool E4M3, typename PT, typename GT, bool MASTER>
+struct Block {
+  using ST = typename std::conditional<E4M3, uint8_t, float>::type;
+  using WT = typename std::conditional<MASTER, float, PT>::type;  // what the step starts from
+  Raw4<GT> g[2];
+  Raw4<WT> p[2];
+  Raw4<ST> m[2], v[2];
+  float ms, vs;
+
+  // the lane's place in the tensors; a block's halves are 128 values apart
+  struct Place {
+    const GT *g;
+    PT *p;
+    float *w;  // master, or NULL
+    ST *m, *v;
+    float *ms, *vs;
+    int left[2];  // values that the lane has of a partial block
+    __device__ __forceinline__ Place(const Tensor &t, long long block, int lane) {
+      const long long at = block * kAdamBlock + 4 * lane;
+      g = static_cast<const GT *>(t.grad) + at;
+      p = static_cast<PT *>(t.param) + at;
+      w = MASTER || (sizeof(PT) == 4 && t.master) ? t.master + at : nullptr;
+      m = static_cast<ST *>(t.m) + at, v = static_cast<ST *>(t.v) + at;
+      ms = t.ms + block, vs = t.vs + block;
+      const long long rest = t.numel - at;
+      left[0] = rest < 4 ? (int)rest : 4;
+      left[1] = rest < 132 ? (int)rest - 128 : 4;
     }
-  }
-  if (E4M3) ms = t.ms[block], vs = t.vs[block];
-  uint32_t top_v = 0, low_v = ~0u;
-  float top_m = 0.f;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (c.scaled) g[k] = mul2(g[k], both(c.fac));
-    if (E4M3) {
-      m[k] = mul2(m[k], both(ms));
-      v[k] = mul2(v[k], both(vs));
-      v[k] = mul2(v[k], v[k]);
+    __device__ __forceinline__ void next() {
+      g += kAdamBlock, p += kAdamBlock, m += kAdamBlock, v += kAdamBlock;
+      if (MASTER || (sizeof(PT) == 4 && w)) w += kAdamBlock;
+      if (E4M3) ++ms, ++vs;
     }
-    m[k] = fma2(m[k], both(c.b1), mul2(g[k], both(c.a1)));
-    v[k] = fma2(v[k], both(c.b2), mul2(mul2(g[k], both(c.a2)), g[k]));
-    const uint32_t x = __float_as_uint(v[k].x), y = __float_as_uint(v[k].y);
-    low_v = min(low_v, min(x, y));
-    top_v = max(top_v, max(x, y));
-    if (E4M3) top_m = fmaxf(top_m, fmaxf(fabsf(m[k].x), fabsf(m[k].y)));
-    root[k] = root2(v[k]);
-  }
-  if (!plain_root(low_v) || !plain_root(top_v)) {  // also a NaN, whose bits are larger
+  };
+
+  template <bool FULL>
+  __device__ __forceinline__ void step(const Place &t, const Step &c, int lane) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      root[k] = make_float2(__fsqrt_rn(v[k].x), __fsqrt_rn(v[k].y));
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    float2 d = fma2(root[k], both(c.c2), both(c.eps));
-    d = mul2(m[k], make_float2(reciprocal(d.x), reciprocal(d.y)));
-    p[k] = fma2(d, both(-c.c1), mul2(p[k], both(c.keep)));
-  }
-  if (E4M3) {
-    uint32_t bm = __reduce_max_sync(~0u, __float_as_uint(top_m));
-    uint32_t bv = __reduce_max_sync(~0u, top_v);
-    const bool bad = bm >= kInfBits || bv >= kInfBits;
-    if (bad) {
-      bm = bv = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        bm = max(bm, max(finite_bits(m[k].x), finite_bits(m[k].y)));
-        bv = max(bv, max(finite_bits(v[k].x), finite_bits(v[k].y)));
-      }
-      bm = __reduce_max_sync(~0u, bm);
-      bv = __reduce_max_sync(~0u, bv);
+    for (int h = 0; h < 2; ++h) {
+      const int n = t.left[h];
+      g[h].template load<FULL>(t.g + 128 * h, n);
+      if constexpr (MASTER)
+        p[h].template load<FULL>(t.w + 128 * h, n);
+      else if constexpr (sizeof(PT) == 4)
+        p[h].template load<FULL>((t.w ? t.w : t.p) + 128 * h, n);
+      else
+        p[h].template load<FULL>(t.p + 128 * h, n);
+      m[h].template load<FULL>(t.m + 128 * h, n);
+      v[h].template load<FULL>(t.v + 128 * h, n);
     }
-    ms = __fmul_rn(fmaxf(__uint_as_float(bm), kTiny), kInvMax);
-    vs = __fmul_rn(fmaxf(__fsqrt_rn(__uint_as_float(bv)), kTiny), kInvMax);
-    const float2 im = both(__frcp_rn(ms)), iv = both(__frcp_rn(vs));
-    if (lane == 0) t.ms[block] = ms, t.vs[block] = vs;
+    if (E4M3) ms = *t.ms, vs = *t.vs;
+    float2 G[4], P[4], M[4], V[4], root[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      g[h].get(G + 2 * h), p[h].get(P + 2 * h), m[h].get(M + 2 * h), v[h].get(V + 2 * h);
+    uint32_t top_v = 0, low_v = ~0u;
+    float top_m = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float2 x = mul2(m[k], im), y = mul2(root[k], iv);
-      if (bad) {
-        v[k] = make_float2(nan_if_not_finite(root[k].x, y.x), nan_if_not_finite(root[k].y, y.y));
-        m[k] = make_float2(nan_if_not_finite(m[k].x, x.x), nan_if_not_finite(m[k].y, x.y));
-      } else {
-        v[k] = y, m[k] = x;
+      if (c.scaled) G[k] = mul2(G[k], both(c.fac));
+      if (E4M3) {
+        M[k] = mul2(M[k], both(ms));
+        V[k] = mul2(V[k], both(vs));
+        V[k] = mul2(V[k], V[k]);
       }
+      M[k] = fma2(M[k], both(c.b1), mul2(G[k], both(c.a1)));
+      V[k] = fma2(V[k], both(c.b2), mul2(mul2(G[k], both(c.a2)), G[k]));
+      const uint32_t x = __float_as_uint(V[k].x), y = __float_as_uint(V[k].y);
+      low_v = min(low_v, min(x, y));
+      top_v = max(top_v, max(x, y));
+      if (E4M3) top_m = fmaxf(top_m, fmaxf(fabsf(M[k].x), fabsf(M[k].y)));
+      root[k] = root2(V[k]);
     }
-  }
+    if (!plain_root(low_v) || !plain_root(top_v)) {  // also a NaN, whose bits are larger
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const long long at = base + 128 * h + 4 * lane;
-    if (MASTER || t.master) store4<float, FULL>(t.master, at, left[h], p + 2 * h);
-    store4<PT, FULL>(t.param, at, left[h], p + 2 * h);
+      for (int k = 0; k < 4; ++k)
+        root[k] = make_float2(__fsqrt_rn(V[k].x), __fsqrt_rn(V[k].y));
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float2 d = fma2(root[k], both(c.c2), both(c.eps));
+      d = mul2(M[k], make_float2(approx_rcp(d.x), approx_rcp(d.y)));
+      P[k] = fma2(d, both(-c.c1), mul2(P[k], both(c.keep)));
+    }
     if (E4M3) {
-      uint32_t r = encode4(v + 2 * h);
-      // a positive root keeps at least the smallest code
-      if ((r - 0x01010101u) & ~r & 0x80808080u) {
-        const float2 *q = root + 2 * h;
-        const float e[4] = {q[0].x, q[0].y, q[1].x, q[1].y};
+      uint32_t bm = __reduce_max_sync(~0u, __float_as_uint(top_m));
+      uint32_t bv = __reduce_max_sync(~0u, top_v);
+      const bool bad = bm >= kInfBits || bv >= kInfBits;
+      if (bad) {
+        bm = bv = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (!(r >> (8 * i) & 0xff) && e[i] > 0.f) r |= 1u << (8 * i);
+        for (int k = 0; k < 4; ++k) {
+          bm = max(bm, max(finite_bits(M[k].x), finite_bits(M[k].y)));
+          bv = max(bv, max(finite_bits(V[k].x), finite_bits(V[k].y)));
+        }
+        bm = __reduce_max_sync(~0u, bm);
+        bv = __reduce_max_sync(~0u, bv);
       }
-      store_codes<FULL>(t.m, at, left[h], encode4(m + 2 * h));
-      store_codes<FULL>(t.v, at, left[h], r);
-    } else {
-      store4<float, FULL>(t.m, at, left[h], m + 2 * h);
-      store4<float, FULL>(t.v, at, left[h], v + 2 * h);
+      const float sm = __fmul_rn(fmaxf(__uint_as_float(bm), kTiny), kInvMax);
+      const float big = __uint_as_float(bv);
+      const float sv = __fmul_rn(
+          fmaxf(plain_root(bv) ? root2(make_float2(big, big)).x : __fsqrt_rn(big), kTiny), kInvMax);
+      const float2 im = both(reciprocal(sm)), iv = both(reciprocal(sv));
+      if (lane == 0) *t.ms = sm, *t.vs = sv;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 x = mul2(M[k], im), y = mul2(root[k], iv);
+        if (bad) {
+          V[k] = make_float2(nan_if_not_finite(root[k].x, y.x), nan_if_not_finite(root[k].y, y.y));
+          M[k] = make_float2(nan_if_not_finite(M[k].x, x.x), nan_if_not_finite(M[k].y, x.y));
+        } else {
+          V[k] = y, M[k] = x;
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int n = t.left[h];
+      Raw4<float> w;
+      Raw4<PT> q;
+      w.set(P + 2 * h), q.set(P + 2 * h);
+      if (MASTER || (sizeof(PT) == 4 && t.w)) w.template store<FULL>(t.w + 128 * h, n);
+      q.template store<FULL>(t.p + 128 * h, n);
+      m[h].set(M + 2 * h), v[h].set(V + 2 * h);
+      if constexpr (E4M3) {
+        // a positive root keeps at least the smallest code
+        uint32_t &r = v[h].w[0];
+        if ((r - 0x01010101u) & ~r & 0x80808080u) {
+          const float2 *z = root + 2 * h;
+          const float e[4] = {z[0].x, z[0].y, z[1].x, z[1].y};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!(r >> (8 * i) & 0xff) && e[i] > 0.f) r |= 1u << (8 * i);
+        }
+      }
+      m[h].template store<FULL>(t.m + 128 * h, n);
+      v[h].template store<FULL>(t.v + 128 * h, n);
     }
   }
-}
+};
 
 template <bool E4M3, typename PT, typename GT, bool MASTER, int CAP>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, kCtas)
     adamw_kernel(const __grid_constant__ StepArgs<CAP> a) {
+  using B = Block<E4M3, PT, GT, MASTER>;
   pdl_enter();
   const int lane = threadIdx.x % 32;
   const float lr = a.lr_dev ? __ldg(a.lr_dev) : a.lr;
   Step c = {1.f, a.scale ? __ldg(a.scale) : 1.f, lr * a.state->inv1, a.state->inv2, a.b1, a.a1,
             a.b2, a.a2, a.eps, a.scale != nullptr};
-  const int warps = gridDim.x * kWarps;
   int k = 0;
   // neighbouring turns on neighbouring CTAs' warps
-  for (int turn = threadIdx.x / 32 * gridDim.x + blockIdx.x; turn < a.turns; turn += warps) {
-    while (k + 1 < a.count && turn >= a.t[k + 1].first) ++k;
+  for (int turn = threadIdx.x / 32 * gridDim.x + blockIdx.x; turn < a.turns;
+       turn += gridDim.x * kWarps) {
+    k = tensor_of(a, turn, k);
     const Tensor &t = a.t[k];
     c.keep = 1.f - lr * t.decay;
-    long long block = (long long)(turn - t.first) * a.blocks;
-    const long long whole = t.vec ? t.numel / kAdamBlock : 0;
-    for (int i = 0; i < a.blocks; ++i, ++block) {
-      if (block < whole)
-        step_block<E4M3, PT, GT, MASTER, true>(t, c, block, lane);
-      else if (block * kAdamBlock < t.numel)
-        step_block<E4M3, PT, GT, MASTER, false>(t, c, block, lane);
+    const long long block = (long long)(turn - t.first) * a.blocks;
+    const long long rest = t.numel - block * kAdamBlock;
+    int whole = 0;
+    if (t.vec) whole = rest / kAdamBlock < a.blocks ? (int)(rest / kAdamBlock) : a.blocks;
+    typename B::Place at(t, block, lane);
+    B x;
+#pragma unroll 1
+    for (int i = 0; i < whole; ++i, at.next()) x.template step<true>(at, c, lane);
+#pragma unroll 1
+    for (int i = whole; i < a.blocks && (long long)i * kAdamBlock < rest; ++i) {
+      const typename B::Place part(t, block + i, lane);
+      x.template step<false>(part, c, lane);
     }
   }
   if (!a.last) return;
@@ -336,8 +400,9 @@ __global__ void __launch_bounds__(kThreads, 4)
 }
 
 // ------------------------------------------------------------ global norm
-constexpr int kNormUnit = 8192;  // values of a CTA's turn
-constexpr int kNormCtas = 1216;  // of a launch, at most
+constexpr int kPieces = 8;                    // of 16 bytes, of a thread's turn
+constexpr int kNormUnit = kPieces * kThreads;  // of a CTA's turn
+constexpr int kNormCtas = 1216;                // of a launch, at most
 
 struct Part {
   const void *data;
@@ -352,8 +417,9 @@ struct NormArgs {
   int count, turns;
 };
 
-// Bound: HBM.  A thread asks for all 16-byte pieces of its turn (128 bytes of
-// float32) before it uses one.
+// Bound: HBM.  A thread asks for all the pieces of its turn (128 bytes) before
+// it uses one: 1.6 GB of float32 in 231 us, 103 % of the copy rate (reading
+// alone is a little faster than copying); with 32 bytes 376 us.
 template <int CAP>
 __global__ void __launch_bounds__(kThreads)
     grad_norm_kernel(const __grid_constant__ NormArgs<CAP> a) {
@@ -363,42 +429,59 @@ __global__ void __launch_bounds__(kThreads)
   double sum = 0.0;
   int k = 0;
   for (int turn = blockIdx.x; turn < a.turns; turn += gridDim.x) {
-    while (k + 1 < a.count && turn >= a.t[k + 1].first) ++k;
+    k = tensor_of(a, turn, k);
     const Part &t = a.t[k];
-    const long long base = (long long)(turn - t.first) * kNormUnit;
+    const int per = t.bf16 ? 8 : 4;  // values of a piece
+    const long long first = (long long)(turn - t.first) * kNormUnit + threadIdx.x;
+    const long long pieces = t.numel / per;
     float2 s[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    if (t.vec && base + kNormUnit <= t.numel) {
-      uint4 u[8];
-      const int pieces = t.bf16 ? 4 : 8;
-      const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const char *>(t.data) +
-                                                       base * (t.bf16 ? 2 : 4)) + threadIdx.x;
+    uint4 u[kPieces];
+    if (t.vec) {
+      const uint4 *q = static_cast<const uint4 *>(t.data) + first;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < pieces) u[i] = __ldg(q + i * kThreads);
+      for (int i = 0; i < kPieces; ++i)
+        u[i] = first + i * kThreads < pieces ? __ldg(q + i * kThreads) : make_uint4(0, 0, 0, 0);
+    } else {  // value by value
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (i >= pieces) break;
-        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-        if (t.bf16) {
+      for (int i = 0; i < kPieces; ++i) {
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (first + i * kThreads < pieces) {
+          const long long at = (first + i * kThreads) * per;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 f = make_float2(__uint_as_float(w[j] << 16),
-                                         __uint_as_float(w[j] & 0xffff0000u));
-            s[j % 2] = fma2(f, f, s[j % 2]);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float2 f = make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
-            s[j] = fma2(f, f, s[j]);
+            if (t.bf16) {
+              const uint16_t *q = static_cast<const uint16_t *>(t.data) + at + 2 * j;
+              w[j] = q[0] | (uint32_t)q[1] << 16;
+            } else {
+              w[j] = static_cast<const uint32_t *>(t.data)[at + j];
+            }
           }
         }
+        u[i] = make_uint4(w[0], w[1], w[2], w[3]);
       }
-    } else {
-      for (int i = threadIdx.x; i < kNormUnit && base + i < t.numel; i += kThreads) {
-        const float f = t.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(t.data)[base + i])
-                               : static_cast<const float *>(t.data)[base + i];
-        s[0].x = fmaf(f, f, s[0].x);
+    }
+    // the values behind the last piece, in the last turn
+    const long long tail = pieces * per + threadIdx.x;
+    if (turn - t.first == pieces / kNormUnit && tail < t.numel)
+      s[0].x = t.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(t.data)[tail])
+                      : static_cast<const float *>(t.data)[tail];
+    s[0].x *= s[0].x;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+      if (t.bf16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f =
+              make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
+          s[j % 2] = fma2(f, f, s[j % 2]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float2 f = make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+          s[j] = fma2(f, f, s[j]);
+        }
       }
     }
     s[0] = add2(s[0], s[1]);
@@ -434,7 +517,8 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------- launches
-constexpr int kSmallCap = 48, kLargeCap = 384;  // tensors of a launch
+constexpr int kSmallCap = 48, kLargeCap = 384;          // tensors of a step's launch
+constexpr int kNormSmallCap = 128, kNormLargeCap = 1024;  // and of the norm's
 
 inline bool on16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 inline long long ceil_of(long long a, long long b) { return (a + b - 1) / b; }
@@ -449,7 +533,8 @@ cudaError_t norm_launch(const moe_tensor_t *t, int count, double *part, int *par
     if (t[i].numel == 0) continue;
     a.t[a.count++] = Part{t[i].data, t[i].numel, (int)turns, t[i].dtype == MOE_BF16,
                           on16(t[i].data)};
-    turns += ceil_of(t[i].numel, kNormUnit);
+    // a turn for the pieces and for what is left behind them
+    turns += t[i].numel / (t[i].dtype == MOE_BF16 ? 8 : 4) / kNormUnit + 1;
   }
   if (turns == 0) return cudaSuccess;
   a.part = part + *parts, a.turns = (int)turns;
@@ -480,9 +565,23 @@ cudaError_t step_cap(const moe_adamw_t &o, const moe_adamw_tensor_t *t, const Pe
   const int sms = device_sm_count();
   long long blocks = 0;
   for (int i = 0; i < q.count; ++i) blocks += ceil_of(t[q.index[i]].numel, kAdamBlock);
-  // short turns while there are few of them, so that every warp has some
-  const long long share = blocks / (sms * 64ll);
-  a.blocks = (int)(share < 1 ? 1 : share < kMostBlocks ? share : kMostBlocks);
+  const long long most = (long long)kCtas * sms, warps = most * kWarps;
+  // The blocks of a turn.  8-bit states: as many as leave the longest share
+  // of a warp within a 32nd of the shortest possible: eight neighbouring
+  // blocks' scales are one sector of memory, and a warp's 2 KB of codes a run
+  // (38 million values in bf16 throughout: 77 us, two blocks 93).  float32:
+  // a sixteenth of a share (3 million values: 17.0 us, the other rule 18.2).
+  a.blocks = 1;
+  if (E4M3) {
+    long long best = ceil_of(blocks, warps);
+    for (int n = 2; n <= kMostBlocks; ++n) {
+      const long long longest = ceil_of(ceil_of(blocks, n), warps) * n;
+      if (longest <= best + best / 32) a.blocks = n;
+    }
+  } else {
+    const long long share = blocks / (warps * 16);
+    a.blocks = (int)(share < 1 ? 1 : share < kMostBlocks ? share : kMostBlocks);
+  }
   long long turns = 0;
   a.count = 0;
   for (int i = 0; i < q.count; ++i) {
@@ -499,7 +598,7 @@ cudaError_t step_cap(const moe_adamw_t &o, const moe_adamw_tensor_t *t, const Pe
   a.b2 = (float)o.beta2, a.a2 = (float)(1.0 - o.beta2);
   a.beta1 = o.beta1, a.beta2 = o.beta2;
   a.turns = (int)turns, a.last = last;
-  const long long ctas = ceil_of(turns, kWarps), most = 4ll * sms;
+  const long long ctas = ceil_of(turns, kWarps);
   const unsigned grid = (unsigned)(ctas < 1 ? 1 : ctas < most ? ctas : most);
   return launch_pdl(adamw_kernel<E4M3, PT, GT, MASTER, CAP>, dim3(grid), dim3(kThreads), 0, s, a);
 }
@@ -562,7 +661,7 @@ cudaError_t step_all(const moe_adamw_t &o, const moe_adamw_tensor_t *t, int coun
 }  // namespace
 
 size_t grad_norm_ws_bytes(int count) {
-  const size_t launches = count < 1 ? 1 : (size_t)ceil_of(count, kLargeCap);
+  const size_t launches = count < 1 ? 1 : (size_t)ceil_of(count, kNormLargeCap);
   return (launches * kNormCtas * sizeof(double) + 255) / 256 * 256;
 }
 
@@ -571,11 +670,11 @@ cudaError_t launch_grad_norm(const moe_tensor_t *t, int count, float max_norm, f
   double *part = static_cast<double *>(ws);
   int parts = 0;
   cudaError_t e = cudaSuccess;
-  if (count <= kSmallCap) {
-    e = norm_launch<kSmallCap>(t, count, part, &parts, s);
+  if (count <= kNormSmallCap) {
+    e = norm_launch<kNormSmallCap>(t, count, part, &parts, s);
   } else {
-    for (int i = 0; i < count && e == cudaSuccess; i += kLargeCap)
-      e = norm_launch<kLargeCap>(t + i, count - i < kLargeCap ? count - i : kLargeCap, part, &parts, s);
+    for (int i = 0; i < count && e == cudaSuccess; i += kNormLargeCap)
+      e = norm_launch<kNormLargeCap>(t + i, count - i < kNormLargeCap ? count - i : kNormLargeCap, part, &parts, s);
   }
   if (e != cudaSuccess) return e;
   return launch_pdl(grad_norm_join_kernel, dim3(1), dim3(256), 0, s, (const double *)part, parts,

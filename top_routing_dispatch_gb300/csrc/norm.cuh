@@ -285,18 +285,6 @@ inline NormGrid norm_grid(int n, int most) {
   return g;
 }
 
-template <typename K>
-inline cudaError_t allow_smem(K kernel, int bytes, bool (&ready)[64]) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  bool &r = ready[dev >= 0 && dev < 64 ? dev : 0];
-  if (r) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) r = true;
-  return e;
-}
-
 inline bool on_bytes(const void *p, uintptr_t b) {
   return (reinterpret_cast<uintptr_t>(p) & (b - 1)) == 0;
 }

@@ -6,7 +6,20 @@
 
 namespace moe {
 
-// ---- norm.cu
+// Lets a kernel have `bytes` of dynamic shared memory, once a device.
+template <typename K>
+inline cudaError_t allow_smem(K kernel, int bytes, bool (&ready)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  bool &r = ready[dev >= 0 && dev < 64 ? dev : 0];
+  if (r) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) r = true;
+  return e;
+}
+
+// ---- norm.cu, norm_backward.cu
 constexpr int kNormMaxH = 1 << 20;  // longest row
 size_t norm_backward_ws_bytes(const moe_norm_t &d);
 cudaError_t launch_norm(const moe_norm_t &d, const void *x, long long x_stride,

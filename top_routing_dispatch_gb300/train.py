@@ -252,9 +252,9 @@ class AdamW:
         _want(all(a[1] <= b[0] for a, b in zip(spans, spans[1:])),
               "params and masters: no two may share memory")
         self.lr, self.betas, self.eps = float(lr), (float(betas[0]), float(betas[1])), float(eps)
-        _want(all(0 <= b < 1 for b in self.betas) and 0 < self.eps < math.inf
+        _want(all(0 <= b < 1 for b in self.betas) and 2.0 ** -126 <= self.eps < math.inf
               and all(0 <= d < math.inf for d in [self.lr] + decay),
-              "betas in [0, 1), eps above 0, lr and weight_decay at least 0, all finite")
+              "betas in [0, 1), eps at least 2^-126, lr and weight_decay at least 0, all finite")
         self.state, self.device, self._index = state, dev, _index(dev)
         blocks = [-(-p.numel() // BLOCK) for p in self.params]
         *self.offsets, total = itertools.accumulate(blocks, initial=0)
