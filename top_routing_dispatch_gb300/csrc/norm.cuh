@@ -19,7 +19,8 @@
 
 namespace moe {
 
-constexpr int kNormThreads = 512;  // of a CTA of groups, at most
+template <int GS>
+constexpr int kCta = GS > 512 ? GS : 512;  // threads of a CTA, at most
 constexpr int kNormParts = 304;    // CTAs of the backward, at most
 
 template <typename T>
@@ -173,6 +174,22 @@ struct RowIO {
                     : to_f(static_cast<const T *>(w)[at(k)]);
     }
   }
+  // column sums in float32 at the same columns; aligned: out + first(c) on 16 bytes
+  __device__ __forceinline__ void put(float *out, bool aligned, const float2 (&f)[P]) const {
+#pragma unroll
+    for (int c = 0; c < PIECES; ++c) {
+      if ((!SHIFT || o == 0) && aligned && full[c]) {
+#pragma unroll
+        for (int j = 0; j < V; j += 4)
+          *reinterpret_cast<float4 *>(out + first(c) + j) =
+              *reinterpret_cast<const float4 *>(&f[(c * V + j) / 2]);
+      } else if (live[c]) {
+#pragma unroll
+        for (int k = c * V; k < (c + 1) * V; ++k)
+          if (has(k)) out[at(k)] = k % 2 ? f[k / 2].y : f[k / 2].x;
+      }
+    }
+  }
   // f(c, k) for the pairs k of every piece c that the row has some of
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
@@ -245,17 +262,19 @@ __device__ __forceinline__ F group_sum(F v, float2 *places, int group) {
   return v;
 }
 
-// Slots of the ring for N tensors: as many of 8, 4 or 2 as fit in 200 KB
-// beside the other groups' (0: none of them, rows too long).
-template <typename T, int VALS, int N>
-constexpr int ring_slots() {
-  constexpr int one = kNormThreads * VALS * (int)sizeof(T) * N;
-  return one * 8 <= 200 * 1024 ? 8 : one * 4 <= 200 * 1024 ? 4 : one * 2 <= 200 * 1024 ? 2 : 0;
+// Slots of the ring for N tensors: `most`, or as many as fit in 200 KB (0:
+// rows too long).
+template <typename T, int GS, int VALS, int N>
+constexpr int ring_slots(int most) {
+  const int one = kCta<GS> * VALS * (int)sizeof(T) * N;
+  const int fit = 200 * 1024 / one;
+  return fit < 2 ? 0 : fit < most ? fit : most;
 }
 
-// The group for rows of H values: the smallest of which a thread takes 16, or
-// 512 threads of 32 values.  False where rows are longer.
-template <typename T, bool SHIFT, template <typename, int, int, bool> class G, typename A>
+// The group for rows of H values: the smallest of which a thread takes 16, and
+// beyond 4096 by what was measured.  False where rows are longer.
+template <bool BACK, typename T, bool SHIFT, template <typename, int, int, bool> class G,
+          typename A>
 bool by_length(A &a, cudaStream_t s, cudaError_t *e) {
   const int H = a.H + (SHIFT ? kPer<T> - 1 : 0);
   if (H <= 8 * 16) return G<T, 8, 16, SHIFT>::go(a, s, e);
@@ -263,8 +282,14 @@ bool by_length(A &a, cudaStream_t s, cudaError_t *e) {
   if (H <= 64 * 16) return G<T, 64, 16, SHIFT>::go(a, s, e);
   if (H <= 128 * 16) return G<T, 128, 16, SHIFT>::go(a, s, e);
   if (H <= 256 * 16) return G<T, 256, 16, SHIFT>::go(a, s, e);
-  if (H <= 512 * 16) return G<T, 512, 16, SHIFT>::go(a, s, e);
-  if (H <= 512 * 32) return G<T, 512, 32, SHIFT>::go(a, s, e);
+  // Rows of up to 8192: the backward on 1024 threads of 8 values, which leaves
+  // it twice the warps beside its columns' sums (8192 x 7168 bf16 with ds 84
+  // us, 512 threads of 16 values 94); the forward on 512 of 16 (45 us, 50).
+  if (H <= 8192) return G<T, BACK ? 1024 : 512, BACK ? 8 : 16, SHIFT>::go(a, s, e);
+  // up to 16384: the forward on 1024 threads of 16 (3001 x 16384 bf16 with
+  // residual 65 us, 512 of 32 values 73), the backward on 512 of 32 (143 us,
+  // 1024 of 16 169: its sums spill)
+  if (H <= 16384) return G<T, BACK ? 512 : 1024, BACK ? 32 : 16, SHIFT>::go(a, s, e);
   return false;
 }
 
@@ -279,7 +304,7 @@ inline NormGrid norm_grid(int n, int most) {
   NormGrid g;
   most = most < 8 ? 8 : most - most % 8;
   g.ctas = n < most ? n : most;
-  const int rows = (int)(((long long)n + g.ctas - 1) / g.ctas), all = kNormThreads / GS;
+  const int rows = (int)(((long long)n + g.ctas - 1) / g.ctas), all = kCta<GS> / GS;
   constexpr int warp = GS < 32 ? 32 / GS : 1;  // whole warps
   g.groups = rows < all ? (rows + warp - 1) / warp * warp : all;
   return g;

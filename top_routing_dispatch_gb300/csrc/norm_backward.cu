@@ -25,11 +25,11 @@ struct BackArgs {
 
 // N: tensors read (dy and s; and ds)
 template <typename T, int GS, int VALS, bool SHIFT, int N, int D>
-__global__ void __launch_bounds__(kNormThreads) norm_back_kernel(const BackArgs a) {
+__global__ void __launch_bounds__(kCta<GS>) norm_back_kernel(const BackArgs a) {
   using IO = RowIO<T, GS, VALS, SHIFT>;
   pdl_enter();
   extern __shared__ __align__(16) char ring[];
-  __shared__ __align__(16) float2 parts[2][kNormThreads / 32];
+  __shared__ __align__(16) float2 parts[2][kCta<GS> / 32];
   const int t = threadIdx.x % GS, group = threadIdx.x / GS, groups = blockDim.x / GS;
   const int H = a.H, first = threadIdx.x / GS * GS / 32;
   char *mine = ring + group * (D * N * IO::BYTES);
@@ -122,11 +122,10 @@ __global__ void __launch_bounds__(kNormThreads) norm_back_kernel(const BackArgs 
     __syncthreads();
     float *all = reinterpret_cast<float *>(ring);
     for (int pass = 0; pass < (a.bias ? 2 : 1); ++pass, out += (size_t)a.parts * H) {
-#pragma unroll
-      for (int k = 0; k < VALS; ++k) {
-        const float2 v = (pass ? db : dw)[k / 2];
-        if (io.has(k)) all[group * H + io.at(k)] = k % 2 ? v.y : v.x;
-      }
+      if (pass)
+        io.put(all + group * H, H % 4 == 0, db);
+      else
+        io.put(all + group * H, H % 4 == 0, dw);
       __syncthreads();
       for (int c = threadIdx.x; c < H; c += blockDim.x) {
         float v = all[c];
@@ -137,13 +136,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_back_kernel(const BackArgs 
     }
     return;
   }
-#pragma unroll
-  for (int k = 0; k < VALS; ++k) {
-    if (io.has(k)) {
-      out[io.at(k)] = k % 2 ? dw[k / 2].y : dw[k / 2].x;
-      if (a.bias) out[(size_t)a.parts * H + io.at(k)] = k % 2 ? db[k / 2].y : db[k / 2].x;
-    }
-  }
+  io.put(out, H % 4 == 0, dw);
+  if (a.bias) io.put(out + (size_t)a.parts * H, H % 4 == 0, db);
 }
 
 // Rows of any length and alignment, first part: dx, a CTA a row.
@@ -205,25 +199,27 @@ __global__ void __launch_bounds__(32 * kWarps) norm_columns_kernel(const BackArg
   if (a.bias) a.part[((size_t)a.parts + blockIdx.y) * a.H + col] = db;
 }
 
+constexpr int kJoinWarps = 16;
+
 // dweight (blockIdx.y 0) and dbias (1): the parts in a fixed order
-__global__ void __launch_bounds__(32 * kWarps)
+__global__ void __launch_bounds__(32 * kJoinWarps)
     norm_join_kernel(const float *part, int parts, int H, float *dweight, float *dbias) {
   pdl_enter();
-  __shared__ float acc[kWarps][32];
+  __shared__ float acc[kJoinWarps][32];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int col = blockIdx.x * 32 + lane;
   float *out = blockIdx.y ? dbias : dweight;
   const float *p = part + (size_t)blockIdx.y * parts * H + col;
   float v = 0.f;
   if (col < H) {
-#pragma unroll 8
-    for (int i = warp; i < parts; i += kWarps) v += p[(size_t)i * H];
+#pragma unroll 10
+    for (int i = warp; i < parts; i += kJoinWarps) v += p[(size_t)i * H];
   }
   acc[warp][lane] = v;
   __syncthreads();
   if (warp || col >= H) return;
 #pragma unroll
-  for (int i = 1; i < kWarps; ++i) v += acc[i][lane];
+  for (int i = 1; i < kJoinWarps; ++i) v += acc[i][lane];
   out[col] = v;
 }
 
@@ -231,7 +227,8 @@ template <typename T, int GS, int VALS, bool SHIFT>
 struct Backward {
   template <int N>
   static bool with(BackArgs &a, cudaStream_t s, cudaError_t *e) {
-    constexpr int D = ring_slots<T, VALS, N>();
+    // 8192 rows of 7168 bf16 with ds: four slots 84 us, three 101
+    constexpr int D = ring_slots<T, GS, VALS, N>(4);
     if constexpr (D == 0) {
       return false;
     } else {
@@ -243,7 +240,7 @@ struct Backward {
       static_assert(one >= GS * VALS * 4, "ring");
       auto kernel = norm_back_kernel<T, GS, VALS, SHIFT, N, D>;
       static bool ready[64] = {false};
-      *e = allow_smem(kernel, one * (kNormThreads / GS), ready);
+      *e = allow_smem(kernel, one * (kCta<GS> / GS), ready);
       if (*e == cudaSuccess)
         *e = launch_pdl(kernel, dim3(g.ctas), dim3(g.groups * GS), one * g.groups, s, a);
       return true;
@@ -261,16 +258,16 @@ cudaError_t backward(BackArgs &a, float *dweight, float *dbias, cudaStream_t s) 
   a.phase = ph.step;
   a.vec = on_bytes(a.w, 16);
   cudaError_t e = cudaSuccess;
-  if (!ph.one || !(ph.step || a.H % kPer<T> ? by_length<T, true, Backward>(a, s, &e)
-                                          : by_length<T, false, Backward>(a, s, &e))) {
+  if (!ph.one || !(ph.step || a.H % kPer<T> ? by_length<true, T, true, Backward>(a, s, &e)
+                                          : by_length<true, T, false, Backward>(a, s, &e))) {
     e = launch_pdl(norm_back_long_kernel<T>, dim3(a.n), dim3(1024), 0, s, a);
     if (e == cudaSuccess)
       e = launch_pdl(norm_columns_kernel<T>, dim3((a.H + 31) / 32, a.parts), dim3(32 * kWarps), 0,
                      s, a);
   }
   if (e != cudaSuccess) return e;
-  return launch_pdl(norm_join_kernel, dim3((a.H + 31) / 32, dbias ? 2 : 1), dim3(32 * kWarps), 0,
-                    s, (const float *)a.part, a.parts, a.H, dweight, dbias);
+  return launch_pdl(norm_join_kernel, dim3((a.H + 31) / 32, dbias ? 2 : 1), dim3(32 * kJoinWarps),
+                    0, s, (const float *)a.part, a.parts, a.H, dweight, dbias);
 }
 
 }  // namespace
