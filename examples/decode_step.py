@@ -7,8 +7,9 @@ A step takes one new token of each running sequence through the layer:
 Keys and values go into a paged cache (PagedKVCache.append, which also rotates
 queries and keys), the new tokens attend to their sequences over the cache
 (PagedKVCache.attend), the router picks their experts (moe_route_topk) and the
-experts run on 4-bit weights (W4Experts).  Norms and projections are plain
-torch.  Pages are handed out as sequences grow.
+experts run on 4-bit weights (W4Experts); the norms are LayerNorm in its root
+mean square form, the second with the residual added on the way.  Projections
+are plain torch.  Pages are handed out as sequences grow.
 
     python examples/decode_step.py [--seqs 8] [--steps 64] [--cache bf16|e4m3] [--graph]
 """
@@ -28,11 +29,6 @@ if ROOT not in sys.path:
 import top_routing_dispatch_gb300 as M  # noqa: E402
 
 
-def rms_norm(x, eps=1e-6):
-    f = x.float()
-    return (f * torch.rsqrt(f.square().mean(-1, keepdim=True) + eps)).to(x.dtype)
-
-
 class DecoderLayer:
     """Weights (random, from `seed`), cache and buffers of one layer for up to
     `seqs` sequences of up to `max_len` tokens."""
@@ -45,6 +41,9 @@ class DecoderLayer:
         rand = lambda *s: torch.randn(s, generator=g, device=dev)  # noqa: E731
         self.heads, self.dim = (q_heads, kv_heads, kv_heads), head_dim
         width = head_dim * sum(self.heads)
+        ones = lambda: torch.ones(hidden, device=dev)  # noqa: E731
+        self.norm_in, self.norm_ffn = (M.LayerNorm(ones(), eps=1e-6, rms=True, dtype=bf)
+                                       for _ in range(2))
         self.w_qkv = (rand(hidden, width) / hidden ** 0.5).to(bf)
         self.w_out = (rand(q_heads * head_dim, hidden) / (q_heads * head_dim) ** 0.5).to(bf)
         self.w_gate = (rand(hidden, experts) * 0.05).to(bf)
@@ -84,13 +83,12 @@ class DecoderLayer:
         """One new token of every sequence: x (seqs, hidden) bf16 -> the same."""
         positions = self.lens.clone()
         self.lens += 1
-        qkv = rms_norm(x) @ self.w_qkv
+        qkv = self.norm_in(x) @ self.w_qkv
         q, k, v = (t.unflatten(1, (-1, self.dim))
                    for t in qkv.split([h * self.dim for h in self.heads], 1))
         q = self.cache.append(q, k, v, self.seq_ids, positions)
         a = self.cache.attend(q, self.lens)
-        x = x + a.flatten(1) @ self.w_out
-        h = rms_norm(x)
+        h, x = self.norm_ffn(x, a.flatten(1) @ self.w_out)
         M.moe_route_topk(self.route, h, self.w_gate, None, self.idx, self.weights, self.logits)
         return x + self.experts(h, self.idx, self.weights)
 

@@ -17,4 +17,4 @@ from .api import (  # noqa: E402,F401
     moe_set_gemm_tails,
 )
 from .decode import PagedKVCache, W4Experts, quantize_weights_w4, rope_table  # noqa: E402,F401
-from .train import AdamW, GradNorm, LayerNorm  # noqa: E402,F401
+from .train import AdamW, GradNorm, LayerNorm, MoEBlock  # noqa: E402,F401

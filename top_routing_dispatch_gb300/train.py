@@ -17,9 +17,9 @@ import math
 
 import torch
 
-from . import _lib, decode
+from . import _lib, api, decode
 from .api import MoEError, _check, _p
-from .decode import _BF16, _F32, _DT, _empty, _handle, _index, _want, _Workspaces
+from .decode import _BF16, _DT, _F32, _I32, _Workspaces, _empty, _handle, _index, _want
 
 _E4M3 = torch.float8_e4m3fn
 BLOCK = 256  # values of a tensor that share a scale where states are held in 8 bits
@@ -338,3 +338,114 @@ class AdamW:
             if to is not None:
                 to.copy_(src)
         self._set_steps(int(d["steps"]))
+
+
+class MoEBlock:
+    """A residual block for training: s = x + residual; out = experts(norm(s)),
+    with the layer's own forward and backward calls on buffers kept here.
+
+    desc: a bf16 layer (make_desc; H % 256 == 0, row-major weights); norm: a
+    LayerNorm of bf16 rows; w_gate (H, E), w13 (E, H, 2I), w2 (E, I, H)
+    bfloat16, bias (E,) float32 or None.
+    params and grads: the block's parameters and their float32 gradients, in
+    one order, as AdamW and GradNorm take them; backward overwrites the
+    gradients.  One forward's intermediates are kept, for the backward that
+    follows it; calls of one block are ordered by the caller.
+    """
+
+    def __init__(self, desc, norm, w_gate, bias, w13, w2):
+        _want(norm.dtype == _BF16 and norm.H == desc.H, "norm: of bfloat16 rows of the layer's H")
+        nbytes = api.moe_backward_workspace_size(desc)
+        _want(nbytes > 0 and not desc.weight_layout,
+              "desc: a bf16 layer that moe_backward takes, row-major weights")
+        self.desc, self.norm = desc, norm
+        self.w_gate, self.bias, self.w13, self.w2 = w_gate, bias, w13, w2
+        n, H, I, E, K = desc.n, desc.H, desc.I, desc.E, desc.K
+        dev = w13.device
+        for t, shape, dt, name in ((w_gate, (H, E), _BF16, "w_gate"), (bias, (E,), _F32, "bias"),
+                                   (w13, (E, H, 2 * I), _BF16, "w13"), (w2, (E, I, H), _BF16, "w2")):
+            _want(t is None and name == "bias" or (
+                t.dtype == dt and t.shape == shape and t.is_contiguous() and t.device == dev),
+                f"{name}: contiguous {shape} {dt}")
+        _want(norm.device == dev, "all tensors on one device")
+        decode._ready(dev)
+        new = lambda *shape, dtype=_I32: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
+        self.stats = new(2, n, dtype=_F32)
+        self.h_in, self.s = new(n, H, dtype=_BF16), new(n, H, dtype=_BF16)
+        self.logits, self.topk_w = new(n, E, dtype=_F32), new(n, K, dtype=_F32)
+        self.topk_idx, self.counts, self.offsets = new(n, K), new(E), new(E + 1)
+        self.perm, self.inv_perm = new(n * K), new(n * K)
+        self.x_perm, self.y_perm = new(n * K, H, dtype=_BF16), new(n * K, H, dtype=_BF16)
+        self.h = new(n * K, I, dtype=_BF16)
+        self.d_in = new(n, H, dtype=_BF16)
+        self.status = torch.zeros(1, dtype=_I32, device=dev)
+        self._layout_ws = new(max(api.moe_layout_workspace_size(desc), 1), dtype=torch.uint8)
+        self._ws = new(nbytes, dtype=torch.uint8)
+        zeros = lambda t: torch.zeros(t.shape, dtype=_F32, device=dev)  # noqa: E731
+        self.params = [t for t in (norm.weight, norm.bias, w_gate, bias, w13, w2) if t is not None]
+        self._grads = {name: None if t is None else zeros(t) for name, t in (
+            ("norm", norm.weight), ("norm_bias", norm.bias), ("w_gate", w_gate), ("bias", bias),
+            ("w13", w13), ("w2", w2))}
+        self.grads = [g for g in self._grads.values() if g is not None]
+        self._rows = None  # what the last forward normalised
+        kept = [t for t in vars(self).values() if isinstance(t, torch.Tensor)] + self.grads
+        # a stream's first call waits for what was enqueued here
+        self._index = _index(dev)
+        self._streams = _Workspaces(dev, lambda: self._ws, kept)
+
+    def _enter(self, stream):
+        _here(self.status.device, self._index)
+        handle = _handle(stream, self._index)
+        if handle not in self._streams.pointers:
+            self._streams.add(handle)
+
+    def forward(self, x, residual=None, out=None, stream=None):
+        """(out, s) for x (n, H) bfloat16 and residual like it, or None (then s
+        is x).  out is allocated when not given; s is a buffer of the block
+        where there is a residual, and holds until the next forward; backward
+        reads it (or x, which then must not change meanwhile)."""
+        d = self.desc
+        self._enter(stream)
+        if residual is None:
+            self.norm(x, y=self.h_in, stats=self.stats, stream=stream)
+            rows = x
+        else:
+            self.norm(x, residual, y=self.h_in, s=self.s, stats=self.stats, stream=stream)
+            rows = self.s
+        if out is None:
+            out = _empty(x.shape, _BF16, x.device, stream)
+        _want(out.shape == x.shape and out.dtype == _BF16 and out.is_contiguous()
+              and out.device == x.device, "out: like x, contiguous")
+        api.moe_route_topk(d, self.h_in, self.w_gate, self.bias, self.topk_idx, self.topk_w,
+                           self.logits, stream)
+        api.moe_dispatch_layout(d, self.topk_idx, self.counts, self.offsets, self.perm,
+                                self.inv_perm, self.status, self._layout_ws, stream)
+        api.moe_permute(d, self.h_in, self.perm, self.x_perm, self.status, stream)
+        api.moe_expert_gemm1_swiglu(d, self.x_perm, self.w13, self.offsets, self.h,
+                                    status_word=self.status, stream=stream)
+        api.moe_expert_gemm2(d, self.h, self.w2, self.offsets, self.y_perm,
+                             status_word=self.status, stream=stream)
+        api.moe_combine(d, self.y_perm, self.topk_w, self.inv_perm, out, self.status, stream)
+        self._rows = rows
+        return out, rows
+
+    def backward(self, dout, ds=None, dx=None, stream=None):
+        """dx (n, H): the gradient of x, and of residual alike, for dout = dL/dout
+        and ds = dL/ds by other ways (None: there are none).  Fills the gradients."""
+        g = self._grads
+        _want(self._rows is not None, "backward before a forward")
+        _want(dout.dtype == _BF16 and dout.shape == self.h_in.shape and dout.is_contiguous()
+              and dout.device == self.h_in.device, "dout: like out, contiguous")
+        self._enter(stream)
+        api.moe_backward(self.desc, self.h_in, self.w_gate, self.w13, self.w2, dout, self.logits,
+                         self.topk_idx, self.topk_w, self.offsets, self.inv_perm, self.x_perm,
+                         self.h, self.y_perm, self.d_in, g["w_gate"], g["bias"], g["w13"], g["w2"],
+                         self._ws, self.status, stream)
+        return self.norm.backward(self.d_in, self._rows, self.stats, ds=ds, dx=dx,
+                                  dweight=g["norm"], dbias=g["norm_bias"], stream=stream)[0]
+
+    def check(self, stream=None):
+        """Waits for the stream (the calls' one) and raises MoEError if a call
+        flagged bad routing, an inconsistent layout or a timeout."""
+        decode._ready(self.status.device)
+        _check(api.moe_check_status(self.status, stream), "device status")
