@@ -636,3 +636,129 @@ def test_norm_row_strides_of_unequal_phase():
             check_norm(layer, x.cpu(), res.cpu(), w, b, eps, False, y, s, stats)
             out = layer.backward(x, s, stats, ds=res)
             check_backward(layer, x.cpu(), s.cpu(), stats, w, res.cpu(), False, out, True)
+
+
+# ------------------------------------------------------------------ scratch
+def test_calls_of_threads_on_one_stream():
+    """Threads' backward calls and gradient norms, of unequal sizes, share a
+    stream's scratch memory."""
+    import threading
+    work = []
+    for i, (n, H) in enumerate(((400, 2048), (3, 40), (1200, 136), (90, 1031))):
+        layer, x, _, w, b, eps = norm_case(n, H, BF16, F32, False, True, False, seed=70 + i)
+        x, stats = x.cuda(), torch.empty((2, n), device="cuda")
+        layer(x, stats=stats)
+        norm = M().GradNorm([x, stats])
+        work.append((layer, x, stats, norm, layer.backward(x, x, stats) + norm(1.0), []))
+    torch.cuda.synchronize()
+
+    def calls(layer, x, stats, norm, want, got):
+        for _ in range(25):
+            got.append(layer.backward(x, x, stats) + norm(1.0))
+    threads = [threading.Thread(target=calls, args=w) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for *_, want, got in work:
+        assert len(got) == 25
+        assert all(torch.equal(a, c) for g in got for a, c in zip(g, want))
+
+
+def test_scratch_grows_between_calls():
+    """A larger call behind a smaller one on the same streams, eager and captured."""
+    small, large = ((norm_case(n, H, BF16, F32, False, True, False)) for n, H in ((2, 64), (700, 8192)))
+    want = []
+    for layer, x, *_ in (small, large):
+        x = x.cuda()
+        stats = torch.empty((2, len(x)), device="cuda")
+        layer(x, stats=stats)
+        want.append((layer, x, stats, layer.backward(x, x, stats)))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (None, side):
+        for layer, x, stats, out in want + want[::-1]:
+            got = layer.backward(x, x, stats, stream=stream)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, c) for a, c in zip(got, out))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = [layer.backward(x, x, stats) for layer, x, stats, _ in want]
+    for _ in range(2):
+        graph.replay()
+        want[1][0].backward(*want[1][1:2] * 2, want[1][2])
+    torch.cuda.synchronize()
+    for got, (*_, out) in zip(outs, want):
+        assert all(torch.equal(a, c) for a, c in zip(got, out))
+
+
+# ------------------------------------------------- mixed lists of parameters
+@pytest.mark.parametrize("state", [F32, E4M3], ids=["f32", "e4m3"])
+def test_adamw_mixed_kinds(state):
+    """Parameters and gradients of every pair of types in one optimizer, with
+    masters for some of either type, more of one kind than a launch takes, and
+    tensors off 16 bytes beside aligned ones."""
+    kinds = [(F32, F32, False), (BF16, F32, True), (BF16, BF16, False), (F32, BF16, True), (BF16, BF16, True),
+             (BF16, F32, False), (F32, F32, True), (F32, BF16, False)] + [(BF16, F32, True)] * 60
+    params, grads, masters = [], [], []
+    for i, (pt, gt, has) in enumerate(kinds):
+        n, off = 1 + 613 * i % 2900, i % 3
+        p = torch.empty(n + off, dtype=pt, device="cuda")[off:]
+        p.copy_(rand(i, n, std=0.05))
+        params.append(p)
+        grads.append(rand(100 + i, n).to(gt).cuda())
+        masters.append(p.clone().float() if has else None)
+    opt = M().AdamW(params, grads, lr=LR, betas=(B1, B2), eps=EPS, weight_decay=WD, state=state, masters=masters)
+    plain = Plain(opt, state)
+    for t in (1, 2):
+        for i, (p, w) in enumerate(zip(params, masters)):
+            if w is None and p.dtype == BF16:
+                plain.p[i], plain.err[i] = f64(p), torch.zeros(p.shape, dtype=torch.float64)
+        opt.step()
+        plain.step(t, grads, LR, [WD] * len(kinds), None)
+        plain.check(opt)
+    assert opt.steps == 2
+
+
+def test_adamw_leaves_what_lies_between_tensors():
+    """Parameters, gradients and masters as parts of larger buffers."""
+    for state in (F32, E4M3):
+        line = torch.full((3, 2000), 7.0, device="cuda")
+        parts = [slice(3, 4), slice(10, 700), slice(701, 1999)]
+        params, grads = [line[0, p] for p in parts], [line[1, p] for p in parts]
+        opt = M().AdamW(params, grads, state=state)
+        opt.step()
+        touched = torch.zeros(2000, dtype=torch.bool)
+        for p in parts:
+            touched[p] = True
+        assert (line[0].cpu()[~touched] == 7).all() and (line[0].cpu()[touched] != 7).all()
+        assert (line[1:] == 7).all()
+
+
+@pytest.mark.parametrize("T", [F32, BF16])
+def test_norm_gaps_between_rows(T):
+    """What lies between rows does not reach the results, NaN included, and
+    stays as it was where a result lies in a larger buffer."""
+    for H, pad in ((40, 8), (41, 8), (1031, 5), (2048, 16), (8190, 3), (5, 3)):
+        n = 170
+        wide = torch.full((n, H + pad), math.nan)
+        wide[:, :H] = rand(1, n, H)
+        x = wide.to(T).cuda()[:, :H]
+        layer, _, _, w, b, eps = norm_case(2, H, T, F32, False, True, True)
+        stats = torch.empty((2, n), device="cuda")
+        buf = torch.full((n * H + 16,), 7.0, dtype=T, device="cuda")
+        y, s = layer(x, x, y=buf[8:8 + n * H].view(n, H), stats=stats)
+        assert (buf[:8] == 7).all() and (buf[8 + n * H:] == 7).all()
+        check_norm(layer, x.cpu(), x.cpu(), w, b, eps, False, y, s, stats)
+        out = layer.backward(x, s, stats, ds=x, dx=buf[8:8 + n * H].view(n, H))
+        assert (buf[:8] == 7).all() and (buf[8 + n * H:] == 7).all()
+        check_backward(layer, x.cpu(), s.cpu(), stats, w, x.cpu(), False, out, True)
+
+
+def test_optimizer_takes_leaf_parameters():
+    """Parameters of a module: written in place, no graph kept."""
+    p = torch.nn.Parameter(torch.ones(300, device="cuda", dtype=BF16))
+    opt = M().AdamW([p], [torch.ones(300, device="cuda")], lr=0.25, weight_decay=0.0, masters=True)
+    opt.step()
+    assert not opt.masters[0].requires_grad and torch.equal(p.detach(), torch.full_like(p, 0.75))

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kCta<GS>) norm_back_kernel(const BackArgs a) {
   if (a.bias) io.put(out + (size_t)a.parts * H, H % 4 == 0, db);
 }
 
-// Rows of any length and alignment, first part: dx, a CTA a row.
+// Rows of any length and alignment, second part: dx, a CTA a row.
 template <typename T>
 __global__ void __launch_bounds__(1024) norm_back_long_kernel(const BackArgs a) {
   pdl_enter();
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(1024) norm_back_long_kernel(const BackArgs a) 
 
 constexpr int kWarps = 8;  // of a column kernel's CTA
 
-// Second part: sums of dy xh and of dy over a range of rows, 32 columns a CTA
+// First part: sums of dy xh and of dy over a range of rows, 32 columns a CTA
 template <typename T>
 __global__ void __launch_bounds__(32 * kWarps) norm_columns_kernel(const BackArgs a) {
   pdl_enter();
@@ -260,10 +260,10 @@ cudaError_t backward(BackArgs &a, float *dweight, float *dbias, cudaStream_t s) 
   cudaError_t e = cudaSuccess;
   if (!ph.one || !(ph.step || a.H % kPer<T> ? by_length<true, T, true, Backward>(a, s, &e)
                                           : by_length<true, T, false, Backward>(a, s, &e))) {
-    e = launch_pdl(norm_back_long_kernel<T>, dim3(a.n), dim3(1024), 0, s, a);
+    e = launch_pdl(norm_columns_kernel<T>, dim3((a.H + 31) / 32, a.parts), dim3(32 * kWarps), 0,
+                   s, a);
     if (e == cudaSuccess)
-      e = launch_pdl(norm_columns_kernel<T>, dim3((a.H + 31) / 32, a.parts), dim3(32 * kWarps), 0,
-                     s, a);
+      e = launch_pdl(norm_back_long_kernel<T>, dim3(a.n), dim3(1024), 0, s, a);
   }
   if (e != cudaSuccess) return e;
   return launch_pdl(norm_join_kernel, dim3((a.H + 31) / 32, dbias ? 2 : 1), dim3(32 * kJoinWarps),

@@ -5,15 +5,18 @@ norm of all gradients, AdamW the step that takes them.  As in api.py the work
 is done by the library's kernels; here arguments are checked and turned into
 pointers.  Tensors are on the current CUDA device, where the library launches.
 
-Calls run on `stream`, or the current stream.  What a call allocates is
-allocated on its stream, scratch included, so calls of one LayerNorm or GradNorm
-may run on several streams at the same time.
+Calls run on `stream`, or the current stream.  Results that a call allocates
+are ready for that stream's next work.  Scratch memory belongs to the stream
+(calls on one stream run one after another), or to the graph where a call is
+captured, so calls of one LayerNorm or GradNorm may run on several streams, and
+in several graphs, at the same time.
 """
 from __future__ import annotations
 
 import ctypes
 import itertools
 import math
+import threading
 
 import torch
 
@@ -23,6 +26,27 @@ from .decode import _BF16, _DT, _F32, _I32, _Workspaces, _empty, _handle, _index
 
 _E4M3 = torch.float8_e4m3fn
 BLOCK = 256  # values of a tensor that share a scale where states are held in 8 bits
+
+
+_scratch = {}  # (device, stream handle): the stream's scratch memory
+# a call with scratch is two kernels: threads' calls enter a stream one after another
+_scratch_lock = threading.Lock()
+
+
+def _scratch_for(nbytes, device, index, stream, handle):
+    """Scratch memory of a call on `stream`, under the lock."""
+    if stream is None:
+        capturing = torch.cuda.is_current_stream_capturing()
+    else:
+        with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device)):
+            capturing = torch.cuda.is_current_stream_capturing()
+    if capturing:  # memory of the graph
+        return _empty(nbytes, torch.uint8, device, stream)
+    t = _scratch.get((index, handle))
+    if t is None or t.numel() < nbytes:
+        # the old one's memory is reused in the stream's order
+        t = _scratch[index, handle] = _empty(max(nbytes, 1 << 20), torch.uint8, device, stream)
+    return t
 
 
 def _here(device, index):
@@ -143,11 +167,12 @@ class LayerNorm:
         elif dbias is not None:
             raise ValueError("dbias without a bias")
         ref, nbytes = self._ref_for(n)
-        ws = _empty(nbytes, torch.uint8, self.device, stream)
-        st = self._backward(ref, dp, dst, sp, sst, tp, self._w, ep, est,
-                            self._out(dx, shape, self.dtype, "dx"),
-                            self._out(dweight, vec, _F32, "dweight"), bp, ws.data_ptr(), nbytes,
-                            _handle(stream, self._index))
+        xp, wp = self._out(dx, shape, self.dtype, "dx"), self._out(dweight, vec, _F32, "dweight")
+        handle = _handle(stream, self._index)
+        with _scratch_lock:
+            ws = _scratch_for(nbytes, self.device, self._index, stream, handle)
+            st = self._backward(ref, dp, dst, sp, sst, tp, self._w, ep, est, xp, wp, bp,
+                                ws.data_ptr(), nbytes, handle)
         if st:
             raise MoEError(st, "moe_layer_norm_backward")
         return dx, dweight, dbias
@@ -167,7 +192,8 @@ def _scalar(t, device, name):
     """Pointer of one float32 on the device, None for None."""
     if t is None:
         return None
-    if t.dtype is not _F32 or t.numel() != 1 or t.device != device:
+    if t.dtype is not _F32 or t.numel() != 1 or t.get_device() != (
+            -1 if device.type == "cpu" else device.index):
         raise ValueError(f"{name}: one float32 on {device}")
     return t.data_ptr()
 
@@ -196,9 +222,11 @@ class GradNorm:
         norm = _empty(1, _F32, self.device, stream) if norm is None else norm
         factor = _empty(1, _F32, self.device, stream) if factor is None else factor
         np_, fp = _scalar(norm, self.device, "norm"), _scalar(factor, self.device, "factor")
-        ws = _empty(self._nbytes, torch.uint8, self.device, stream)
-        st = self._call(self._list, len(self.grads), max_norm, np_, fp, ws.data_ptr(),
-                        self._nbytes, _handle(stream, self._index))
+        handle = _handle(stream, self._index)
+        with _scratch_lock:
+            ws = _scratch_for(self._nbytes, self.device, self._index, stream, handle)
+            st = self._call(self._list, len(self.grads), max_norm, np_, fp, ws.data_ptr(),
+                            self._nbytes, handle)
         if st:
             raise MoEError(st, "moe_grad_norm")
         return norm, factor
@@ -240,7 +268,8 @@ class AdamW:
             float(d) for d in weight_decay]
         _want(len(decay) == n, "weight_decay: a number, or one for every parameter")
         if masters is None or masters is True:
-            masters = [p.float() if masters and p.dtype == _BF16 else None for p in self.params]
+            masters = [p.detach().float() if masters and p.dtype == _BF16 else None
+                       for p in self.params]
         self.masters = list(masters)
         _want(len(self.masters) == n and all(
             w is None or (w.dtype == _F32 and w.shape == p.shape and w.is_contiguous()
@@ -332,8 +361,8 @@ class AdamW:
             (a is None) == (b is None) and (a is None or a.shape == b.shape)
             for a, b in zip(masters, self.masters))), "masters: other shapes")
         for name in ("m", "v", "m_scale", "v_scale"):
-            if d[name] is not None:
-                getattr(self, name).view(torch.uint8).copy_(d[name].view(torch.uint8))
+            if d[name] is not None:  # the bits move
+                getattr(self, name).view(torch.uint8).copy_(d[name].contiguous().view(torch.uint8))
         for to, src in zip(self.masters, masters or []):
             if to is not None:
                 to.copy_(src)
