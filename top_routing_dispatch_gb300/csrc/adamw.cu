@@ -248,7 +248,7 @@ struct Block {
   };
 
   template <bool FULL>
-  __device__ __forceinline__ void step(const Place &t, const Step &c, int lane) {
+  __device__ __forceinline__ void load(const Place &t) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int n = t.left[h];
@@ -263,6 +263,10 @@ struct Block {
       v[h].template load<FULL>(t.v + 128 * h, n);
     }
     if (E4M3) ms = *t.ms, vs = *t.vs;
+  }
+
+  template <bool FULL>
+  __device__ __forceinline__ void step(const Place &t, const Step &c, int lane) {
     float2 G[4], P[4], M[4], V[4], root[4];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -376,10 +380,14 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     typename B::Place at(t, block, lane);
     B x;
 #pragma unroll 1
-    for (int i = 0; i < whole; ++i, at.next()) x.template step<true>(at, c, lane);
+    for (int i = 0; i < whole; ++i, at.next()) {
+      x.template load<true>(at);
+      x.template step<true>(at, c, lane);
+    }
 #pragma unroll 1
     for (int i = whole; i < a.blocks && (long long)i * kAdamBlock < rest; ++i) {
       const typename B::Place part(t, block + i, lane);
+      x.template load<false>(part);
       x.template step<false>(part, c, lane);
     }
   }
@@ -566,17 +574,18 @@ cudaError_t step_cap(const moe_adamw_t &o, const moe_adamw_tensor_t *t, const Pe
   long long blocks = 0;
   for (int i = 0; i < q.count; ++i) blocks += ceil_of(t[q.index[i]].numel, kAdamBlock);
   const long long most = (long long)kCtas * sms, warps = most * kWarps;
-  // The blocks of a turn.  8-bit states: as many as leave the longest share
-  // of a warp within a 32nd of the shortest possible: eight neighbouring
-  // blocks' scales are one sector of memory, and a warp's 2 KB of codes a run
-  // (38 million values in bf16 throughout: 77 us, two blocks 93).  float32:
-  // a sixteenth of a share (3 million values: 17.0 us, the other rule 18.2).
+  // The blocks of a turn.  8-bit states: eight neighbouring blocks' scales are
+  // one sector of memory and their codes a run of 2 KB, so short turns cost
+  // more (38 million values in bf16 throughout: two blocks 93 us, fourteen 77),
+  // about 0.4 / n of the time; against that stands the longest share of a warp.
+  // float32: a sixteenth of a share (3 million values: 17.0 us, the other rule
+  // 18.2).
   a.blocks = 1;
   if (E4M3) {
-    long long best = ceil_of(blocks, warps);
-    for (int n = 2; n <= kMostBlocks; ++n) {
-      const long long longest = ceil_of(ceil_of(blocks, n), warps) * n;
-      if (longest <= best + best / 32) a.blocks = n;
+    double best = 1e300;
+    for (int n = 1; n <= kMostBlocks; ++n) {
+      const double cost = (double)(ceil_of(ceil_of(blocks, n), warps) * n) * (1.0 + 0.4 / n);
+      if (cost < best) a.blocks = n, best = cost;
     }
   } else {
     const long long share = blocks / (warps * 16);
