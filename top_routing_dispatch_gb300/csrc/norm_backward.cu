@@ -120,19 +120,19 @@ __global__ void __launch_bounds__(kCta<GS>) norm_back_kernel(const BackArgs a) {
   if (groups > 1) {
     ptx::cp_async_wait<0>();
     __syncthreads();
-    float *all = reinterpret_cast<float *>(ring);
-    for (int pass = 0; pass < (a.bias ? 2 : 1); ++pass, out += (size_t)a.parts * H) {
-      if (pass)
-        io.put(all + group * H, H % 4 == 0, db);
-      else
-        io.put(all + group * H, H % 4 == 0, dw);
-      __syncthreads();
-      for (int c = threadIdx.x; c < H; c += blockDim.x) {
-        float v = all[c];
-        for (int q = 1; q < groups; ++q) v += all[q * H + c];
-        out[c] = v;
+    float *all = reinterpret_cast<float *>(ring), *all_b = all + groups * H;
+    io.put(all + group * H, H % 4 == 0, dw);
+    if (a.bias) io.put(all_b + group * H, H % 4 == 0, db);
+    __syncthreads();
+    for (int c = threadIdx.x; c < H; c += blockDim.x) {
+      float v = all[c];
+      for (int q = 1; q < groups; ++q) v += all[q * H + c];
+      out[c] = v;
+      if (a.bias) {
+        v = all_b[c];
+        for (int q = 1; q < groups; ++q) v += all_b[q * H + c];
+        out[(size_t)a.parts * H + c] = v;
       }
-      __syncthreads();
     }
     return;
   }
@@ -199,28 +199,28 @@ __global__ void __launch_bounds__(32 * kWarps) norm_columns_kernel(const BackArg
   if (a.bias) a.part[((size_t)a.parts + blockIdx.y) * a.H + col] = db;
 }
 
-constexpr int kJoinWarps = 16;
-
-// dweight (blockIdx.y 0) and dbias (1): the parts in a fixed order
-__global__ void __launch_bounds__(32 * kJoinWarps)
+// dweight (blockIdx.y 0) and dbias (1): the parts in a fixed order, 32 columns a
+// CTA.  Bound: latency.  Every warp's few parts are asked for at once, then
+// each warp adds one column's sums (4096 x 2048: 32 warps 2.9 us, 8 4.6).
+__global__ void __launch_bounds__(1024)
     norm_join_kernel(const float *part, int parts, int H, float *dweight, float *dbias) {
   pdl_enter();
-  __shared__ float acc[kJoinWarps][32];
+  __shared__ float acc[32][33];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int col = blockIdx.x * 32 + lane;
   float *out = blockIdx.y ? dbias : dweight;
   const float *p = part + (size_t)blockIdx.y * parts * H + col;
   float v = 0.f;
   if (col < H) {
-#pragma unroll 10
-    for (int i = warp; i < parts; i += kJoinWarps) v += p[(size_t)i * H];
+#pragma unroll 5
+    for (int i = warp; i < parts; i += 32) v += p[(size_t)i * H];
   }
   acc[warp][lane] = v;
   __syncthreads();
-  if (warp || col >= H) return;
+  v = acc[lane][warp];
 #pragma unroll
-  for (int i = 1; i < kJoinWarps; ++i) v += acc[i][lane];
-  out[col] = v;
+  for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(~0u, v, o);
+  if (lane == 0 && blockIdx.x * 32 + warp < H) out[blockIdx.x * 32 + warp] = v;
 }
 
 template <typename T, int GS, int VALS, bool SHIFT>
@@ -237,7 +237,7 @@ struct Backward {
       a.parts = g.ctas;
       constexpr int one = D * N * RowIO<T, GS, VALS, SHIFT>::BYTES;
       // the groups' sums are joined in the ring
-      static_assert(one >= GS * VALS * 4, "ring");
+      static_assert(one >= 2 * GS * VALS * 4, "ring");
       auto kernel = norm_back_kernel<T, GS, VALS, SHIFT, N, D>;
       static bool ready[64] = {false};
       *e = allow_smem(kernel, one * (kCta<GS> / GS), ready);
@@ -266,8 +266,8 @@ cudaError_t backward(BackArgs &a, float *dweight, float *dbias, cudaStream_t s) 
       e = launch_pdl(norm_back_long_kernel<T>, dim3(a.n), dim3(1024), 0, s, a);
   }
   if (e != cudaSuccess) return e;
-  return launch_pdl(norm_join_kernel, dim3((a.H + 31) / 32, dbias ? 2 : 1), dim3(32 * kJoinWarps),
-                    0, s, (const float *)a.part, a.parts, a.H, dweight, dbias);
+  return launch_pdl(norm_join_kernel, dim3((a.H + 31) / 32, dbias ? 2 : 1), dim3(1024), 0, s,
+                     (const float *)a.part, a.parts, a.H, dweight, dbias);
 }
 
 }  // namespace
