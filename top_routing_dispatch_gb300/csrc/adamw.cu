@@ -19,10 +19,19 @@
 // further on, in pairs for the two-operation instructions.
 //
 // Bound: HBM with float32 states (28 bytes a value in float32 throughout);
-// instructions come next, which is why the 8-bit form counts them: the largest
-// root is the root of the largest v, one warp-wide maximum of integers does for
-// a block (positive floats order as their bits), and what only an infinity, a
-// NaN, a tiny v or a zero code needs stands apart behind one test.
+// instructions and the loads' latency come next, which is why the 8-bit form
+// counts operations (36 a value): the largest root is the root of the largest
+// v, one warp-wide maximum of integers does for a block (positive floats order
+// as their bits), and what only an infinity, a NaN, a tiny v or a zero code
+// needs stands apart behind one test.  24 warps an SM: with more the memory
+// serves less (32: 403 million values 1.20 instead of 1.10 ms).
+//
+// Measured, 403 million values (bf16 parameters, float32 masters and
+// gradients): float32 states 1.87 ms, 6.5 TB/s; 8-bit 1.10 ms, 6.6 TB/s.  38
+// million in bf16 throughout with 8-bit states 76 us, 5.0 TB/s; 3.2 million
+// float32 in 64 tensors 17.7 us.  Not kept: loads of the next block during this
+// one's work in registers (the 8-bit layer 1.25 ms: registers spill) and by
+// asynchronous copies of 4 to 16 bytes a lane into shared memory (1.3 ms).
 #include <cuda_fp8.h>
 
 #include <type_traits>

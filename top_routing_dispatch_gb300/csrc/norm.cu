@@ -5,7 +5,13 @@
 //
 // Bound: HBM, every value read once and written once.  A row stays in its
 // group's registers between the sums and the result; weight and bias stay there
-// over all rows of a persistent CTA.
+// over all rows of a persistent CTA.  One CTA an SM: its groups are at
+// different points of their rows, which overlaps loads, sums and stores.
+//
+// Measured: 4096 rows of 2048 bf16 with residual (67 MB) 11.9 us, 5.6 TB/s;
+// 8192 rows of 7168 42 us (5.6 TB/s), with residual 79 (5.9); 1777 rows of 1031
+// float32 6.9 us; one row of 2048 2.0.  A CTA per row without a ring took 34 us
+// for the first; the float32 operations one by one, 63 for the second.
 #include "norm.cuh"
 
 namespace moe {

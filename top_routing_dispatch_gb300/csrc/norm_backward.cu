@@ -2,10 +2,18 @@
 //   dx = r (t - sum t / H - xh sum(t xh) / H) + ds,
 //   dw = sum over rows of dy xh, db = sum over rows of dy.
 //
-// Bound: HBM, every value read once and written once.  A group of threads
-// keeps its columns' sums for dw and db in registers over all its rows; the
-// groups of a CTA join them in shared memory, the CTAs through one float32 row
-// each in the workspace, added in a fixed order by a second kernel.
+// Bound: HBM, every value read once and written once; instructions come next
+// (33 a value of a long row).  A group of threads keeps its columns' sums for dw
+// and db in registers over all its rows; the groups of a CTA join them in
+// shared memory, the CTAs through one float32 row each in the workspace, added
+// in a fixed order by a second kernel.  A separate pass for dw and db would read
+// s and dy twice.
+//
+// Measured, both kernels: 4096 rows of 2048 bf16 with ds (67 MB) 16.9 us, of
+// which 1.6 store the ranges' sums and 2.6 add them; 8192 rows of 7168 (470 MB)
+// 83 us, 5.7 TB/s; 152 rows of 7168 7.5 us; 301 rows of 1031 float32 7.2.  Two
+// passes (a CTA a row, then columns) took 58 us for the first and 286 for the
+// second.
 #include "norm.cuh"
 
 namespace moe {
