@@ -4,6 +4,8 @@ LayerNorm is the norm before the layer with its gradients, GradNorm the global
 norm of all gradients, AdamW the step that takes them.  As in api.py the work
 is done by the library's kernels; here arguments are checked and turned into
 pointers.  Tensors are on the current CUDA device, where the library launches.
+Gradients are computed by explicit calls; torch's automatic differentiation does
+not see them.
 
 Calls run on `stream`, or the current stream.  Results that a call allocates
 are ready for that stream's next work.  Scratch memory belongs to the stream
