@@ -118,6 +118,28 @@ def test_block_refusals():
             M.MoEBlock(*[bad if j == i else a for j, a in enumerate(args)])
 
 
+def test_a_refused_forward_leaves_the_last_one():
+    """A forward that is refused has not touched what the last one left for its
+    backward; one that fails on the way leaves nothing to go back from."""
+    block, x, r, dout, ds = make_block(40, False, True)
+    block.forward(x, r)
+    want = [block.backward(dout, ds)] + [g.clone() for g in block.grads]
+    for kw in (dict(x=r, residual=x, out=torch.empty(40, 512, dtype=BF16, device="cuda")[:, ::2]),
+               dict(x=r, out=r.float()), dict(x=r, residual=x[:5])):
+        with pytest.raises(ValueError):
+            block.forward(**kw)
+    got = [block.backward(dout, ds)] + block.grads
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    w13, block.w13 = block.w13, None
+    with pytest.raises(Exception):
+        block.forward(r, x)
+    with pytest.raises(ValueError):
+        block.backward(dout, ds)
+    block.w13 = w13
+    block.forward(x, r)
+    assert torch.equal(block.backward(dout, ds), want[0])
+
+
 @pytest.mark.parametrize("state", ["f32", "e4m3"])
 def test_stack_step_is_its_single_calls(state):
     """A step of the example's stack: gradients clipped by the norm of them all,

@@ -436,6 +436,9 @@ class MoEBlock:
         where there is a residual, and holds until the next forward; backward
         reads it (or x, which then must not change meanwhile)."""
         d = self.desc
+        _want(out is None or (out.shape == self.h_in.shape and out.dtype == _BF16
+                              and out.is_contiguous() and out.device == self.h_in.device),
+              "out: like x, contiguous")
         self._enter(stream)
         if residual is None:
             self.norm(x, y=self.h_in, stats=self.stats, stream=stream)
@@ -443,10 +446,9 @@ class MoEBlock:
         else:
             self.norm(x, residual, y=self.h_in, s=self.s, stats=self.stats, stream=stream)
             rows = self.s
+        self._rows = None  # until the call's last kernel is enqueued
         if out is None:
             out = _empty(x.shape, _BF16, x.device, stream)
-        _want(out.shape == x.shape and out.dtype == _BF16 and out.is_contiguous()
-              and out.device == x.device, "out: like x, contiguous")
         api.moe_route_topk(d, self.h_in, self.w_gate, self.bias, self.topk_idx, self.topk_w,
                            self.logits, stream)
         api.moe_dispatch_layout(d, self.topk_idx, self.counts, self.offsets, self.perm,
