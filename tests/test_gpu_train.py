@@ -129,6 +129,35 @@ def test_norm_backward(n, H, form):
     assert all(a is None if b_ is None else torch.equal(a, b_) for a, b_ in zip(again, out))
 
 
+# rows of several CTAs: two to eight of them, a few rows and more than one turn
+# of all clusters, odd lengths in every phase, both sides of the last length
+CLUSTERS = [(1, 8200), (200, 8193), (170, 12296), (90, 16383), (161, 16384), (155, 16385), (7, 24576),
+            (60, 24577), (1, 32769), (150, 32768), (9, 40003), (8, 57344), (41, 65528), (37, 65529),
+            (40, 65536), (3, 65537)]
+
+
+@pytest.mark.parametrize("n,H", CLUSTERS)
+@pytest.mark.parametrize("T,rms", [(F32, False), (BF16, False), (BF16, True)], ids=["f32", "bf16", "bf16-rms"])
+def test_norm_rows_of_several_ctas(n, H, T, rms):
+    """Sums over a cluster have shorter chains than R.row_chain's: eight values
+    of a thread, five steps in a warp, eight warps' sums, five steps.  A cluster
+    takes at most n / 8 + 1 rows, and the sums of up to 76 of them are joined in
+    chains of 3 + 5: fewer than rows_chain's."""
+    layer, x, res, w, b, eps = norm_case(n, H, T, F32, rms, not rms, True, seed=40)
+    stats = torch.empty((2, n), device="cuda")
+    y, s = layer(x.cuda(), res.cuda(), stats=stats)
+    check_norm(layer, x, res, w, b, eps, rms, y, s, stats)
+    y2 = layer(s)
+    check_norm(layer, s.cpu(), None, w, b, eps, rms, y2, None, None)
+    dy, s = rand(41, n, H).to(T), s.cpu()
+    for ds in (None, res):
+        args = (dy.cuda(), s.cuda(), stats, None if ds is None else ds.cuda())
+        out = layer.backward(*args)
+        check_backward(layer, dy, s, stats, w, ds, rms, out, not rms)
+        again = layer.backward(*args)
+        assert all(p is None if q is None else torch.equal(p, q) for p, q in zip(again, out))
+
+
 @pytest.mark.parametrize("T", [F32, BF16])
 @pytest.mark.parametrize("H", [64, 256, 2048])
 def test_norm_rows_apart_and_off_alignment(T, H):

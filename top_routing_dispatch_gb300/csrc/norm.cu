@@ -32,7 +32,7 @@ struct NormArgs {
 // N: tensors read (x; x and residual)
 template <typename T, int GS, int VALS, bool SHIFT, int N, int D>
 __global__ void __launch_bounds__(kCta<GS>) norm_kernel(const NormArgs a) {
-  using IO = RowIO<T, GS, VALS, SHIFT>;
+  using IO = RowIO<T, GS, VALS, SHIFT, false>;
   pdl_enter();
   extern __shared__ __align__(16) char ring[];
   __shared__ __align__(16) float2 parts[2][kCta<GS> / 32];
@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kCta<GS>) norm_kernel(const NormArgs a) {
   const T *x_in = static_cast<const T *>(a.x) + row * a.xs;
   const T *res_in = static_cast<const T *>(a.res) + (N == 2 ? row * a.rs : 0);
   T *y = static_cast<T *>(a.y) + row * H, *s = static_cast<T *>(a.s) + (N == 2 ? row * H : 0);
-  const IO io(H, t, (int)(row * a.phase % IO::V));
+  const IO io(H, t, (int)(row * a.phase % IO::V), 0, 0);
   auto issue = [&](int slot) {
     if (ahead < a.n) {
       const uint32_t to = mine32 + slot * (N * IO::BYTES);
@@ -58,11 +58,8 @@ __global__ void __launch_bounds__(kCta<GS>) norm_kernel(const NormArgs a) {
 #pragma unroll 1
   for (int i = 0; i < D - 1; ++i) issue(i);
   float2 w[IO::P], b[IO::P];
-  constexpr bool KEEP = VALS <= 16;  // weight and bias in registers over all rows
-  if (KEEP) {
-    io.param(a.w, a.wide, a.vec, w);
-    if (a.b) io.param(a.b, a.wide, a.vec, b);
-  }
+  io.param(a.w, a.wide, a.vec, w);
+  if (a.b) io.param(a.b, a.wide, a.vec, b);
   const float inv = 1.f / (float)H;
   // all groups of a CTA take the same number of turns: those of a warp share
   // its shuffles
@@ -115,10 +112,6 @@ __global__ void __launch_bounds__(kCta<GS>) norm_kernel(const NormArgs a) {
     }
     const float r = rsqrt_of(var + a.eps);
     if (on) {
-      if (!KEEP) {
-        io.param(a.w, a.wide, a.vec, w);
-        if (a.b) io.param(a.b, a.wide, a.vec, b);
-      }
       const float2 r2 = both(r), o2 = both(-off);
 #pragma unroll
       for (int k = 0; k < IO::P; ++k) f[k] = mul2(a.rms ? f[k] : add2(f[k], o2), r2);
@@ -193,7 +186,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
   }
 }
 
-template <typename T, int GS, int VALS, bool SHIFT>
+template <typename T, int GS, int VALS, bool SHIFT, bool>
 struct Forward {
   template <int N>
   static bool with(const NormArgs &a, cudaStream_t s, cudaError_t *e) {
@@ -204,7 +197,7 @@ struct Forward {
       return false;
     } else {
       const NormGrid g = norm_grid<GS>(a.n, device_sm_count());
-      constexpr int one = D * N * RowIO<T, GS, VALS, SHIFT>::BYTES;
+      constexpr int one = D * N * RowIO<T, GS, VALS, SHIFT, false>::BYTES;
       auto kernel = norm_kernel<T, GS, VALS, SHIFT, N, D>;
       static bool ready[64] = {false};
       *e = allow_smem(kernel, one * (kCta<GS> / GS), ready);
@@ -213,7 +206,7 @@ struct Forward {
       return true;
     }
   }
-  static bool go(const NormArgs &a, cudaStream_t s, cudaError_t *e) {
+  static bool go(const NormArgs &a, int, cudaStream_t s, cudaError_t *e) {
     return a.res ? with<2>(a, s, e) : with<1>(a, s, e);
   }
 };

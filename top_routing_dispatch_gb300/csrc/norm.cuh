@@ -11,6 +11,10 @@
 // of 8 apart, so they all begin at the same place within 16 bytes (the phase):
 // the group works on the aligned pieces that cover a row, its columns shifted
 // by the phase, and masks the row's ends.
+//
+// In the backward, rows too long for one CTA belong to a cluster of up to 8, a
+// CTA being the group of its part of the row; the sums go through the cluster's
+// shared memory.
 #pragma once
 
 #include "pairs.cuh"
@@ -21,7 +25,8 @@ namespace moe {
 
 template <int GS>
 constexpr int kCta = GS > 512 ? GS : 512;  // threads of a CTA, at most
-constexpr int kNormParts = 304;    // CTAs of the backward, at most
+constexpr int kNormParts = 304;    // CTAs (or clusters) of the backward, at most
+constexpr int kMostCluster = 8;    // CTAs of a cluster, at most
 
 template <typename T>
 constexpr int kPer = 16 / (int)sizeof(T);  // values of 16 bytes
@@ -47,23 +52,29 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int by
 
 // A thread's VALS values of a row, in pairs: pieces of V values, GS apart.
 // SHIFT: rows have phases; else every piece lies inside the row or outside.
-template <typename T, int GS, int VALS, bool SHIFT>
+// CLUSTER: the group has `part` columns of a row, from `base` on.
+template <typename T, int GS, int VALS, bool SHIFT, bool CLUSTER>
 struct RowIO {
   static constexpr int V = kPer<T>, PIECES = VALS / V, P = VALS / 2;
   static constexpr int BYTES = GS * VALS * (int)sizeof(T);
   int H, t, o;       // row length, thread of the group, phase
+  int base;          // of the group's part of a row, without the phase
   bool full[PIECES]; // all of the piece lies inside the row
-  bool live[PIECES]; // some of it does
+  bool live[PIECES]; // some of it does, and it belongs to the group's part
 
-  __device__ __forceinline__ RowIO(int H_, int t_, int o_) : H(H_), t(t_), o(SHIFT ? o_ : 0) {
+  __device__ __forceinline__ RowIO(int H_, int t_, int o_, int base_, int part)
+      : H(H_), t(t_), o(SHIFT ? o_ : 0), base(CLUSTER ? base_ : 0) {
 #pragma unroll
     for (int c = 0; c < PIECES; ++c) {
       live[c] = first(c) < H;  // begins less than a piece before the row
       full[c] = SHIFT ? first(c) >= 0 && first(c) + V <= H : live[c];
+      if (CLUSTER && (c * GS + t) * V >= part) live[c] = full[c] = false;
     }
   }
   // column of a piece's first value
-  __device__ __forceinline__ int first(int c) const { return (c * GS + t) * V - (SHIFT ? o : 0); }
+  __device__ __forceinline__ int first(int c) const {
+    return base + (c * GS + t) * V - (SHIFT ? o : 0);
+  }
   // column of value k, and whether the row has it
   __device__ __forceinline__ int at(int k) const { return first(k / V) + k % V; }
   __device__ __forceinline__ bool has(int k) const { return (unsigned)at(k) < (unsigned)H; }
@@ -262,6 +273,52 @@ __device__ __forceinline__ F group_sum(F v, float2 *places, int group) {
   return v;
 }
 
+// A CTA's place among those that share its rows: the part of a row that it
+// takes, and which rows.
+template <int GS, int VALS, int V, bool CLUSTER>
+struct Share {
+  int size = 1, rank = 0, base = 0, part = GS * VALS;
+  int index = blockIdx.x, count = gridDim.x;  // of the CTA, or of the cluster
+  // span: columns of a row with its phases
+  __device__ __forceinline__ explicit Share(int span) {
+    if constexpr (CLUSTER) {
+      asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
+      rank = (int)ptx::cluster_ctarank();
+      part = ((span + V - 1) / V + size - 1) / size * V;  // equal parts, of whole pieces
+      base = rank * part;
+      index /= size, count /= size;
+    }
+  }
+};
+
+// Sum of a value (or of two) over the cluster, the same in every thread of it:
+// each warp's sum goes to all CTAs, each warp adds all of them.  `places`: one
+// per warp of the cluster, which the next sum must not use.
+template <int GS, typename F>
+__device__ __forceinline__ F cluster_sum(F v, float2 *places, int size, int rank) {
+  constexpr int W = GS / 32;
+  const int lane = threadIdx.x % 32;
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) v = plus(v, from_lane(v, o));
+  F *part = reinterpret_cast<F *>(places);
+  if (lane < size) {
+    const uint32_t to =
+        ptx::mapa_shared(ptx::smem_u32(part + rank * W + threadIdx.x / 32), (uint32_t)lane);
+    if constexpr (sizeof(F) == 8) {
+      ptx::st_cluster_v2(to, v.x, v.y);
+    } else {
+      ptx::st_cluster_u32(to, __float_as_uint(v));
+    }
+  }
+  __syncwarp();
+  ptx::cluster_sync();
+  v = lane < size * W ? part[lane] : F{};
+  for (int i = lane + 32; i < size * W; i += 32) v = plus(v, part[i]);
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) v = plus(v, from_lane(v, o));
+  return v;
+}
+
 // Slots of the ring for N tensors: `most`, or as many as fit in 200 KB (0:
 // rows too long).
 template <typename T, int GS, int VALS, int N>
@@ -273,23 +330,35 @@ constexpr int ring_slots(int most) {
 
 // The group for rows of H values: the smallest of which a thread takes 16, and
 // beyond 4096 by what was measured.  False where rows are longer.
-template <bool BACK, typename T, bool SHIFT, template <typename, int, int, bool> class G,
+template <bool BACK, typename T, bool SHIFT, template <typename, int, int, bool, bool> class G,
           typename A>
 bool by_length(A &a, cudaStream_t s, cudaError_t *e) {
   const int H = a.H + (SHIFT ? kPer<T> - 1 : 0);
-  if (H <= 8 * 16) return G<T, 8, 16, SHIFT>::go(a, s, e);
-  if (H <= 32 * 16) return G<T, 32, 16, SHIFT>::go(a, s, e);
-  if (H <= 64 * 16) return G<T, 64, 16, SHIFT>::go(a, s, e);
-  if (H <= 128 * 16) return G<T, 128, 16, SHIFT>::go(a, s, e);
-  if (H <= 256 * 16) return G<T, 256, 16, SHIFT>::go(a, s, e);
+  if (H <= 8 * 16) return G<T, 8, 16, SHIFT, false>::go(a, 1, s, e);
+  // 246723 x 136 bf16 with residual 46 us, on 32 threads 74
+  if (H <= 16 * 16) return G<T, 16, 16, SHIFT, false>::go(a, 1, s, e);
+  if (H <= 32 * 16) return G<T, 32, 16, SHIFT, false>::go(a, 1, s, e);
+  if (H <= 64 * 16) return G<T, 64, 16, SHIFT, false>::go(a, 1, s, e);
+  if (H <= 128 * 16) return G<T, 128, 16, SHIFT, false>::go(a, 1, s, e);
+  if (H <= 256 * 16) return G<T, 256, 16, SHIFT, false>::go(a, 1, s, e);
   // Rows of up to 8192: the backward on 1024 threads of 8 values, which leaves
   // it twice the warps beside its columns' sums (8192 x 7168 bf16 with ds 84
   // us, 512 threads of 16 values 94); the forward on 512 of 16 (45 us, 50).
-  if (H <= 8192) return G<T, BACK ? 1024 : 512, BACK ? 8 : 16, SHIFT>::go(a, s, e);
-  // up to 16384: the forward on 1024 threads of 16 (3001 x 16384 bf16 with
-  // residual 65 us, 512 of 32 values 73), the backward on 512 of 32 (143 us,
-  // 1024 of 16 169: its sums spill)
-  if (H <= 16384) return G<T, BACK ? 512 : 1024, BACK ? 32 : 16, SHIFT>::go(a, s, e);
+  constexpr int GS = BACK ? 1024 : 512;
+  if (H <= 8192) return G<T, GS, 8192 / GS, SHIFT, false>::go(a, 1, s, e);
+  if constexpr (BACK) {
+    // Longer ones on a cluster of 2, 4 or 8 such CTAs (with ds, bf16: 4096 x
+    // 16384 158 us, 512 threads of 32 values 175; 2048 x 32768 175, a CTA a row
+    // 760; three CTAs, for which the device has fewer places, cost more than
+    // four: 2730 x 24576 292 and 211).
+    int size = 2;
+    while (size * 8192 < H) size *= 2;
+    if (size <= kMostCluster) return G<T, GS, 8192 / GS, SHIFT, true>::go(a, size, s, e);
+  } else if (H <= 16384) {
+    // 1024 threads of 16, where two rows fit into the ring (3001 x 16384 bf16
+    // with residual 65 us, 512 of 32 values 73)
+    return G<T, 1024, 16, SHIFT, false>::go(a, 1, s, e);
+  }
   return false;
 }
 
@@ -308,6 +377,33 @@ inline NormGrid norm_grid(int n, int most) {
   constexpr int warp = GS < 32 ? 32 / GS : 1;  // whole warps
   g.groups = rows < all ? (rows + warp - 1) / warp * warp : all;
   return g;
+}
+
+// Clusters of a launch over n rows, at most `most` and as many as the device
+// holds at a time.  A cluster's next row keeps its phase where rows have one.
+template <typename K>
+inline cudaError_t cluster_grid(K kernel, int threads, int smem, int size, int n, int most, int per,
+                                int (&resident)[64][kMostCluster + 1], int *clusters) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int &r = resident[dev >= 0 && dev < 64 ? dev : 0][size];
+  if (r == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    cfg.gridDim = dim3(size), cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = size, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr, cfg.numAttrs = 1;
+    int found = 0;
+    e = cudaOccupancyMaxActiveClusters(&found, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    r = found < 1 ? 1 : found;
+  }
+  most = r < most ? r : most;
+  most = most < per ? per : most - most % per;
+  *clusters = n < most ? n : most;
+  return cudaSuccess;
 }
 
 inline bool on_bytes(const void *p, uintptr_t b) {

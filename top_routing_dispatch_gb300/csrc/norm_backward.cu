@@ -9,11 +9,14 @@
 // in a fixed order by a second kernel.  A separate pass for dw and db would read
 // s and dy twice.
 //
+// Rows of more than 8192 values belong to clusters of CTAs; their sums' barrier
+// bounds them (2.4 us a row of a cluster, whatever its length).
+//
 // Measured, both kernels: 4096 rows of 2048 bf16 with ds (67 MB) 16.9 us, of
 // which 1.6 store the ranges' sums and 2.6 add them; 8192 rows of 7168 (470 MB)
-// 83 us, 5.7 TB/s; 152 rows of 7168 7.5 us; 301 rows of 1031 float32 7.2.  Two
-// passes (a CTA a row, then columns) took 58 us for the first and 286 for the
-// second.
+// 83 us, 5.7 TB/s; 4096 rows of 16384 (537 MB) 158 us, 3.4 TB/s; 152 rows of
+// 7168 7.5 us; 301 rows of 1031 float32 7.2.  Two passes (a CTA a row, then
+// columns) took 58 us for the first and 286 for the second.
 #include "norm.cuh"
 
 namespace moe {
@@ -32,22 +35,23 @@ struct BackArgs {
 };
 
 // N: tensors read (dy and s; and ds)
-template <typename T, int GS, int VALS, bool SHIFT, int N, int D>
+template <typename T, int GS, int VALS, bool SHIFT, bool CLUSTER, int N, int D>
 __global__ void __launch_bounds__(kCta<GS>) norm_back_kernel(const BackArgs a) {
-  using IO = RowIO<T, GS, VALS, SHIFT>;
+  using IO = RowIO<T, GS, VALS, SHIFT, CLUSTER>;
   pdl_enter();
   extern __shared__ __align__(16) char ring[];
-  __shared__ __align__(16) float2 parts[2][kCta<GS> / 32];
+  __shared__ __align__(16) float2 parts[2][(CLUSTER ? kMostCluster : 1) * kCta<GS> / 32];
   const int t = threadIdx.x % GS, group = threadIdx.x / GS, groups = blockDim.x / GS;
   const int H = a.H, first = threadIdx.x / GS * GS / 32;
   char *mine = ring + group * (D * N * IO::BYTES);
   const uint32_t mine32 = ptx::smem_u32(mine);
-  const long long step = (long long)gridDim.x * groups;
-  long long row = blockIdx.x + (long long)gridDim.x * group, ahead = row;
+  const Share<GS, VALS, IO::V, CLUSTER> share(H + (SHIFT ? IO::V - 1 : 0));
+  const long long step = (long long)share.count * groups;
+  long long row = share.index + (long long)share.count * group, ahead = row;
   const T *dy_in = static_cast<const T *>(a.dy) + row * a.dys;
   const T *s_in = static_cast<const T *>(a.s) + row * a.ss;
   const T *ds_in = static_cast<const T *>(a.ds) + (N == 3 ? row * a.dss : 0);
-  const IO io(H, t, (int)(row * a.phase % IO::V));
+  const IO io(H, t, (int)(row * a.phase % IO::V), share.base, share.part);
   T *dx = static_cast<T *>(a.dx) + row * H;
   auto issue = [&](int slot) {
     if (ahead < a.n) {
@@ -63,13 +67,19 @@ __global__ void __launch_bounds__(kCta<GS>) norm_back_kernel(const BackArgs a) {
   };
 #pragma unroll 1
   for (int i = 0; i < D - 1; ++i) issue(i);
-  constexpr bool HOLD = VALS <= 16;  // a row's values in registers over its sum
+  if (CLUSTER) __syncwarp(), ptx::cluster_sync();  // the other CTAs' shared memory is there
+  auto sum_of = [&](auto v, float2 *places) {
+    if constexpr (CLUSTER)
+      return cluster_sum<GS>(v, places, share.size, share.rank);
+    else
+      return group_sum<GS>(v, places + first, group);
+  };
   float2 w[IO::P], dw[IO::P], db[IO::P];
-  if (HOLD) io.param(a.w, a.wide, a.vec, w);
+  io.param(a.w, a.wide, a.vec, w);
 #pragma unroll
   for (int k = 0; k < IO::P; ++k) dw[k] = db[k] = make_float2(0.f, 0.f);
   const float inv = 1.f / (float)H;
-  const int turns = (int)((a.n - blockIdx.x + step - 1) / step);
+  const int turns = (int)((a.n - share.index + step - 1) / step);
   // the statistics of the next row are on their way during a row
   float mu_in = 0.f, r_in = 0.f;
   auto stats = [&](long long at) {
@@ -91,10 +101,11 @@ __global__ void __launch_bounds__(kCta<GS>) norm_back_kernel(const BackArgs a) {
     // give r c1 and c2
     float2 g[IO::P], d[IO::P];
     float2 s1 = make_float2(0.f, 0.f), s2 = s1;
+    // `sums` is always true, but without it the compiler orders this part so that
+    // 8192 rows of 7168 take 99 us instead of 83
     auto fetch = [&](bool sums) {
       io.read(slot, g);
       io.read(slot + IO::BYTES, d);
-      if (!HOLD) io.param(a.w, a.wide, a.vec, w);
 #pragma unroll
       for (int k = 0; k < IO::P; ++k) d[k] = add2(d[k], mu);
 #pragma unroll
@@ -108,10 +119,9 @@ __global__ void __launch_bounds__(kCta<GS>) norm_back_kernel(const BackArgs a) {
       });
     };
     if (on) fetch(true);
-    s1 = group_sum<GS>(make_float2(s1.x + s1.y, s2.x + s2.y), parts[i & 1] + first, group);
+    s1 = sum_of(make_float2(s1.x + s1.y, s2.x + s2.y), parts[i & 1]);
     if (on) {
       const float2 c1 = both(a.rms ? 0.f : -s1.x * inv), c2 = both(-s1.y * inv * r.x * r.x);
-      if (!HOLD) fetch(false);
 #pragma unroll
       for (int k = 0; k < IO::P; ++k) g[k] = fma2(d[k], c2, add2(g[k], c1));
       if (N == 3) {
@@ -123,8 +133,8 @@ __global__ void __launch_bounds__(kCta<GS>) norm_back_kernel(const BackArgs a) {
     }
     row += step, dx += step * H;
   }
-  // the CTA's sums, group by group
-  float *out = a.part + (size_t)blockIdx.x * H;
+  // the CTA's (or cluster's) sums, group by group
+  float *out = a.part + (size_t)share.index * H;
   if (groups > 1) {
     ptx::cp_async_wait<0>();
     __syncthreads();
@@ -231,31 +241,37 @@ __global__ void __launch_bounds__(1024)
   if (lane == 0 && blockIdx.x * 32 + warp < H) out[blockIdx.x * 32 + warp] = v;
 }
 
-template <typename T, int GS, int VALS, bool SHIFT>
+template <typename T, int GS, int VALS, bool SHIFT, bool CLUSTER>
 struct Backward {
   template <int N>
-  static bool with(BackArgs &a, cudaStream_t s, cudaError_t *e) {
+  static bool with(BackArgs &a, int size, cudaStream_t s, cudaError_t *e) {
     // 8192 rows of 7168 bf16 with ds: four slots 84 us, three 101
     constexpr int D = ring_slots<T, GS, VALS, N>(4);
     if constexpr (D == 0) {
       return false;
     } else {
-      const int sms = device_sm_count();
-      const NormGrid g = norm_grid<GS>(a.n, sms < kNormParts ? sms : kNormParts);
-      a.parts = g.ctas;
-      constexpr int one = D * N * RowIO<T, GS, VALS, SHIFT>::BYTES;
+      constexpr int one = D * N * RowIO<T, GS, VALS, SHIFT, CLUSTER>::BYTES;
       // the groups' sums are joined in the ring
       static_assert(one >= 2 * GS * VALS * 4, "ring");
-      auto kernel = norm_back_kernel<T, GS, VALS, SHIFT, N, D>;
+      auto kernel = norm_back_kernel<T, GS, VALS, SHIFT, CLUSTER, N, D>;
       static bool ready[64] = {false};
       *e = allow_smem(kernel, one * (kCta<GS> / GS), ready);
-      if (*e == cudaSuccess)
+      if (*e != cudaSuccess) return true;
+      if constexpr (CLUSTER) {
+        static int resident[64][kMostCluster + 1] = {};
+        *e = cluster_grid(kernel, GS, one, size, a.n, kNormParts, SHIFT ? kPer<T> : 1, resident, &a.parts);
+        if (*e == cudaSuccess) *e = launch_pdl_cluster(kernel, a.parts, size, GS, one, s, a);
+      } else {
+        const int sms = device_sm_count();
+        const NormGrid g = norm_grid<GS>(a.n, sms < kNormParts ? sms : kNormParts);
+        a.parts = g.ctas;
         *e = launch_pdl(kernel, dim3(g.ctas), dim3(g.groups * GS), one * g.groups, s, a);
+      }
       return true;
     }
   }
-  static bool go(BackArgs &a, cudaStream_t s, cudaError_t *e) {
-    return a.ds ? with<3>(a, s, e) : with<2>(a, s, e);
+  static bool go(BackArgs &a, int size, cudaStream_t s, cudaError_t *e) {
+    return a.ds ? with<3>(a, size, s, e) : with<2>(a, size, s, e);
   }
 };
 

@@ -188,6 +188,11 @@ __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+// 8-byte store to (possibly another CTA's) shared memory of the cluster
+__device__ __forceinline__ void st_cluster_v2(uint32_t addr, float a, float b) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
+}
+
 // Arrive on an mbarrier given by its shared::cluster address (this CTA's or
 // a peer's), with release semantics at cluster scope.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {

@@ -19,6 +19,23 @@ inline cudaError_t allow_smem(K kernel, int bytes, bool (&ready)[64]) {
   return e;
 }
 
+// launch_pdl of clusters of `size` CTAs
+template <typename K, typename A>
+inline cudaError_t launch_pdl_cluster(K kernel, int clusters, int size, int threads, int smem,
+                                      cudaStream_t s, const A &a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(clusters * size), cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem, cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = size;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr, cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 // ---- norm.cu, norm_backward.cu
 constexpr int kNormMaxH = 1 << 20;  // longest row
 size_t norm_backward_ws_bytes(const moe_norm_t &d);
