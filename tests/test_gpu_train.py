@@ -129,6 +129,29 @@ def test_norm_backward(n, H, form):
     assert all(a is None if b_ is None else torch.equal(a, b_) for a, b_ in zip(again, out))
 
 
+# lengths of the groups between the powers of two, both ends of each, more than
+# one turn of all groups
+BETWEEN = [(900, 1025), (1600, 1529), (800, 2049), (470, 2553), (460, 2560), (310, 4089), (310, 4097),
+           (330, 5113), (320, 5120), (310, 5128), (320, 6137), (310, 6144), (170, 6152), (160, 7161),
+           (310, 7168), (160, 8185), (5000, 121), (5000, 249), (4999, 256)]
+
+
+@pytest.mark.parametrize("n,H", BETWEEN)
+@pytest.mark.parametrize("T,rms", [(F32, False), (BF16, False), (BF16, True)], ids=["f32", "bf16", "bf16-rms"])
+def test_norm_groups_between_powers_of_two(n, H, T, rms):
+    """Chains of a row: 16 values of a thread, five steps in a warp, five steps
+    (or five warps) more: fewer than R.row_chain's."""
+    layer, x, res, w, b, eps = norm_case(n, H, T, F32, rms, not rms, True, seed=50)
+    stats = torch.empty((2, n), device="cuda")
+    y, s = layer(x.cuda(), res.cuda(), stats=stats)
+    check_norm(layer, x, res, w, b, eps, rms, y, s, stats)
+    check_norm(layer, s.cpu(), None, w, b, eps, rms, layer(s), None, None)
+    dy, s = rand(51, n, H).to(T), s.cpu()
+    for ds in (None, res):
+        out = layer.backward(dy.cuda(), s.cuda(), stats, None if ds is None else ds.cuda())
+        check_backward(layer, dy, s, stats, w, ds, rms, out, not rms)
+
+
 # rows of several CTAs: two to eight of them, a few rows and more than one turn
 # of all clusters, odd lengths in every phase, both sides of the last length
 CLUSTERS = [(1, 8200), (200, 8193), (170, 12296), (90, 16383), (161, 16384), (155, 16385), (7, 24576),
@@ -218,6 +241,29 @@ def test_norm_keeps_a_bad_value_in_its_row(bad, H):
         assert torch.isnan(got[11].float()).all()
         keep = torch.arange(50) != 11
         assert torch.equal(got[keep.cuda()], want[keep.cuda()])
+
+
+@pytest.mark.parametrize("T", [F32, BF16])
+@pytest.mark.parametrize("H", [9, 121, 257, 1030, 2049, 4099, 5121, 7169, 8201, 16390])
+def test_norm_bad_values_at_a_rows_ends(T, H):
+    """NaN at both ends of a row, beside the neighbouring rows' ends: no other
+    row's results change, with residual and in the gradients of the rows."""
+    n = 400 if H < 3000 else 170
+    layer, x, res, w, b, eps = norm_case(n, H, T, F32, False, True, True)
+    dy, ds = rand(61, n, H).to(T), rand(62, n, H).to(T)
+    stats = torch.empty((2, n), device="cuda")
+
+    def run():
+        y, s = layer(x.cuda(), res.cuda(), stats=stats)
+        return y, s, layer.backward(dy.cuda(), s, stats, ds=ds.cuda())[0]
+
+    want = run()
+    keep = torch.ones(n, dtype=torch.bool)
+    for row, t in ((0, x), (7, res), (n // 2, dy), (n // 2 + 3, ds), (n - 1, x)):
+        t[row, 0] = t[row, -1] = math.nan
+        keep[row] = False
+    for got, clean in zip(run(), want):
+        assert torch.equal(got[keep.cuda()], clean[keep.cuda()])
 
 
 def test_norm_squares_beyond_float32():

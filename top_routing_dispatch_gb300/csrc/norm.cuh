@@ -23,8 +23,10 @@
 
 namespace moe {
 
+// Threads of a CTA, at most: whole groups of about 512 threads, with 128 registers
+// each (two groups of 320: the forward is content with 96)
 template <int GS>
-constexpr int kCta = GS > 512 ? GS : 512;  // threads of a CTA, at most
+constexpr int kCta = GS > 512 ? GS : GS == 320 ? 640 : 512 / GS * GS;
 constexpr int kNormParts = 304;    // CTAs (or clusters) of the backward, at most
 constexpr int kMostCluster = 8;    // CTAs of a cluster, at most
 
@@ -129,13 +131,15 @@ struct RowIO {
         if (!has(k)) (k % 2 ? f[k / 2].y : f[k / 2].x) = 0.f;
     }
   }
+  // CLEAN: with zeros for what the row does not have, else other rows' values
+  template <bool CLEAN>
   __device__ __forceinline__ void read(const char *slot, float2 (&f)[P]) const {
 #pragma unroll
     for (int c = 0; c < PIECES; ++c) {
       uint4 u = make_uint4(0, 0, 0, 0);
       if (live[c]) u = *reinterpret_cast<const uint4 *>(slot + (c * GS + t) * 16);
       widen(u, f + c * V / 2);
-      if (live[c]) mask(c, f);
+      if (CLEAN && live[c]) mask(c, f);
     }
   }
   // the values rounded to T
@@ -261,15 +265,21 @@ __device__ __forceinline__ F group_sum(F v, float2 *places, int group) {
   F *part = reinterpret_cast<F *>(places);
   if (threadIdx.x % 32 == 0) part[threadIdx.x / 32 % W] = v;
   group_sync<GS>(group);
-  if (W <= 4) {
+  if (W <= 5) {
     v = part[0];
 #pragma unroll
     for (int i = 1; i < W; ++i) v = plus(v, part[i]);
     return v;
   }
-  v = part[threadIdx.x % W];
+  if constexpr ((W & (W - 1)) == 0) {
+    v = part[threadIdx.x % W];
 #pragma unroll
-  for (int o = W / 2; o > 0; o /= 2) v = plus(v, from_lane(v, o));
+    for (int o = W / 2; o > 0; o /= 2) v = plus(v, from_lane(v, o));
+  } else {
+    v = threadIdx.x % 32 < W ? part[threadIdx.x % 32] : F{};
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) v = plus(v, from_lane(v, o));
+  }
   return v;
 }
 
@@ -330,6 +340,13 @@ constexpr int ring_slots(int most) {
 
 // The group for rows of H values: the smallest of which a thread takes 16, and
 // beyond 4096 by what was measured.  False where rows are longer.
+//
+// Sizes between the powers of two: with phases a length just above (or, counting
+// the phase, just below) one leaves half of a larger group's threads to masks,
+// so there every such size is worth it (bf16 with residual: 16376 x 2049 on 160
+// threads 45 us, its backward 58, on 256 79 and 103; 8186 x 4099 on 320 47, 512
+// 81).  Without phases idle threads cost little: 96 and 160 threads were slower
+// (21845 x 1536 backward 51 us, on 128 45).
 template <bool BACK, typename T, bool SHIFT, template <typename, int, int, bool, bool> class G,
           typename A>
 bool by_length(A &a, cudaStream_t s, cudaError_t *e) {
@@ -339,12 +356,28 @@ bool by_length(A &a, cudaStream_t s, cudaError_t *e) {
   if (H <= 16 * 16) return G<T, 16, 16, SHIFT, false>::go(a, 1, s, e);
   if (H <= 32 * 16) return G<T, 32, 16, SHIFT, false>::go(a, 1, s, e);
   if (H <= 64 * 16) return G<T, 64, 16, SHIFT, false>::go(a, 1, s, e);
+  if constexpr (SHIFT)
+    if (H <= 96 * 16) return G<T, 96, 16, SHIFT, false>::go(a, 1, s, e);
   if (H <= 128 * 16) return G<T, 128, 16, SHIFT, false>::go(a, 1, s, e);
+  if constexpr (SHIFT)
+    if (H <= 160 * 16) return G<T, 160, 16, SHIFT, false>::go(a, 1, s, e);
   if (H <= 256 * 16) return G<T, 256, 16, SHIFT, false>::go(a, 1, s, e);
-  // Rows of up to 8192: the backward on 1024 threads of 8 values, which leaves
-  // it twice the warps beside its columns' sums (8192 x 7168 bf16 with ds 84
-  // us, 512 threads of 16 values 94); the forward on 512 of 16 (45 us, 50).
-  constexpr int GS = BACK ? 1024 : 512;
+  // Rows of up to 8192: the backward on as many threads of 8 values as a row
+  // needs, which leaves it twice the warps beside its columns' sums (bf16 with
+  // ds: 8192 x 7168 on 896 79 us, on 1024 83, 512 of 16 values 94; 6553 x 5120
+  // on 640 49, 1024 65; float32 the same on all).  With phases the long ones are
+  // on 512 of 16, where fewer warps wait for those at a row's ends (4680 x 7169
+  // bf16 69 us, 1024 of 8 80).  The forward on 512 of 16 (8192 x 7168 45 us,
+  // 1024 of 8 50).
+  if constexpr (BACK && (SHIFT || sizeof(T) == 2)) {
+    if (H <= 640 * 8) return G<T, 640, 8, SHIFT, false>::go(a, 1, s, e);
+    if (H <= 768 * 8) return G<T, 768, 8, SHIFT, false>::go(a, 1, s, e);
+  }
+  if constexpr (BACK && !SHIFT && sizeof(T) == 2)
+    if (H <= 896 * 8) return G<T, 896, 8, SHIFT, false>::go(a, 1, s, e);
+  if constexpr (SHIFT && !BACK)
+    if (H <= 320 * 16) return G<T, 320, 16, SHIFT, false>::go(a, 1, s, e);
+  constexpr int GS = BACK && !SHIFT ? 1024 : 512;
   if (H <= 8192) return G<T, GS, 8192 / GS, SHIFT, false>::go(a, 1, s, e);
   if constexpr (BACK) {
     // Longer ones on a cluster of 2, 4 or 8 such CTAs (with ds, bf16: 4096 x
@@ -353,7 +386,7 @@ bool by_length(A &a, cudaStream_t s, cudaError_t *e) {
     // four: 2730 x 24576 292 and 211).
     int size = 2;
     while (size * 8192 < H) size *= 2;
-    if (size <= kMostCluster) return G<T, GS, 8192 / GS, SHIFT, true>::go(a, size, s, e);
+    if (size <= kMostCluster) return G<T, 1024, 8, SHIFT, true>::go(a, size, s, e);
   } else if (H <= 16384) {
     // 1024 threads of 16, where two rows fit into the ring (3001 x 16384 bf16
     // with residual 65 us, 512 of 32 values 73)

@@ -14,7 +14,7 @@
 //
 // Measured, both kernels: 4096 rows of 2048 bf16 with ds (67 MB) 16.9 us, of
 // which 1.6 store the ranges' sums and 2.6 add them; 8192 rows of 7168 (470 MB)
-// 83 us, 5.7 TB/s; 4096 rows of 16384 (537 MB) 158 us, 3.4 TB/s; 152 rows of
+// 79 us, 6.0 TB/s; 4096 rows of 16384 (537 MB) 158 us, 3.4 TB/s; 152 rows of
 // 7168 7.5 us; 301 rows of 1031 float32 7.2.  Two passes (a CTA a row, then
 // columns) took 58 us for the first and 286 for the second.
 #include "norm.cuh"
@@ -102,10 +102,10 @@ __global__ void __launch_bounds__(kCta<GS>) norm_back_kernel(const BackArgs a) {
     float2 g[IO::P], d[IO::P];
     float2 s1 = make_float2(0.f, 0.f), s2 = s1;
     // `sums` is always true, but without it the compiler orders this part so that
-    // 8192 rows of 7168 take 99 us instead of 83
+    // 8192 rows of 7168, on 1024 threads, take 99 us instead of 83
     auto fetch = [&](bool sums) {
-      io.read(slot, g);
-      io.read(slot + IO::BYTES, d);
+      io.template read<true>(slot, g);
+      io.template read<false>(slot + IO::BYTES, d);
 #pragma unroll
       for (int k = 0; k < IO::P; ++k) d[k] = add2(d[k], mu);
 #pragma unroll
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kCta<GS>) norm_back_kernel(const BackArgs a) {
 #pragma unroll
       for (int k = 0; k < IO::P; ++k) g[k] = fma2(d[k], c2, add2(g[k], c1));
       if (N == 3) {
-        io.read(slot + 2 * IO::BYTES, d);
+        io.template read<false>(slot + 2 * IO::BYTES, d);
 #pragma unroll
         for (int k = 0; k < IO::P; ++k) g[k] = add2(g[k], d[k]);
       }
