@@ -3,7 +3,7 @@
 //   dw = sum over rows of dy xh, db = sum over rows of dy.
 //
 // Bound: HBM, every value read once and written once; instructions come next
-// (33 a value of a long row).  A group of threads keeps its columns' sums for dw
+// (31 a value of a long row).  A group of threads keeps its columns' sums for dw
 // and db in registers over all its rows; the groups of a CTA join them in
 // shared memory, the CTAs through one float32 row each in the workspace, added
 // in a fixed order by a second kernel.  A separate pass for dw and db would read
