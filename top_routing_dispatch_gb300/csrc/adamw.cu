@@ -528,9 +528,10 @@ __global__ void __launch_bounds__(256)
   if (threadIdx.x) return;
   for (int i = 1; i < 8; ++i) sum += warps[i];
   const float n = (float)sqrt(sum);
-  const float f = max_norm / (n + 1e-6f);
+  // without a limit nothing is clipped, whatever the norm; a NaN stays
+  const float f = max_norm < INFINITY ? max_norm / (n + 1e-6f) : n == n ? 1.f : n;
   *norm = n;
-  *factor = f < 1.f ? f : f >= 1.f ? 1.f : f;  // NaN stays
+  *factor = f > 1.f ? 1.f : f;
 }
 
 // ---------------------------------------------------------------- launches

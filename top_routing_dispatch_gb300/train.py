@@ -219,7 +219,8 @@ class GradNorm:
     def __call__(self, max_norm=float("inf"), norm=None, factor=None, stream=None):
         """(norm, factor), one float32 each on the device (allocated when not
         given): the root of the sum of all squares, and min(1, max_norm / (norm
-        + 1e-6)), the grad_scale of a clipped AdamW step."""
+        + 1e-6)), the grad_scale of a clipped AdamW step.  The factor of an
+        infinite norm is 0, but 1 where max_norm is infinite too."""
         _here(self.device, self._index)
         norm = _empty(1, _F32, self.device, stream) if norm is None else norm
         factor = _empty(1, _F32, self.device, stream) if factor is None else factor
