@@ -37,3 +37,24 @@ def test_nothing_is_clipped_without_a_limit(state, bad):
     assert torch.equal(params[0][keep], params[1][keep])
     # a limit, however large, clips an infinite norm to nothing
     assert float(M().GradNorm([g])(3e38)[1]) == 0.0
+
+
+# ------------------------------------------------------- steps of other streams
+def test_steps_waits_for_every_stream():
+    """The number of steps, and a state to be saved, while steps on another
+    stream are still to run."""
+    p, g = torch.ones(5000, device="cuda"), torch.ones(5000, device="cuda")
+    opt = M().AdamW([p], [g])
+    opt.step()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)  # about 50 ms of work before the steps
+    for _ in range(3):
+        opt.step(stream=side)
+    assert opt.steps == 4
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    opt.step(stream=side)
+    d = opt.state_dict()
+    assert d["steps"] == 5

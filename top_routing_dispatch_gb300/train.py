@@ -343,7 +343,8 @@ class AdamW:
 
     @property
     def steps(self):
-        """Steps taken (waits for the device)."""
+        """Steps taken (waits for the device, whatever stream the steps ran on)."""
+        torch.cuda.synchronize(self.device)
         return int(self.step_state[:8].view(torch.int64).item())
 
     def state_dict(self):
