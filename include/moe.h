@@ -718,11 +718,33 @@ moe_status_t moe_grad_norm(const moe_tensor_t *tensors, int32_t count, float max
  * values share a scale:
  *   m = code * m_scale;  sqrt(v) = code * v_scale
  *   scale = (1/448) * max(largest finite magnitude of the 256, 2^-100)
- *   code = value * (1 / scale) rounded to nearest even; a positive sqrt(v) has
- *   at least the smallest positive code; an infinity or NaN has the NaN code.
+ *   code = value * (1 / scale) rounded; a positive sqrt(v) has at least the
+ *   smallest positive code; an infinity or NaN has the NaN code.
  * The step is taken with m and v before that rounding.  New states are zeros
  * (codes and scales too).
+ *
+ * rounding of the codes (read with MOE_E4M3 states only):
+ *   MOE_ROUND_NEAREST: to nearest even.  A change of a moment by less than half
+ *   a step of its code (3 to 6 % of it, or 2^-10 scale) is lost, and lost again
+ *   at the next step, unless the block's largest value moves the codes: v can
+ *   stay many times too large where beta2 is near 1 or the gradients of a block
+ *   have constant magnitudes, and m does not reach zero, so that a parameter
+ *   without a gradient, beside others that have one, keeps moving by a fraction
+ *   of lr a step.
+ *   MOE_ROUND_RANDOM: to one of the two neighbouring codes at random, so that
+ *   the expectations of m and of v are the values before rounding, and the codes
+ *   follow the recurrences on average over many values or steps; v of one value
+ *   scatters around its own by some tens of per cent.  The choice is a function
+ *   of the number of steps taken, the value's place in its block and its v: the
+ *   same call on the same states gives the same codes.
+ *   MOE_ROUND_BY_BETA2 (0): at random where beta2 is above 31/32, else to nearest.
  */
+typedef enum {
+  MOE_ROUND_BY_BETA2 = 0,
+  MOE_ROUND_NEAREST = 1,
+  MOE_ROUND_RANDOM = 2
+} moe_rounding_t;
+
 typedef struct {
   void *param;        /* numel values of dtype */
   float *master;      /* numel float32, or NULL */
@@ -742,6 +764,7 @@ typedef struct {
   const float *grad_scale; /* one float32 (device), or NULL: 1 */
   double beta1, beta2;     /* at least 0, below 1 */
   float eps;               /* at least 2^-126 */
+  int32_t rounding;        /* moe_rounding_t, of MOE_E4M3 states */
 } moe_adamw_t;
 
 /*

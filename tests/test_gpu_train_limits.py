@@ -58,3 +58,154 @@ def test_steps_waits_for_every_stream():
     opt.step(stream=side)
     d = opt.state_dict()
     assert d["steps"] == 5
+
+
+@pytest.mark.parametrize("kind", [(F32, F32, None, 0), (BF16, F32, True, 0), (BF16, BF16, None, 0), (F32, BF16, None, 1),
+                                  (BF16, F32, True, 3)], ids=["f32", "master", "bf16", "bf16-grad-off", "master-off"])
+def test_random_codes_are_the_stated_ones(kind):
+    """Every code and scale of five steps, from the hash of the step's number."""
+    from tests import train_random_reference as Q
+    from tests import train_reference as R
+    dtype, grad, masters, off = kind
+    shapes = [(1,), (255,), (257,), (100, 33), (30011,)]
+    gen = torch.Generator()
+    gen.manual_seed(3)
+
+    def make(n, dt, std):
+        buf = torch.empty(n + off, dtype=dt, device="cuda")
+        buf[off:] = (torch.randn(n, generator=gen) * std).to(dt).cuda()
+        return buf[off:]
+    params = [make(math.prod(s), dtype, 0.02).view(s) for s in shapes]
+    grads = [make(math.prod(s), grad, 10.0 ** -i).view(s) for i, s in enumerate(shapes)]
+    opt = M().AdamW(params, grads, lr=1e-3, betas=(0.9, 0.99), state=E4M3, masters=masters)
+    held = []
+    for s in shapes:
+        rows = -(-math.prod(s) // 256)
+        held.append((torch.zeros(rows, 256), torch.zeros(rows), torch.zeros(rows, 256), torch.zeros(rows)))
+    for t in range(5):
+        opt.step()
+        for i, (g, n) in enumerate(zip(grads, map(math.prod, shapes))):
+            held[i] = Q.step(R.blocks(g.cpu().float()), held[i], t, 0.9, 0.99)[0]
+            b, e = opt.offsets[i], opt.offsets[i] + len(held[i][1])
+            live = torch.arange(256 * (e - b)).view(-1, 256) < n
+            for got, want in ((opt.m, held[i][0]), (opt.v, held[i][2])):
+                got, want = got[b:e].cpu().float(), want.float()
+                assert torch.equal(got[live], want[live]) and not got[~live].any()
+            assert torch.equal(opt.m_scale[b:e].cpu(), held[i][1])
+            assert torch.equal(opt.v_scale[b:e].cpu(), held[i][3])
+        for g in grads:
+            g.copy_((torch.randn(g.shape, generator=gen) * 10.0 ** -(t % 3)))
+
+
+def test_rounding_goes_by_beta2_unless_given():
+    """To nearest up to 31/32, at random above; either where asked for."""
+    def codes(b2, rounding):
+        g = torch.linspace(-1, 1.7, 4000, device="cuda")
+        opt = M().AdamW([torch.zeros(4000, device="cuda")], [g], betas=(0.9, b2), state=E4M3, rounding=rounding)
+        for _ in range(2):
+            opt.step()
+        return torch.cat([opt.m.view(torch.uint8), opt.v.view(torch.uint8)])
+    for b2, default, other in ((0.5, "nearest", "random"), (31 / 32, "nearest", "random"),
+                               (0.969, "random", "nearest"), (0.999, "random", "nearest")):
+        assert torch.equal(codes(b2, None), codes(b2, default))
+        assert not torch.equal(codes(b2, None), codes(b2, other))
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_random_codes_keep_a_bad_gradient_where_it_is(bad):
+    def run(value):
+        g = torch.linspace(-1, 2, 700, device="cuda")
+        g[300] = value
+        p = torch.ones(700, device="cuda")
+        opt = M().AdamW([p], [g], state=E4M3)
+        for _ in range(3):
+            opt.step()
+        return p, opt
+    (p, opt), (q, good) = run(bad), run(0.0)
+    keep = (torch.arange(700) != 300).cuda()
+    assert torch.equal(p[keep], q[keep]) and torch.isfinite(p[keep]).all()
+    for a, b in ((opt.m, good.m), (opt.v, good.v)):
+        a, b = a.float().view(-1)[:700], b.float().view(-1)[:700]
+        assert torch.isnan(a[300]) and torch.equal(a[keep], b[keep])
+    assert torch.equal(opt.m_scale, good.m_scale) and torch.equal(opt.v_scale, good.v_scale)
+
+
+def test_random_codes_of_a_captured_step_are_the_eager_ones():
+    def make():
+        g = torch.linspace(-1, 1.7, 40_000, device="cuda")
+        return M().AdamW([torch.zeros(40_000, device="cuda")], [g], state=E4M3)
+    eager, captured = make(), make()
+    captured.step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured.step()
+    for _ in range(4):
+        graph.replay()
+    for _ in range(5):
+        eager.step()
+    assert captured.steps == eager.steps == 5
+    assert torch.equal(captured.params[0], eager.params[0])
+    for a, b in ((captured.m, eager.m), (captured.v, eager.v)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+# --------------------------------------------------- 8-bit states over many steps
+def long_run(b2, quiet, steps, **kw):
+    """An optimizer with 8-bit states and one with float32 states on the same
+    random gradients of unit size, a quarter of each block `quiet` times that
+    after 500 steps."""
+    n = 256 * 256
+    g, size = torch.empty(n, device="cuda"), torch.ones(256, 256, device="cuda")
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    opts = [M().AdamW([torch.zeros(n, device="cuda")], [g], lr=1e-3, betas=(0.9, b2), weight_decay=0.0, state=s, **k)
+            for s, k in ((E4M3, kw), (F32, {}))]
+    for t in range(steps):
+        if t == 500:
+            size[:, :64] = quiet
+        g.normal_(generator=gen).mul_(size.view(-1))
+        if t == steps - 400:
+            kept = opts[0].params[0].clone()
+        for o in opts:
+            o.step()
+    small, full = opts
+    m = small.m.double() * small.m_scale.double()[:, None]
+    v = (small.v.double() * small.v_scale.double()[:, None]).square()
+    return m, v, full.m.double(), full.v.double(), (small.params[0] - kept).view(256, 256)
+
+
+@pytest.mark.parametrize("b2,kw", [(0.999, {}), (0.98, {}), (0.95, dict(rounding="random"))],
+                         ids=["0.999", "0.98", "0.95-random"])
+def test_moments_in_8_bits_follow_their_recurrences(b2, kw):
+    """The sums of v over many values, and each m, against float32 states.
+
+    v: each step's rounding is unbiased, so V8 - V32 is a sum of martingale
+    differences times powers of b2.  Before a step v lies on a code; the step
+    moves it, against the codes at the new scale, by at most (1 - b2) c v with c
+    = 1 + g^2/v + |g_top^2/v_top - 1|, on average about 3.  The variance of a
+    rounding is at most the distance to one neighbour times the gap, 0.27 v:
+    0.8 (1 - b2) v^2 a step, 0.4 v^2 in all, for which v^2 = V32^2 (1 + cv^2):
+    cv^2 = 0.4 / 0.6, cv at most 0.82.  Six deviations of a mean of N values, and
+    (1000 steps of 3 u) 2e-4.  The values share each gradient's chance.
+
+    m: a rounding's deviation is at most half a gap, |m| / 16, and those of
+    earlier steps count 0.81 each: sqrt(1 / 0.19) / 16 = 0.144 of m's root mean
+    square, taken over 16384 values of a spread below 1.5 (six deviations of
+    their mean square: 1.5 * 6 / 128 = 7 %)."""
+    m, v, m32, v32, _ = long_run(b2, 0.01, 500 + int(14 / (1 - b2)), **kw)
+    for part in (slice(0, 64), slice(64, 256)):
+        N = v[:, part].numel()
+        assert abs(float(v[:, part].sum() / v32[:, part].sum()) - 1) <= 6 * 0.82 / N ** 0.5 + 2e-4
+        off = (m - m32)[:, part].square().mean().sqrt() / m32[:, part].square().mean().sqrt()
+        assert float(off) <= 0.144 * 1.07
+
+
+@pytest.mark.parametrize("b2,kw", [(0.999, {}), (0.98, {}), (0.95, dict(rounding="random"))],
+                         ids=["0.999", "0.98", "0.95-random"])
+def test_no_gradient_no_step_in_8_bits(b2, kw):
+    """Values without a gradient, beside others that have one: m goes to zero
+    and the parameter stays (a code of the smallest size has a chance of one in
+    ten to go at each step)."""
+    m, v, m32, v32, moved = long_run(b2, 0.0, 3000, **kw)
+    assert not m[:, :64].any() and (v[:, :64] > 0).all()
+    assert not moved[:, :64].any() and moved[:, 64:].all()

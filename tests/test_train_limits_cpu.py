@@ -1,0 +1,114 @@
+"""The training calls without a GPU, beside test_train_cpu.py: the rounding of
+8-bit states, and how calls handle their arguments and memory."""
+import ctypes
+import math
+import os
+import shutil
+
+import pytest
+import torch
+
+from tests import train_random_reference as Q
+from tests import train_reference as R
+
+pytestmark = pytest.mark.skipif(
+    not (shutil.which("nvcc") or os.path.exists("/usr/local/cuda/bin/nvcc")),
+    reason="CUDA toolkit not installed")
+
+BF16, F32, E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+P = 1 << 20  # a fake, well aligned pointer
+
+
+# ------------------------------------------------------- rounding of 8-bit states
+def test_rounding_refusals():
+    import top_routing_dispatch_gb300 as M
+    from top_routing_dispatch_gb300 import _lib
+    from top_routing_dispatch_gb300 import build as B
+    B.build()
+    lib = _lib.load()
+    t = _lib.AdamWTensor(param=P, grad=P, m=P, v=P, m_scale=P, v_scale=P, numel=300, weight_decay=0.1)
+    for state in (0, 2):
+        for rounding in (-1, 3):
+            o = _lib.AdamWDesc(state_dtype=state, lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, rounding=rounding)
+            assert lib.moe_adamw_step(ctypes.byref(o), ctypes.byref(t), 1, P, None) == 1
+    p, g = [torch.zeros(300)], [torch.zeros(300)]
+    for kw in (dict(state=E4M3, rounding="up"), dict(state=E4M3, rounding=True), dict(rounding="random"),
+               dict(rounding="nearest")):
+        with pytest.raises(ValueError, match="rounding"):
+            M.AdamW(p, g, **kw)
+
+
+def test_plain_random_codes_are_neighbours():
+    """A code stays, a value between two codes becomes one of them, and what is
+    past the largest becomes the largest."""
+    codes = torch.arange(0, 127, dtype=torch.uint8).view(E4M3).float()  # 0 to 448
+    chance = torch.arange(0, 1 << 32, 0xFFFFF7)[:, None]
+    for f in (Q.random_code, Q.random_root):
+        assert torch.equal(f(codes.expand(len(chance), -1), chance), codes.expand(len(chance), -1))
+        lo, hi = codes[:-1], codes[1:]
+        for part in (0.01, 0.3, 0.5, 0.99):
+            got = f((lo + (hi - lo) * part).expand(len(chance), -1), chance)
+            assert ((got == lo) | (got == hi)).all() and (got != got[:1]).any(0).all()
+    for f in (Q.random_code, Q.random_root):
+        assert (f(torch.full((len(chance),), 448 * (1 + 2.0 ** -22)), chance[:, 0]) == 448).all()
+    x = torch.linspace(-40, 40, 1000)
+    assert torch.equal(Q.random_code(-x, chance[:50]), -Q.random_code(x, chance[:50]))
+
+
+def test_plain_random_codes_are_unbiased():
+    """Over every chance of 20 bits: the mean code is y (below 2^-6 rounded once
+    more, by 2^-30 at most); over chances 2^-18 apart: the mean square of a
+    root's code is y^2 within that of the gap's (and float32)."""
+    y = torch.cat([torch.logspace(-4.2, 2.64, 60), torch.tensor([2.0 ** -6 * (1 - 2.0 ** -24), 2.0 ** -9, 447.9999, 3e-9])])
+    every, some = torch.arange(1 << 20) << 12, (torch.arange(1 << 18) << 14) + (1 << 13)
+    for v in y:
+        lo, hi = (t.double() for t in Q.neighbours(v.view(1)))
+        got = Q.random_code(v.expand(1 << 20), every).double().mean()
+        assert abs(got - v.double()) <= 2.0 ** -30 + 1e-12 * v
+        got = Q.random_root(v.expand(1 << 18), some).double().square().mean()
+        assert abs(got - v.double() ** 2) <= (hi ** 2 - lo ** 2) * (2.0 ** -18 + 2.0 ** -20)
+
+
+def test_plain_hash_looks_random():
+    """Over steps, places and values: each of the codes' chances is spread
+    evenly (deviations of a mean of N: six times sqrt(1 / 12 / N)), and those of
+    neighbouring steps, places and values are not correlated (six over sqrt N)."""
+    v = torch.full((64, 256), 0.37) * (1 + torch.arange(64)[:, None] * 2.0 ** -23)
+    pairs = [Q.chances(v, s) for s in [*range(64), *range(2 ** 33, 2 ** 33 + 64)]]
+    both = [(torch.stack([p[i] for p in pairs]).double() + 0.5) / 2 ** 32 - 0.5 for i in (0, 1)]
+    assert abs((both[0] * both[1]).mean()) * 12 <= 6 / math.sqrt(both[0].numel())
+    for u in both:
+        n = u.numel()
+        assert abs(u.mean()) <= 6 * math.sqrt(1 / 12 / n)
+        assert abs(u.square().mean() - 1 / 12) <= 6 * math.sqrt(1 / 180 / n)
+        for axis in range(3):
+            a, b = u.narrow(axis, 0, u.shape[axis] - 1), u.narrow(axis, 1, u.shape[axis] - 1)
+            assert abs((a * b).mean()) * 12 <= 6 / math.sqrt(a.numel())
+        for axis in range(3):  # the mean along each line
+            line = u.mean(axis)
+            assert line.abs().max() <= 7 * math.sqrt(1 / 12 / u.shape[axis])
+
+
+@pytest.mark.parametrize("random", [False, True])
+def test_plain_states_over_many_steps(random):
+    """Constant gradients, a quarter 100 times smaller after 100 steps, beta2
+    0.98: what the codes hold after 700 more (float32: v of the quarter within
+    0.02 of 1e-4 of the others').  At random it is there within the chance of
+    64 * 4 values (0.4 / 0.6 of v^2 and more in small steps: one deviation
+    below 1, six of the mean 0.38); to nearest it has not moved."""
+    b1, b2 = 0.9, 0.98
+    g = torch.ones(4, 256)
+    zeros = lambda: (torch.zeros(4, 256), torch.zeros(4))  # noqa: E731
+    m, ms, r, rs = *zeros(), *zeros()
+    for t in range(800):
+        if t == 100:
+            g[:, :64] = 0.01
+        if random:
+            (m, ms, r, rs), _, _ = Q.step(g, (m, ms, r, rs), t, b1, b2)
+        else:
+            root = R.decode(r, rs)
+            mm, v, root = R.adamw_moments(g, R.decode(m, ms), root * root, b1, b2)
+            (m, ms), (r, rs) = R.encode(mm, False), R.encode(root, True)
+    v = R.decode(r, rs).double().square()
+    ratio = float(v[:, :64].mean() / (1e-4 * v[:, 64:].mean()))
+    assert abs(ratio - 1) <= 0.4 if random else ratio > 5000

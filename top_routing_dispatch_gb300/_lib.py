@@ -37,6 +37,7 @@ DEV_BAD_ROUTING, DEV_BAD_LAYOUT, DEV_TIMEOUT, DEV_BAD_CACHE = 0x1, 0x2, 0x4, 0x8
 W4_MAX_PAIRS = 4096  # largest n * K of moe_experts_w4
 NOALLOC_MAX_PAIRS = 524288  # MOE_NOALLOC_MAX_PAIRS
 ADAMW_STATE_BYTES = 64  # MOE_ADAMW_STATE_BYTES
+ROUNDING = {None: 0, "nearest": 1, "random": 2}  # moe_rounding_t
 
 # workspace slots of moe_workspace_slot
 SLOT = dict(logits=0, topk_idx=1, topk_w=2, counts=3, offsets=4, perm=5, inv_perm=6,
@@ -82,7 +83,8 @@ class AdamWDesc(ctypes.Structure):
     """moe_adamw_t"""
     _fields_ = [("state_dtype", ctypes.c_int32), ("lr", ctypes.c_float),
                 ("lr_device", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p),
-                ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_float)]
+                ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_float),
+                ("rounding", ctypes.c_int32)]
 
 
 _vp = ctypes.c_void_p

@@ -15,6 +15,26 @@
 // because the step divides by it.  Infinities and NaN become NaN codes and do
 // not enter the scale, so they stay where they are.
 //
+// Rounding of the codes.  To nearest, what moves a moment by less than half a
+// step (3 to 6 %) is lost, step after step: beta2 = 0.999 moves a root by a
+// thousandth.  At random (RANDOM), the chance of the upper code is such that the
+// expectation of m, and of v (not of its root), is what was rounded, so the
+// codes follow the recurrences on average.  65536 values of unit gradients, a
+// quarter of each block 100 times smaller after 500 steps, 14 / (1 - beta2) later:
+// sum of v against float32 states, for the quarter and for the others; and, where
+// the quarter's gradients become zero, its movement 3000 steps later:
+//   beta2 0.999: nearest 1e4, 1.04; random 0.999, 1.000
+//   beta2 0.98: nearest 2e4, 2.4; random 1.000, 0.999
+//   beta2 0.95: nearest 2.4, 1.12, 0.17 lr a step (m stays at its smallest
+//   codes); random 0.999, 0.999, none
+// (5 to 95 % of the single roots: 0.75 to 1.27 at random.)  With only the roots at
+// random, m's smallest codes would move those parameters by 0.44 lr.  So beta2
+// above 31/32 is rounded at random unless the caller says otherwise.  That costs
+// 22 operations a value: the large layer below 1.12 instead of 1.10 ms, 38 million
+// values in bf16 throughout 92 instead of 76 us.
+// The chance comes from a hash of the step's number, the place in the block and
+// v's bits: a step repeats itself, captured or not, wherever the block lies.
+//
 // A warp takes 256 values at a time: lane l those at 4 l .. 4 l + 3 and 128
 // further on, in pairs for the two-operation instructions.
 //
@@ -204,6 +224,46 @@ struct Raw4 {
   }
 };
 
+// Bits that look random, the upper ones most: xor-shifts and products with odd
+// constants (fractions of the roots of 2, 3 and 5)
+__device__ __forceinline__ uint32_t mixed(uint32_t x, uint32_t salt) {
+  x = x * 0x6a09e667u + salt;
+  x ^= x >> 15;
+  x *= 0xbb67ae85u;
+  x ^= x >> 16;
+  return x * 0x3c6ef373u;
+}
+constexpr uint32_t kPlaceSalt = 0x9e3779b9u;  // for the next place of a block
+
+// Rounding at random works on bits: 2^-120 of a value in units of the scale has
+// float32's subnormals where e4m3 has its own, so codes are what the upper 12
+// bits hold, and the lower 20 are the way from one to the next.
+constexpr float kDown = 0x1p-120f, kUp = 0x1p120f;
+constexpr uint32_t kGap = 1u << 20;
+__device__ __forceinline__ float code_of(uint32_t bits) {
+  return __uint_as_float(bits & ~(kGap - 1));
+}
+// Codes beside x: its mean over the chances (upper 20 bits) is x
+__device__ __forceinline__ float2 random_codes(float2 x, uint32_t ca, uint32_t cb) {
+  x = mul2(x, both(kDown));
+  return mul2(make_float2(code_of(__float_as_uint(x.x) + (ca >> 12)),
+                          code_of(__float_as_uint(x.y) + (cb >> 12))),
+              both(kUp));
+}
+// Codes beside y >= 0, of which the mean square over the chances (upper 23 bits)
+// is y^2: the upper one where y^2 - lo^2 is more than the chance times hi^2 - lo^2
+__device__ __forceinline__ float2 random_roots(float2 y, uint32_t ca, uint32_t cb) {
+  const float2 x = mul2(y, both(kDown));
+  const uint32_t a = __float_as_uint(x.x) & ~(kGap - 1), b = __float_as_uint(x.y) & ~(kGap - 1);
+  const float2 lo = mul2(make_float2(__uint_as_float(a), __uint_as_float(b)), both(kUp));
+  const float2 hi = mul2(make_float2(__uint_as_float(a + kGap), __uint_as_float(b + kGap)), both(kUp));
+  const float2 ll = mul2(mul2(lo, both(-1.f)), lo);
+  const float2 u = add2(make_float2(__uint_as_float(ca >> 9 | 0x3f800000u),
+                                    __uint_as_float(cb >> 9 | 0x3f800000u)), both(-1.f));
+  const float2 way = fma2(y, y, ll), part = mul2(u, fma2(hi, hi, ll));
+  return make_float2(way.x > part.x ? hi.x : lo.x, way.y > part.y ? hi.y : lo.y);
+}
+
 // Magnitude that counts for a scale: that of a finite value
 __device__ __forceinline__ uint32_t finite_bits(float v) {
   const uint32_t b = __float_as_uint(v) & 0x7fffffffu;
@@ -216,12 +276,13 @@ __device__ __forceinline__ float nan_if_not_finite(float v, float code) {
 struct Step {
   float keep, fac, c1, c2, b1, a1, b2, a2, eps;
   bool scaled;
+  uint32_t salt;  // of the step's number and the lane
 };
 
 // A lane's part of a block of 256 values.  PT, GT: types of parameter and
 // gradient; MASTER: a bf16 parameter's float32 master (a float32 parameter's
-// is a copy, written where there is one).
-template <bool E4M3, typename PT, typename GT, bool MASTER>
+// is a copy, written where there is one); RANDOM: codes rounded at random.
+template <bool E4M3, bool RANDOM, typename PT, typename GT, bool MASTER>
 struct Block {
   using ST = typename std::conditional<E4M3, uint8_t, float>::type;
   using WT = typename std::conditional<MASTER, float, PT>::type;  // what the step starts from
@@ -331,7 +392,14 @@ struct Block {
       if (lane == 0) *t.ms = sm, *t.vs = sv;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float2 x = mul2(M[k], im), y = mul2(root[k], iv);
+        float2 x = mul2(M[k], im), y = mul2(root[k], iv);
+        if constexpr (RANDOM) {
+          const uint32_t salt = c.salt + (k / 2 * 128 + k % 2 * 2) * kPlaceSalt;
+          const uint32_t g = mixed(__float_as_uint(V[k].x), salt);
+          const uint32_t h = mixed(__float_as_uint(V[k].y), salt + kPlaceSalt);
+          x = random_codes(x, g * kPlaceSalt, h * kPlaceSalt);
+          y = random_roots(y, g, h);
+        }
         if (bad) {
           V[k] = make_float2(nan_if_not_finite(root[k].x, y.x), nan_if_not_finite(root[k].y, y.y));
           M[k] = make_float2(nan_if_not_finite(M[k].x, x.x), nan_if_not_finite(M[k].y, x.y));
@@ -366,15 +434,19 @@ struct Block {
   }
 };
 
-template <bool E4M3, typename PT, typename GT, bool MASTER, int CAP>
+template <bool E4M3, bool RANDOM, typename PT, typename GT, bool MASTER, int CAP>
 __global__ void __launch_bounds__(kThreads, kCtas)
     adamw_kernel(const __grid_constant__ StepArgs<CAP> a) {
-  using B = Block<E4M3, PT, GT, MASTER>;
+  using B = Block<E4M3, RANDOM, PT, GT, MASTER>;
   pdl_enter();
   const int lane = threadIdx.x % 32;
   const float lr = a.lr_dev ? __ldg(a.lr_dev) : a.lr;
   Step c = {1.f, a.scale ? __ldg(a.scale) : 1.f, lr * a.state->inv1, a.state->inv2, a.b1, a.a1,
-            a.b2, a.a2, a.eps, a.scale != nullptr};
+            a.b2, a.a2, a.eps, a.scale != nullptr, 0u};
+  if constexpr (RANDOM) {
+    const unsigned long long steps = (unsigned long long)a.state->steps;
+    c.salt = mixed((uint32_t)steps, mixed((uint32_t)(steps >> 32), 1u)) + 4 * lane * kPlaceSalt;
+  }
   int k = 0;
   // neighbouring turns on neighbouring CTAs' warps
   for (int turn = threadIdx.x / 32 * gridDim.x + blockIdx.x; turn < a.turns;
@@ -576,7 +648,7 @@ struct Pending {  // tensors of one kind, by index
   int count = 0;
 };
 
-template <bool E4M3, typename PT, typename GT, bool MASTER, int CAP>
+template <bool E4M3, bool RANDOM, typename PT, typename GT, bool MASTER, int CAP>
 cudaError_t step_cap(const moe_adamw_t &o, const moe_adamw_tensor_t *t, const Pending &q, bool last,
                      StepState *state, cudaStream_t s) {
   StepArgs<CAP> a;
@@ -619,35 +691,37 @@ cudaError_t step_cap(const moe_adamw_t &o, const moe_adamw_tensor_t *t, const Pe
   a.turns = (int)turns, a.last = last;
   const long long ctas = ceil_of(turns, kWarps);
   const unsigned grid = (unsigned)(ctas < 1 ? 1 : ctas < most ? ctas : most);
-  return launch_pdl(adamw_kernel<E4M3, PT, GT, MASTER, CAP>, dim3(grid), dim3(kThreads), 0, s, a);
+  return launch_pdl(adamw_kernel<E4M3, RANDOM, PT, GT, MASTER, CAP>, dim3(grid), dim3(kThreads), 0, s,
+                    a);
 }
 
-template <bool E4M3, typename PT, typename GT, bool MASTER>
+template <bool E4M3, bool RANDOM, typename PT, typename GT, bool MASTER>
 cudaError_t step_kind(const moe_adamw_t &o, const moe_adamw_tensor_t *t, const Pending &q,
                       bool last, StepState *state, cudaStream_t s) {
-  return q.count <= kSmallCap ? step_cap<E4M3, PT, GT, MASTER, kSmallCap>(o, t, q, last, state, s)
-                              : step_cap<E4M3, PT, GT, MASTER, kLargeCap>(o, t, q, last, state, s);
+  return q.count <= kSmallCap
+             ? step_cap<E4M3, RANDOM, PT, GT, MASTER, kSmallCap>(o, t, q, last, state, s)
+             : step_cap<E4M3, RANDOM, PT, GT, MASTER, kLargeCap>(o, t, q, last, state, s);
 }
 
-template <bool E4M3>
+template <bool E4M3, bool RANDOM>
 cudaError_t step_launch(const moe_adamw_t &o, const moe_adamw_tensor_t *t, Kind k, Pending &q,
                         bool last, StepState *st, cudaStream_t s) {
   using B = __nv_bfloat16;
   cudaError_t e;
   if (!k.param_bf16)
-    e = k.grad_bf16 ? step_kind<E4M3, float, B, false>(o, t, q, last, st, s)
-                    : step_kind<E4M3, float, float, false>(o, t, q, last, st, s);
+    e = k.grad_bf16 ? step_kind<E4M3, RANDOM, float, B, false>(o, t, q, last, st, s)
+                    : step_kind<E4M3, RANDOM, float, float, false>(o, t, q, last, st, s);
   else if (k.master)
-    e = k.grad_bf16 ? step_kind<E4M3, B, B, true>(o, t, q, last, st, s)
-                    : step_kind<E4M3, B, float, true>(o, t, q, last, st, s);
+    e = k.grad_bf16 ? step_kind<E4M3, RANDOM, B, B, true>(o, t, q, last, st, s)
+                    : step_kind<E4M3, RANDOM, B, float, true>(o, t, q, last, st, s);
   else
-    e = k.grad_bf16 ? step_kind<E4M3, B, B, false>(o, t, q, last, st, s)
-                    : step_kind<E4M3, B, float, false>(o, t, q, last, st, s);
+    e = k.grad_bf16 ? step_kind<E4M3, RANDOM, B, B, false>(o, t, q, last, st, s)
+                    : step_kind<E4M3, RANDOM, B, float, false>(o, t, q, last, st, s);
   q.count = 0;
   return e;
 }
 
-template <bool E4M3>
+template <bool E4M3, bool RANDOM>
 cudaError_t step_all(const moe_adamw_t &o, const moe_adamw_tensor_t *t, int count,
                      StepState *state, cudaStream_t s) {
   // every kind's tensors, and which kind has the last launch
@@ -659,7 +733,7 @@ cudaError_t step_all(const moe_adamw_t &o, const moe_adamw_tensor_t *t, int coun
   int left = 0;
   for (int n : of) left += n;
   Pending q;
-  if (left == 0) return step_launch<E4M3>(o, t, Kind{false, false, false}, q, true, state, s);
+  if (left == 0) return step_launch<E4M3, RANDOM>(o, t, Kind{false, false, false}, q, true, state, s);
   cudaError_t e = cudaSuccess;
   for (int id = 0; id < 8; ++id) {
     if (!of[id]) continue;
@@ -671,7 +745,8 @@ cudaError_t step_all(const moe_adamw_t &o, const moe_adamw_tensor_t *t, int coun
         continue;
       q.index[q.count++] = i;
       --left, --of[id];
-      if (q.count == kLargeCap || of[id] == 0) e = step_launch<E4M3>(o, t, k, q, left == 0, state, s);
+      if (q.count == kLargeCap || of[id] == 0)
+        e = step_launch<E4M3, RANDOM>(o, t, k, q, left == 0, state, s);
     }
   }
   return e;
@@ -709,8 +784,11 @@ cudaError_t launch_adamw_set_steps(double p1, double p2, long long steps, void *
 cudaError_t launch_adamw(const moe_adamw_t &o, const moe_adamw_tensor_t *t, int count, void *state,
                          cudaStream_t s) {
   StepState *st = static_cast<StepState *>(state);
-  return o.state_dtype == MOE_E4M3 ? step_all<true>(o, t, count, st, s)
-                                   : step_all<false>(o, t, count, st, s);
+  if (o.state_dtype != MOE_E4M3) return step_all<false, false>(o, t, count, st, s);
+  const bool random = o.rounding == MOE_ROUND_RANDOM ||
+                      (o.rounding == MOE_ROUND_BY_BETA2 && o.beta2 > 31.0 / 32.0);
+  return random ? step_all<true, true>(o, t, count, st, s)
+                : step_all<true, false>(o, t, count, st, s);
 }
 
 }  // namespace moe

@@ -121,6 +121,8 @@ moe_status_t moe_adamw_step(const moe_adamw_t *opt, const moe_adamw_tensor_t *te
                             int32_t count, void *step_state, moe_stream_t stream) {
   if (!opt || count < 0 || (count && !tensors)) return MOE_ERR_INVALID_ARG;
   if (opt->state_dtype != MOE_F32 && opt->state_dtype != MOE_E4M3) return MOE_ERR_INVALID_ARG;
+  if (opt->rounding < MOE_ROUND_BY_BETA2 || opt->rounding > MOE_ROUND_RANDOM)
+    return MOE_ERR_INVALID_ARG;
   if (!betas_ok(opt->beta1, opt->beta2) || !(opt->eps >= 0x1p-126f) || isinf(opt->eps))
     return MOE_ERR_INVALID_ARG;
   if (!(opt->lr >= 0.f) || isinf(opt->lr)) return MOE_ERR_INVALID_ARG;
