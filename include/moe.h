@@ -680,10 +680,11 @@ moe_status_t moe_layer_norm_backward(const moe_norm_t *desc, const void *dy, int
 
 /*
  * Global norm of gradients: norm = sqrt(sum of g^2 over all values of all
- * tensors), factor = min(1, max_norm / (norm + 1e-6)).  Squares are float32
- * (a value beyond 1.8e19 makes the norm infinite and the factor 0), their sum
- * double in a fixed order.  max_norm infinite: nothing is clipped, the factor
- * is 1 whatever the norm.  A NaN gives NaN for both.
+ * tensors), factor = min(1, max_norm / (norm + 1e-6)).  A value whose square is
+ * beyond float32 (1.8e19) makes the norm infinite and the factor 0; smaller ones
+ * and their sums do not, and values count however small they are.  Sums have a
+ * fixed order.  max_norm infinite: nothing is clipped, the factor is 1 whatever
+ * the norm.  A NaN gives NaN for both.
  *   tensors: host array of `count` descriptions, read during the call; data
  *   numel contiguous values of dtype (MOE_F32 or MOE_BF16; NULL where numel is
  *   0).  At most 65536 tensors of 2^40 values in all (else

@@ -209,3 +209,49 @@ def test_no_gradient_no_step_in_8_bits(b2, kw):
     m, v, m32, v32, moved = long_run(b2, 0.0, 3000, **kw)
     assert not m[:, :64].any() and (v[:, :64] > 0).all()
     assert not moved[:, :64].any() and moved[:, 64:].all()
+
+
+# --------------------------------------------------- gradient norm's range
+def check_grad_norm(grads, slack=0):
+    total = math.sqrt(math.fsum(float(t.detach().cpu().double().square().sum()) for t in grads))
+    norm, factor = M().GradNorm(grads)(1.0)
+    # nine roundings of a square and of its short sum, halved by the root, and the root's own;
+    # the result may be subnormal
+    tol = (4.5 + 1) * 2.0 ** -24 * total + 2.0 ** -150
+    assert abs(float(norm) - total) <= tol, (float(norm), total)
+    want = min(1.0, 1 / (total + 1e-6))
+    assert abs(float(factor) - want) <= (5.5 + 4) * 2.0 ** -24 * want + 2.0 ** -150
+
+
+@pytest.mark.parametrize("T", [F32, BF16])
+@pytest.mark.parametrize("off", [0, 1])
+@pytest.mark.parametrize("size", [4e18, 1.3e19, 1.84e19])
+def test_grad_norm_of_large_values(T, off, size):
+    """Squares that float32 holds (below 3.4e38, the square of 1.84e19), sums of
+    them that it does not: beside each other, one at the end, on all threads."""
+    for n, at in ((64, slice(0, 64)), (70_003, slice(5_000, 5_128)), (30_011, slice(30_004, 30_011)),
+                  (40_000, slice(0, 40_000))):
+        t = torch.full((n + off,), 1e-3, device="cuda")[off:]
+        t[at] = size
+        check_grad_norm([t.to(T) if not off else torch.cat([t[:1], t]).to(T)[1:]])
+
+
+@pytest.mark.parametrize("T", [F32, BF16])
+@pytest.mark.parametrize("off", [0, 1])
+@pytest.mark.parametrize("size", [1e-21, 1e-23, 3e-30, 1.2e-38, 1e-44])
+def test_grad_norm_of_small_values(T, off, size):
+    """Values whose squares float32 rounds to few bits, or to zero."""
+    if T == BF16 and size < 1e-40:
+        size = 1e-40  # a subnormal of bfloat16
+    for n in (1, 3, 64, 5_003, 100_000):
+        t = torch.full((n + off,), size, device="cuda")
+        t[off::2] *= -1
+        t = t.to(T)[off:]
+        check_grad_norm([t, torch.zeros(3000, device="cuda")])
+    check_grad_norm([torch.full((3000,), size, device="cuda", dtype=T), torch.full((10,), 1e-19, device="cuda"),
+                     torch.full((5000,), 1e-17, device="cuda")])
+
+
+def test_grad_norm_of_zeros():
+    z = torch.zeros(70_001, device="cuda")
+    assert [float(t) for t in M().GradNorm([z, -z, z.to(BF16)])(1.0)] == [0.0, 1.0]
