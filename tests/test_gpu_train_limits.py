@@ -255,3 +255,25 @@ def test_grad_norm_of_small_values(T, off, size):
 def test_grad_norm_of_zeros():
     z = torch.zeros(70_001, device="cuda")
     assert [float(t) for t in M().GradNorm([z, -z, z.to(BF16)])(1.0)] == [0.0, 1.0]
+
+
+# ------------------------------------------------------------ refused calls
+def test_a_refused_backward_changes_no_gradient():
+    """Every argument of a block's backward is checked before its first kernel."""
+    from tests.test_gpu_train_step import make_block
+    block, x, r, dout, ds = make_block(40, False, True)
+    block.forward(x, r)
+    block.backward(dout, ds)
+    want = [g.clone() for g in block.grads] + [block.d_in.clone()]
+    wide = torch.empty(40, 512, dtype=BF16, device="cuda")
+    for kw in (dict(ds=ds.float()), dict(ds=ds[:5]), dict(ds=ds.t().contiguous().t()), dict(ds=ds.cpu()),
+               dict(ds=ds[:1].expand(40, 256)),
+               dict(dx=ds.float()), dict(dx=ds[:5]), dict(dx=wide[:, ::2]), dict(dx=wide[:, :256]),
+               dict(dx=ds.cpu())):
+        with pytest.raises(ValueError):
+            block.backward(ds if kw.get("ds") is None else r, **kw)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, block.grads + [block.d_in]))
+    # rows of ds a stride apart are taken
+    wide[:, :256] = ds
+    assert torch.equal(block.backward(dout, wide[:, :256]), block.backward(dout, ds))

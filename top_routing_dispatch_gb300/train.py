@@ -481,6 +481,11 @@ class MoEBlock:
         _want(self._rows is not None, "backward before a forward")
         _want(dout.dtype == _BF16 and dout.shape == self.h_in.shape and dout.is_contiguous()
               and dout.device == self.h_in.device, "dout: like out, contiguous")
+        if ds is not None:  # the norm's checks, before the first kernel
+            stride = self.norm._rows(ds, self.h_in.shape, "ds")[1]
+            _want(self.desc.n < 2 or stride >= self.desc.H, "ds: rows that do not overlap")
+        if dx is not None:
+            self.norm._out(dx, self.h_in.shape, _BF16, "dx")
         self._enter(stream)
         api.moe_backward(self.desc, self.h_in, self.w_gate, self.w13, self.w2, dout, self.logits,
                          self.topk_idx, self.topk_w, self.offsets, self.inv_perm, self.x_perm,
