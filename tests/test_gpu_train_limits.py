@@ -277,3 +277,28 @@ def test_a_refused_backward_changes_no_gradient():
     # rows of ds a stride apart are taken
     wide[:, :256] = ds
     assert torch.equal(block.backward(dout, wide[:, :256]), block.backward(dout, ds))
+
+
+# ------------------------------------------------------------- scratch memory
+def norm_inputs(n, H, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    x, dy = (torch.randn(n, H, device="cuda", generator=g).to(BF16) for _ in range(2))
+    layer, stats = M().LayerNorm(torch.ones(H, device="cuda"), torch.zeros(H, device="cuda"), dtype=BF16), None
+    stats = torch.empty((2, n), device="cuda")
+    layer(x, stats=stats)
+    return layer, dy, x, stats
+
+
+def test_scratch_of_long_rows_is_not_kept():
+    from top_routing_dispatch_gb300 import train
+    layer, dy, x, stats = norm_inputs(320, 65536, 1)
+    want = layer.backward(dy, x, stats)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (None, side):
+        for _ in range(3):
+            got = layer.backward(dy, x, stats, stream=stream)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(t.numel() <= 32 << 20 for t in train._scratch.values())

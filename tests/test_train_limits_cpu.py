@@ -112,3 +112,53 @@ def test_plain_states_over_many_steps(random):
     v = R.decode(r, rs).double().square()
     ratio = float(v[:, :64].mean() / (1e-4 * v[:, 64:].mean()))
     assert abs(ratio - 1) <= 0.4 if random else ratio > 5000
+
+
+# -------------------------------------------------------------- scratch memory
+def scratch(monkeypatch, capturing=False):
+    """_scratch_for with what it asks of torch recorded, not done."""
+    import contextlib
+
+    from top_routing_dispatch_gb300 import train
+    made = []
+
+    def empty(nbytes, dtype, device, stream):
+        made.append((nbytes, stream))
+        return torch.empty(nbytes, dtype=dtype)
+    monkeypatch.setattr(train, "_empty", empty)
+    monkeypatch.setattr(train, "_scratch", {})
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: h)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device: 0)
+    ask = lambda nbytes, handle, stream=None: train._scratch_for(  # noqa: E731
+        nbytes, torch.device("cpu"), 0, stream, handle)
+    return train, made, ask
+
+
+def test_scratch_is_kept_for_a_stream(monkeypatch):
+    train, made, ask = scratch(monkeypatch)
+    a = ask(1000, 7)
+    assert ask(1 << 20, 7) is a and ask(500, 7, 7) is a and len(made) == 1
+    b = ask(1000, 8, 8)
+    assert b is not a and b.data_ptr() != a.data_ptr()
+    big = ask(3 << 20, 7)
+    assert ask(10, 7) is big and big.numel() == 3 << 20
+
+
+def test_large_scratch_is_not_kept(monkeypatch):
+    train, made, ask = scratch(monkeypatch)
+    kept = ask(32 << 20, 7)
+    assert ask(5, 7) is kept
+    for stream in (None, 7):
+        t = ask((32 << 20) + 1, 7, stream)
+        assert t is not kept and t.numel() == (32 << 20) + 1 and made[-1] == (t.numel(), stream)
+    assert list(train._scratch.values()) == [kept] and ask(5, 7) is kept
+
+
+def test_scratch_of_a_capture_is_the_graphs(monkeypatch):
+    train, made, ask = scratch(monkeypatch, capturing=True)
+    for handle, stream in ((7, None), (7, 7)):
+        a, b = ask(1000, handle, stream), ask(1000, handle, stream)
+        assert a.data_ptr() != b.data_ptr()
+    assert not train._scratch

@@ -11,7 +11,9 @@ Calls run on `stream`, or the current stream.  Results that a call allocates
 are ready for that stream's next work.  Scratch memory belongs to the stream
 (calls on one stream run one after another), or to the graph where a call is
 captured, so calls of one LayerNorm or GradNorm may run on several streams, and
-in several graphs, at the same time.
+in several graphs, at the same time.  Up to 32 MiB are kept for each stream; more
+is allocated for the call.  A stream that is given by its handle, and is not
+torch's, is to be destroyed only behind the work of its calls.
 """
 from __future__ import annotations
 
@@ -31,6 +33,7 @@ BLOCK = 256  # values of a tensor that share a scale where states are held in 8 
 
 
 _scratch = {}  # (device, stream handle): the stream's scratch memory
+_KEPT = 32 << 20  # bytes of it, at most: a norm's backward of up to 13797 columns
 # a call with scratch is two kernels: threads' calls enter a stream one after another
 _scratch_lock = threading.Lock()
 
@@ -43,6 +46,8 @@ def _scratch_for(nbytes, device, index, stream, handle):
         with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device)):
             capturing = torch.cuda.is_current_stream_capturing()
     if capturing:  # memory of the graph
+        return _empty(nbytes, torch.uint8, device, stream)
+    if nbytes > _KEPT:  # memory of the call: reused in the stream's order
         return _empty(nbytes, torch.uint8, device, stream)
     t = _scratch.get((index, handle))
     if t is None or t.numel() < nbytes:
