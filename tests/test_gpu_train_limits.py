@@ -302,3 +302,29 @@ def test_scratch_of_long_rows_is_not_kept():
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert all(t.numel() <= 32 << 20 for t in train._scratch.values())
+
+
+def test_calls_on_the_threads_own_streams():
+    """Backward calls and gradient norms of two threads, each on its thread's
+    default stream (handle 2)."""
+    import threading
+    work = []
+    for seed, (n, H) in enumerate(((600, 2048), (500, 1024))):
+        args = norm_inputs(n, H, seed)
+        norm = M().GradNorm([args[1], args[2]])
+        work.append((args, norm, [*args[0].backward(*args[1:]), *norm(1.0)], []))
+    torch.cuda.synchronize()
+
+    def calls(args, norm, want, got):
+        layer, *rest = args
+        for _ in range(25):
+            got.append([*layer.backward(*rest, stream=2), *norm(1.0, stream=2)])
+        torch.cuda.ExternalStream(2).synchronize()
+    threads = [threading.Thread(target=calls, args=w) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for *_, want, got in work:
+        assert len(got) == 25 and all(torch.equal(a, b) for g in got for a, b in zip(g, want))

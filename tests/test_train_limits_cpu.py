@@ -156,9 +156,55 @@ def test_large_scratch_is_not_kept(monkeypatch):
     assert list(train._scratch.values()) == [kept] and ask(5, 7) is kept
 
 
+@pytest.mark.parametrize("stream", [None, 2])
+def test_threads_streams_of_one_handle_share_no_scratch(monkeypatch, stream):
+    """The per-thread default stream has the handle 2 in every thread."""
+    train, made, ask = scratch(monkeypatch)
+    a, b = ask(1000, 2, stream), ask(1000, 2, stream)
+    assert a.data_ptr() != b.data_ptr() and not train._scratch
+    assert made == [(1000, 2)] * 2
+
+
 def test_scratch_of_a_capture_is_the_graphs(monkeypatch):
     train, made, ask = scratch(monkeypatch, capturing=True)
-    for handle, stream in ((7, None), (7, 7)):
+    for handle, stream in ((7, None), (7, 7), (2, 2)):
         a, b = ask(1000, handle, stream), ask(1000, handle, stream)
         assert a.data_ptr() != b.data_ptr()
     assert not train._scratch
+
+
+def test_workspaces_of_the_threads_own_streams(monkeypatch):
+    """One workspace for each thread's default stream, although it has one handle."""
+    import contextlib
+    import threading
+
+    from top_routing_dispatch_gb300 import decode
+    waits = []
+
+    class Stream:
+        def __init__(self, handle, device=None):
+            self.cuda_stream = handle
+
+        def wait_event(self, event):
+            waits.append(("event", self.cuda_stream))
+
+        def wait_stream(self, other):
+            waits.append(("stream", self.cuda_stream, other.cuda_stream))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device: Stream(0))
+    ws = decode._Workspaces(torch.device("cpu"), lambda: torch.zeros(8), [])
+    got = {}
+
+    def ask(i):
+        got[i] = [ws.add(2) for _ in range(3)]
+    for i in range(2):
+        t = threading.Thread(target=ask, args=(i,))
+        t.start()
+        t.join()
+    ask(2)
+    assert all(len(set(p)) == 1 for p in got.values()) and len({p[0] for p in got.values()}) == 3
+    assert waits == [("event", 2), ("stream", 2, 0)] * 3 and 2 not in ws.pointers
+    a = ws.add(5)
+    assert ws.pointers[5] == a and len(ws.all) == 5

@@ -19,6 +19,7 @@ from .api import MoEError, _check, _p, _stream, make_desc  # noqa: F401
 
 _DT = {torch.float32: _lib.MOE_F32, torch.bfloat16: _lib.MOE_BF16,
        torch.float8_e4m3fn: _lib.MOE_E4M3}
+_PER_THREAD = 2  # cudaStreamPerThread: one handle for a stream of every thread
 _I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -59,10 +60,18 @@ def _empty(shape, dtype, device, stream):
     current one, where the result is used."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    current = torch.cuda.current_stream(device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(_handle(stream, None), device=device)):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(current)
+    current, handle = torch.cuda.current_stream(device), _handle(stream, None)
+    own = torch.cuda.ExternalStream(handle, device=device)
+    with torch.cuda.stream(own):
+        if handle != _PER_THREAD or torch.cuda.is_current_stream_capturing():
+            t = torch.empty(shape, dtype=dtype, device=device)
+            t.record_stream(current)
+            return t
+    # the allocator takes threads' streams of one handle for one stream: memory of
+    # the current one, which this thread's waits for
+    t = torch.empty(shape, dtype=dtype, device=device)
+    own.wait_stream(current)
+    t.record_stream(own)
     return t
 
 
@@ -74,7 +83,7 @@ class _Workspaces:
     tensors, filled on the stream that is current now.  Another stream's first
     call waits for that.  A call under stream capture on a stream that has no
     workspace yet uses the first one (memory allocated by a capture belongs to
-    its graph)."""
+    its graph).  The per-thread default stream is one of each thread."""
 
     def __init__(self, device, make, kept):
         self._device, self._make, self._kept = device, make, kept
@@ -83,19 +92,36 @@ class _Workspaces:
         if device.type == "cuda":
             stream = torch.cuda.current_stream(device)
             self._made, handle = stream.record_event(), stream.cuda_stream
-        self.pointers = {handle: self.all[0].data_ptr()}  # by stream handle
+        self._thread = threading.local()  # pointer: of the thread's default stream
+        self.pointers = {}  # by stream handle
+        if handle == _PER_THREAD:
+            self._thread.pointer = self.all[0].data_ptr()
+        else:
+            self.pointers[handle] = self.all[0].data_ptr()
 
     def add(self, handle):
         """The workspace of a stream's first call."""
+        own = handle == _PER_THREAD
+        if own and hasattr(self._thread, "pointer"):
+            return self._thread.pointer
         stream = torch.cuda.ExternalStream(handle, device=self._device)
         with torch.cuda.stream(stream):
             if torch.cuda.is_current_stream_capturing():
                 return self.all[0].data_ptr()
             stream.wait_event(self._made)
-            ws = self._make()
+            if not own:
+                ws = self._make()
+        if own:  # not of the handle's memory, which the allocator takes for one stream's
+            home = torch.cuda.default_stream(self._device)
+            with torch.cuda.stream(home):
+                ws = self._make()
+            stream.wait_stream(home)
         for t in self._kept:
             t.record_stream(stream)
         self.all.append(ws)
+        if own:
+            self._thread.pointer = ws.data_ptr()
+            return ws.data_ptr()
         return self.pointers.setdefault(handle, ws.data_ptr())
 
 

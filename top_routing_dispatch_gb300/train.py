@@ -26,7 +26,8 @@ import torch
 
 from . import _lib, api, decode
 from .api import MoEError, _check, _p
-from .decode import _BF16, _DT, _F32, _I32, _Workspaces, _empty, _handle, _index, _want
+from .decode import (_BF16, _DT, _F32, _I32, _PER_THREAD, _Workspaces, _empty, _handle, _index,
+                     _want)
 
 _E4M3 = torch.float8_e4m3fn
 BLOCK = 256  # values of a tensor that share a scale where states are held in 8 bits
@@ -47,6 +48,9 @@ def _scratch_for(nbytes, device, index, stream, handle):
             capturing = torch.cuda.is_current_stream_capturing()
     if capturing:  # memory of the graph
         return _empty(nbytes, torch.uint8, device, stream)
+    if handle == _PER_THREAD:  # another stream in every thread: memory of the call
+        with torch.cuda.stream(torch.cuda.default_stream(device)):
+            return _empty(nbytes, torch.uint8, device, handle)
     if nbytes > _KEPT:  # memory of the call: reused in the stream's order
         return _empty(nbytes, torch.uint8, device, stream)
     t = _scratch.get((index, handle))
