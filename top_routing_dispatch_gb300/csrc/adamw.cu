@@ -57,6 +57,7 @@
 #include <type_traits>
 
 #include "pairs.cuh"
+#include "roots.cuh"
 #include "train.cuh"
 
 namespace moe {
@@ -126,31 +127,8 @@ __device__ __forceinline__ int tensor_of(const A &a, int turn, int k) {
   return lo;
 }
 
-// Roots and reciprocals rounded to nearest, by one Newton step with a fused
-// residual (Markstein) from the hardware's approximations.  Compared with
-// __fsqrt_rn and __frcp_rn on every float32: equal from 2^-102 up (below, the
-// residual underflows), and from 2^-126 to 2^126.
-__device__ __forceinline__ float approx_rsqrt(float v) {
-  float y;
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
-  return y;
-}
-__device__ __forceinline__ float approx_rcp(float x) {  // within 2 u
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float2 root2(float2 v) {
-  const float2 y = make_float2(approx_rsqrt(v.x), approx_rsqrt(v.y));
-  const float2 s = mul2(v, y);
-  return fma2(fma2(mul2(s, both(-1.f)), s, v), mul2(y, both(0.5f)), s);
-}
 __device__ __forceinline__ bool plain_root(uint32_t bits) {
   return bits >= 0x0f800000u && bits < kInfBits;  // 2^-96 to the largest finite
-}
-__device__ __forceinline__ float reciprocal(float x) {
-  const float y = approx_rcp(x);
-  return fmaf(fmaf(-x, y, 1.f), y, y);
 }
 
 // 4 neighbouring values as they lie in memory; those past `left` are 0

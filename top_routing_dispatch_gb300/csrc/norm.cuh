@@ -19,6 +19,7 @@
 
 #include "pairs.cuh"
 #include "ptx.cuh"
+#include "roots.cuh"
 #include "train.cuh"
 
 namespace moe {
@@ -230,13 +231,6 @@ struct Phases {
     one = one && (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % per == step;
   }
 };
-
-// 1 / sqrt(v), within 2 u: one Newton step from the approximation
-__device__ __forceinline__ float rsqrt_of(float v) {
-  const float r = rsqrtf(v);
-  const float e = fmaf(-v * r, r, 1.f);
-  return v > 0.f && v < INFINITY ? fmaf(0.5f * r, e, r) : r;
-}
 
 // Barrier of the group's threads
 template <int GS>
