@@ -208,3 +208,29 @@ def test_workspaces_of_the_threads_own_streams(monkeypatch):
     assert waits == [("event", 2), ("stream", 2, 0)] * 3 and 2 not in ws.pointers
     a = ws.add(5)
     assert ws.pointers[5] == a and len(ws.all) == 5
+
+
+# ----------------------------------------------------------- refused before work
+def test_a_refused_state_changes_nothing(monkeypatch):
+    """Every entry is checked before the first one is copied."""
+    from top_routing_dispatch_gb300 import train
+    opt = train.AdamW.__new__(train.AdamW)
+    taken = []
+    monkeypatch.setattr(train.AdamW, "_set_steps", lambda self, steps: taken.append(steps))
+    opt.m, opt.v = torch.zeros(2, 256), torch.zeros(2, 256)
+    opt.m_scale = opt.v_scale = None
+    opt.masters = [torch.zeros(300), None]
+    good = dict(steps=7, m=torch.ones(2, 256), v=torch.ones(2, 256), m_scale=None, v_scale=None,
+                masters=[torch.ones(300), None])
+    for kw in (dict(steps=-1), dict(steps="x"), dict(steps=2 ** 63), dict(m=torch.ones(3, 256)), dict(v=torch.ones(2, 256).double()),
+               dict(v_scale=torch.ones(2)), dict(masters=[torch.ones(300)]), dict(masters=[None, None]),
+               dict(masters=[torch.ones(299), None])):
+        with pytest.raises(ValueError):
+            opt.load_state_dict({**good, **kw})
+        assert not opt.m.any() and not opt.v.any() and not opt.masters[0].any() and not taken
+    for name in ("steps", "m", "v", "m_scale", "v_scale"):
+        with pytest.raises(KeyError):
+            opt.load_state_dict({k: v for k, v in good.items() if k != name})
+        assert not opt.m.any() and not taken
+    opt.load_state_dict(good)
+    assert opt.m.all() and opt.v.all() and opt.masters[0].all() and taken == [7]

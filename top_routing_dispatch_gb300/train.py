@@ -375,6 +375,8 @@ class AdamW:
     def load_state_dict(self, d):
         """Copies states and the number of steps, and masters where d has them,
         on the current stream."""
+        steps = int(d["steps"])
+        _want(0 <= steps < 2 ** 63, "steps: a number of steps")
         for name in ("m", "v", "m_scale", "v_scale"):
             to, src = getattr(self, name), d[name]
             _want((to is None) == (src is None) and (to is None or (
@@ -389,7 +391,7 @@ class AdamW:
         for to, src in zip(self.masters, masters or []):
             if to is not None:
                 to.copy_(src)
-        self._set_steps(int(d["steps"]))
+        self._set_steps(steps)
 
 
 class MoEBlock:
