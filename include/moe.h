@@ -775,7 +775,7 @@ typedef struct {
  * it on the device, so that a step captured in a CUDA graph counts on when it
  * is replayed.  Its first 8 bytes are the number, an int64.
  *   tensors: host array of `count` descriptions, read during the call; no two
- *   may share memory that the step writes.  At most 65536 tensors of 2^40
+ *   may share memory that the step writes, nor may a gradient lie in it.  At most 65536 tensors of 2^40
  *   values in all (else MOE_ERR_UNSUPPORTED).  Steps on one step_state or on
  *   one tensor are ordered by the caller.
  */

@@ -234,3 +234,20 @@ def test_a_refused_state_changes_nothing(monkeypatch):
         assert not opt.m.any() and not taken
     opt.load_state_dict(good)
     assert opt.m.all() and opt.v.all() and opt.masters[0].all() and taken == [7]
+
+
+def test_gradients_in_the_memory_of_parameters_are_refused():
+    """A step reads gradients and writes parameters and masters in no order."""
+    import top_routing_dispatch_gb300 as M
+    line = torch.zeros(2000)
+    p, g = [line[:300], line[300:700]], [torch.zeros(300), torch.zeros(400)]
+    masters = [None, torch.zeros(400)]
+    bf = [torch.zeros(300), torch.zeros(400, dtype=BF16)]
+    for kw in (dict(grads=[line[:300], g[1]]), dict(grads=[g[0], line[299:699]]), dict(grads=[line[699:999], g[1]]),
+               dict(params=bf, masters=masters, grads=[g[0], masters[1]])):
+        with pytest.raises(ValueError, match="memory"):
+            M.AdamW(**{**dict(params=p, grads=g), **kw})
+    # beside them, and one gradient of two parameters, are taken (and refused for the device)
+    for grads in ([line[700:1000], line[1000:1400]], [line[1000:1300], line[900:1300]]):
+        with pytest.raises(ValueError, match="CUDA"):
+            M.AdamW(p, grads)

@@ -17,6 +17,7 @@ torch's, is to be destroyed only behind the work of its calls.
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import itertools
 import math
@@ -295,11 +296,16 @@ class AdamW:
             w is None or (w.dtype == _F32 and w.shape == p.shape and w.is_contiguous()
                           and w.device == dev) for p, w in zip(self.params, self.masters)),
               "masters: a contiguous float32 tensor of its shape, or None, for every parameter")
-        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
-                       for t in self.params + [w for w in self.masters if w is not None]
-                       if t.numel())
-        _want(all(a[1] <= b[0] for a, b in zip(spans, spans[1:])),
+        span = lambda t: (t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())  # noqa: E731
+        written = sorted(span(t) for t in self.params + [w for w in self.masters if w is not None]
+                         if t.numel())
+        _want(all(a[1] <= b[0] for a, b in zip(written, written[1:])),
               "params and masters: no two may share memory")
+        ends = [b for _, b in written]
+        for a, b in (span(g) for g in self.grads if g.numel()):
+            i = bisect.bisect_right(ends, a)  # the first that ends behind the gradient's beginning
+            _want(i == len(written) or b <= written[i][0],
+                  "grads: none may share memory with a parameter or a master")
         self.lr, self.betas, self.eps = float(lr), (float(betas[0]), float(betas[1])), float(eps)
         _want(all(0 <= b < 1 for b in self.betas) and 2.0 ** -126 <= self.eps < math.inf
               and all(0 <= d < math.inf for d in [self.lr] + decay),
