@@ -775,9 +775,9 @@ typedef struct {
  * it on the device, so that a step captured in a CUDA graph counts on when it
  * is replayed.  Its first 8 bytes are the number, an int64.
  *   tensors: host array of `count` descriptions, read during the call; no two
- *   may share memory that the step writes, nor may a gradient lie in it.  At most 65536 tensors of 2^40
- *   values in all (else MOE_ERR_UNSUPPORTED).  Steps on one step_state or on
- *   one tensor are ordered by the caller.
+ *   may share memory that the step writes, nor may a gradient lie in it.  At
+ *   most 65536 tensors of 2^40 values in all (else MOE_ERR_UNSUPPORTED).  Steps
+ *   on one step_state or on one tensor are ordered by the caller.
  */
 #define MOE_ADAMW_STATE_BYTES 64
 moe_status_t moe_adamw_set_steps(double beta1, double beta2, int64_t steps, void *step_state,

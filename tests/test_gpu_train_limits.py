@@ -328,3 +328,21 @@ def test_calls_on_the_threads_own_streams():
     torch.cuda.synchronize()
     for *_, want, got in work:
         assert len(got) == 25 and all(torch.equal(a, b) for g in got for a, b in zip(g, want))
+
+
+def test_a_block_refuses_results_in_its_inputs():
+    """out in the memory of what the backward reads again, or of an input."""
+    from tests.test_gpu_train_step import make_block
+    block, x, r, dout, ds = make_block(40, False, True)
+    line = torch.empty(60, 256, dtype=BF16, device="cuda")
+    for kw in (dict(x=x, out=x), dict(x=x, residual=r, out=x), dict(x=x, residual=r, out=r),
+               dict(x=x, residual=r, out=block.s), dict(x=x, out=block.h_in), dict(x=line[:40], out=line[20:]),
+               dict(x=line[20:], residual=r, out=line[:40])):
+        with pytest.raises(ValueError, match="memory"):
+            block.forward(**kw)
+    out, s = block.forward(line[:20].repeat(2, 1), r, out=line[20:])
+    assert out.data_ptr() == line[20:].data_ptr()
+    block.forward(x, r)
+    for kw in (dict(dx=block.d_in), dict(dx=block.s)):
+        with pytest.raises(ValueError, match="memory"):
+            block.backward(dout, ds, **kw)

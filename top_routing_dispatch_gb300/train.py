@@ -210,6 +210,18 @@ def _scalar(t, device, name):
     return t.data_ptr()
 
 
+def _apart(t, others):
+    """Whether a contiguous tensor shares no memory with others (None: not there),
+    what lies between their rows counted as theirs."""
+    a, b = t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+    for o in others:
+        if o is not None and o.numel() and t.numel():
+            size = (sum((n - 1) * st for n, st in zip(o.shape, o.stride())) + 1) * o.element_size()
+            if a < o.data_ptr() + size and o.data_ptr() < b:
+                return False
+    return True
+
+
 class GradNorm:
     """The global norm of a list of gradients, and the factor that clips it.
 
@@ -463,11 +475,14 @@ class MoEBlock:
         """(out, s) for x (n, H) bfloat16 and residual like it, or None (then s
         is x).  out is allocated when not given; s is a buffer of the block
         where there is a residual, and holds until the next forward; backward
-        reads it (or x, which then must not change meanwhile)."""
+        reads it (or x, which then must not change meanwhile).  out shares no
+        memory with them."""
         d = self.desc
         _want(out is None or (out.shape == self.h_in.shape and out.dtype == _BF16
                               and out.is_contiguous() and out.device == self.h_in.device),
               "out: like x, contiguous")
+        _want(out is None or _apart(out, (x, residual, self.s, self.h_in)),
+              "out: shares memory with x, residual or a buffer of the block")
         self._enter(stream)
         if residual is None:
             self.norm(x, y=self.h_in, stats=self.stats, stream=stream)
@@ -503,6 +518,8 @@ class MoEBlock:
             _want(self.desc.n < 2 or stride >= self.desc.H, "ds: rows that do not overlap")
         if dx is not None:
             self.norm._out(dx, self.h_in.shape, _BF16, "dx")
+            _want(_apart(dx, (self.d_in, self._rows)),
+                  "dx: shares memory with the rows of the forward or a buffer of the block")
         self._enter(stream)
         api.moe_backward(self.desc, self.h_in, self.w_gate, self.w13, self.w2, dout, self.logits,
                          self.topk_idx, self.topk_w, self.offsets, self.inv_perm, self.x_perm,
