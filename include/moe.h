@@ -643,7 +643,9 @@ typedef struct {
  *   mu = sum s / H (0 if rms);  r = 1 / sqrt(sum (s - mu)^2 / H + eps)
  *   y = (s - mu) r weight + bias, rounded once
  * The mean is subtracted before the squares are summed.  A row whose squares
- * pass float32 gives y = bias; a NaN or infinity stays in its row.
+ * pass float32 gives y = bias (0 without one).  One whose own sum passes it, or
+ * with a NaN or infinity in it, gives NaN; if rms, a sum does no harm, and an
+ * infinity gives NaN in its place only.  No other row changes.
  *   x, residual (n, H): rows x_stride and residual_stride elements apart (at
  *   least H; not looked at where n < 2); s, y (n, H) contiguous; weight (H),
  *   bias (H) or NULL; s is written where residual is given, and NULL

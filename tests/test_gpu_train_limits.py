@@ -346,3 +346,47 @@ def test_a_block_refuses_results_in_its_inputs():
     for kw in (dict(dx=block.d_in), dict(dx=block.s)):
         with pytest.raises(ValueError, match="memory"):
             block.backward(dout, ds, **kw)
+
+
+# -------------------------------------------------------------- rows at the range's end
+@pytest.mark.parametrize("H", [64, 257, 2048, 20000, 70001])
+@pytest.mark.parametrize("T", [F32, BF16])
+def test_rows_beyond_float32(T, H):
+    """Squares beyond float32: y is the bias.  A sum of the row itself beyond it:
+    NaN, in that row only; without a mean there is no such sum."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    x = torch.randn(20, H, device="cuda", generator=g).to(T)
+    b = torch.randn(H, device="cuda", generator=g)
+    w = torch.ones(H, device="cuda")
+    for rms in (False, True):
+        layer = M().LayerNorm(w, b, rms=rms, dtype=T)
+        want = layer(x)
+        wild = x.clone()
+        wild[3] = 3e38  # their sum is infinite
+        wild[7] = torch.where(torch.arange(H, device="cuda") % 2 == 0, 1e25, -1e25).to(T)
+        got = layer(wild)
+        keep = torch.ones(20, dtype=torch.bool, device="cuda")
+        keep[3] = keep[7] = False
+        assert torch.equal(got[keep], want[keep])
+        assert torch.equal(got[7], b.to(T))
+        assert torch.equal(got[3], b.to(T)) if rms else torch.isnan(got[3].float()).all()
+
+
+def test_a_resumed_optimizer_rounds_as_the_first_one():
+    """beta2 0.999, 8 bits: states and their number of steps are all that the
+    random rounding depends on."""
+    def make():
+        return M().AdamW([torch.linspace(-1, 1, 5000, device="cuda")], [torch.linspace(-1, 1.7, 5000, device="cuda")],
+                         state=E4M3)
+    a, b = make(), make()
+    for _ in range(3):
+        a.step()
+    b.params[0].copy_(a.params[0])
+    b.load_state_dict({k: v.clone() if torch.is_tensor(v) else v for k, v in a.state_dict().items()})
+    for _ in range(2):
+        a.step()
+        b.step()
+    assert torch.equal(a.params[0], b.params[0]) and a.steps == b.steps == 5
+    for x, y in ((a.m, b.m), (a.v, b.v)):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
