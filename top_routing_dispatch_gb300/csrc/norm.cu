@@ -10,8 +10,9 @@
 //
 // Measured: 4096 rows of 2048 bf16 with residual (67 MB) 11.9 us, 5.6 TB/s;
 // 8192 rows of 7168 42 us (5.6 TB/s), with residual 79 (5.9); 1777 rows of 1031
-// float32 6.7 us, 4097 of 4099 bf16 with residual 34; one row of 2048 2.0.  A CTA per row without a ring took 34 us
-// for the first; the float32 operations one by one, 63 for the second.
+// float32 6.7 us, 4097 of 4099 bf16 with residual 34; one row of 2048 2.0.  A CTA
+// per row without a ring took 34 us for the first; the float32 operations one by
+// one, 63 for the second.
 #include "norm.cuh"
 
 namespace moe {
@@ -193,7 +194,9 @@ struct Forward {
   template <int N>
   static bool with(const NormArgs &a, cudaStream_t s, cudaError_t *e) {
     // 4096 rows of 2048 bf16 with residual: three slots 11.7 us, two 12.1, four
-    // 13.2; shifted, 4097 rows of 4099: four 51 us, three 56
+    // 13.2; shifted, bf16 with residual: 4097 x 4099 four 34 us, three 35; 21859 x
+    // 1535 49 and 57; 11646 x 2881 51 and 59 (14588 x 2300 45 and 43; float32 the
+    // same on both)
     constexpr int D = ring_slots<T, GS, VALS, N>(SHIFT ? 4 : 3);
     if constexpr (D == 0) {
       return false;

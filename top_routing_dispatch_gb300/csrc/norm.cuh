@@ -25,7 +25,8 @@
 namespace moe {
 
 // Threads of a CTA, at most: whole groups of about 512 threads, with 128 registers
-// each (two groups of 320: the forward is content with 96)
+// each (two groups of 320: the forward is content with 96; float32 with residual
+// spills 28 bytes)
 template <int GS>
 constexpr int kCta = GS > 512 ? GS : GS == 320 ? 640 : 512 / GS * GS;
 constexpr int kNormParts = 304;    // CTAs (or clusters) of the backward, at most
@@ -337,9 +338,10 @@ constexpr int ring_slots(int most) {
 //
 // Sizes between the powers of two: with phases a length just above (or, counting
 // the phase, just below) one leaves half of a larger group's threads to masks,
-// so there every such size is worth it (bf16 with residual: 16376 x 2049 on 160
-// threads 45 us, its backward 58, on 256 79 and 103; 8186 x 4099 on 320 47, 512
-// 81).  Without phases idle threads cost little: 96 and 160 threads were slower
+// so there such sizes are worth it (bf16 with residual: 32736 x 1025 on 96
+// threads 54 us, its backward 68, on 128 82 and 97; 16376 x 2049 on 160 45 and
+// 58, on 256 75 and 90; 8186 x 4099 on 320 47, on 512 78; float32 within 10 % of
+// the larger ones, 1025 values 45 and 59).  Without phases idle threads cost little: 96 and 160 threads were slower
 // (21845 x 1536 backward 51 us, on 128 45).
 template <bool BACK, typename T, bool SHIFT, template <typename, int, int, bool, bool> class G,
           typename A>
@@ -383,7 +385,9 @@ bool by_length(A &a, cudaStream_t s, cudaError_t *e) {
     if (size <= kMostCluster) return G<T, 1024, 8, SHIFT, true>::go(a, size, s, e);
   } else if (H <= 16384) {
     // 1024 threads of 16, where two rows fit into the ring (3001 x 16384 bf16
-    // with residual 65 us, 512 of 32 values 73)
+    // with residual 65 us, 512 of 32 values 73).  With 64 registers bf16 spills
+    // 80 bytes a thread, 144 with residual; half idle, just above 8192 values,
+    // it runs at 56 % of the copy rate
     return G<T, 1024, 16, SHIFT, false>::go(a, 1, s, e);
   }
   return false;

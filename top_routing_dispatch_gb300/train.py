@@ -73,7 +73,9 @@ class LayerNorm:
     weight, bias: (H,), float32 or of the rows' type; bias may be None.
     dtype: of the rows, float32 or bfloat16 (weight's type when None).  Both
     tensors are the caller's and are kept alive here; they may be changed in
-    place between calls."""
+    place between calls.  Results share no memory with arguments or each other,
+    and carry no graph for torch's automatic differentiation: gradients come
+    from backward."""
 
     def __init__(self, weight, bias=None, eps=1e-5, rms=False, dtype=None):
         _want(weight.dim() == 1 and weight.is_contiguous() and weight.dtype in (_F32, _BF16),
@@ -422,7 +424,8 @@ class MoEBlock:
     params and grads: the block's parameters and their float32 gradients, in
     one order, as AdamW and GradNorm take them; backward overwrites the
     gradients.  One forward's intermediates are kept, for the backward that
-    follows it; calls of one block are ordered by the caller.
+    follows it; calls of one block are ordered by the caller.  Torch's automatic
+    differentiation does not see them.
     """
 
     def __init__(self, desc, norm, w_gate, bias, w13, w2):
